@@ -287,6 +287,122 @@ int qmoe_read_error(const void* workspace_dev, void* stream, uint32_t* flags_out
 int qmoe_selftest_dequant(uint16_t* out_dev, void* stream);
 int qmoe_selftest_timeout(void* workspace_dev, long long limit_ns, void* stream);
 
+/*
+ * ------------------------------------------------------------------------------------
+ * Operators around the layer: the expert gate that produces its routing, tokens in expert
+ * order and back with their gradients, and a projection with per-request low-rank
+ * adapters.  Activations are bf16, fp16 or fp32 (QMOE_DTYPE_*), sums are fp32, and every
+ * result is deterministic.  Row strides (ld*) are in elements: at least the row's
+ * length, or 0 for the same row throughout (ldx of qmoe_lora_linear: not 0); outputs are
+ * contiguous.  The same conventions and limits hold as above
+ * (1 <= E <= 2048, 1 <= top_k <= 64, M * top_k < 2^27); M == 0 is a no-op.
+ */
+#define QMOE_DTYPE_BF16 0
+#define QMOE_DTYPE_FP16 1
+#define QMOE_DTYPE_FP32 2
+
+/* Scores of moe_gate. */
+#define QMOE_GATE_SOFTMAX 0
+#define QMOE_GATE_SIGMOID 1
+
+/*
+ * moe_gate — each token's experts and routing weights from the router's logits: the
+ * topk_ids and topk_weights that moe_route and moe_nvfp4_forward take.
+ *   logits_dev   [M][E] of `dtype`, rows ld apart
+ *   scoring      QMOE_GATE_SOFTMAX: an expert's choice value is its logit;
+ *                QMOE_GATE_SIGMOID: sigmoid(logit) + bias
+ *   bias_dev     fp32 [E] or NULL, QMOE_GATE_SIGMOID only (QMOE_ERR_ARG otherwise); it
+ *                takes part in the choice, not in the weights
+ *   n_group, topk_group  the experts are n_group equal runs (n_group <= 32 divides E);
+ *                only the topk_group best are chosen from, a run counting by its largest
+ *                choice value (softmax) or the sum of its two largest (sigmoid);
+ *                1, 1 for none
+ *   renormalize  nonzero: the weights of a token's chosen experts sum to `scale`
+ *                (softmax over the chosen; sigmoid scores over their sum + 1e-20);
+ *                zero: scale * softmax over all unmasked experts, or scale * sigmoid
+ *   topk_ids_dev int32 [M][top_k], by choice value, ties to the lowest expert
+ *   topk_weights_dev fp32 [M][top_k]
+ * An expert whose logit (or choice value) is -infinity or NaN is masked: it is never
+ * chosen.  Slots left over (fewer than top_k experts unmasked in the kept groups) get id
+ * -1, which the layer skips, and weight 0.  top_k <= E * topk_group / n_group
+ * (QMOE_ERR_SHAPE otherwise).
+ */
+int moe_gate(const void* logits_dev, int dtype, long long ld, int M, int E, int top_k, int scoring,
+             const float* bias_dev, int n_group, int topk_group, int renormalize, float scale,
+             int32_t* topk_ids_dev, float* topk_weights_dev, void* stream);
+
+/*
+ * moe_gate_backward — gradient of moe_gate's weights with respect to the logits, the
+ * choice of experts held fixed (the bias has no gradient).
+ *   dweights_dev fp32 [M][top_k], topk_ids_dev as moe_gate returned them (ids outside
+ *   [0, E) are left out; a token's ids are distinct); logits, scoring, renormalize and
+ *   scale as given to moe_gate
+ *   dlogits_dev  [M][E] of `dtype`, contiguous; every element is written
+ */
+int moe_gate_backward(const float* dweights_dev, const void* logits_dev, int dtype, long long ld,
+                      const int32_t* topk_ids_dev, int M, int E, int top_k, int scoring,
+                      int renormalize, float scale, void* dlogits_dev, void* stream);
+
+/*
+ * moe_sort_tokens — the activation rows of the routed pairs in expert order:
+ * xs[pair_pos[i]] = x[i / top_k], rows from offsets[E] on are zeros.  Ids as for
+ * moe_route, whose offsets, sorted_pair and pair_pos it also writes.
+ *   x_dev   [M][H] of `dtype`, rows ldx apart;  xs_dev  [M*top_k][H]
+ *   workspace_dev >= qmoe_sort_workspace_size(M, top_k, E) bytes, 256-byte aligned; its
+ *           first 4 bytes are the error word (qmoe_read_error)
+ */
+size_t qmoe_sort_workspace_size(int M, int top_k, int E);
+int moe_sort_tokens(const void* x_dev, int dtype, long long ldx, const int32_t* topk_ids_dev, int M,
+                    int H, int top_k, int E, void* xs_dev, int32_t* offsets_dev,
+                    int32_t* sorted_pair_dev, int32_t* pair_pos_dev, void* workspace_dev,
+                    size_t ws_bytes, void* stream);
+
+/* moe_sort_tokens_backward — dx[m] = sum over the token's routed pairs of dxs[pos], in
+ * slot order.  dxs_dev [M*top_k][H], rows ld apart; dx_dev [M][H]. */
+int moe_sort_tokens_backward(const void* dxs_dev, int dtype, long long ld,
+                             const int32_t* pair_pos_dev, int M, int H, int top_k, void* dx_dev,
+                             void* stream);
+
+/* moe_unsort_tokens — out[m] = sum over the token's routed pairs of w[m][k] * y[pos], in
+ * slot order.  y_dev [M*top_k][H], rows ldy apart; topk_weights_dev fp32 [M][top_k];
+ * out_dev [M][H].  Rows of y past the routed pairs are not read. */
+int moe_unsort_tokens(const void* y_dev, int dtype, long long ldy, const int32_t* pair_pos_dev,
+                      const float* topk_weights_dev, int M, int H, int top_k, void* out_dev,
+                      void* stream);
+
+/* moe_unsort_tokens_backward — dy[pos] = w[m][k] * dout[m] and
+ * dweights[m][k] = <dout[m], y[pos]>; skipped pairs have dweights 0, rows of dy past the
+ * routed pairs are zeros.  dout_dev [M][H], rows ldd apart; y_dev as above; dy_dev
+ * [M*top_k][H]; dweights_dev fp32 [M][top_k]. */
+int moe_unsort_tokens_backward(const void* dout_dev, long long ldd, const void* y_dev,
+                               long long ldy, int dtype, const int32_t* sorted_pair_dev,
+                               const int32_t* pair_pos_dev, const float* topk_weights_dev, int M,
+                               int H, int top_k, void* dy_dev, float* dweights_dev, void* stream);
+
+/*
+ * qmoe_lora_linear — a projection shared by all requests with a low-rank adapter each:
+ *   out[m] = base[m] + x[m] . w^T + scales[a] * (x[m] . A[a]^T) . B[a]^T,  a = adapter_ids[m]
+ *   x_dev     bf16 or fp16 [M][K], rows ldx apart
+ *   w_dev     [N][K], or NULL: no shared product (an adapter beside a projection computed
+ *             elsewhere, given as base)
+ *   a_dev, b_dev  [L][R][K] and [L][N][R]; an adapter of a lower rank is padded with zeros
+ *   adapter_ids_dev int32 [M]: -1 (or any negative) for a token without an adapter; ids
+ *             of L or more count as none and set QMOE_FLAG_BAD_ID
+ *   scales_dev fp32 [L]
+ *   base_dev  [M][N], rows ldbase apart, or NULL; may be out_dev itself
+ *   out_dev   [M][N]
+ * K % 8 == 0, R % 8 == 0, 8 <= R <= 128, K <= 65536, N <= 131072, 1 <= L <= 65536; x, w, a
+ * and b are 16-byte aligned and ldx is a multiple of 8.
+ *   workspace_dev >= qmoe_lora_workspace_size(M, K, N, R, L) bytes, 256-byte aligned,
+ *             starting with the error word
+ */
+size_t qmoe_lora_workspace_size(int M, int K, int N, int R, int L);
+int qmoe_lora_linear(const void* x_dev, int dtype, long long ldx, const void* w_dev,
+                     const void* a_dev, const void* b_dev, const int32_t* adapter_ids_dev,
+                     const float* scales_dev, const void* base_dev, long long ldbase,
+                     void* out_dev, int M, int K, int N, int R, int L, void* workspace_dev,
+                     size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -21,6 +21,8 @@ constexpr int kMaxDevices = 64;
 std::atomic<int> g_num_sms[kMaxDevices];
 std::atomic<int> g_arch_ok[kMaxDevices];  // 0 unknown, 1 ok, -1 unsupported
 
+}  // namespace
+
 int device_info(int* num_sms) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return QMOE_ERR_CUDA;
@@ -39,6 +41,8 @@ int device_info(int* num_sms) {
   *num_sms = g_num_sms[dev].load(std::memory_order_relaxed);
   return QMOE_OK;
 }
+
+namespace {
 
 // Driver entry points, resolved once (a function-local static is initialised once even
 // when several threads get here first).

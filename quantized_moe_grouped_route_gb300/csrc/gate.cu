@@ -1,0 +1,365 @@
+// The expert gate: each token's top_k experts and their routing weights from the router's
+// logits, and the gradient of the logits.
+//
+// A row of logits l[0..E) gives every expert a choice value: l itself (softmax scoring) or
+// sigmoid(l) + bias (sigmoid scoring).  An expert whose logit or choice value is -infinity
+// or NaN is masked.  With groups, only the topk_group best of n_group equal runs of experts
+// stay, a group counting by its largest choice value (softmax) or by the sum of its two
+// largest (sigmoid).  The top_k unmasked experts are taken by choice value, ties to the
+// lowest index; a slot without an expert gets id -1 and weight 0.  Weights:
+//   softmax, renormalized  w = scale exp(l_e) / sum over the chosen of exp(l)
+//   softmax                w = scale exp(l_e) / sum over all unmasked of exp(l)
+//   sigmoid, renormalized  w = scale s_e / (sum over the chosen of s + 1e-20)
+//   sigmoid                w = scale s_e
+// The choice value is computed with the same fp32 operations as its definition (one
+// expf, one addition, one division, one addition), so which experts are chosen does not
+// depend on how a kernel is arranged; only the weights' sums have an order of their own.
+#include <math.h>
+
+#include "common.cuh"
+#include "launch.h"
+#include "pack.cuh"
+
+namespace qmoe {
+namespace {
+
+constexpr int kGateWarps = 4;
+
+// An unsigned key in the order of the float (both zeros equal); 0 is kept for masked.
+__device__ __forceinline__ uint32_t order_key(float v) {
+  const uint32_t u = __float_as_uint(v + 0.0f);
+  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+
+__device__ __forceinline__ float sigmoid_f32(float l) { return __fdiv_rn(1.0f, 1.0f + expf(-l)); }
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+
+// Which groups stay, as a bit mask: the warp's choice values are in row[E] (shared).  The
+// lanes of a warp are dealt to the groups (a power of two of them each); a group's rank is
+// the count of groups before it by (score, index).
+__device__ __forceinline__ uint32_t best_groups(const float* row, int E, int n_group,
+                                                int topk_group, bool top2, int lane) {
+  const int size = E / n_group;
+  int per = 32;  // lanes per group
+  while (per * n_group > 32) per >>= 1;
+  const int g = lane / per, sub = lane % per;
+  float a = -INFINITY, b = -INFINITY;  // the two largest
+  if (g < n_group) {
+    const int n = (size + per - 1) / per;
+    int i = g % n;  // start apart, so that the groups' reads fall on different banks
+    for (int t = 0; t < n; ++t) {
+      const int e = i * per + sub;
+      const float v = e < size ? row[g * size + e] : -INFINITY;
+      if (v > a) {
+        b = a;
+        a = v;
+      } else if (v > b) {
+        b = v;
+      }
+      if (++i == n) i = 0;
+    }
+  }
+  for (int o = 1; o < per; o <<= 1) {
+    const float a2 = __shfl_xor_sync(0xffffffffu, a, o);
+    const float b2 = __shfl_xor_sync(0xffffffffu, b, o);
+    const float lo = fminf(a, a2);
+    a = fmaxf(a, a2);
+    b = fmaxf(lo, fmaxf(b, b2));
+  }
+  // a group of one expert has no second: it counts by that expert alone
+  const float score = top2 && size > 1 ? a + b : a;
+  int rank = 0;
+  for (int h = 0; h < n_group; ++h) {
+    const float s = __shfl_sync(0xffffffffu, score, h * per);
+    rank += s > score || (s == score && h < g);
+  }
+  const uint32_t lanes = __ballot_sync(0xffffffffu, g < n_group && sub == 0 && rank < topk_group);
+  uint32_t keep = 0;
+  for (int h = 0; h < n_group; ++h) keep |= ((lanes >> (h * per)) & 1u) << h;
+  return keep;
+}
+
+// A warp per row; lane holds the experts lane, lane + 32, ..  The row's keys stay in
+// registers; each of the top_k rounds takes the warp's largest key (one redux), and only
+// the winning lane looks for its next best.
+template <class T, int VPT>
+__global__ void __launch_bounds__(kGateWarps * 32) gate_kernel(const GateArgs p) {
+  extern __shared__ float rows[];  // [kGateWarps][E], with groups only
+  grid_dep_wait();
+  grid_dep_launch();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const bool sigmoid = p.scoring == QMOE_GATE_SIGMOID;
+  for (long long m = (long long)blockIdx.x * kGateWarps + warp; m < p.M;
+       m += (long long)gridDim.x * kGateWarps) {
+    const T* l = reinterpret_cast<const T*>(p.logits) + m * p.ld;
+    float v[VPT];
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      const int e = j * 32 + lane;
+      v[j] = e < p.E ? to_f32(l[e]) : -INFINITY;
+    }
+    float top = 0.f, total = 0.f;  // over all unmasked experts
+    if (!sigmoid && !p.renormalize) {
+      top = -INFINITY;
+#pragma unroll
+      for (int j = 0; j < VPT; ++j) top = fmaxf(top, v[j]);  // fmaxf ignores NaN
+      top = warp_max(top);
+#pragma unroll
+      for (int j = 0; j < VPT; ++j)
+        if (v[j] > -INFINITY) total += expf(v[j] - top);
+      total = warp_sum(total);
+    }
+    uint32_t key[VPT];
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      const int e = j * 32 + lane;
+      float c = v[j];
+      if (sigmoid && c > -INFINITY) {
+        c = sigmoid_f32(c);
+        if (p.bias) c += p.bias[e];
+      }
+      if (!(c > -INFINITY)) c = -INFINITY;
+      v[j] = c;
+      key[j] = c > -INFINITY ? order_key(c) : 0u;
+    }
+    if (p.n_group > 1) {
+      float* row = rows + warp * p.E;
+      __syncwarp();
+#pragma unroll
+      for (int j = 0; j < VPT; ++j)
+        if (j * 32 + lane < p.E) row[j * 32 + lane] = v[j];
+      __syncwarp();
+      const uint32_t keep = best_groups(row, p.E, p.n_group, p.topk_group, sigmoid, lane);
+#pragma unroll
+      for (int j = 0; j < VPT; ++j) {
+        const int g = (j * 32 + lane) / (p.E / p.n_group);
+        if (!((keep >> (g & 31)) & 1u)) key[j] = 0u;
+      }
+    }
+    int mine[2] = {-1, -1};  // lane r: the experts of slots r and r + 32
+    uint32_t best = 0;
+    int best_j = 0;
+#pragma unroll
+    for (int j = 0; j < VPT; ++j)
+      if (key[j] > best) {
+        best = key[j];
+        best_j = j;
+      }
+    for (int r = 0; r < p.top_k; ++r) {
+      const uint32_t w = __reduce_max_sync(0xffffffffu, best);
+      if (w == 0u) break;
+      const int e_here = best == w ? best_j * 32 + lane : 0x7fffffff;
+      const int e = (int)__reduce_min_sync(0xffffffffu, (unsigned)e_here);
+      if (lane == (r & 31)) {
+        if (r < 32)
+          mine[0] = e;
+        else
+          mine[1] = e;
+      }
+      if (e_here == e) {
+        best = 0;
+        const int gone = best_j;
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+          if (j == gone) key[j] = 0u;
+          if (key[j] > best) {
+            best = key[j];
+            best_j = j;
+          }
+        }
+      }
+    }
+    float s[2] = {0.f, 0.f};
+    float lv[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) lv[i] = mine[i] >= 0 ? to_f32(l[mine[i]]) : -INFINITY;
+    if (sigmoid) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        if (mine[i] >= 0) s[i] = sigmoid_f32(lv[i]);
+      if (p.renormalize) {
+        const float d = warp_sum(s[0] + s[1]) + 1e-20f;
+        s[0] /= d;
+        s[1] /= d;
+      }
+    } else {
+      if (p.renormalize) top = __shfl_sync(0xffffffffu, lv[0], 0);  // slot 0 has the largest
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        if (mine[i] >= 0) s[i] = expf(lv[i] - top);
+      if (p.renormalize) total = warp_sum(s[0] + s[1]);
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        if (mine[i] >= 0) s[i] /= total;
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = lane + 32 * i;
+      if (r < p.top_k) {
+        p.ids[m * p.top_k + r] = mine[i];
+        p.weights[m * p.top_k + r] = mine[i] >= 0 ? s[i] * p.scale : 0.f;
+      }
+    }
+  }
+}
+
+// Gradient of the logits, a warp per row (p = the chosen experts' scores, c = scale):
+//   softmax, renormalized  dl_e = c p_e (dw_e - sum p dw) on the chosen, 0 elsewhere
+//   softmax                dl_e = c p_e (dw_e [chosen] - sum over the chosen of p dw)
+//   sigmoid, renormalized  dl_e = c / S (dw_e - sum (s / S) dw) s_e (1 - s_e), S = sum s + 1e-20
+//   sigmoid                dl_e = c dw_e s_e (1 - s_e)
+// The chosen experts' gradients go through a shared row, so that the (mostly zero) output
+// row leaves in wide stores.
+template <class T, int N>
+__global__ void __launch_bounds__(kGateWarps * 32) gate_backward_kernel(const GateArgs p) {
+  extern __shared__ float rows[];  // [kGateWarps][E]
+  using P_ = Pack<T, N>;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  float* row = rows + warp * p.E;
+  for (int e = lane; e < p.E; e += 32) row[e] = 0.f;
+  __syncwarp();
+  grid_dep_wait();
+  grid_dep_launch();
+  const bool sigmoid = p.scoring == QMOE_GATE_SIGMOID;
+  for (long long m = (long long)blockIdx.x * kGateWarps + warp; m < p.M;
+       m += (long long)gridDim.x * kGateWarps) {
+    const T* l = reinterpret_cast<const T*>(p.logits) + m * p.ld;
+    int e[2];
+    float s[2], dw[2], lv[2], d[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = lane + 32 * i;
+      e[i] = r < p.top_k ? p.ids_in[m * p.top_k + r] : -1;
+      if ((unsigned)e[i] >= (unsigned)p.E) e[i] = -1;
+      dw[i] = e[i] >= 0 ? p.dweights[m * p.top_k + r] : 0.f;
+      lv[i] = e[i] >= 0 ? to_f32(l[e[i]]) : -INFINITY;
+      s[i] = d[i] = 0.f;
+    }
+    float top = 0.f, dense = 0.f;  // dense: what every expert's exp(l - top) is multiplied by
+    if (sigmoid) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        if (e[i] >= 0) s[i] = sigmoid_f32(lv[i]);
+      float S = 1.f, inner = 0.f;
+      if (p.renormalize) {
+        S = warp_sum(s[0] + s[1]) + 1e-20f;
+        inner = warp_sum(s[0] / S * dw[0] + s[1] / S * dw[1]);
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) d[i] = p.scale / S * (dw[i] - inner) * s[i] * (1.f - s[i]);
+    } else {
+      float total = 0.f;
+      if (p.renormalize) {
+        top = warp_max(fmaxf(lv[0], lv[1]));
+      } else {
+        top = -INFINITY;
+        for (int i = lane; i < p.E; i += 32) top = fmaxf(top, to_f32(l[i]));
+        top = warp_max(top);
+        for (int i = lane; i < p.E; i += 32) {
+          const float li = to_f32(l[i]);
+          if (li > -INFINITY) total += expf(li - top);
+        }
+        total = warp_sum(total);
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        if (e[i] >= 0) s[i] = expf(lv[i] - top);
+      if (p.renormalize) total = warp_sum(s[0] + s[1]);
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        if (e[i] >= 0) s[i] /= total;
+      const float inner = warp_sum(s[0] * dw[0] + s[1] * dw[1]);
+      const bool any = __any_sync(0xffffffffu, e[0] >= 0 || e[1] >= 0);
+      if (!p.renormalize && any) dense = -p.scale * inner / total;
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        d[i] = p.scale * s[i] * (dw[i] - (p.renormalize ? inner : 0.f));
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      if (e[i] >= 0) row[e[i]] = d[i];
+    __syncwarp();
+    T* out = reinterpret_cast<T*>(p.dlogits) + (size_t)m * p.E;
+    for (int c = lane; c < p.E / N; c += 32) {
+      P_ o;
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        float g = row[c * N + i];
+        if (dense != 0.f) {
+          const float li = to_f32(l[c * N + i]);
+          if (li > -INFINITY) g += dense * expf(li - top);
+        }
+        o.v[i] = from_f32<T>(g);
+      }
+      *reinterpret_cast<typename P_::raw_t*>(out + (size_t)c * N) = o.raw;
+    }
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      if (e[i] >= 0) row[e[i]] = 0.f;
+    __syncwarp();
+  }
+}
+
+template <class K>
+cudaError_t launch(K* kernel, const GateArgs& p, size_t smem, int num_sms, cudaStream_t stream) {
+  cudaError_t rc =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (rc != cudaSuccess) return rc;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1] = {pdl_attribute()};
+  long long blocks = ((long long)p.M + kGateWarps - 1) / kGateWarps;
+  if (blocks > num_sms * 32LL) blocks = num_sms * 32LL;
+  cfg.gridDim = dim3((unsigned)blocks);
+  cfg.blockDim = dim3(kGateWarps * 32);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+template <class T>
+cudaError_t gate(const GateArgs& p, int num_sms, cudaStream_t stream) {
+  const size_t smem = p.n_group > 1 ? (size_t)kGateWarps * p.E * sizeof(float) : 0;
+  if (p.E <= 32) return launch(gate_kernel<T, 1>, p, smem, num_sms, stream);
+  if (p.E <= 64) return launch(gate_kernel<T, 2>, p, smem, num_sms, stream);
+  if (p.E <= 128) return launch(gate_kernel<T, 4>, p, smem, num_sms, stream);
+  if (p.E <= 256) return launch(gate_kernel<T, 8>, p, smem, num_sms, stream);
+  if (p.E <= 512) return launch(gate_kernel<T, 16>, p, smem, num_sms, stream);
+  if (p.E <= 1024) return launch(gate_kernel<T, 32>, p, smem, num_sms, stream);
+  return launch(gate_kernel<T, 64>, p, smem, num_sms, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_gate(const GateArgs& p, int dtype, int num_sms, cudaStream_t stream) {
+  if (dtype == QMOE_DTYPE_BF16) return gate<__nv_bfloat16>(p, num_sms, stream);
+  if (dtype == QMOE_DTYPE_FP16) return gate<__half>(p, num_sms, stream);
+  return gate<float>(p, num_sms, stream);
+}
+
+cudaError_t launch_gate_backward(const GateArgs& p, int dtype, bool vec, int num_sms,
+                                 cudaStream_t stream) {
+  const size_t smem = (size_t)kGateWarps * p.E * sizeof(float);
+  if (dtype == QMOE_DTYPE_BF16)
+    return vec ? launch(gate_backward_kernel<__nv_bfloat16, 8>, p, smem, num_sms, stream)
+               : launch(gate_backward_kernel<__nv_bfloat16, 1>, p, smem, num_sms, stream);
+  if (dtype == QMOE_DTYPE_FP16)
+    return vec ? launch(gate_backward_kernel<__half, 8>, p, smem, num_sms, stream)
+               : launch(gate_backward_kernel<__half, 1>, p, smem, num_sms, stream);
+  return vec ? launch(gate_backward_kernel<float, 4>, p, smem, num_sms, stream)
+             : launch(gate_backward_kernel<float, 1>, p, smem, num_sms, stream);
+}
+
+}  // namespace qmoe

@@ -24,6 +24,10 @@ cudaError_t launch_route(const int32_t* ids, int P, int E, int tile_n, int32_t* 
                          int32_t* order = nullptr, int small_rows = 0, int clear_words = 1,
                          bool pdl = false);
 
+// api.cu
+// SM count of the current device; QMOE_ERR_ARCH unless it runs sm_103a code
+int device_info(int* num_sms);
+
 // misc.cu
 // scale_layout: QMOE_SCALES_PLAIN, _SWIZZLED_128X4 or _PACKED_U32
 cudaError_t launch_repack(const uint8_t* w, const uint8_t* s, int E, int N, int K, bool w13,
@@ -111,5 +115,68 @@ cudaError_t launch_gemm2(GemmKind kind, const CUtensorMap& tmap_b, const GemmPar
 // elements.
 int gemm_b_box_rows(int sched);
 int gemm_b_box_slabs(int sched);
+
+// gate.cu
+struct GateArgs {
+  const void* logits;  // [M][E], rows ld elements apart
+  long long ld;
+  int M, E, top_k;
+  int scoring;  // QMOE_GATE_*
+  const float* bias;
+  int n_group, topk_group;
+  int renormalize;
+  float scale;
+  int32_t* ids;  // forward's outputs
+  float* weights;
+  const float* dweights;  // backward's inputs and output
+  const int32_t* ids_in;
+  void* dlogits;
+};
+cudaError_t launch_gate(const GateArgs& p, int dtype, int num_sms, cudaStream_t stream);
+// vec: the output rows are 16-byte aligned and a multiple of 16 bytes long
+cudaError_t launch_gate_backward(const GateArgs& p, int dtype, bool vec, int num_sms,
+                                 cudaStream_t stream);
+
+// tokens.cu
+// xs[pair_pos[i]] = x[i / top_k] in chunks of chunk_bytes (16, 4 or 2, dividing the rows,
+// their stride and the pointers), zeros from row n_routed[0] on
+cudaError_t launch_sort_copy(const void* x, long long ldx_bytes, const int32_t* pair_pos,
+                             const int32_t* n_routed, int M, int top_k, long long row_bytes,
+                             int chunk_bytes, void* xs, int num_sms, cudaStream_t stream);
+struct TokenArgs {
+  const void* y;  // pair rows [M * top_k][H], rows ldy elements apart
+  long long ldy;
+  const void* dout;  // token rows [M][H], rows ldd elements apart (unsort backward)
+  long long ldd;
+  const int32_t* sorted_pair;
+  const int32_t* pair_pos;
+  const float* weights;  // NULL: all ones
+  int M, H, top_k;
+  void* out;
+  float* dweights;
+};
+// vec: every row is 16-byte aligned and a multiple of 16 bytes long
+cudaError_t launch_unsort(const TokenArgs& a, int dtype, bool vec, int num_sms,
+                          cudaStream_t stream);
+cudaError_t launch_unsort_backward(const TokenArgs& a, int dtype, bool vec, int num_sms,
+                                   cudaStream_t stream);
+
+// lora.cu
+struct LoraArgs {
+  const void* x;  // [M][K], rows ldx elements apart
+  long long ldx;
+  const void* w;  // [N][K] or NULL
+  const void* a;  // [L][R][K]
+  const void* b;  // [L][N][R]
+  const int32_t* ids;
+  const float* scales;
+  const void* base;  // [M][N], rows ldbase elements apart, or NULL
+  long long ldbase;
+  void* out;  // [M][N]
+  int M, K, N, R, L;
+  unsigned int* err;
+  float* t;  // [M][R] scaled low-rank activations
+};
+cudaError_t launch_lora(const LoraArgs& p, int dtype, int num_sms, cudaStream_t stream);
 
 }  // namespace qmoe

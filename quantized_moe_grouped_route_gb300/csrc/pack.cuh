@@ -1,0 +1,59 @@
+// Chunks of consecutive elements: loads, stores and the conversion to and from fp32 of
+// the three element types (QMOE_DTYPE_*) the token operators take.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <stdint.h>
+
+namespace qmoe {
+
+__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
+__device__ __forceinline__ float to_f32(float v) { return v; }
+template <class T>
+__device__ __forceinline__ T from_f32(float v);
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) {
+  return __float2bfloat16_rn(v);
+}
+template <>
+__device__ __forceinline__ __half from_f32<__half>(float v) {
+  return __float2half_rn(v);
+}
+template <>
+__device__ __forceinline__ float from_f32<float>(float v) {
+  return v;
+}
+
+// Bytes elements of one chunk move as: the unsigned type of that width.
+template <int BYTES>
+struct Raw;
+template <>
+struct Raw<16> {
+  using type = uint4;
+};
+template <>
+struct Raw<8> {
+  using type = uint2;
+};
+template <>
+struct Raw<4> {
+  using type = uint32_t;
+};
+template <>
+struct Raw<2> {
+  using type = uint16_t;
+};
+
+// N consecutive elements of type T, moved in one access.
+template <class T, int N>
+union Pack {
+  static constexpr int kN = N;
+  using raw_t = typename Raw<sizeof(T) * N>::type;
+  raw_t raw;
+  T v[N];
+  __device__ Pack() {}
+};
+
+}  // namespace qmoe

@@ -66,6 +66,7 @@ def lib():
 
 def _bind(L):
     P, i32, sz, i64 = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_longlong
+    f32 = ctypes.c_float
     sig = {
         "qmoe_sched_tile_n": (i32, [i32, i32, i32, i32]),
         "qmoe_max_tiles": (i32, [i32, i32, i32, i32]),
@@ -91,6 +92,17 @@ def _bind(L):
         "qmoe_noalloc_read_error": (i32, [P, ctypes.POINTER(ctypes.c_uint32)]),
         "qmoe_selftest_dequant": (i32, [P, P]),
         "qmoe_selftest_timeout": (i32, [P, i64, P]),
+        "moe_gate": (i32, [P, i32, i64, i32, i32, i32, i32, P, i32, i32, i32, f32, P, P, P]),
+        "moe_gate_backward": (i32, [P, P, i32, i64, P, i32, i32, i32, i32, i32, f32, P, P]),
+        "qmoe_sort_workspace_size": (sz, [i32, i32, i32]),
+        "moe_sort_tokens": (i32, [P, i32, i64, P, i32, i32, i32, i32, P, P, P, P, P, sz, P]),
+        "moe_sort_tokens_backward": (i32, [P, i32, i64, P, i32, i32, i32, P, P]),
+        "moe_unsort_tokens": (i32, [P, i32, i64, P, P, i32, i32, i32, P, P]),
+        "moe_unsort_tokens_backward": (i32, [P, i64, P, i64, i32, P, P, P, i32, i32, i32, P, P,
+                                             P]),
+        "qmoe_lora_workspace_size": (sz, [i32, i32, i32, i32, i32]),
+        "qmoe_lora_linear": (i32, [P, i32, i64, P, P, P, P, P, P, i64, P, i32, i32, i32, i32, i32,
+                                   P, sz, P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(L, name)
