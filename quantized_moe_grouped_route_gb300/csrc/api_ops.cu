@@ -252,14 +252,40 @@ int moe_unsort_tokens_backward(const void* dout_dev, long long ldd, const void* 
 
 static int check_lora(int M, int K, int N, int R, int L) {
   if (M < 0 || K < 8 || K > 65536 || K % 8 || N < 1 || N > 131072 || R < 8 || R > 128 || R % 8 ||
-      L < 1 || L > 65536 || M >= (1 << 27))
+      L < 1 || L > 65536 || (long long)M * R >= (1LL << 31))
     return QMOE_ERR_SHAPE;
   return QMOE_OK;
 }
 
+// Workspace of qmoe_lora_linear: the error word's block, arrival counters, the tiles'
+// adapter lists, the low-rank activations, partial sums.
+struct LoraLayout {
+  size_t cnt, count, bad, list, t, part, total;
+  int n_cnt;
+};
+
+static LoraLayout lora_layout(const LoraPlan& P, int M, int R) {
+  LoraLayout L;
+  const size_t units = (size_t)P.tiles * P.blocks;
+  L.n_cnt = P.splits > 1 ? (int)(units * P.cg * 4) : 0;
+  L.cnt = kWsHeaderBytes;
+  L.count = align_up(L.cnt + 4 * (size_t)L.n_cnt, 256);
+  L.bad = align_up(L.count + 4 * (size_t)P.tiles, 256);
+  L.list = align_up(L.bad + 4 * (size_t)P.tiles, 256);
+  L.t = align_up(L.list + 4 * (size_t)P.tiles * P.tile_n, 256);
+  L.part = align_up(L.t + 4 * (size_t)M * R, 256);
+  L.total = L.part;
+  if (P.splits > 1) L.total += units * P.splits * P.cg * P.tile_n * 128 * sizeof(float);
+  return L;
+}
+
+// The larger of the plans with and without w, so that one workspace serves both.
 size_t qmoe_lora_workspace_size(int M, int K, int N, int R, int L) {
   if (check_lora(M, K, N, R, L) != QMOE_OK) return 0;
-  return align_up(kWsHeaderBytes + (size_t)M * R * sizeof(float), 256);
+  if (M == 0) return kWsHeaderBytes;
+  const size_t with_w = lora_layout(lora_plan(M, K, N, true), M, R).total;
+  const size_t without = lora_layout(lora_plan(M, K, N, false), M, R).total;
+  return with_w > without ? with_w : without;
 }
 
 int qmoe_lora_linear(const void* x_dev, int dtype, long long ldx, const void* w_dev,
@@ -282,13 +308,14 @@ int qmoe_lora_linear(const void* x_dev, int dtype, long long ldx, const void* w_
   int sms = 0;
   rc = device_info(&sms);
   if (rc != QMOE_OK) return rc;
-  uint8_t* ws = reinterpret_cast<uint8_t*>(workspace_dev);
   LoraArgs p = {};
+  static_cast<LoraPlan&>(p) = lora_plan(M, K, N, w_dev != nullptr);
+  const LoraLayout W = lora_layout(p, M, R);
+  uint8_t* ws = reinterpret_cast<uint8_t*>(workspace_dev);
+  p.dtype = dtype;
   p.x = x_dev;
   p.ldx = ldx;
-  p.w = w_dev;
   p.a = a_dev;
-  p.b = b_dev;
   p.ids = adapter_ids_dev;
   p.scales = scales_dev;
   p.base = base_dev;
@@ -300,8 +327,28 @@ int qmoe_lora_linear(const void* x_dev, int dtype, long long ldx, const void* w_
   p.R = R;
   p.L = L;
   p.err = reinterpret_cast<unsigned int*>(ws);
-  p.t = reinterpret_cast<float*>(ws + kWsHeaderBytes);
-  return cuda_rc(launch_lora(p, dtype, sms, reinterpret_cast<cudaStream_t>(stream)));
+  p.cnt = reinterpret_cast<int*>(ws + W.cnt);
+  p.n_cnt = W.n_cnt;
+  p.count = reinterpret_cast<int*>(ws + W.count);
+  p.bad = reinterpret_cast<int*>(ws + W.bad);
+  p.list = reinterpret_cast<int*>(ws + W.list);
+  p.t = reinterpret_cast<float*>(ws + W.t);
+  p.part = reinterpret_cast<float*>(ws + W.part);
+
+  LoraMaps maps;
+  const uint64_t dx[2] = {(uint64_t)K, (uint64_t)M}, sx[1] = {(uint64_t)ldx * 2};
+  const uint32_t bx[2] = {64, (uint32_t)(p.tile_n / p.cg)};
+  const uint64_t dw[2] = {(uint64_t)K, (uint64_t)N}, sw[1] = {(uint64_t)K * 2};
+  const uint32_t bw[2] = {64, 128};
+  const uint64_t db[3] = {(uint64_t)R, (uint64_t)N, (uint64_t)L};
+  const uint64_t sb[2] = {(uint64_t)R * 2, (uint64_t)N * R * 2};
+  const uint32_t bb[3] = {64, 128, 1};
+  rc = make_tmap16(&maps.x, dtype, x_dev, 2, dx, sx, bx);
+  if (rc == QMOE_OK && w_dev) rc = make_tmap16(&maps.w, dtype, w_dev, 2, dw, sw, bw);
+  if (rc == QMOE_OK && !w_dev) maps.w = maps.x;  // never read
+  if (rc == QMOE_OK) rc = make_tmap16(&maps.b, dtype, b_dev, 3, db, sb, bb);
+  if (rc != QMOE_OK) return rc;
+  return cuda_rc(launch_lora(p, maps, sms, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -93,6 +93,15 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, err));
 }
 
+// Wait for copies or MMAs in flight before the CTA exits or releases TMEM (at most 50 ms).
+__device__ __forceinline__ bool drain_wait(uint32_t bar, uint32_t parity) {
+  const unsigned long long t0 = globaltimer_ns();
+  while (!mbar_try_wait(bar, parity)) {
+    if ((long long)(globaltimer_ns() - t0) > 50000000LL) return false;  // 50 ms
+  }
+  return true;
+}
+
 // One lane of a converged warp; used as a predicate so that the single-thread
 // instructions below (TMA, MMA, commit) are issued once while the warp's control
 // flow stays uniform (issuing the copies from a divergent single thread was several

@@ -229,14 +229,6 @@ __device__ __forceinline__ int part_tile(const GemmParams& p, int j) {
   return p.tile_order[(p.tile_part == 1 ? 0 : p.n_tiles[1]) + j];
 }
 
-__device__ __forceinline__ bool drain_wait(uint32_t bar, uint32_t parity) {
-  const unsigned long long t0 = globaltimer_ns();
-  while (!mbar_try_wait(bar, parity)) {
-    if ((long long)(globaltimer_ns() - t0) > 50000000LL) return false;  // 50 ms
-  }
-  return true;
-}
-
 template <int NMAX, int RS, int SL, int ACCB, int DG, int NMW, int KS, bool BIN, bool FC1,
           bool CLAMP = false>
 __global__ void __launch_bounds__(gemm_threads(DG), 1)

@@ -27,6 +27,10 @@ cudaError_t launch_route(const int32_t* ids, int P, int E, int tile_n, int32_t* 
 // api.cu
 // SM count of the current device; QMOE_ERR_ARCH unless it runs sm_103a code
 int device_info(int* num_sms);
+// Tensor map of 16-bit elements (QMOE_DTYPE_BF16 or _FP16), 128-byte swizzle, zeros out of
+// bounds; strides in bytes, of all dimensions but the innermost
+int make_tmap16(CUtensorMap* map, int dtype, const void* base, int rank, const uint64_t* dims,
+                const uint64_t* strides, const uint32_t* box);
 
 // misc.cu
 // scale_layout: QMOE_SCALES_PLAIN, _SWIZZLED_128X4 or _PACKED_U32
@@ -162,21 +166,37 @@ cudaError_t launch_unsort_backward(const TokenArgs& a, int dtype, bool vec, int 
                                    cudaStream_t stream);
 
 // lora.cu
-struct LoraArgs {
+// How a problem is cut: token tiles of tile_n (a multiple of 16, at most 256), units of one
+// tile x 128 * cg rows of w (cg: CTAs per unit), each unit's ksteps steps of 64 of K in
+// `splits` segments.
+struct LoraPlan {
+  int cg, tile_n, tiles, blocks, ksteps, splits;
+};
+LoraPlan lora_plan(int M, int K, int N, bool has_w);
+struct LoraArgs : LoraPlan {
+  int dtype;
   const void* x;  // [M][K], rows ldx elements apart
   long long ldx;
-  const void* w;  // [N][K] or NULL
   const void* a;  // [L][R][K]
-  const void* b;  // [L][N][R]
   const int32_t* ids;
   const float* scales;
   const void* base;  // [M][N], rows ldbase elements apart, or NULL
   long long ldbase;
   void* out;  // [M][N]
   int M, K, N, R, L;
+  int stages;  // of the GEMM's ring (launch_lora)
   unsigned int* err;
-  float* t;  // [M][R] scaled low-rank activations
+  int* cnt;    // arrival counters [tiles * blocks][cg][4], n_cnt in all
+  int n_cnt;
+  int* count;  // [tiles] distinct adapters of a tile
+  int* bad;    // [tiles] whether an id of the tile is L or more
+  int* list;   // [tiles][tile_n] the distinct adapters
+  float* t;    // [M][R] x . A^T
+  float* part; // [tiles * blocks][splits][cg][tile_n][128] partial sums, splits > 1
 };
-cudaError_t launch_lora(const LoraArgs& p, int dtype, int num_sms, cudaStream_t stream);
+struct LoraMaps {
+  CUtensorMap x, w, b;
+};
+cudaError_t launch_lora(LoraArgs& p, const LoraMaps& maps, int num_sms, cudaStream_t stream);
 
 }  // namespace qmoe
