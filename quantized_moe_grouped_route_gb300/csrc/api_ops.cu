@@ -273,7 +273,7 @@ static LoraLayout lora_layout(const LoraPlan& P, int M, int R) {
   L.bad = align_up(L.count + 4 * (size_t)P.tiles, 256);
   L.list = align_up(L.bad + 4 * (size_t)P.tiles, 256);
   L.t = align_up(L.list + 4 * (size_t)P.tiles * P.tile_n, 256);
-  L.part = align_up(L.t + 4 * (size_t)M * R, 256);
+  L.part = align_up(L.t + 4 * (size_t)M * R * (P.tsplits > 1 ? P.tsplits : 1), 256);
   L.total = L.part;
   if (P.splits > 1) L.total += units * P.splits * P.cg * P.tile_n * 128 * sizeof(float);
   return L;
@@ -283,8 +283,8 @@ static LoraLayout lora_layout(const LoraPlan& P, int M, int R) {
 size_t qmoe_lora_workspace_size(int M, int K, int N, int R, int L) {
   if (check_lora(M, K, N, R, L) != QMOE_OK) return 0;
   if (M == 0) return kWsHeaderBytes;
-  const size_t with_w = lora_layout(lora_plan(M, K, N, true), M, R).total;
-  const size_t without = lora_layout(lora_plan(M, K, N, false), M, R).total;
+  const size_t with_w = lora_layout(lora_plan(M, K, N, R, true), M, R).total;
+  const size_t without = lora_layout(lora_plan(M, K, N, R, false), M, R).total;
   return with_w > without ? with_w : without;
 }
 
@@ -309,7 +309,7 @@ int qmoe_lora_linear(const void* x_dev, int dtype, long long ldx, const void* w_
   rc = device_info(&sms);
   if (rc != QMOE_OK) return rc;
   LoraArgs p = {};
-  static_cast<LoraPlan&>(p) = lora_plan(M, K, N, w_dev != nullptr);
+  static_cast<LoraPlan&>(p) = lora_plan(M, K, N, R, w_dev != nullptr);
   const LoraLayout W = lora_layout(p, M, R);
   uint8_t* ws = reinterpret_cast<uint8_t*>(workspace_dev);
   p.dtype = dtype;
@@ -347,6 +347,14 @@ int qmoe_lora_linear(const void* x_dev, int dtype, long long ldx, const void* w_
   if (rc == QMOE_OK && w_dev) rc = make_tmap16(&maps.w, dtype, w_dev, 2, dw, sw, bw);
   if (rc == QMOE_OK && !w_dev) maps.w = maps.x;  // never read
   if (rc == QMOE_OK) rc = make_tmap16(&maps.b, dtype, b_dev, 3, db, sb, bb);
+  if (rc == QMOE_OK && p.tsplits > 0) {
+    const uint32_t bxs[2] = {64, (uint32_t)p.tile_n};
+    const uint64_t da[3] = {(uint64_t)K, (uint64_t)R, (uint64_t)L};
+    const uint64_t sa[2] = {(uint64_t)K * 2, (uint64_t)K * R * 2};
+    const uint32_t ba[3] = {64, (uint32_t)R, 1};
+    rc = make_tmap16(&maps.xs, dtype, x_dev, 2, dx, sx, bxs);
+    if (rc == QMOE_OK) rc = make_tmap16(&maps.a, dtype, a_dev, 3, da, sa, ba);
+  }
   if (rc != QMOE_OK) return rc;
   return cuda_rc(launch_lora(p, maps, sms, reinterpret_cast<cudaStream_t>(stream)));
 }

@@ -168,11 +168,12 @@ cudaError_t launch_unsort_backward(const TokenArgs& a, int dtype, bool vec, int 
 // lora.cu
 // How a problem is cut: token tiles of tile_n (a multiple of 16, at most 256), units of one
 // tile x 128 * cg rows of w (cg: CTAs per unit), each unit's ksteps steps of 64 of K in
-// `splits` segments.
+// `splits` segments; the shrink on the tensor cores with tsplits segments of K, or (0) with
+// plain products.
 struct LoraPlan {
-  int cg, tile_n, tiles, blocks, ksteps, splits;
+  int cg, tile_n, tiles, blocks, ksteps, splits, tsplits;
 };
-LoraPlan lora_plan(int M, int K, int N, bool has_w);
+LoraPlan lora_plan(int M, int K, int N, int R, bool has_w);
 struct LoraArgs : LoraPlan {
   int dtype;
   const void* x;  // [M][K], rows ldx elements apart
@@ -191,11 +192,12 @@ struct LoraArgs : LoraPlan {
   int* count;  // [tiles] distinct adapters of a tile
   int* bad;    // [tiles] whether an id of the tile is L or more
   int* list;   // [tiles][tile_n] the distinct adapters
-  float* t;    // [M][R] x . A^T
+  float* t;    // [max(tsplits, 1)][M][R] x . A^T
   float* part; // [tiles * blocks][splits][cg][tile_n][128] partial sums, splits > 1
 };
 struct LoraMaps {
-  CUtensorMap x, w, b;
+  CUtensorMap x, w, b;  // the GEMM's
+  CUtensorMap xs, a;    // the tensor-core shrink's
 };
 cudaError_t launch_lora(LoraArgs& p, const LoraMaps& maps, int num_sms, cudaStream_t stream);
 

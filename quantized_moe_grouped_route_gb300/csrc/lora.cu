@@ -2,7 +2,8 @@
 //   t[m] = scales[a] * (x[m] . A[a]^T),  out[m] = base[m] + x[m] . w^T + t[m] . B[a]^T
 // with a = adapter_ids[m].
 //
-// Two kernels.  The first (shrink) forms the sums x . A^T in fp32 and lists, for each tile
+// Two kernels.  The first (shrink: plain fp32 products for few tokens, tensor cores for
+// many) forms the sums x . A^T in fp32 and lists, for each tile
 // of tokens, the distinct adapters its tokens use.  The second is one GEMM whose
 // contraction runs over K and then over the ranks of the tile's adapters: the MMA's M side
 // is 128 rows of w (or of B[a]), its N side a tile of up to 256 tokens, and for each of
@@ -43,33 +44,61 @@ namespace {
 // the error word and the arrival counters.
 constexpr int kShrinkThreads = 256;
 
-// The distinct valid ids of a tile's tokens, in order of first appearance, into list;
-// whole block.  Returns their count; *bad is set where an id is L or more.
+// The distinct valid ids of a tile's tokens, in order of first appearance, into list
+// (shared, one entry per token of the tile); whole block of kShrinkThreads.  Returns their
+// count; *mine is this thread's token's place in the list (-1: none), *bad whether its id
+// is L or more.
+struct ListScratch {
+  int id[kShrinkThreads], place[kShrinkThreads], warp_count[kShrinkThreads / 32];
+};
 __device__ __forceinline__ int list_adapters(const int32_t* __restrict__ ids, int m0, int rows,
-                                             int L, int* sid, int* scan, int32_t* list, bool* bad) {
+                                             int L, ListScratch& w, int* list, int* mine,
+                                             bool* bad) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  int id = -1;
-  if (tid < rows) {
-    id = ids[m0 + tid];
-    if (id >= L) {
-      *bad = true;
-      id = -1;
-    }
-  }
-  sid[tid] = id;
+  int id = tid < rows ? ids[m0 + tid] : -1;
+  *bad = id >= L;
+  if (id >= L || id < 0) id = -1;
+  w.id[tid] = id;
   __syncthreads();
-  bool first = id >= 0;
-  for (int i = 0; i < tid && first; ++i) first = sid[i] != id;
+  int lead = tid;  // the first token with this id
+  if (id >= 0)
+    for (int i = 0; i < tid; ++i)
+      if (w.id[i] == id) {
+        lead = i;
+        break;
+      }
+  const bool first = id >= 0 && lead == tid;
   const unsigned mask = __ballot_sync(0xffffffffu, first);
-  if (lane == 0) scan[warp] = __popc(mask);
+  if (lane == 0) w.warp_count[warp] = __popc(mask);
   __syncthreads();
   int before = 0, total = 0;
-  for (int w = 0; w < kShrinkThreads / 32; ++w) {
-    if (w < warp) before += scan[w];
-    total += scan[w];
+  for (int i = 0; i < kShrinkThreads / 32; ++i) {
+    if (i < warp) before += w.warp_count[i];
+    total += w.warp_count[i];
   }
-  if (first) list[before + __popc(mask & ((1u << lane) - 1u))] = id;
+  if (first) {
+    w.place[tid] = before + __popc(mask & ((1u << lane) - 1u));
+    list[w.place[tid]] = id;
+  }
+  __syncthreads();
+  *mine = id >= 0 ? w.place[lead] : -1;
   return total;
+}
+
+// What the GEMM needs of the lists, and zeros where it counts; by one block per tile.
+__device__ __forceinline__ void publish_list(const LoraArgs& p, int t, const int* list, int n,
+                                             bool bad) {
+  const int tid = threadIdx.x;
+  if (t == 0) {
+    if (tid == 0) p.err[0] = 0u;
+    for (int i = tid; i < p.n_cnt; i += kShrinkThreads) p.cnt[i] = 0;
+  }
+  for (int i = tid; i < n; i += kShrinkThreads) p.list[(size_t)t * p.tile_n + i] = list[i];
+  const bool any = __syncthreads_or(bad);
+  if (tid == 0) {
+    p.count[t] = n;
+    p.bad[t] = any;
+  }
 }
 
 template <class T>
@@ -79,20 +108,14 @@ __global__ void __launch_bounds__(kShrinkThreads) lora_shrink_kernel(const LoraA
   constexpr int kWarps = kShrinkThreads / 32;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if ((int)blockIdx.x < p.tiles) {
-    __shared__ int sid[kShrinkThreads], scan[kWarps];
+    __shared__ ListScratch scratch;
+    __shared__ int list[kShrinkThreads];
     const int t = blockIdx.x, m0 = t * p.tile_n;
-    if (t == 0) {
-      if (tid == 0) p.err[0] = 0u;
-      for (int i = tid; i < p.n_cnt; i += kShrinkThreads) p.cnt[i] = 0;
-    }
-    bool bad = false;
-    const int n = list_adapters(p.ids, m0, min(p.tile_n, p.M - m0), p.L, sid, scan,
-                                p.list + (size_t)t * p.tile_n, &bad);
-    const bool any = __syncthreads_or(bad);
-    if (tid == 0) {
-      p.count[t] = n;
-      p.bad[t] = any;
-    }
+    int mine;
+    bool bad;
+    const int n =
+        list_adapters(p.ids, m0, min(p.tile_n, p.M - m0), p.L, scratch, list, &mine, &bad);
+    publish_list(p, t, list, n, bad);
     return;
   }
   __shared__ float part[kWarps][8];
@@ -160,8 +183,166 @@ __device__ __forceinline__ void mma_ss(uint32_t cg, uint32_t d, uint64_t a, uint
         : "memory");
 }
 
+// Instruction descriptor, kind::f16: A and B both bf16 or both fp16, fp32 D.
+__device__ __forceinline__ uint32_t idesc_16bit(int M, int N, int dtype) {
+  return idesc_bf16_f32(M, N) & (dtype == QMOE_DTYPE_BF16 ? ~0u : ~((1u << 7) | (1u << 10)));
+}
+
 __device__ __forceinline__ void fence_proxy_async() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
+// ----------------------------------------------------------------- shrink, many tokens
+// A CTA per (token tile, K segment): D[rank of adapter][token] = A[a] . x^T on the tensor
+// cores, with the 128 / R adapters of a pass stacked on the MMA's 128 rows, so that a tile
+// of few adapters (requests one after another) takes one pass over its token rows.  Each
+// token keeps the rows of its own adapter; the segments' sums are added by the GEMM's
+// builders.  gridDim.y CTAs share a tile's passes.
+__host__ __device__ constexpr int shrink_stages(int tile_n) { return tile_n > 128 ? 4 : 6; }
+
+template <class T>
+__global__ void __launch_bounds__(kShrinkThreads, 1)
+    lora_shrink_mma_kernel(const __grid_constant__ CUtensorMap map_x,
+                           const __grid_constant__ CUtensorMap map_a, const LoraArgs p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  __shared__ ListScratch scratch;
+  __shared__ int list[kShrinkThreads], place[kShrinkThreads];
+  __shared__ __align__(8) uint64_t full[6], empty[6], accf, acce, drain;
+  __shared__ uint32_t tmem_slot;
+  __shared__ int abort_word;
+  volatile int* abort_flag = &abort_word;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int stages = shrink_stages(p.tile_n);
+  const int stage_bytes = kStageA + p.tile_n * 128;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < stages; ++s) {
+      mbar_init(smem_u32(&full[s]), 1);
+      mbar_init(smem_u32(&empty[s]), 1);
+    }
+    mbar_init(smem_u32(&accf), 1);
+    mbar_init(smem_u32(&acce), 4);
+    mbar_init(smem_u32(&drain), 1);
+    abort_word = 0;
+    fence_mbar_init();
+    prefetch_tmap(&map_x);
+    prefetch_tmap(&map_a);
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(&tmem_slot), kAccCols);
+    tmem_relinquish();
+  }
+  grid_dep_wait();
+  grid_dep_launch();
+  const int t = blockIdx.x / p.tsplits, seg = blockIdx.x - t * p.tsplits;
+  const int m0 = t * p.tile_n, cols = min(p.tile_n, p.M - m0);
+  int mine;
+  bool bad;
+  const int n = list_adapters(p.ids, m0, cols, p.L, scratch, list, &mine, &bad);
+  place[threadIdx.x] = mine;
+  if (seg == 0 && blockIdx.y == 0) publish_list(p, t, list, n, bad);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+  const int cap = 128 / p.R;
+  const int passes = (n + cap - 1) / cap;
+  const int ksteps = (p.K + 63) / 64;
+  const int k0 = (int)((long long)ksteps * seg / p.tsplits);
+  const int k1 = (int)((long long)ksteps * (seg + 1) / p.tsplits);
+
+  if (warp == 0) {
+    const uint32_t lead = elect_one();
+    const uint64_t pol = l2_policy_evict_last();  // the GEMM reads the token rows next
+    uint32_t s = 0, ph = 1;
+    bool ok = true;
+    for (int ps = blockIdx.y; ps < passes && ok; ps += gridDim.y) {
+      const int here = min(cap, n - ps * cap);
+      for (int k = k0; k < k1; ++k) {
+        if (!warp_wait(smem_u32(&empty[s]), ph, abort_flag, p.err)) {
+          ok = false;
+          break;
+        }
+        const uint32_t st = smem_u32(smem) + s * stage_bytes, fb = smem_u32(&full[s]);
+        mbar_arrive_expect_tx_if(lead, fb, (uint32_t)(here * p.R * 128 + p.tile_n * 128));
+        for (int i = 0; i < here; ++i)
+          tma_load_3d_if(lead, st + i * p.R * 128, &map_a, k * 64, 0, list[ps * cap + i], fb, pol);
+        tma_load_2d_if(lead, st + kStageA, &map_x, k * 64, m0, fb, pol);
+        if (++s == (uint32_t)stages) {
+          s = 0;
+          ph ^= 1;
+        }
+      }
+    }
+    if (!ok) {  // the copies of the last steps may still be landing
+      const unsigned long long t0 = globaltimer_ns();
+      while (globaltimer_ns() - t0 < 2000000ull) {
+      }
+    }
+  } else if (warp == 1) {
+    const uint32_t lead = elect_one();
+    const uint32_t idesc = idesc_16bit(128, p.tile_n, p.dtype);
+    const uint64_t desc0 = sdesc_sw128(smem_u32(smem));
+    uint32_t s = 0, ph = 0, aph = 1;
+    bool ok = true;
+    for (int ps = blockIdx.y; ps < passes && ok; ps += gridDim.y) {
+      if (!warp_wait(smem_u32(&acce), aph, abort_flag, p.err)) break;
+      aph ^= 1;
+      tc_fence_after();
+      for (int k = k0; k < k1; ++k) {
+        if (!warp_wait(smem_u32(&full[s]), ph, abort_flag, p.err)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint64_t a = desc0 + ((s * stage_bytes) >> 4);
+        if (lead) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            mma_ss(1, tmem, a + 2 * j, a + (kStageA >> 4) + 2 * j, idesc, k > k0 || j > 0);
+        }
+        tc_commit_if(lead, smem_u32(&empty[s]));
+        if (++s == (uint32_t)stages) {
+          s = 0;
+          ph ^= 1;
+        }
+      }
+      if (ok) tc_commit_if(lead, smem_u32(&accf));
+    }
+    tc_commit_if(lead, smem_u32(&drain));
+    drain_wait(smem_u32(&drain), 0);
+  } else if (warp >= 4) {
+    const int q = warp & 3, row = q * 32 + lane;
+    const int slot = row / p.R, r = row - slot * p.R;
+    float* dst = p.t + ((size_t)seg * p.M + m0) * p.R + r;
+    uint32_t ph = 0;
+    for (int ps = blockIdx.y; ps < passes; ps += gridDim.y) {
+      if (!warp_wait(smem_u32(&accf), ph, abort_flag, p.err)) break;
+      ph ^= 1;
+      tc_fence_after();
+      const int want = slot < cap ? ps * cap + slot : -2;
+      for (int c0 = 0; c0 < cols; c0 += 16) {
+        uint32_t v[16];
+        tmem_ld_x16(tmem + ((uint32_t)(q * 32) << 16) + c0, v);
+        tmem_wait_ld();
+        tmem_ld_ready(v);
+#pragma unroll
+        for (int k = 0; k < 16; ++k)
+          if (c0 + k < cols && place[c0 + k] == want)
+            dst[(size_t)(c0 + k) * p.R] = __uint_as_float(v[k]);
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&acce));
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kAccCols);
+  }
 }
 
 template <class T, int CG>
@@ -323,9 +504,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     if (rank == 0) {
       // ------------------------------------------------------------------ MMA issue
       const uint32_t lead = elect_one();
-      const bool bf16 = sizeof(T) == 2 && p.dtype == QMOE_DTYPE_BF16;
-      const uint32_t idesc =
-          idesc_bf16_f32(128 * CG, p.tile_n) & (bf16 ? ~0u : ~((1u << 7) | (1u << 10)));
+      const uint32_t idesc = idesc_16bit(128 * CG, p.tile_n, p.dtype);
       const uint64_t desc0 = sdesc_sw128(smem_u32(smem));
       const uint32_t t0 = (uint32_t)(tbuf - smem) >> 4;
       uint32_t s = 0, ph = 0, ts = 0, tph = 0, local = 0;
@@ -417,9 +596,14 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             Pack<T, 8> o;
             o.raw = make_uint4(0u, 0u, 0u, 0u);
             if (m < p.M && r < p.R && p.ids[m] == id) {
-              const float4* src = reinterpret_cast<const float4*>(p.t + (size_t)m * p.R + r);
-              const float4 v0 = src[0], v1 = src[1];
-              const float v[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+              float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+              for (int g = 0; g < p.tsplits; ++g) {
+                const float4* src =
+                    reinterpret_cast<const float4*>(p.t + ((size_t)g * p.M + m) * p.R + r);
+                const float4 v0 = src[0], v1 = src[1];
+                v[0] += v0.x, v[1] += v0.y, v[2] += v0.z, v[3] += v0.w;
+                v[4] += v1.x, v[5] += v1.y, v[6] += v1.z, v[7] += v1.w;
+              }
 #pragma unroll
               for (int e = 0; e < 8; ++e) {
                 const float f = v[e] * scale;
@@ -562,12 +746,26 @@ cudaError_t run(LoraArgs& p, const LoraMaps& maps, int num_sms, cudaStream_t str
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
   attr[0] = pdl_attribute();
-  cfg.gridDim = dim3((unsigned)(p.tiles + (long long)p.M * (p.R / 8)));
   cfg.blockDim = dim3(kShrinkThreads);
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, lora_shrink_kernel<T>, p);
+  cudaError_t e;
+  if (p.tsplits == 0) {
+    p.tsplits = 1;
+    cfg.gridDim = dim3((unsigned)(p.tiles + (long long)p.M * (p.R / 8)));
+    e = cudaLaunchKernelEx(&cfg, lora_shrink_kernel<T>, p);
+  } else {
+    const int ctas = p.tiles * p.tsplits, cap = 128 / p.R;
+    const int most = ((p.L < p.tile_n ? p.L : p.tile_n) + cap - 1) / cap;
+    const int share = num_sms / ctas < 1 ? 1 : num_sms / ctas;
+    cfg.gridDim = dim3(ctas, share < most ? share : most);
+    cfg.dynamicSmemBytes = 1024 + (size_t)shrink_stages(p.tile_n) * (kStageA + p.tile_n * 128);
+    e = cudaFuncSetAttribute(lora_shrink_mma_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)cfg.dynamicSmemBytes);
+    if (e == cudaSuccess)
+      e = cudaLaunchKernelEx(&cfg, lora_shrink_mma_kernel<T>, maps.xs, maps.a, p);
+  }
   if (e != cudaSuccess) return e;
   const int stage = kStageA + token_bytes(p.tile_n, p.cg);
   const int rest = kSmemLimit - 1024 - kCtrl - 2 * token_bytes(p.tile_n, p.cg);
@@ -601,11 +799,13 @@ cudaError_t run(LoraArgs& p, const LoraMaps& maps, int num_sms, cudaStream_t str
 // Tiles, pairs and splits for a problem (SMs of a GB300: the workspace size must not depend
 // on the device).  Up to 256 tokens are one tile and one CTA a unit; more go to CTA pairs,
 // with the tile width whose last round of units leaves the least idle.  A unit is split
-// along K when there are fewer units than workers, into segments of at least 4 steps.
-LoraPlan lora_plan(int M, int K, int N, bool has_w) {
+// along K when there are fewer units than workers, into segments of at least 4 steps; the
+// tensor-core shrink likewise, into at most 8.
+LoraPlan lora_plan(int M, int K, int N, int R, bool has_w) {
   LoraPlan L;
   const int sms = 152;
-  L.ksteps = has_w ? (K + 63) / 64 : 0;
+  const int ksteps = (K + 63) / 64;
+  L.ksteps = has_w ? ksteps : 0;
   if (M <= 256) {
     L.cg = 1;
     L.tile_n = (M + 15) / 16 * 16;
@@ -630,6 +830,13 @@ LoraPlan lora_plan(int M, int K, int N, bool has_w) {
   if (units * 2 <= sms / L.cg) {
     L.splits = (int)(sms / L.cg / units);
     if (L.splits > L.ksteps / 4) L.splits = L.ksteps / 4 > 0 ? L.ksteps / 4 : 1;
+  }
+  // the fp32 shrink reads a token's adapter anew for each token: up to 16 MB of such reads
+  L.tsplits = 0;
+  if ((long long)M * R * K * 2 > (16LL << 20)) {
+    int s = sms / L.tiles;
+    if (s > ksteps / 4) s = ksteps / 4;
+    L.tsplits = s < 1 ? 1 : s > 8 ? 8 : s;
   }
   return L;
 }

@@ -490,9 +490,18 @@ LORAS = [  # M, K, N, R, L, with w, with base, ids
 ]
 
 
+# enough tokens times ranks that x . A^T runs on the tensor cores: adapters stacked 1 to 16
+# at a time, more of them than one pass holds, a rank that does not divide the 128 rows
+LORAS_WIDE = [
+    (256, 4096, 96, 24, 40, True, False, "mixed"), (200, 2048, 130, 128, 50, True, False, "mixed"),
+    (1100, 1024, 300, 8, 500, True, True, "mixed"), (33, 8192, 64, 64, 9, False, True, "mixed"),
+    (2047, 1096, 512, 48, 11, True, False, "runs"), (700, 968, 200, 128, 3, True, False, "none"),
+]
+
+
 @gpu
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
-@pytest.mark.parametrize("M,K,N,R,L,with_w,with_base,how", LORAS)
+@pytest.mark.parametrize("M,K,N,R,L,with_w,with_base,how", LORAS + LORAS_WIDE)
 def test_lora_linear(M, K, N, R, L, with_w, with_base, how, dtype):
     g = _gen(M * 3 + K)
     x = _rows(g, M, K, dtype, pad=8)
