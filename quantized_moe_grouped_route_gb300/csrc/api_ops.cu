@@ -273,7 +273,7 @@ static LoraLayout lora_layout(const LoraPlan& P, int M, int R) {
   L.bad = align_up(L.count + 4 * (size_t)P.tiles, 256);
   L.list = align_up(L.bad + 4 * (size_t)P.tiles, 256);
   L.t = align_up(L.list + 4 * (size_t)P.tiles * P.tile_n, 256);
-  L.part = align_up(L.t + 4 * (size_t)M * R * (P.tsplits > 1 ? P.tsplits : 1), 256);
+  L.part = align_up(L.t + 4 * (size_t)M * R, 256);
   L.total = L.part;
   if (P.splits > 1) L.total += units * P.splits * P.cg * P.tile_n * 128 * sizeof(float);
   return L;
@@ -332,7 +332,7 @@ int qmoe_lora_linear(const void* x_dev, int dtype, long long ldx, const void* w_
   p.count = reinterpret_cast<int*>(ws + W.count);
   p.bad = reinterpret_cast<int*>(ws + W.bad);
   p.list = reinterpret_cast<int*>(ws + W.list);
-  p.t = reinterpret_cast<float*>(ws + W.t);
+  p.t = ws + W.t;
   p.part = reinterpret_cast<float*>(ws + W.part);
 
   LoraMaps maps;

@@ -168,8 +168,8 @@ cudaError_t launch_unsort_backward(const TokenArgs& a, int dtype, bool vec, int 
 // lora.cu
 // How a problem is cut: token tiles of tile_n (a multiple of 16, at most 256), units of one
 // tile x 128 * cg rows of w (cg: CTAs per unit), each unit's ksteps steps of 64 of K in
-// `splits` segments; the shrink on the tensor cores with tsplits segments of K, or (0) with
-// plain products.
+// `splits` segments; the shrink with plain products (tsplits 0) or on the tensor cores
+// (tsplits its segments of K, chosen at launch).
 struct LoraPlan {
   int cg, tile_n, tiles, blocks, ksteps, splits, tsplits;
 };
@@ -192,7 +192,7 @@ struct LoraArgs : LoraPlan {
   int* count;  // [tiles] distinct adapters of a tile
   int* bad;    // [tiles] whether an id of the tile is L or more
   int* list;   // [tiles][tile_n] the distinct adapters
-  float* t;    // [max(tsplits, 1)][M][R] x . A^T
+  void* t;     // [M][2][R] scales[a] * (x . A^T): rounded, and what the rounding left
   float* part; // [tiles * blocks][splits][cg][tile_n][128] partial sums, splits > 1
 };
 struct LoraMaps {

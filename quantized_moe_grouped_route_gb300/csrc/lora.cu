@@ -13,23 +13,27 @@
 //
 // t enters the tensor cores as the sum of two values of the activation type (t rounded,
 // and what the rounding left): 16 (bf16) or 22 (fp16) significant bits for twice the MMAs
-// of a contraction that is short, instead of a second rounding of the result's size.
+// of a contraction that is short, instead of a second rounding of the result's size.  The
+// shrink kernel writes both.
 //
 // GEMM pipeline (a unit is 128 rows of w per CTA x one token tile, its contraction split
 // into S segments when there are fewer units than SMs):
 //   warp 0      TMA producer: steps of 64 of K, [128 rows of w | token rows], then per
-//               adapter and 64 ranks twice [128 rows of B[a]]
+//               adapter and 64 ranks [128 rows of B[a]]
 //   warp 1      MMA issue: 4 x tcgen05.mma kind::f16 per step, fp32 accumulator in TMEM,
 //               two accumulators, so that the epilogue overlaps the next unit
 //   warps 4-7   epilogue: TMEM -> registers -> base, rounding, global stores; with S > 1
 //               the segments' partial sums are added in K order by the last to arrive
-//   warps 8-11  builders: the token operand of the adapter steps into two slots of their
-//               own
+//   warps 8-11  builders: the token operand (both values of t) of the adapter steps, in
+//               slots of their own; one warp (few tokens) or two build a step, so that
+//               several steps are in the making at once
 // Few tokens (one tile): one CTA per unit, w streamed once, HBM bound.  More: CTA pairs
 // (cta_group::2, M = 256), each SM loading half of the token rows, since a 128 x 256 tile
 // fed by one SM alone asks more of its L2 port (96 bytes a clock) than it has.
 //
 // Every wait is bounded, as in the layer's GEMMs.
+#include <atomic>
+
 #include "cluster.cuh"
 #include "common.cuh"
 #include "launch.h"
@@ -39,37 +43,42 @@ namespace qmoe {
 namespace {
 
 // ------------------------------------------------------------------ shrink, few tokens
-// A block per (token, 8 ranks): its warps share out K, and the eight sums are reduced in a
-// fixed order.  The blocks before them list the tiles' adapters (one block each) and zero
+// A block per (token, 8 ranks) with a thread per 8 elements of K (up to 1024), so that a
+// single token's latency is about one round trip to memory; the eight sums are reduced in
+// a fixed order.  The blocks before them list the tiles' adapters (one block each) and zero
 // the error word and the arrival counters.
 constexpr int kShrinkThreads = 256;
 
 // The distinct valid ids of a tile's tokens, in order of first appearance, into list
-// (shared, one entry per token of the tile); whole block of kShrinkThreads.  Returns their
+// (shared, one entry per token of the tile); whole block of at least kShrinkThreads.  Returns their
 // count; *mine is this thread's token's place in the list (-1: none), *bad whether its id
 // is L or more.
-struct ListScratch {
+struct __align__(16) ListScratch {
   int id[kShrinkThreads], place[kShrinkThreads], warp_count[kShrinkThreads / 32];
 };
 __device__ __forceinline__ int list_adapters(const int32_t* __restrict__ ids, int m0, int rows,
                                              int L, ListScratch& w, int* list, int* mine,
                                              bool* bad) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const bool here = tid < kShrinkThreads;
   int id = tid < rows ? ids[m0 + tid] : -1;
   *bad = id >= L;
   if (id >= L || id < 0) id = -1;
-  w.id[tid] = id;
+  if (here) w.id[tid] = id;
   __syncthreads();
   int lead = tid;  // the first token with this id
-  if (id >= 0)
-    for (int i = 0; i < tid; ++i)
-      if (w.id[i] == id) {
-        lead = i;
-        break;
-      }
+  const int4* four = reinterpret_cast<const int4*>(w.id);
+#pragma unroll 4
+  for (int i = (rows - 1) / 4; i >= 0; --i) {  // backwards: the last match found is the first
+    const int4 v = four[i];
+    if (v.w == id) lead = 4 * i + 3;
+    if (v.z == id) lead = 4 * i + 2;
+    if (v.y == id) lead = 4 * i + 1;
+    if (v.x == id) lead = 4 * i;
+  }
   const bool first = id >= 0 && lead == tid;
   const unsigned mask = __ballot_sync(0xffffffffu, first);
-  if (lane == 0) w.warp_count[warp] = __popc(mask);
+  if (here && lane == 0) w.warp_count[warp] = __popc(mask);
   __syncthreads();
   int before = 0, total = 0;
   for (int i = 0; i < kShrinkThreads / 32; ++i) {
@@ -91,9 +100,9 @@ __device__ __forceinline__ void publish_list(const LoraArgs& p, int t, const int
   const int tid = threadIdx.x;
   if (t == 0) {
     if (tid == 0) p.err[0] = 0u;
-    for (int i = tid; i < p.n_cnt; i += kShrinkThreads) p.cnt[i] = 0;
+    for (int i = tid; i < p.n_cnt; i += blockDim.x) p.cnt[i] = 0;
   }
-  for (int i = tid; i < n; i += kShrinkThreads) p.list[(size_t)t * p.tile_n + i] = list[i];
+  for (int i = tid; i < n; i += blockDim.x) p.list[(size_t)t * p.tile_n + i] = list[i];
   const bool any = __syncthreads_or(bad);
   if (tid == 0) {
     p.count[t] = n;
@@ -101,11 +110,12 @@ __device__ __forceinline__ void publish_list(const LoraArgs& p, int t, const int
   }
 }
 
+constexpr int kShrinkMost = 1024;  // threads of the plain shrink
 template <class T>
-__global__ void __launch_bounds__(kShrinkThreads) lora_shrink_kernel(const LoraArgs p) {
+__global__ void __launch_bounds__(kShrinkMost) lora_shrink_kernel(const LoraArgs p) {
   grid_dep_wait();
   grid_dep_launch();
-  constexpr int kWarps = kShrinkThreads / 32;
+  constexpr int kWarps = kShrinkMost / 32;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if ((int)blockIdx.x < p.tiles) {
     __shared__ ListScratch scratch;
@@ -130,7 +140,7 @@ __global__ void __launch_bounds__(kShrinkThreads) lora_shrink_kernel(const LoraA
     const uint4* a =
         reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(p.a) + ((size_t)id * p.R + r0) * p.K);
     const int chunks = p.K / 8;
-    for (int c = tid; c < chunks; c += kShrinkThreads) {
+    for (int c = tid; c < chunks; c += blockDim.x) {
       P_ xv, av[8];
       xv.raw = x[c];
 #pragma unroll
@@ -150,9 +160,14 @@ __global__ void __launch_bounds__(kShrinkThreads) lora_shrink_kernel(const LoraA
   __syncthreads();
   if (tid < 8) {
     float s = 0.f;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) s += part[w][tid];
-    p.t[(size_t)m * p.R + r0 + tid] = s;
+    for (int w = 0; w < (int)(blockDim.x >> 5); ++w) s += part[w][tid];
+    if (id >= 0 && id < p.L) {
+      s *= p.scales[id];
+      T* dst = reinterpret_cast<T*>(p.t) + (size_t)m * 2 * p.R + r0 + tid;
+      const T hi = from_f32<T>(s);
+      dst[0] = hi;
+      dst[p.R] = from_f32<T>(s - to_f32(hi));
+    }
   }
 }
 
@@ -164,8 +179,10 @@ constexpr int kAccCols = 256;  // TMEM columns of one accumulator
 constexpr int kCtrl = 1024;
 constexpr int kSmemLimit = 232448;
 
-// Token rows per CTA of a tile, and the bytes of one step of them.
+// Bytes of one step of a CTA's token rows; slots of the builders' operand (two of them
+// each: t rounded, and the rest): four of one warp each for up to 32 rows, else two of two.
 __host__ __device__ constexpr int token_bytes(int tile_n, int cg) { return tile_n / cg * 128; }
+__host__ __device__ constexpr int token_slots(int tile_n, int cg) { return tile_n / cg <= 32 ? 4 : 2; }
 
 __device__ __forceinline__ void mma_ss(uint32_t cg, uint32_t d, uint64_t a, uint64_t b,
                                        uint32_t idesc, uint32_t accumulate) {
@@ -196,9 +213,21 @@ __device__ __forceinline__ void fence_proxy_async() {
 // A CTA per (token tile, K segment): D[rank of adapter][token] = A[a] . x^T on the tensor
 // cores, with the 128 / R adapters of a pass stacked on the MMA's 128 rows, so that a tile
 // of few adapters (requests one after another) takes one pass over its token rows.  Each
-// token keeps the rows of its own adapter; the segments' sums are added by the GEMM's
-// builders.  gridDim.y CTAs share a tile's passes.
-__host__ __device__ constexpr int shrink_stages(int tile_n) { return tile_n > 128 ? 4 : 6; }
+// token keeps the rows of its own adapter, in shared memory; the segments of a tile are one
+// cluster, whose CTAs then add up a share of the tokens each over all segments, in order.
+// gridDim.y clusters share a tile's passes.
+constexpr int kShrinkStages = 6;
+constexpr int kShrinkSegments = 8;  // CTAs of a cluster, at most
+__host__ __device__ constexpr int shrink_stage_bytes(int tile_n) { return kStageA + tile_n * 128; }
+// bytes of a CTA's sums [tile_n][R]
+__host__ __device__ constexpr int shrink_sum_bytes(int tile_n, int R) { return tile_n * R * 4; }
+// Stages of the ring beside `other` bytes.  A CTA with one pass writes its sums over the
+// ring, which it no longer needs then; with more, they have a place of their own.
+constexpr int kShrinkBytes = kSmemLimit - 8192;  // less the static shared memory
+__host__ __device__ constexpr int shrink_stages(int tile_n, int other) {
+  const int n = (kShrinkBytes - other) / shrink_stage_bytes(tile_n);
+  return n < kShrinkStages ? n : kShrinkStages;
+}
 
 template <class T>
 __global__ void __launch_bounds__(kShrinkThreads, 1)
@@ -209,15 +238,14 @@ __global__ void __launch_bounds__(kShrinkThreads, 1)
                                              ~static_cast<uintptr_t>(1023));
   __shared__ ListScratch scratch;
   __shared__ int list[kShrinkThreads], place[kShrinkThreads];
-  __shared__ __align__(8) uint64_t full[6], empty[6], accf, acce, drain;
+  __shared__ __align__(8) uint64_t full[kShrinkStages], empty[kShrinkStages], accf, acce, drain;
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_word;
   volatile int* abort_flag = &abort_word;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int stages = shrink_stages(p.tile_n);
-  const int stage_bytes = kStageA + p.tile_n * 128;
+  const int stage_bytes = shrink_stage_bytes(p.tile_n);
   if (threadIdx.x == 0) {
-    for (int s = 0; s < stages; ++s) {
+    for (int s = 0; s < kShrinkStages; ++s) {
       mbar_init(smem_u32(&full[s]), 1);
       mbar_init(smem_u32(&empty[s]), 1);
     }
@@ -237,6 +265,21 @@ __global__ void __launch_bounds__(kShrinkThreads, 1)
   grid_dep_launch();
   const int t = blockIdx.x / p.tsplits, seg = blockIdx.x - t * p.tsplits;
   const int m0 = t * p.tile_n, cols = min(p.tile_n, p.M - m0);
+  const int ksteps = (p.K + 63) / 64;
+  const int k0 = (int)((long long)ksteps * seg / p.tsplits);
+  const int k1 = (int)((long long)ksteps * (seg + 1) / p.tsplits);
+  const int sum_bytes = shrink_sum_bytes(p.tile_n, p.R);
+  const uint64_t pol = l2_policy_evict_last();  // the GEMM reads the token rows next
+  // the first token rows are fetched while the list is made (their bytes count on a phase
+  // that the adapters' copies have yet to arrive at)
+  const int early = min(shrink_stages(p.tile_n, sum_bytes), k1 - k0);
+  if (warp == 0) {
+    __syncwarp();
+    const uint32_t lead = elect_one();
+    for (int i = 0; i < early; ++i)
+      tma_load_2d_if(lead, smem_u32(smem) + i * stage_bytes + kStageA, &map_x, (k0 + i) * 64, m0,
+                     smem_u32(&full[i]), pol);
+  }
   int mine;
   bool bad;
   const int n = list_adapters(p.ids, m0, cols, p.L, scratch, list, &mine, &bad);
@@ -248,15 +291,15 @@ __global__ void __launch_bounds__(kShrinkThreads, 1)
   const uint32_t tmem = tmem_slot;
   const int cap = 128 / p.R;
   const int passes = (n + cap - 1) / cap;
-  const int ksteps = (p.K + 63) / 64;
-  const int k0 = (int)((long long)ksteps * seg / p.tsplits);
-  const int k1 = (int)((long long)ksteps * (seg + 1) / p.tsplits);
+  const bool once = passes <= (int)(blockIdx.y + gridDim.y);
+  const int stages = shrink_stages(p.tile_n, once ? 0 : sum_bytes);
+  float* sums = reinterpret_cast<float*>(smem + (once ? 0 : kShrinkBytes - sum_bytes));  // [tile_n][R]
 
   if (warp == 0) {
     const uint32_t lead = elect_one();
-    const uint64_t pol = l2_policy_evict_last();  // the GEMM reads the token rows next
     uint32_t s = 0, ph = 1;
     bool ok = true;
+    int fetched = early;
     for (int ps = blockIdx.y; ps < passes && ok; ps += gridDim.y) {
       const int here = min(cap, n - ps * cap);
       for (int k = k0; k < k1; ++k) {
@@ -268,12 +311,20 @@ __global__ void __launch_bounds__(kShrinkThreads, 1)
         mbar_arrive_expect_tx_if(lead, fb, (uint32_t)(here * p.R * 128 + p.tile_n * 128));
         for (int i = 0; i < here; ++i)
           tma_load_3d_if(lead, st + i * p.R * 128, &map_a, k * 64, 0, list[ps * cap + i], fb, pol);
-        tma_load_2d_if(lead, st + kStageA, &map_x, k * 64, m0, fb, pol);
+        if (fetched > 0)
+          --fetched;
+        else
+          tma_load_2d_if(lead, st + kStageA, &map_x, k * 64, m0, fb, pol);
         if (++s == (uint32_t)stages) {
           s = 0;
           ph ^= 1;
         }
       }
+    }
+    // no adapters in these passes: the early rows are awaited all the same
+    for (int i = early - fetched; i < early; ++i) {
+      mbar_arrive_expect_tx_if(lead, smem_u32(&full[i]), (uint32_t)p.tile_n * 128);
+      warp_wait(smem_u32(&full[i]), 0, abort_flag, p.err);
     }
     if (!ok) {  // the copies of the last steps may still be landing
       const unsigned long long t0 = globaltimer_ns();
@@ -315,7 +366,6 @@ __global__ void __launch_bounds__(kShrinkThreads, 1)
   } else if (warp >= 4) {
     const int q = warp & 3, row = q * 32 + lane;
     const int slot = row / p.R, r = row - slot * p.R;
-    float* dst = p.t + ((size_t)seg * p.M + m0) * p.R + r;
     uint32_t ph = 0;
     for (int ps = blockIdx.y; ps < passes; ps += gridDim.y) {
       if (!warp_wait(smem_u32(&accf), ph, abort_flag, p.err)) break;
@@ -330,7 +380,7 @@ __global__ void __launch_bounds__(kShrinkThreads, 1)
 #pragma unroll
         for (int k = 0; k < 16; ++k)
           if (c0 + k < cols && place[c0 + k] == want)
-            dst[(size_t)(c0 + k) * p.R] = __uint_as_float(v[k]);
+            sums[(c0 + k) * p.R + r] = __uint_as_float(v[k]);
       }
       tc_fence_before();
       __syncwarp();
@@ -343,6 +393,36 @@ __global__ void __launch_bounds__(kShrinkThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, kAccCols);
   }
+  // the tokens c = seg, seg + segments, .. of this cluster's passes, summed over the segments
+  cluster_sync_all();
+  // (four ranks a thread, the segments' values in flight together)
+  const uint32_t sums0 = smem_u32(sums);
+  const int share = (cols - seg + p.tsplits - 1) / p.tsplits, quads = p.R / 4;
+  for (int i = threadIdx.x; i < share * quads; i += kShrinkThreads) {
+    const int c = i / quads * p.tsplits + seg, r = i % quads * 4;
+    const int at = place[c];
+    if (at < 0 || at / cap % (int)gridDim.y != (int)blockIdx.y) continue;
+    float4 v[kShrinkSegments];
+#pragma unroll
+    for (int g = 0; g < kShrinkSegments; ++g)
+      if (g < p.tsplits) v[g] = ld_cluster_f32x4(peer_addr(sums0 + (c * p.R + r) * 4, g));
+    float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int g = 0; g < kShrinkSegments; ++g)
+      if (g < p.tsplits) t.x += v[g].x, t.y += v[g].y, t.z += v[g].z, t.w += v[g].w;
+    const float s = p.scales[list[at]];
+    const float f[4] = {t.x * s, t.y * s, t.z * s, t.w * s};
+    Pack<T, 4> hi, lo;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      hi.v[e] = from_f32<T>(f[e]);
+      lo.v[e] = from_f32<T>(f[e] - to_f32(hi.v[e]));
+    }
+    uint2* dst = reinterpret_cast<uint2*>(reinterpret_cast<T*>(p.t) + (size_t)(m0 + c) * 2 * p.R + r);
+    dst[0] = hi.raw;
+    dst[p.R / 4] = lo.raw;
+  }
+  cluster_sync_all();  // no CTA leaves while its sums may still be read
 }
 
 template <class T, int CG>
@@ -356,13 +436,14 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   const int bytes_b = token_bytes(p.tile_n, CG);
   const int stage_bytes = kStageA + bytes_b;
   const int stages = p.stages;
-  uint8_t* tbuf = smem + stages * stage_bytes;  // [2][bytes_b]
-  uint8_t* ctrl = tbuf + 2 * bytes_b;
+  const int tslots = token_slots(p.tile_n, CG);
+  uint8_t* tbuf = smem + stages * stage_bytes;  // [tslots][2][bytes_b]
+  uint8_t* ctrl = tbuf + 2 * tslots * bytes_b;
   uint64_t* full = reinterpret_cast<uint64_t*>(ctrl);
   uint64_t* empty = full + kMaxStages;
   uint64_t* tfull = empty + kMaxStages;
-  uint64_t* tempty = tfull + 2;
-  uint64_t* accf = tempty + 2;
+  uint64_t* tempty = tfull + 4;
+  uint64_t* accf = tempty + 4;
   uint64_t* acce = accf + 2;
   uint64_t* drain = acce + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
@@ -377,9 +458,11 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       mbar_init(smem_u32(&full[s]), 1);
       mbar_init(smem_u32(&empty[s]), 1);
     }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(smem_u32(&tfull[i]), 4 * CG);
+    for (int i = 0; i < tslots; ++i) {
+      mbar_init(smem_u32(&tfull[i]), 4 / tslots * CG);
       mbar_init(smem_u32(&tempty[i]), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&accf[i]), 1);
       mbar_init(smem_u32(&acce[i]), 4 * CG);
     }
@@ -431,14 +514,13 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     if (CG == 2) return warp_wait_cl(smem_u32(bar), parity, abort_flag, p.err);
     return warp_wait(smem_u32(bar), parity, abort_flag, p.err);
   };
-  // Adapter steps of a tile (twice per adapter and 64 ranks), in a unit's last segment.
-  // The shrink kernel writes the lists, so its completion is awaited first.
+  // The tile's adapters d = seg, seg + S, .. < adapters(tile), one step per 64 ranks, follow
+  // a segment's K steps.  The shrink kernel writes the lists, so it is awaited first.
   bool waited = false;
-  auto adapters = [&](const Piece& c) -> int {
-    if (c.seg != S - 1) return 0;
+  auto adapters = [&](int tile) -> int {
     if (!waited) grid_dep_wait();
     waited = true;
-    return p.count[c.tile];
+    return p.count[tile];
   };
 
   if (warp == 0) {
@@ -477,10 +559,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         }
         next();
       }
-      const int n = ok ? adapters(c) : 0;
-      for (int d = 0; d < n && ok; ++d) {
+      const int n = ok ? adapters(c.tile) : 0;
+      for (int d = c.seg; d < n && ok; d += S) {
         const int id = p.list[(size_t)c.tile * p.tile_n + d];
-        for (int h = 0; h < 2 * chunks; ++h) {
+        for (int h = 0; h < chunks; ++h) {
           if (!wait(&empty[s], ph)) {
             ok = false;
             break;
@@ -488,9 +570,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
           const uint32_t st = smem_u32(smem) + s * stage_bytes;
           if (rank == 0) mbar_arrive_expect_tx_if(lead, smem_u32(&full[s]), CG * (uint32_t)kStageA);
           if (CG == 2)
-            tma_load_3d_pair_if(lead, st, &map_b, (h >> 1) * 64, row, id, full0 + s * 8, pol_x);
+            tma_load_3d_pair_if(lead, st, &map_b, h * 64, row, id, full0 + s * 8, pol_x);
           else
-            tma_load_3d_if(lead, st, &map_b, (h >> 1) * 64, row, id, full0 + s * 8, pol_x);
+            tma_load_3d_if(lead, st, &map_b, h * 64, row, id, full0 + s * 8, pol_x);
           next();
         }
       }
@@ -529,7 +611,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
           break;
         }
         tc_fence_after();
-        const uint32_t d = tmem + ab * kAccCols;
+        const uint32_t dst = tmem + ab * kAccCols;
         uint32_t acc = 0;
         for (int k = c.k0; k < c.k1; ++k) {
           if (!wait(&full[s], ph)) {
@@ -541,31 +623,37 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
           if (lead) {
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-              mma_ss(CG, d, a + 2 * j, a + (kStageA >> 4) + 2 * j, idesc, acc | (j > 0));
+              mma_ss(CG, dst, a + 2 * j, a + (kStageA >> 4) + 2 * j, idesc, acc | (j > 0));
           }
           acc = 1;
           commit(&empty[s]);
           next();
         }
-        const int n = ok ? adapters(c) : 0;
-        for (int h = 0; h < n * 2 * chunks && ok; ++h) {
-          const int c0 = ((h >> 1) % chunks) * 64;
-          const int slices = (min(64, p.R - c0) + 15) / 16;
-          if (!wait(&full[s], ph) || !wait(&tfull[ts], tph)) {
-            ok = false;
-            break;
+        const int n = ok ? adapters(c.tile) : 0;
+        for (int d = c.seg; d < n && ok; d += S) {
+          for (int h = 0; h < chunks; ++h) {
+            const int slices = (min(64, p.R - h * 64) + 15) / 16;
+            if (!wait(&full[s], ph) || !wait(&tfull[ts], tph)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint64_t a = desc0 + ((s * stage_bytes) >> 4);
+            const uint64_t hi = desc0 + t0 + ((2 * ts * bytes_b) >> 4), lo = hi + (bytes_b >> 4);
+            if (lead)
+              for (int j = 0; j < slices; ++j) {
+                mma_ss(CG, dst, a + 2 * j, hi + 2 * j, idesc, acc | (j > 0));
+                mma_ss(CG, dst, a + 2 * j, lo + 2 * j, idesc, 1u);
+              }
+            acc = 1;
+            commit(&empty[s]);
+            commit(&tempty[ts]);
+            next();
+            if (++ts == (uint32_t)tslots) {
+              ts = 0;
+              tph ^= 1;
+            }
           }
-          tc_fence_after();
-          const uint64_t a = desc0 + ((s * stage_bytes) >> 4);
-          const uint64_t b = desc0 + t0 + ((ts * bytes_b) >> 4);
-          if (lead)
-            for (int j = 0; j < slices; ++j) mma_ss(CG, d, a + 2 * j, b + 2 * j, idesc, acc | (j > 0));
-          acc = 1;
-          commit(&empty[s]);
-          commit(&tempty[ts]);
-          next();
-          ts ^= 1;
-          if (ts == 0) tph ^= 1;
         }
         if (ok) commit(&accf[ab]);
       }
@@ -573,57 +661,50 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     }
   } else if (warp >= 8) {
     // ------------------------------------------------------------------- builders
-    const int tid = threadIdx.x - 256;
-    uint32_t ts = 0, tph = 1;
+    // step i goes to the warps of slot i % tslots
+    const int group = 4 / tslots;
+    const int own = (warp - 8) / group;
+    const int tid = (warp - 8) % group * 32 + lane;
+    uint8_t* const dst = tbuf + 2 * own * bytes_b;
+    uint32_t step = 0, tph = 1;
     bool ok = true;
     const uint32_t tfull0 = CG == 2 ? peer_addr(smem_u32(tfull), 0) : smem_u32(tfull);
     for (int i = worker; i < pieces && ok; i += workers) {
       const Piece c = piece_of(i);
-      const int n = adapters(c);
+      const int n = adapters(c.tile);
       const int m0 = c.tile * p.tile_n + (int)rank * rows_b;
-      for (int d = 0; d < n && ok; ++d) {
-        const int id = p.list[(size_t)c.tile * p.tile_n + d];
-        const float scale = p.scales[id];
-        for (int h = 0; h < 2 * chunks; ++h) {
-          if (!wait(&tempty[ts], tph)) {
+      for (int d = c.seg; d < n && ok; d += S) {
+        for (int h = 0; h < chunks; ++h, ++step) {
+          if ((int)(step % tslots) != own) continue;
+          const int id = p.list[(size_t)c.tile * p.tile_n + d];
+          const int units = (min(64, p.R - h * 64) + 15) / 16 * 2;  // 16-byte units of a row
+          if (!wait(&tempty[own], tph)) {
             ok = false;
             break;
           }
-          uint8_t* dst = tbuf + ts * bytes_b;
-          for (int u = tid; u < rows_b * 8; u += 128) {
-            const int row = u >> 3, j = u & 7;
-            const int m = m0 + row, r = (h >> 1) * 64 + j * 8;
-            Pack<T, 8> o;
-            o.raw = make_uint4(0u, 0u, 0u, 0u);
+          tph ^= 1;
+          for (int u = tid; u < rows_b * units; u += group * 32) {
+            const int row = u / units, j = u - row * units;
+            const int m = m0 + row, r = h * 64 + j * 8;
+            uint4 hi = make_uint4(0u, 0u, 0u, 0u), lo = hi;
             if (m < p.M && r < p.R && p.ids[m] == id) {
-              float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-              for (int g = 0; g < p.tsplits; ++g) {
-                const float4* src =
-                    reinterpret_cast<const float4*>(p.t + ((size_t)g * p.M + m) * p.R + r);
-                const float4 v0 = src[0], v1 = src[1];
-                v[0] += v0.x, v[1] += v0.y, v[2] += v0.z, v[3] += v0.w;
-                v[4] += v1.x, v[5] += v1.y, v[6] += v1.z, v[7] += v1.w;
-              }
-#pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                const float f = v[e] * scale;
-                const T hi = from_f32<T>(f);
-                o.v[e] = (h & 1) ? from_f32<T>(f - to_f32(hi)) : hi;
-              }
+              const T* src = reinterpret_cast<const T*>(p.t) + (size_t)m * 2 * p.R + r;
+              hi = *reinterpret_cast<const uint4*>(src);
+              lo = *reinterpret_cast<const uint4*>(src + p.R);
             }
             // rows of 128 bytes, 16-byte units swizzled by the row (128-byte swizzle)
-            *reinterpret_cast<uint4*>(dst + row * 128 + ((j ^ (row & 7)) << 4)) = o.raw;
+            uint8_t* at = dst + row * 128 + ((j ^ (row & 7)) << 4);
+            *reinterpret_cast<uint4*>(at) = hi;
+            *reinterpret_cast<uint4*>(at + bytes_b) = lo;
           }
           fence_proxy_async();
           __syncwarp();
           if (lane == 0) {
             if (CG == 2 && rank != 0)
-              mbar_arrive_remote(tfull0 + ts * 8);
+              mbar_arrive_remote(tfull0 + own * 8);
             else
-              mbar_arrive(smem_u32(&tfull[ts]));
+              mbar_arrive(smem_u32(&tfull[own]));
           }
-          ts ^= 1;
-          if (ts == 0) tph ^= 1;
         }
       }
     }
@@ -647,7 +728,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       const int m0 = c.tile * p.tile_n;
       const int cols = min(p.tile_n, p.M - m0);
       const int n = (c.block * CG + (int)rank) * 128 + q * 32 + lane;
-      const bool any = c.k1 > c.k0 || (c.seg == S - 1 && p.count[c.tile] > 0);
+      const bool any = c.k1 > c.k0 || p.count[c.tile] > c.seg;
       if (!wait(&accf[ab], (local >> 1) & 1)) break;
       tc_fence_after();
       const uint32_t tbase = tmem + ((uint32_t)(q * 32) << 16) + ab * kAccCols;
@@ -674,7 +755,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
           float v[16];
           load(c0, v);
 #pragma unroll
-          for (int k = 0; k < 16; ++k) mine[(size_t)(c0 + k) * 128] = v[k];
+          for (int k = 0; k < 16; ++k)
+            if (c0 + k < cols) mine[(size_t)(c0 + k) * 128] = v[k];
         }
         __threadfence();
         __syncwarp();
@@ -691,10 +773,12 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
           } else {
 #pragma unroll
             for (int k = 0; k < 16; ++k) v[k] = 0.f;
+#pragma unroll 4
             for (int g = 0; g < S; ++g) {
               const float* src = p.part + slot0 + g * slot_step + q * 32 + lane;
 #pragma unroll
-              for (int k = 0; k < 16; ++k) v[k] += __ldcg(src + (size_t)(c0 + k) * 128);
+              for (int k = 0; k < 16; ++k)
+                if (c0 + k < cols) v[k] += __ldcg(src + (size_t)(c0 + k) * 128);
             }
           }
           if (n < p.N) {
@@ -741,36 +825,93 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   }
 }
 
+// Clusters of `size` CTAs of a kernel that the device holds at once: asked of the runtime
+// once per size and kept (a property of the kernel and the device model).
+template <class K>
+int resident_clusters(K* kernel, int size, int threads, size_t smem, std::atomic<int>& kept,
+                      int num_sms) {
+  int n = kept.load(std::memory_order_relaxed);
+  if (n == 0) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = size;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.gridDim = dim3(num_sms / size * size);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1) return 0;
+    kept.store(n, std::memory_order_relaxed);
+  }
+  return n;
+}
+
+// Segments of K of the tensor-core shrink, one cluster per tile: the count whose rounds of
+// resident clusters take the fewest K steps, a round counting 20 steps for what does not
+// shrink with them (36 clusters of four CTAs are resident, so that 37 tiles of four segments
+// took two rounds and 54 us; of three, see lora_shrink_mma_kernel).
+template <class T>
+int shrink_segments(int tiles, int ksteps, int num_sms) {
+  static std::atomic<int> kept[kShrinkSegments + 1];
+  int best = 1;
+  long long least = -1;
+  for (int s = 1; s <= kShrinkSegments && (s == 1 || s * 4 <= ksteps); ++s) {
+    const int held = s == 1 ? num_sms
+                            : resident_clusters(lora_shrink_mma_kernel<T>, s, kShrinkThreads,
+                                                1024 + kShrinkBytes, kept[s], num_sms);
+    if (held < 1) continue;
+    const long long cost = (long long)((tiles + held - 1) / held) * ((ksteps + s - 1) / s + 20);
+    if (least < 0 || cost < least) {
+      least = cost;
+      best = s;
+    }
+  }
+  return best;
+}
+
 template <class T>
 cudaError_t run(LoraArgs& p, const LoraMaps& maps, int num_sms, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
   attr[0] = pdl_attribute();
-  cfg.blockDim = dim3(kShrinkThreads);
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   cudaError_t e;
   if (p.tsplits == 0) {
-    p.tsplits = 1;
+    int threads = (p.K / 8 + 31) / 32 * 32;
+    threads = threads < kShrinkThreads ? kShrinkThreads : threads > kShrinkMost ? kShrinkMost : threads;
+    cfg.blockDim = dim3(threads);
     cfg.gridDim = dim3((unsigned)(p.tiles + (long long)p.M * (p.R / 8)));
     e = cudaLaunchKernelEx(&cfg, lora_shrink_kernel<T>, p);
   } else {
+    e = cudaFuncSetAttribute(lora_shrink_mma_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             1024 + kShrinkBytes);
+    if (e != cudaSuccess) return e;
+    p.tsplits = shrink_segments<T>(p.tiles, (p.K + 63) / 64, num_sms);
     const int ctas = p.tiles * p.tsplits, cap = 128 / p.R;
     const int most = ((p.L < p.tile_n ? p.L : p.tile_n) + cap - 1) / cap;
     const int share = num_sms / ctas < 1 ? 1 : num_sms / ctas;
+    cfg.blockDim = dim3(kShrinkThreads);
     cfg.gridDim = dim3(ctas, share < most ? share : most);
-    cfg.dynamicSmemBytes = 1024 + (size_t)shrink_stages(p.tile_n) * (kStageA + p.tile_n * 128);
-    e = cudaFuncSetAttribute(lora_shrink_mma_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)cfg.dynamicSmemBytes);
-    if (e == cudaSuccess)
-      e = cudaLaunchKernelEx(&cfg, lora_shrink_mma_kernel<T>, maps.xs, maps.a, p);
+    cfg.dynamicSmemBytes = 1024 + kShrinkBytes;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = p.tsplits;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.numAttrs = 2;
+    e = cudaLaunchKernelEx(&cfg, lora_shrink_mma_kernel<T>, maps.xs, maps.a, p);
+    cfg.numAttrs = 1;
   }
   if (e != cudaSuccess) return e;
   const int stage = kStageA + token_bytes(p.tile_n, p.cg);
-  const int rest = kSmemLimit - 1024 - kCtrl - 2 * token_bytes(p.tile_n, p.cg);
+  const int tslots = 2 * token_slots(p.tile_n, p.cg) * token_bytes(p.tile_n, p.cg);
+  const int rest = kSmemLimit - 1024 - kCtrl - tslots;
   p.stages = rest / stage < kMaxStages ? rest / stage : kMaxStages;
-  const size_t smem = 1024 + kCtrl + (size_t)p.stages * stage + 2 * token_bytes(p.tile_n, p.cg);
+  const size_t smem = 1024 + kCtrl + (size_t)p.stages * stage + tslots;
   auto* k = p.cg == 2 ? lora_gemm_kernel<T, 2> : lora_gemm_kernel<T, 1>;
   e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
@@ -785,9 +926,8 @@ cudaError_t run(LoraArgs& p, const LoraMaps& maps, int num_sms, cudaStream_t str
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
     cfg.numAttrs = 2;
-    int clusters = 0;
-    e = cudaOccupancyMaxActiveClusters(&clusters, k, &cfg);
-    if (e != cudaSuccess) return e;
+    static std::atomic<int> kept;  // every plan's shared memory leaves one CTA an SM
+    const int clusters = resident_clusters(k, 2, kGemmThreads, smem, kept, num_sms);
     if (clusters < 1) return cudaErrorInvalidConfiguration;
     if (2 * clusters < (int)cfg.gridDim.x) cfg.gridDim = dim3((unsigned)(2 * clusters));
   }
@@ -797,16 +937,15 @@ cudaError_t run(LoraArgs& p, const LoraMaps& maps, int num_sms, cudaStream_t str
 }  // namespace
 
 // Tiles, pairs and splits for a problem (SMs of a GB300: the workspace size must not depend
-// on the device).  Up to 256 tokens are one tile and one CTA a unit; more go to CTA pairs,
+// on the device).  Up to 128 tokens are one tile and one CTA a unit; more go to CTA pairs,
 // with the tile width whose last round of units leaves the least idle.  A unit is split
-// along K when there are fewer units than workers, into segments of at least 4 steps; the
-// tensor-core shrink likewise, into at most 8.
+// along K when there are fewer units than workers, into segments of at least 4 steps.
 LoraPlan lora_plan(int M, int K, int N, int R, bool has_w) {
   LoraPlan L;
   const int sms = 152;
   const int ksteps = (K + 63) / 64;
   L.ksteps = has_w ? ksteps : 0;
-  if (M <= 256) {
+  if (M <= 128) {
     L.cg = 1;
     L.tile_n = (M + 15) / 16 * 16;
     L.tiles = 1;
@@ -832,12 +971,7 @@ LoraPlan lora_plan(int M, int K, int N, int R, bool has_w) {
     if (L.splits > L.ksteps / 4) L.splits = L.ksteps / 4 > 0 ? L.ksteps / 4 : 1;
   }
   // the fp32 shrink reads a token's adapter anew for each token: up to 16 MB of such reads
-  L.tsplits = 0;
-  if ((long long)M * R * K * 2 > (16LL << 20)) {
-    int s = sms / L.tiles;
-    if (s > ksteps / 4) s = ksteps / 4;
-    L.tsplits = s < 1 ? 1 : s > 8 ? 8 : s;
-  }
+  L.tsplits = (long long)M * R * K * 2 > (16LL << 20) ? 1 : 0;
   return L;
 }
 
