@@ -1,7 +1,9 @@
-"""Build libqmoe.so (the CUDA kernels and the C-ABI) in-tree for sm_103a.
+"""Build libqmoe.so (the CUDA kernels and the C-ABI) in-tree for sm_103a, and qmoe_torch.so,
+the compiled part of operators.py.
 
 Each .cu file is compiled in parallel with nvcc, then linked into
-``quantized_moe_grouped_route_gb300/_lib/libqmoe.so``.  Runs on a machine without a
+``quantized_moe_grouped_route_gb300/_lib/libqmoe.so``; the host compiler builds
+``_lib/qmoe_torch.so`` against it, PyTorch and Python.  Runs on a machine without a
 GPU (nvcc cross-compiles).  ``python -m quantized_moe_grouped_route_gb300.build``.
 """
 
@@ -12,6 +14,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -20,6 +23,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIBDIR = os.path.join(PKG, "_lib")
 LIB = os.path.join(LIBDIR, "libqmoe.so")
+BINDING = os.path.join(LIBDIR, "qmoe_torch.so")
 
 SOURCES = ["api.cu", "route.cu", "misc.cu", "gemm.cu", "gemm2.cu", "api_ops.cu", "gate.cu", "tokens.cu",
            "lora.cu"]
@@ -38,8 +42,39 @@ def _inputs_mtime() -> float:
     return max(os.path.getmtime(p) for p in paths)
 
 
+def _compile_binding() -> str:
+    """binding.cpp to an object file; the linking waits for libqmoe.so."""
+    import torch
+    from torch.utils import cpp_extension
+    includes = [INCLUDE, sysconfig.get_paths()["include"], "/usr/local/cuda/include",
+                *cpp_extension.include_paths()]
+    obj = os.path.join(BUILD, "binding.o")
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *[f for d in includes for f in ("-isystem" if d != INCLUDE else "-I", d)],
+           "-c", os.path.join(CSRC, "binding.cpp"), "-o", obj]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{cmd[0]} failed for binding.cpp:\n{r.stdout}\n{r.stderr}")
+    return obj
+
+
+def _link_binding(obj: str):
+    from torch.utils import cpp_extension
+    tmp = BINDING + ".tmp"
+    cmd = [os.environ.get("CXX", "g++"), "-shared", "-o", tmp, obj, LIB,
+           *[f"-L{d}" for d in cpp_extension.library_paths()], "-lc10", "-lc10_cuda",
+           "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python", "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
-    if not force and os.path.exists(LIB) and os.path.getmtime(LIB) >= _inputs_mtime():
+    newest = _inputs_mtime()
+    if not force and all(os.path.exists(f) and os.path.getmtime(f) >= newest
+                         for f in (LIB, BINDING)):
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     os.makedirs(LIBDIR, exist_ok=True)
@@ -57,14 +92,18 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
             print(r.stdout, r.stderr, file=sys.stderr)
         return obj
 
-    with concurrent.futures.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with concurrent.futures.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        binding = ex.submit(_compile_binding)
         objs = list(ex.map(compile_one, SOURCES))
+        binding = binding.result()
     tmp = LIB + ".tmp"
-    cmd = [cc, *ARCH, "-shared", "-o", tmp, *objs, "-cudart", "static"]
+    cmd = [cc, *ARCH, "-shared", "-o", tmp, *objs, "-cudart", "static", "-Xlinker",
+           "-soname=libqmoe.so"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    _link_binding(binding)
     return LIB
 
 

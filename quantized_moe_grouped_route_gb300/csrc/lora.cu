@@ -237,7 +237,8 @@ __global__ void __launch_bounds__(kShrinkThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   __shared__ ListScratch scratch;
-  __shared__ int list[kShrinkThreads], place[kShrinkThreads];
+  __shared__ int list[kShrinkThreads];
+  __shared__ __align__(16) int place[kShrinkThreads];
   __shared__ __align__(8) uint64_t full[kShrinkStages], empty[kShrinkStages], accf, acce, drain;
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_word;
@@ -375,12 +376,21 @@ __global__ void __launch_bounds__(kShrinkThreads, 1)
       for (int c0 = 0; c0 < cols; c0 += 16) {
         uint32_t v[16];
         tmem_ld_x16(tmem + ((uint32_t)(q * 32) << 16) + c0, v);
+        // the tokens' places ahead of the stores (looked up between them, each store waited
+        // for its own: 71 cycles a token); tokens past the tile's end have none
+        int4 at[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) at[k] = reinterpret_cast<const int4*>(place + c0)[k];
         tmem_wait_ld();
         tmem_ld_ready(v);
+        float* dst = sums + c0 * p.R + r;
 #pragma unroll
-        for (int k = 0; k < 16; ++k)
-          if (c0 + k < cols && place[c0 + k] == want)
-            sums[(c0 + k) * p.R + r] = __uint_as_float(v[k]);
+        for (int k = 0; k < 4; ++k) {
+          if (at[k].x == want) dst[(4 * k) * p.R] = __uint_as_float(v[4 * k]);
+          if (at[k].y == want) dst[(4 * k + 1) * p.R] = __uint_as_float(v[4 * k + 1]);
+          if (at[k].z == want) dst[(4 * k + 2) * p.R] = __uint_as_float(v[4 * k + 2]);
+          if (at[k].w == want) dst[(4 * k + 3) * p.R] = __uint_as_float(v[4 * k + 3]);
+        }
       }
       tc_fence_before();
       __syncwarp();
