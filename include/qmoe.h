@@ -295,7 +295,8 @@ int qmoe_selftest_timeout(void* workspace_dev, long long limit_ns, void* stream)
  * result is deterministic.  Row strides (ld*) are in elements: at least the row's
  * length, or 0 for the same row throughout (ldx of qmoe_lora_linear: not 0); outputs are
  * contiguous.  The same conventions and limits hold as above
- * (1 <= E <= 2048, 1 <= top_k <= 64, M * top_k < 2^27); M == 0 is a no-op.
+ * (1 <= E <= 2048, 1 <= top_k <= 64, M * top_k < 2^27); rows of 1 <= H <= 2^20 elements;
+ * M == 0 is a no-op.
  */
 #define QMOE_DTYPE_BF16 0
 #define QMOE_DTYPE_FP16 1

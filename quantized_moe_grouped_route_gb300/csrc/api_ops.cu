@@ -14,7 +14,7 @@ bool known_dtype(int dtype) { return dtype >= QMOE_DTYPE_BF16 && dtype <= QMOE_D
 
 int check_tokens(int dtype, int M, int H, int top_k) {
   if (!known_dtype(dtype)) return QMOE_ERR_ARG;
-  if (M < 0 || H < 1 || top_k < 1 || top_k > 64) return QMOE_ERR_SHAPE;
+  if (M < 0 || H < 1 || H > (1 << 20) || top_k < 1 || top_k > 64) return QMOE_ERR_SHAPE;
   if ((long long)M * top_k >= (1LL << 31) / 16) return QMOE_ERR_SHAPE;
   return QMOE_OK;
 }
@@ -33,22 +33,13 @@ int cuda_rc(cudaError_t e) { return e == cudaSuccess ? QMOE_OK : QMOE_ERR_CUDA; 
 
 size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 
-// Workspace of moe_sort_tokens: the error word's block, the route's scratch, its tile list.
-struct SortLayout {
-  int tile_n;
-  size_t scratch, tiles, n_tiles, total;
+// Bytes of the widest chunk (at most 16) in which every one of some matrices' rows moves.
+struct Chunk {
+  int bytes = 16;
+  void rows(const void* p, long long ld, int H, int es) {
+    while (bytes > es && !chunked(p, ld, H, es, bytes)) bytes >>= 1;
+  }
 };
-
-SortLayout sort_layout(int M, int top_k, int E) {
-  SortLayout L;
-  const long long P = (long long)M * top_k;
-  L.tile_n = 4096;  // the route's tile list is not used: as few entries as it can have
-  L.scratch = kWsHeaderBytes;
-  L.tiles = align_up(L.scratch + route_scratch_bytes(P, E), 256);
-  L.n_tiles = align_up(L.tiles + 12 * (size_t)((P + L.tile_n - 1) / L.tile_n + E), 256);
-  L.total = L.n_tiles + 256;
-  return L;
-}
 
 }  // namespace
 }  // namespace qmoe
@@ -132,7 +123,7 @@ int moe_gate_backward(const float* dweights_dev, const void* logits_dev, int dty
 size_t qmoe_sort_workspace_size(int M, int top_k, int E) {
   if (M < 0 || top_k < 1 || top_k > 64 || E < 1 || E > 2048) return 0;
   if ((long long)M * top_k >= (1LL << 31) / 16) return 0;
-  return sort_layout(M, top_k, E).total;
+  return kWsHeaderBytes + sort_scratch_bytes((long long)M * top_k, E);
 }
 
 int moe_sort_tokens(const void* x_dev, int dtype, long long ldx, const int32_t* topk_ids_dev, int M,
@@ -151,24 +142,26 @@ int moe_sort_tokens(const void* x_dev, int dtype, long long ldx, const int32_t* 
       misaligned(topk_ids_dev, 4) || misaligned(offsets_dev, 4) || misaligned(sorted_pair_dev, 4) ||
       misaligned(pair_pos_dev, 4))
     return QMOE_ERR_ARG;
-  const SortLayout L = sort_layout(M, top_k, E);
-  if (ws_bytes < L.total) return QMOE_ERR_WORKSPACE;
+  if (ws_bytes < qmoe_sort_workspace_size(M, top_k, E)) return QMOE_ERR_WORKSPACE;
   int sms = 0;
   rc = device_info(&sms);
   if (rc != QMOE_OK) return rc;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  uint8_t* ws = reinterpret_cast<uint8_t*>(workspace_dev);
-  cudaError_t e = launch_route(topk_ids_dev, M * top_k, E, L.tile_n, offsets_dev, sorted_pair_dev,
-                               pair_pos_dev, reinterpret_cast<int32_t*>(ws + L.tiles),
-                               reinterpret_cast<int32_t*>(ws + L.n_tiles),
-                               reinterpret_cast<unsigned int*>(ws), ws + L.scratch, s, nullptr, 0, 1,
-                               true);
+  unsigned int* err = reinterpret_cast<unsigned int*>(workspace_dev);
+  const int P = M * top_k;
+  Chunk chunk;
+  chunk.rows(x_dev, ldx, H, es);
+  chunk.rows(xs_dev, H, H, es);
+  if (P <= kSortSmallPairs)
+    return cuda_rc(launch_sort_small(x_dev, ldx * es, topk_ids_dev, M, top_k, E, (long long)H * es,
+                                     chunk.bytes, xs_dev, offsets_dev, sorted_pair_dev,
+                                     pair_pos_dev, err, s));
+  cudaError_t e = launch_sort_route(topk_ids_dev, P, E, offsets_dev, sorted_pair_dev, pair_pos_dev,
+                                    err, reinterpret_cast<uint8_t*>(workspace_dev) + kWsHeaderBytes,
+                                    s);
   if (e != cudaSuccess) return QMOE_ERR_CUDA;
-  int chunk = es;
-  for (int b : {4, 16})
-    if (chunked(x_dev, ldx, H, es, b) && chunked(xs_dev, H, H, es, b)) chunk = b;
   return cuda_rc(launch_sort_copy(x_dev, ldx * es, pair_pos_dev, offsets_dev + E, M, top_k,
-                                  (long long)H * es, chunk, xs_dev, sms, s));
+                                  (long long)H * es, chunk.bytes, xs_dev, sms, s));
 }
 
 static int unsort_call(const void* y_dev, int dtype, long long ldy, const int32_t* pair_pos_dev,
@@ -195,8 +188,10 @@ static int unsort_call(const void* y_dev, int dtype, long long ldy, const int32_
   a.H = H;
   a.top_k = top_k;
   a.out = out_dev;
-  const bool vec = chunked(y_dev, ldy, H, es, 16) && chunked(out_dev, H, H, es, 16);
-  return cuda_rc(launch_unsort(a, dtype, vec, sms, reinterpret_cast<cudaStream_t>(stream)));
+  Chunk chunk;
+  chunk.rows(y_dev, ldy, H, es);
+  chunk.rows(out_dev, H, H, es);
+  return cuda_rc(launch_unsort(a, dtype, chunk.bytes / es, sms, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 int moe_sort_tokens_backward(const void* dxs_dev, int dtype, long long ld,
@@ -245,9 +240,12 @@ int moe_unsort_tokens_backward(const void* dout_dev, long long ldd, const void* 
   a.top_k = top_k;
   a.out = dy_dev;
   a.dweights = dweights_dev;
-  const bool vec = chunked(y_dev, ldy, H, es, 16) && chunked(dout_dev, ldd, H, es, 16) &&
-                   chunked(dy_dev, H, H, es, 16);
-  return cuda_rc(launch_unsort_backward(a, dtype, vec, sms, reinterpret_cast<cudaStream_t>(stream)));
+  Chunk chunk;
+  chunk.rows(y_dev, ldy, H, es);
+  chunk.rows(dout_dev, ldd, H, es);
+  chunk.rows(dy_dev, H, H, es);
+  return cuda_rc(launch_unsort_backward(a, dtype, chunk.bytes / es, sms,
+                                        reinterpret_cast<cudaStream_t>(stream)));
 }
 
 static int check_lora(int M, int K, int N, int R, int L) {

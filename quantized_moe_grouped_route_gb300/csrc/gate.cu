@@ -31,7 +31,33 @@ __device__ __forceinline__ uint32_t order_key(float v) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-__device__ __forceinline__ float sigmoid_f32(float l) { return __fdiv_rn(1.0f, 1.0f + expf(-l)); }
+// The reciprocal is correctly rounded, so this is 1 / (1 + exp(-l)) to the bit.
+__device__ __forceinline__ float sigmoid_f32(float l) { return __frcp_rn(1.0f + expf(-l)); }
+
+// Elements e0 .. e0 + VPT - 1 of a row of E as fp32, -infinity past its end; VEC: in wide
+// loads (the row's start, E and e0 are multiples of their length).
+template <class T, int VPT>
+__host__ __device__ constexpr int run_chunk() {
+  return VPT * sizeof(T) <= 16 ? VPT : 16 / (int)sizeof(T);
+}
+template <class T, int VPT, bool VEC>
+__device__ __forceinline__ void load_run(const T* __restrict__ l, int e0, int E, float (&v)[VPT]) {
+  if constexpr (VEC) {
+    constexpr int N = run_chunk<T, VPT>();
+    using P_ = Pack<T, N>;
+#pragma unroll
+    for (int c = 0; c < VPT / N; ++c) {
+      P_ x;
+      const bool in = e0 + c * N < E;
+      if (in) x.raw = *reinterpret_cast<const typename P_::raw_t*>(l + e0 + c * N);
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[c * N + i] = in ? to_f32(x.v[i]) : -INFINITY;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) v[j] = e0 + j < E ? to_f32(l[e0 + j]) : -INFINITY;
+  }
+}
 
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
@@ -89,25 +115,38 @@ __device__ __forceinline__ uint32_t best_groups(const float* row, int E, int n_g
   return keep;
 }
 
-// A warp per row; lane holds the experts lane, lane + 32, ..  The row's keys stay in
-// registers; each of the top_k rounds takes the warp's largest key (one redux), and only
-// the winning lane looks for its next best.
-template <class T, int VPT>
+// A warp per row; lane holds the VPT experts from lane * VPT on, so that the lowest index
+// among equal keys is the lowest lane's lowest j, and a group of a power of two of lanes is
+// reduced by shuffles.
+//
+// The top_k are found in three steps, without a round per slot over all keys (which was
+// half of the kernel's instructions): the top_k-th largest of the lanes' largest keys bounds
+// the top_k-th largest key from below; the keys that reach the bound (a few more than
+// top_k) are compacted to one per lane; and each of those counts the candidates before it,
+// which is its slot.  More than 32 candidates (many equal keys, or top_k near 32 or above)
+// take a round per slot instead.
+struct GateScratch {
+  uint32_t key[32];
+  int expert[32];
+};
+
+template <class T, int VPT, bool VEC>
 __global__ void __launch_bounds__(kGateWarps * 32) gate_kernel(const GateArgs p) {
-  extern __shared__ float rows[];  // [kGateWarps][E], with groups only
+  extern __shared__ float rows[];  // [kGateWarps][E], with groups that lanes do not align with
+  __shared__ GateScratch scratch[kGateWarps];
+  constexpr unsigned kAll = 0xffffffffu;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const unsigned below = (1u << lane) - 1u;
+  const bool sigmoid = p.scoring == QMOE_GATE_SIGMOID;
+  const int e0 = lane * VPT;
+  GateScratch& cand = scratch[warp];
   grid_dep_wait();
   grid_dep_launch();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const bool sigmoid = p.scoring == QMOE_GATE_SIGMOID;
   for (long long m = (long long)blockIdx.x * kGateWarps + warp; m < p.M;
        m += (long long)gridDim.x * kGateWarps) {
     const T* l = reinterpret_cast<const T*>(p.logits) + m * p.ld;
     float v[VPT];
-#pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-      const int e = j * 32 + lane;
-      v[j] = e < p.E ? to_f32(l[e]) : -INFINITY;
-    }
+    load_run<T, VPT, VEC>(l, e0, p.E, v);
     float top = 0.f, total = 0.f;  // over all unmasked experts
     if (!sigmoid && !p.renormalize) {
       top = -INFINITY;
@@ -119,95 +158,160 @@ __global__ void __launch_bounds__(kGateWarps * 32) gate_kernel(const GateArgs p)
         if (v[j] > -INFINITY) total += expf(v[j] - top);
       total = warp_sum(total);
     }
+    if (sigmoid) {
+#pragma unroll
+      for (int j = 0; j < VPT; ++j)
+        v[j] = v[j] > -INFINITY ? sigmoid_f32(v[j]) : -INFINITY;
+      if (p.bias) {
+#pragma unroll
+        for (int j = 0; j < VPT; ++j)
+          if (e0 + j < p.E) v[j] += p.bias[e0 + j];
+      }
+    }
     uint32_t key[VPT];
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
-      const int e = j * 32 + lane;
-      float c = v[j];
-      if (sigmoid && c > -INFINITY) {
-        c = sigmoid_f32(c);
-        if (p.bias) c += p.bias[e];
-      }
-      if (!(c > -INFINITY)) c = -INFINITY;
-      v[j] = c;
-      key[j] = c > -INFINITY ? order_key(c) : 0u;
+      if (!(v[j] > -INFINITY)) v[j] = -INFINITY;
+      key[j] = v[j] > -INFINITY ? order_key(v[j]) : 0u;
     }
-    if (p.n_group > 1) {
+    if (p.group_lanes > 0) {
+      // groups of group_lanes whole lanes (a power of two)
+      float a = -INFINITY, b = -INFINITY;  // the two largest
+#pragma unroll
+      for (int j = 0; j < VPT; ++j) {
+        b = fmaxf(b, fminf(a, v[j]));
+        a = fmaxf(a, v[j]);
+      }
+      for (int o = 1; o < p.group_lanes; o <<= 1) {
+        const float a2 = __shfl_xor_sync(kAll, a, o), b2 = __shfl_xor_sync(kAll, b, o);
+        b = fmaxf(fminf(a, a2), fmaxf(b, b2));
+        a = fmaxf(a, a2);
+      }
+      const float score = sigmoid && p.E > p.n_group ? a + b : a;
+      const int g = lane / p.group_lanes;
+      int rank = 0;
+      for (int h = 0; h < p.n_group; ++h) {
+        const float s = __shfl_sync(kAll, score, h * p.group_lanes);
+        rank += s > score || (s == score && h < g);
+      }
+      if (rank >= p.topk_group) {
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) key[j] = 0u;
+      }
+    } else if (p.n_group > 1) {
       float* row = rows + warp * p.E;
       __syncwarp();
 #pragma unroll
       for (int j = 0; j < VPT; ++j)
-        if (j * 32 + lane < p.E) row[j * 32 + lane] = v[j];
+        if (e0 + j < p.E) row[e0 + j] = v[j];
       __syncwarp();
       const uint32_t keep = best_groups(row, p.E, p.n_group, p.topk_group, sigmoid, lane);
+      const int size = p.E / p.n_group;
+      int g = e0 / size, left = (g + 1) * size - e0;
 #pragma unroll
       for (int j = 0; j < VPT; ++j) {
-        const int g = (j * 32 + lane) / (p.E / p.n_group);
         if (!((keep >> (g & 31)) & 1u)) key[j] = 0u;
-      }
-    }
-    int mine[2] = {-1, -1};  // lane r: the experts of slots r and r + 32
-    uint32_t best = 0;
-    int best_j = 0;
-#pragma unroll
-    for (int j = 0; j < VPT; ++j)
-      if (key[j] > best) {
-        best = key[j];
-        best_j = j;
-      }
-    for (int r = 0; r < p.top_k; ++r) {
-      const uint32_t w = __reduce_max_sync(0xffffffffu, best);
-      if (w == 0u) break;
-      const int e_here = best == w ? best_j * 32 + lane : 0x7fffffff;
-      const int e = (int)__reduce_min_sync(0xffffffffu, (unsigned)e_here);
-      if (lane == (r & 31)) {
-        if (r < 32)
-          mine[0] = e;
-        else
-          mine[1] = e;
-      }
-      if (e_here == e) {
-        best = 0;
-        const int gone = best_j;
-#pragma unroll
-        for (int j = 0; j < VPT; ++j) {
-          if (j == gone) key[j] = 0u;
-          if (key[j] > best) {
-            best = key[j];
-            best_j = j;
-          }
+        if (--left == 0) {
+          ++g;
+          left = size;
         }
       }
     }
-    float s[2] = {0.f, 0.f};
-    float lv[2];
+    uint32_t best = 0;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) lv[i] = mine[i] >= 0 ? to_f32(l[mine[i]]) : -INFINITY;
+    for (int j = 0; j < VPT; ++j) best = max(best, key[j]);
+    // a bound from below of the top_k-th key
+    uint32_t bound = 0, mx = best;
+    for (int r = 0; r < p.top_k; ++r) {
+      bound = __reduce_max_sync(kAll, mx);
+      if (bound == 0u) break;
+      if (mx == bound) mx = 0u;
+    }
+    if (bound == 0u) bound = 1u;  // every unmasked key
+    int n = 0;
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      const bool in = key[j] >= bound;
+      const unsigned who = __ballot_sync(kAll, in);
+      const int at = n + __popc(who & below);
+      if (in && at < 32) {
+        cand.key[at] = key[j];
+        cand.expert[at] = e0 + j;
+      }
+      n += __popc(who);
+    }
+    __syncwarp();
+    // slot `slot` of the row belongs to this lane, with this expert (and a second one above 32)
+    int slot[2] = {-1, -1}, expert[2] = {-1, -1};
+    if (n <= 32) {
+      const bool here = lane < n;
+      const uint32_t k = here ? cand.key[lane] : 0u;
+      const int e = here ? cand.expert[lane] : 0x7fffffff;
+      int rank = 0;
+      for (int i = 0; i < n; ++i) {
+        const uint32_t k2 = cand.key[i];
+        rank += k2 > k || (k2 == k && cand.expert[i] < e);
+      }
+      // the lanes past the candidates take the slots that are left over, as empty ones
+      slot[0] = here ? rank : lane;
+      if (here) expert[0] = e;
+      slot[1] = lane + 32;
+    } else {
+      for (int r = 0; r < p.top_k; ++r) {
+        const uint32_t w = __reduce_max_sync(kAll, best);
+        if (w == 0u) break;
+        const int winner = __ffs(__ballot_sync(kAll, best == w)) - 1;
+        int j_won = 0;
+        if (lane == winner) {
+          best = 0u;
+          bool gone = false;
+#pragma unroll
+          for (int j = 0; j < VPT; ++j) {
+            if (!gone && key[j] == w) {
+              key[j] = 0u;
+              j_won = j;
+              gone = true;
+            }
+            best = max(best, key[j]);
+          }
+        }
+        const int e = __shfl_sync(kAll, e0 + j_won, winner);
+        if (lane == (r & 31)) expert[r >> 5] = e;
+      }
+      slot[0] = lane;
+      slot[1] = lane + 32;
+    }
+    __syncwarp();  // the candidates have been read
+    float s[2] = {0.f, 0.f}, lv[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      if (slot[i] >= p.top_k) slot[i] = expert[i] = -1;
+      lv[i] = expert[i] >= 0 ? to_f32(l[expert[i]]) : -INFINITY;
+    }
     if (sigmoid) {
 #pragma unroll
       for (int i = 0; i < 2; ++i)
-        if (mine[i] >= 0) s[i] = sigmoid_f32(lv[i]);
+        if (expert[i] >= 0) s[i] = sigmoid_f32(lv[i]);
       if (p.renormalize) {
         const float d = warp_sum(s[0] + s[1]) + 1e-20f;
         s[0] /= d;
         s[1] /= d;
       }
     } else {
-      if (p.renormalize) top = __shfl_sync(0xffffffffu, lv[0], 0);  // slot 0 has the largest
+      if (p.renormalize) top = warp_max(fmaxf(lv[0], lv[1]));
 #pragma unroll
       for (int i = 0; i < 2; ++i)
-        if (mine[i] >= 0) s[i] = expf(lv[i] - top);
+        if (expert[i] >= 0) s[i] = expf(lv[i] - top);
       if (p.renormalize) total = warp_sum(s[0] + s[1]);
 #pragma unroll
       for (int i = 0; i < 2; ++i)
-        if (mine[i] >= 0) s[i] /= total;
+        if (expert[i] >= 0) s[i] /= total;
     }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const int r = lane + 32 * i;
-      if (r < p.top_k) {
-        p.ids[m * p.top_k + r] = mine[i];
-        p.weights[m * p.top_k + r] = mine[i] >= 0 ? s[i] * p.scale : 0.f;
+      if (slot[i] >= 0) {
+        p.ids[m * p.top_k + slot[i]] = expert[i];
+        p.weights[m * p.top_k + slot[i]] = expert[i] >= 0 ? s[i] * p.scale : 0.f;
       }
     }
   }
@@ -327,16 +431,29 @@ cudaError_t launch(K* kernel, const GateArgs& p, size_t smem, int num_sms, cudaS
   return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
+template <class T, int VPT>
+cudaError_t gate_vpt(GateArgs p, int num_sms, cudaStream_t stream) {
+  // groups made of whole lanes, a power of two of them
+  const int size = p.E / p.n_group, lanes = size / VPT;
+  p.group_lanes = p.n_group > 1 && size % VPT == 0 && (lanes & (lanes - 1)) == 0 ? lanes : 0;
+  const size_t smem =
+      p.n_group > 1 && p.group_lanes == 0 ? (size_t)kGateWarps * p.E * sizeof(float) : 0;
+  constexpr int N = run_chunk<T, VPT>();
+  const bool vec = reinterpret_cast<uintptr_t>(p.logits) % (N * sizeof(T)) == 0 && p.ld % N == 0 &&
+                   p.E % N == 0;
+  return vec ? launch(gate_kernel<T, VPT, true>, p, smem, num_sms, stream)
+             : launch(gate_kernel<T, VPT, false>, p, smem, num_sms, stream);
+}
+
 template <class T>
 cudaError_t gate(const GateArgs& p, int num_sms, cudaStream_t stream) {
-  const size_t smem = p.n_group > 1 ? (size_t)kGateWarps * p.E * sizeof(float) : 0;
-  if (p.E <= 32) return launch(gate_kernel<T, 1>, p, smem, num_sms, stream);
-  if (p.E <= 64) return launch(gate_kernel<T, 2>, p, smem, num_sms, stream);
-  if (p.E <= 128) return launch(gate_kernel<T, 4>, p, smem, num_sms, stream);
-  if (p.E <= 256) return launch(gate_kernel<T, 8>, p, smem, num_sms, stream);
-  if (p.E <= 512) return launch(gate_kernel<T, 16>, p, smem, num_sms, stream);
-  if (p.E <= 1024) return launch(gate_kernel<T, 32>, p, smem, num_sms, stream);
-  return launch(gate_kernel<T, 64>, p, smem, num_sms, stream);
+  if (p.E <= 32) return gate_vpt<T, 1>(p, num_sms, stream);
+  if (p.E <= 64) return gate_vpt<T, 2>(p, num_sms, stream);
+  if (p.E <= 128) return gate_vpt<T, 4>(p, num_sms, stream);
+  if (p.E <= 256) return gate_vpt<T, 8>(p, num_sms, stream);
+  if (p.E <= 512) return gate_vpt<T, 16>(p, num_sms, stream);
+  if (p.E <= 1024) return gate_vpt<T, 32>(p, num_sms, stream);
+  return gate_vpt<T, 64>(p, num_sms, stream);
 }
 
 }  // namespace

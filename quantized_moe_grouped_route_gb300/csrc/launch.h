@@ -24,6 +24,14 @@ cudaError_t launch_route(const int32_t* ids, int P, int E, int tile_n, int32_t* 
                          int32_t* order = nullptr, int small_rows = 0, int clear_words = 1,
                          bool pdl = false);
 
+// Route of moe_sort_tokens: as launch_route, without tiles; more than kSortSmallPairs pairs
+// (fewer are placed by the kernel that copies their rows, launch_sort_small)
+constexpr int kSortSmallPairs = 1024;
+size_t sort_scratch_bytes(long long P, int E);
+cudaError_t launch_sort_route(const int32_t* ids, int P, int E, int32_t* offsets,
+                              int32_t* sorted_pair, int32_t* pair_pos, unsigned int* err,
+                              void* scratch, cudaStream_t stream);
+
 // api.cu
 // SM count of the current device; QMOE_ERR_ARCH unless it runs sm_103a code
 int device_info(int* num_sms);
@@ -128,6 +136,7 @@ struct GateArgs {
   int scoring;  // QMOE_GATE_*
   const float* bias;
   int n_group, topk_group;
+  int group_lanes;  // set at launch
   int renormalize;
   float scale;
   int32_t* ids;  // forward's outputs
@@ -142,11 +151,16 @@ cudaError_t launch_gate_backward(const GateArgs& p, int dtype, bool vec, int num
                                  cudaStream_t stream);
 
 // tokens.cu
-// xs[pair_pos[i]] = x[i / top_k] in chunks of chunk_bytes (16, 4 or 2, dividing the rows,
+// xs[pair_pos[i]] = x[i / top_k] in chunks of chunk_bytes (16, 8, 4 or 2, dividing the rows,
 // their stride and the pointers), zeros from row n_routed[0] on
 cudaError_t launch_sort_copy(const void* x, long long ldx_bytes, const int32_t* pair_pos,
                              const int32_t* n_routed, int M, int top_k, long long row_bytes,
                              int chunk_bytes, void* xs, int num_sms, cudaStream_t stream);
+// the same with the route in one launch, at most kSortSmallPairs pairs
+cudaError_t launch_sort_small(const void* x, long long ldx_bytes, const int32_t* ids, int M,
+                              int top_k, int E, long long row_bytes, int chunk_bytes, void* xs,
+                              int32_t* offsets, int32_t* sorted_pair, int32_t* pair_pos,
+                              unsigned int* err, cudaStream_t stream);
 struct TokenArgs {
   const void* y;  // pair rows [M * top_k][H], rows ldy elements apart
   long long ldy;
@@ -159,10 +173,11 @@ struct TokenArgs {
   void* out;
   float* dweights;
 };
-// vec: every row is 16-byte aligned and a multiple of 16 bytes long
-cudaError_t launch_unsort(const TokenArgs& a, int dtype, bool vec, int num_sms,
+// chunk: elements that move together (1, 2, 4, or for 16-bit types 8), dividing every row,
+// stride and pointer
+cudaError_t launch_unsort(const TokenArgs& a, int dtype, int chunk, int num_sms,
                           cudaStream_t stream);
-cudaError_t launch_unsort_backward(const TokenArgs& a, int dtype, bool vec, int num_sms,
+cudaError_t launch_unsort_backward(const TokenArgs& a, int dtype, int chunk, int num_sms,
                                    cudaStream_t stream);
 
 // lora.cu

@@ -291,7 +291,155 @@ __global__ void __launch_bounds__(kRouteThreads)
     sorted_pair[pos] = -1;
 }
 
+// Route of moe_sort_tokens above kSortSmallPairs pairs, two kernels over the same blocks of
+// kWarps warps: the first counts each block's pairs per expert; in the second every block
+// adds up the counts of the blocks before it (and of all, for the offsets) itself, which
+// takes the place of a scan kernel between them: that kernel, one block walking [rows][E]
+// counts, was 22 of the 38 us that 65536 pairs took through route_hist_kernel,
+// route_scan_kernel and route_scatter_kernel.
+__global__ void __launch_bounds__(kRouteThreads)
+    sort_count_kernel(const int32_t* __restrict__ ids, int P, int E, int chunk,
+                      int* __restrict__ counts, int* __restrict__ gbad) {
+  extern __shared__ int hist[];  // [kWarps][E]
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+  for (int i = tid; i < kWarps * E; i += kRouteThreads) hist[i] = 0;
+  grid_dep_wait();
+  grid_dep_launch();
+  __syncthreads();
+  const int lo = min(P, ((int)blockIdx.x * kWarps + w) * chunk);
+  const int bad = warp_histogram(ids, lo, min(P, lo + chunk), E, hist + w * E, lane);
+  const int any = __syncthreads_or(bad);
+  for (int e = tid; e < E; e += kRouteThreads) {
+    int c = 0;
+#pragma unroll
+    for (int r = 0; r < kWarps; ++r) c += hist[r * E + e];
+    counts[(size_t)blockIdx.x * E + e] = c;
+  }
+  if (tid == 0) gbad[blockIdx.x] = any;
+}
+
+__global__ void __launch_bounds__(kRouteThreads)
+    sort_place_kernel(const int32_t* __restrict__ ids, int P, int E, int chunk,
+                      const int* __restrict__ counts, const int* __restrict__ gbad,
+                      int32_t* __restrict__ offsets, int32_t* __restrict__ sorted_pair,
+                      int32_t* __restrict__ pair_pos, unsigned int* __restrict__ err) {
+  extern __shared__ int hist[];  // [kWarps][E], then [2][E]: all pairs, pairs of blocks before
+  __shared__ int scan_scratch[kWarps];
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+  const int B = gridDim.x, b = blockIdx.x;
+  int* all = hist + kWarps * E;
+  int* before = all + E;
+  for (int i = tid; i < (kWarps + 2) * E; i += kRouteThreads) hist[i] = 0;
+  __syncthreads();
+  // the block's own counts need only the ids (which precede the counting kernel)
+  const int lo = min(P, (b * kWarps + w) * chunk), hi = min(P, lo + chunk);
+  warp_histogram(ids, lo, hi, E, hist + w * E, lane);
+  grid_dep_wait();
+  grid_dep_launch();
+  // columns of the count table: `shares` threads per expert, each a run of blocks (integer
+  // sums, so their order does not matter)
+  const int shares = E < kRouteThreads ? kRouteThreads / E : 1;
+  for (int i = tid; i < E * shares; i += kRouteThreads) {
+    const int e = i % E, s = i / E;
+    int t = 0, u = 0;
+#pragma unroll 8
+    for (int r = s; r < B; r += shares) {
+      const int c = counts[(size_t)r * E + e];
+      t += c;
+      u += r < b ? c : 0;
+    }
+    if (shares == 1) {
+      all[e] = t;
+      before[e] = u;
+    } else {
+      atomicAdd(&all[e], t);
+      atomicAdd(&before[e], u);
+    }
+  }
+  __syncthreads();
+  const int ept = (E + kRouteThreads - 1) / kRouteThreads;
+  int mine = 0;
+  for (int j = 0; j < ept; ++j)
+    if (tid * ept + j < E) mine += all[tid * ept + j];
+  int total;
+  int base = block_exclusive_scan(mine, scan_scratch, &total);
+  for (int j = 0; j < ept; ++j) {
+    const int e = tid * ept + j;
+    if (e >= E) break;
+    if (b == 0) offsets[e] = base;
+    int run = base + before[e];
+#pragma unroll
+    for (int r = 0; r < kWarps; ++r) {
+      const int c = hist[r * E + e];
+      hist[r * E + e] = run;
+      run += c;
+    }
+    base += all[e];
+  }
+  if (b == 0) {
+    int bad = 0;
+    for (int i = tid; i < B; i += kRouteThreads) bad |= gbad[i];
+    bad = __syncthreads_or(bad);
+    if (tid == 0) {
+      offsets[E] = total;
+      err[0] = bad ? QMOE_FLAG_BAD_ID : 0u;
+    }
+  }
+  __syncthreads();
+  warp_scatter(ids, lo, hi, E, hist + w * E, lane, sorted_pair, pair_pos);
+  for (int pos = total + b * kRouteThreads + tid; pos < P; pos += B * kRouteThreads)
+    sorted_pair[pos] = -1;
+}
+
+// Pairs per warp and blocks: one 32-pair step a warp up to 65536 pairs, then more, so that
+// the table each block reads stays at 128 rows.
+int sort_chunk(long long P) {
+  const long long per_warp = (P + 128LL * kWarps - 1) / (128LL * kWarps);
+  return (int)((per_warp + 31) / 32 * 32);
+}
+int sort_blocks(long long P) {
+  const long long per_block = (long long)sort_chunk(P) * kWarps;
+  return (int)((P + per_block - 1) / per_block);
+}
+
 }  // namespace
+
+// Rows for the most blocks that up to P pairs can take (128, or one per 512 pairs), so that
+// a workspace made for some batch serves every smaller one.
+size_t sort_scratch_bytes(long long P, int E) {
+  const long long rows = (P + 511) / 512 < 128 ? (P + 511) / 512 : 128;
+  return (size_t)(rows < 1 ? 1 : rows) * (E + 1) * sizeof(int);
+}
+
+cudaError_t launch_sort_route(const int32_t* ids, int P, int E, int32_t* offsets,
+                              int32_t* sorted_pair, int32_t* pair_pos, unsigned int* err,
+                              void* scratch, cudaStream_t stream) {
+  const int blocks = sort_blocks(P), chunk = sort_chunk(P);
+  int* counts = reinterpret_cast<int*>(scratch);
+  int* gbad = counts + (size_t)blocks * E;
+  const size_t smem1 = route_smem_bytes(E), smem2 = smem1 + 2 * (size_t)E * sizeof(int);
+  if (smem2 > 48 * 1024) {
+    cudaError_t rc = cudaFuncSetAttribute(sort_count_kernel,
+                                          cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem1);
+    if (rc == cudaSuccess)
+      rc = cudaFuncSetAttribute(sort_place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                (int)smem2);
+    if (rc != cudaSuccess) return rc;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1] = {pdl_attribute()};
+  cfg.gridDim = dim3(blocks);
+  cfg.blockDim = dim3(kRouteThreads);
+  cfg.dynamicSmemBytes = smem1;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cudaError_t rc = cudaLaunchKernelEx(&cfg, sort_count_kernel, ids, P, E, chunk, counts, gbad);
+  if (rc != cudaSuccess) return rc;
+  cfg.dynamicSmemBytes = smem2;
+  return cudaLaunchKernelEx(&cfg, sort_place_kernel, ids, P, E, chunk, (const int*)counts,
+                            (const int*)gbad, offsets, sorted_pair, pair_pos, err);
+}
 
 size_t route_smem_bytes(int E) { return (size_t)kWarps * (size_t)E * sizeof(int); }
 

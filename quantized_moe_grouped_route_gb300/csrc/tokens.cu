@@ -11,8 +11,8 @@
 // pairs are routed, and each pair row is touched once.  Sums are in fp32 in slot order,
 // rounded once; no atomics, so results are deterministic.
 //
-// A row moves in chunks of 16 bytes where the base pointers, row strides and row length
-// allow it, else in single elements (chunk_bytes in api_ops.cu).
+// A row moves in the widest chunks, up to 16 bytes, that the base pointers, row strides and
+// row length allow (Chunk in api_ops.cu); an odd width moves element by element.
 #include "common.cuh"
 #include "launch.h"
 #include "pack.cuh"
@@ -68,48 +68,129 @@ __global__ void __launch_bounds__(kTokThreads)
   }
 }
 
-// A thread per (token, chunk of N elements): the pairs' chunks are added in slot order.
+// The whole sort of few pairs in one launch: a block per (token, segment of kTokThreads
+// chunks), which finds the positions of its own token's pairs from all ids.  With a skipped
+// pair standing for expert E, pair i goes to
+//   #(j: e_j < e_i) + #(j < i: e_j = e_i),
+// a count over all ids per pair, one warp each; the skipped pairs' positions are the rows
+// past the routed ones, which their tokens' blocks zero.  The offsets (#(j: e_j < e)) are
+// shared out over all warps of the grid.  Against the one-block route and the copy as two
+// launches: 128 pairs of 7168 bf16, 10.8 -> see launch_sort_small.
+template <class C>
+__global__ void __launch_bounds__(kTokThreads)
+    sort_small_kernel(const C* __restrict__ x, long long ldx, const int32_t* __restrict__ ids,
+                      int M, int top_k, int E, int chunks, C* __restrict__ xs,
+                      int32_t* __restrict__ offsets, int32_t* __restrict__ sorted_pair,
+                      int32_t* __restrict__ pair_pos, unsigned int* __restrict__ err) {
+  __shared__ int key[kSortSmallPairs];
+  __shared__ int place[64];
+  grid_dep_wait();
+  grid_dep_launch();
+  constexpr int kWarps = kTokThreads / 32;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int P = M * top_k, m = blockIdx.x, c = blockIdx.y * kTokThreads + threadIdx.x;
+  C v{};
+  if (c < chunks) v = x[(size_t)m * ldx + c];
+  bool bad = false;
+  for (int i = threadIdx.x; i < P; i += kTokThreads) {
+    const int e = ids[i];
+    bad |= e >= E;
+    key[i] = e < 0 || e > E ? E : e;
+  }
+  bad = __syncthreads_or(bad);
+  for (int k = warp; k < top_k; k += kWarps) {
+    const int i = m * top_k + k, e = key[i];
+    int n = 0;
+    for (int j = lane; j < P; j += 32) n += key[j] < e || (key[j] == e && j < i);
+    n = __reduce_add_sync(0xffffffffu, n);
+    if (lane == 0) {
+      place[k] = e < E ? n : ~n;
+      if (blockIdx.y == 0) {
+        sorted_pair[n] = e < E ? i : -1;
+        pair_pos[i] = e < E ? n : -1;
+      }
+    }
+  }
+  const int blocks = gridDim.x * gridDim.y, block = blockIdx.y * gridDim.x + blockIdx.x;
+  for (int e = block * kWarps + warp; e <= E; e += blocks * kWarps) {
+    int n = 0;
+    for (int j = lane; j < P; j += 32) n += key[j] < e;
+    n = __reduce_add_sync(0xffffffffu, n);
+    if (lane == 0) offsets[e] = n;
+  }
+  if (block == 0 && threadIdx.x == 0) err[0] = bad ? QMOE_FLAG_BAD_ID : 0u;
+  __syncthreads();
+  if (c < chunks)
+    for (int k = 0; k < top_k; ++k) {
+      const int at = place[k];
+      xs[(size_t)(at >= 0 ? at : ~at) * chunks + c] = at >= 0 ? v : C{};
+    }
+}
+
+// (token, segment of kPer * 32 chunks of N elements) items, one per warp, so that a lane has
+// kPer * (slots) loads in flight: the pairs' chunks are added in slot order.  kPer is 1 for
+// 16-byte chunks; narrower ones need more of them for the same bytes in flight (fp16 rows
+// of 1001 elements, 1023 tokens of 4 slots: one element a thread took 10.3 us).
+template <class T, int N>
+__host__ __device__ constexpr int chunks_per_lane() {
+  return 16 / (int)(sizeof(T) * N) < 4 ? 16 / (int)(sizeof(T) * N) : 4;
+}
 template <class T, int N, bool WEIGHTED>
 __global__ void __launch_bounds__(kTokThreads)
     unsort_kernel(const T* __restrict__ y, long long ldy, const int32_t* __restrict__ pair_pos,
                   const float* __restrict__ w, int M, int top_k, int chunks, T* __restrict__ out) {
   using P_ = Pack<T, N>;
+  using R_ = typename P_::raw_t;
+  constexpr int kPer = chunks_per_lane<T, N>(), kBatch = 8 / kPer < 4 ? 4 : 8 / kPer;
   grid_dep_wait();
   grid_dep_launch();
   const unsigned P = (unsigned)(M * top_k);
-  const long long total = (long long)M * chunks;
-  const long long step = (long long)gridDim.x * blockDim.x;
-  for (long long it = (long long)blockIdx.x * blockDim.x + threadIdx.x; it < total; it += step) {
-    const int m = (int)(it / chunks);
-    const int c = (int)(it - (long long)m * chunks);
-    const int32_t* pp = pair_pos + (size_t)m * top_k;
-    float acc[N];
+  const int lane = threadIdx.x & 31;
+  const int nseg = (chunks + 32 * kPer - 1) / (32 * kPer);
+  const long long items = (long long)M * nseg;
+  const long long step = ((long long)gridDim.x * blockDim.x) >> 5;
+  for (long long it = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5; it < items;
+       it += step) {
+    const int m = (int)(it / nseg);
+    const int c0 = (int)(it - (long long)m * nseg) * 32 * kPer + lane;
+    const size_t slot0 = (size_t)m * top_k;
+    float acc[kPer][N];
 #pragma unroll
-    for (int i = 0; i < N; ++i) acc[i] = 0.f;
-    constexpr int kBatch = 8;
+    for (int j = 0; j < kPer; ++j)
+#pragma unroll
+      for (int i = 0; i < N; ++i) acc[j][i] = 0.f;
     for (int k0 = 0; k0 < top_k; k0 += kBatch) {
-      P_ v[kBatch];
-      bool has[kBatch];
+      P_ v[kBatch][kPer];
+      float wk[kBatch];
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) {
-        const int pos = k0 + k < top_k ? pp[k0 + k] : -1;
-        has[k] = (unsigned)pos < P;
-        if (has[k])
-          v[k].raw = *reinterpret_cast<const typename P_::raw_t*>(y + (size_t)pos * ldy +
-                                                                  (size_t)c * N);
+        const int pos = k0 + k < top_k ? pair_pos[slot0 + k0 + k] : -1;
+        const bool has = (unsigned)pos < P;
+        // a skipped pair's chunk is zeros, its row is not read
+        wk[k] = !has ? 0.f : WEIGHTED ? w[slot0 + k0 + k] : 1.f;
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) {
+          v[k][j].raw = R_{};
+          if (has && c0 + 32 * j < chunks)
+            v[k][j].raw = *reinterpret_cast<const R_*>(y + (size_t)pos * ldy +
+                                                       (size_t)(c0 + 32 * j) * N);
+        }
       }
 #pragma unroll
-      for (int k = 0; k < kBatch; ++k) {
-        if (!has[k]) continue;
-        const float wk = WEIGHTED ? w[(size_t)m * top_k + k0 + k] : 1.f;
+      for (int k = 0; k < kBatch; ++k)
 #pragma unroll
-        for (int i = 0; i < N; ++i) acc[i] = fmaf(wk, to_f32(v[k].v[i]), acc[i]);
-      }
+        for (int j = 0; j < kPer; ++j)
+#pragma unroll
+          for (int i = 0; i < N; ++i) acc[j][i] = fmaf(wk[k], to_f32(v[k][j].v[i]), acc[j][i]);
     }
-    P_ o;
 #pragma unroll
-    for (int i = 0; i < N; ++i) o.v[i] = from_f32<T>(acc[i]);
-    *reinterpret_cast<typename P_::raw_t*>(out + (size_t)it * N) = o.raw;
+    for (int j = 0; j < kPer; ++j) {
+      if (c0 + 32 * j >= chunks) continue;
+      P_ o;
+#pragma unroll
+      for (int i = 0; i < N; ++i) o.v[i] = from_f32<T>(acc[j][i]);
+      *reinterpret_cast<R_*>(out + ((size_t)m * chunks + c0 + 32 * j) * N) = o.raw;
+    }
   }
 }
 
@@ -218,8 +299,9 @@ cudaError_t sort_copy(const void* x, long long ldx_bytes, const int32_t* pair_po
 template <class T, int N>
 cudaError_t unsort(const TokenArgs& a, int num_sms, cudaStream_t stream) {
   const int chunks = a.H / N;
-  const long long total = (long long)a.M * chunks;
-  long long blocks = (total + kTokThreads - 1) / kTokThreads;
+  const int per_warp = 32 * chunks_per_lane<T, N>();
+  const long long warps = (long long)a.M * ((chunks + per_warp - 1) / per_warp);
+  long long blocks = (warps * 32 + kTokThreads - 1) / kTokThreads;
   if (blocks > num_sms * 8LL) blocks = num_sms * 8LL;
   cudaLaunchAttribute attr[1];
   cudaLaunchConfig_t cfg = config(blocks, kTokThreads, stream, attr);
@@ -252,36 +334,68 @@ cudaError_t unsort_backward(const TokenArgs& a, int num_sms, cudaStream_t stream
 cudaError_t launch_sort_copy(const void* x, long long ldx_bytes, const int32_t* pair_pos,
                              const int32_t* n_routed, int M, int top_k, long long row_bytes,
                              int chunk_bytes, void* xs, int num_sms, cudaStream_t stream) {
-  if (chunk_bytes == 16)
-    return sort_copy<uint4>(x, ldx_bytes, pair_pos, n_routed, M, top_k, row_bytes, xs, num_sms,
-                            stream);
-  if (chunk_bytes == 4)
-    return sort_copy<uint32_t>(x, ldx_bytes, pair_pos, n_routed, M, top_k, row_bytes, xs, num_sms,
-                               stream);
-  return sort_copy<uint16_t>(x, ldx_bytes, pair_pos, n_routed, M, top_k, row_bytes, xs, num_sms,
-                             stream);
+  auto go = [&](auto c) {
+    return sort_copy<decltype(c)>(x, ldx_bytes, pair_pos, n_routed, M, top_k, row_bytes, xs,
+                                  num_sms, stream);
+  };
+  return chunk_bytes == 16  ? go(uint4{})
+         : chunk_bytes == 8 ? go(uint2{})
+         : chunk_bytes == 4 ? go(uint32_t{})
+                            : go(uint16_t{});
 }
 
-cudaError_t launch_unsort(const TokenArgs& a, int dtype, bool vec, int num_sms,
+cudaError_t launch_sort_small(const void* x, long long ldx_bytes, const int32_t* ids, int M,
+                              int top_k, int E, long long row_bytes, int chunk_bytes, void* xs,
+                              int32_t* offsets, int32_t* sorted_pair, int32_t* pair_pos,
+                              unsigned int* err, cudaStream_t stream) {
+  auto go = [&](auto c) {
+    using C = decltype(c);
+    const int chunks = (int)(row_bytes / (long long)sizeof(C));
+    cudaLaunchAttribute attr[1];
+    cudaLaunchConfig_t cfg = config(M, kTokThreads, stream, attr);
+    cfg.gridDim.y = (chunks + kTokThreads - 1) / kTokThreads;
+    return cudaLaunchKernelEx(&cfg, sort_small_kernel<C>, reinterpret_cast<const C*>(x),
+                              ldx_bytes / (long long)sizeof(C), ids, M, top_k, E, chunks,
+                              reinterpret_cast<C*>(xs), offsets, sorted_pair, pair_pos, err);
+  };
+  return chunk_bytes == 16  ? go(uint4{})
+         : chunk_bytes == 8 ? go(uint2{})
+         : chunk_bytes == 4 ? go(uint32_t{})
+                            : go(uint16_t{});
+}
+
+template <class T>
+static cudaError_t unsort_chunk(const TokenArgs& a, int chunk, int num_sms, cudaStream_t stream) {
+  if constexpr (sizeof(T) == 2)
+    if (chunk == 8) return unsort<T, 8>(a, num_sms, stream);
+  return chunk == 4   ? unsort<T, 4>(a, num_sms, stream)
+         : chunk == 2 ? unsort<T, 2>(a, num_sms, stream)
+                      : unsort<T, 1>(a, num_sms, stream);
+}
+
+cudaError_t launch_unsort(const TokenArgs& a, int dtype, int chunk, int num_sms,
                           cudaStream_t stream) {
-  if (dtype == QMOE_DTYPE_BF16)
-    return vec ? unsort<__nv_bfloat16, 8>(a, num_sms, stream)
-               : unsort<__nv_bfloat16, 1>(a, num_sms, stream);
-  if (dtype == QMOE_DTYPE_FP16)
-    return vec ? unsort<__half, 8>(a, num_sms, stream) : unsort<__half, 1>(a, num_sms, stream);
-  return vec ? unsort<float, 4>(a, num_sms, stream) : unsort<float, 1>(a, num_sms, stream);
+  if (dtype == QMOE_DTYPE_BF16) return unsort_chunk<__nv_bfloat16>(a, chunk, num_sms, stream);
+  if (dtype == QMOE_DTYPE_FP16) return unsort_chunk<__half>(a, chunk, num_sms, stream);
+  return unsort_chunk<float>(a, chunk, num_sms, stream);
 }
 
-cudaError_t launch_unsort_backward(const TokenArgs& a, int dtype, bool vec, int num_sms,
+template <class T>
+static cudaError_t unsort_backward_chunk(const TokenArgs& a, int chunk, int num_sms,
+                                         cudaStream_t stream) {
+  if constexpr (sizeof(T) == 2)
+    if (chunk == 8) return unsort_backward<T, 8>(a, num_sms, stream);
+  return chunk == 4   ? unsort_backward<T, 4>(a, num_sms, stream)
+         : chunk == 2 ? unsort_backward<T, 2>(a, num_sms, stream)
+                      : unsort_backward<T, 1>(a, num_sms, stream);
+}
+
+cudaError_t launch_unsort_backward(const TokenArgs& a, int dtype, int chunk, int num_sms,
                                    cudaStream_t stream) {
   if (dtype == QMOE_DTYPE_BF16)
-    return vec ? unsort_backward<__nv_bfloat16, 8>(a, num_sms, stream)
-               : unsort_backward<__nv_bfloat16, 1>(a, num_sms, stream);
-  if (dtype == QMOE_DTYPE_FP16)
-    return vec ? unsort_backward<__half, 8>(a, num_sms, stream)
-               : unsort_backward<__half, 1>(a, num_sms, stream);
-  return vec ? unsort_backward<float, 4>(a, num_sms, stream)
-             : unsort_backward<float, 1>(a, num_sms, stream);
+    return unsort_backward_chunk<__nv_bfloat16>(a, chunk, num_sms, stream);
+  if (dtype == QMOE_DTYPE_FP16) return unsort_backward_chunk<__half>(a, chunk, num_sms, stream);
+  return unsort_backward_chunk<float>(a, chunk, num_sms, stream);
 }
 
 }  // namespace qmoe

@@ -89,6 +89,7 @@ def test_sort_refusals(lib):
     assert call(dtype=9) == ARG and call(H=0) == SHAPE and call(k=65) == SHAPE
     assert call(E=0) == SHAPE and call(E=2049) == SHAPE and call(ld=63) == SHAPE
     assert call(M=1 << 26) == SHAPE and call(M=0) == OK
+    assert call(H=(1 << 20) + 1, ld=1 << 21) == SHAPE
     assert call() == ARG and call(p=a, ws=P(4097)) == ARG and call(p=P(4098), ws=a) == ARG
     assert call(p=a, ws=a, n=256) == WS
     assert lib.qmoe_sort_workspace_size(-1, 2, 8) == 0
@@ -429,6 +430,42 @@ def test_sort_matches_route_above_one_block():
     assert torch.equal(offs, o2) and torch.equal(sp, s2) and torch.equal(pp.reshape(-1), p2)
     n = int(offs[-1])
     assert torch.equal(xs[:n], x[sp[:n].long() // k]) and (xs[n:] == 0).all()
+
+
+@gpu
+@pytest.mark.parametrize("M,k,E", [(128, 8, 256), (129, 8, 256), (1024, 1, 3), (205, 5, 2048),
+                                   (8191, 9, 700), (33000, 4, 2048), (100001, 2, 1)])
+def test_sort_tables_match_route(M, k, E):
+    """The one-launch sort, one 32-pair step a warp, and several."""
+    g = _gen(M)
+    ids = torch.randint(-1, E + (E < 2048), (M, k), generator=g, device="cuda",
+                        dtype=torch.int32)  # some skipped, some out of range
+    x = _rows(g, M, 6, torch.bfloat16)
+    ws = torch.empty(q.qmoe_sort_workspace_size(M, k, E), dtype=torch.uint8, device="cuda")
+    ws.fill_(0xCD)
+    xs, offs, sp, pp = q.moe_sort_tokens(x, ids, E, workspace=ws)
+    o2, s2, p2, _, _, ws2 = q.moe_route(ids, E, 64)
+    assert torch.equal(offs, o2) and torch.equal(sp, s2) and torch.equal(pp.reshape(-1), p2)
+    assert qmoe.qmoe_read_error(ws) == qmoe.qmoe_read_error(ws2)
+    n = int(offs[-1])
+    assert torch.equal(xs[:n], x[sp[:n].long() // k]) and (xs[n:] == 0).all()
+
+
+@gpu
+@pytest.mark.parametrize("M,E,k", [(257, 256, 8), (64, 2048, 8), (100, 64, 64), (31, 40, 33)])
+def test_gate_with_many_equal_logits(M, E, k):
+    """Few distinct values: more candidates for the last slots than a warp has lanes."""
+    g = _gen(M)
+    logits = torch.randint(-1, 2, (M, E), generator=g, device="cuda").float()
+    ids, w = q.moe_gate(logits, k)
+    assert torch.equal(ids, torch.sort(logits, dim=1, descending=True,
+                                       stable=True).indices[:, :k].to(torch.int32))
+    logits[torch.rand(M, E, generator=g, device="cuda") < 0.9] = -math.inf
+    ids, w = q.moe_gate(logits, k)
+    want = torch.sort(logits, dim=1, descending=True, stable=True)
+    left = want.values[:, :k] > -math.inf
+    assert torch.equal(ids, torch.where(left, want.indices[:, :k], -1).to(torch.int32))
+    assert (w[~left] == 0).all()
 
 
 @gpu
