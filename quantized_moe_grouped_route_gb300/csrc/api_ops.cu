@@ -258,7 +258,7 @@ static int check_lora(int M, int K, int N, int R, int L) {
 // Workspace of qmoe_lora_linear: the error word's block, arrival counters, the tiles'
 // adapter lists, the low-rank activations, partial sums.
 struct LoraLayout {
-  size_t cnt, count, bad, list, t, part, total;
+  size_t cnt, count, bad, list, place, t, part, total;
   int n_cnt;
 };
 
@@ -270,7 +270,8 @@ static LoraLayout lora_layout(const LoraPlan& P, int M, int R) {
   L.count = align_up(L.cnt + 4 * (size_t)L.n_cnt, 256);
   L.bad = align_up(L.count + 4 * (size_t)P.tiles, 256);
   L.list = align_up(L.bad + 4 * (size_t)P.tiles, 256);
-  L.t = align_up(L.list + 4 * (size_t)P.tiles * P.tile_n, 256);
+  L.place = align_up(L.list + 4 * (size_t)P.tiles * P.tile_n, 256);
+  L.t = align_up(L.place + 4 * (size_t)P.tiles * P.tile_n, 256);
   L.part = align_up(L.t + 4 * (size_t)M * R, 256);
   L.total = L.part;
   if (P.splits > 1) L.total += units * P.splits * P.cg * P.tile_n * 128 * sizeof(float);
@@ -330,6 +331,7 @@ int qmoe_lora_linear(const void* x_dev, int dtype, long long ldx, const void* w_
   p.count = reinterpret_cast<int*>(ws + W.count);
   p.bad = reinterpret_cast<int*>(ws + W.bad);
   p.list = reinterpret_cast<int*>(ws + W.list);
+  p.place = reinterpret_cast<int*>(ws + W.place);
   p.t = ws + W.t;
   p.part = reinterpret_cast<float*>(ws + W.part);
 

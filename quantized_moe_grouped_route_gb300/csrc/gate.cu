@@ -125,9 +125,10 @@ __device__ __forceinline__ uint32_t best_groups(const float* row, int E, int n_g
 // top_k) are compacted to one per lane; and each of those counts the candidates before it,
 // which is its slot.  More than 32 candidates (many equal keys, or top_k near 32 or above)
 // take a round per slot instead.
+// A candidate is one 64-bit number, its key above the complement of its expert, so that the
+// larger number comes first.
 struct GateScratch {
-  uint32_t key[32];
-  int expert[32];
+  unsigned long long cand[32];
 };
 
 template <class T, int VPT, bool VEC>
@@ -139,7 +140,7 @@ __global__ void __launch_bounds__(kGateWarps * 32) gate_kernel(const GateArgs p)
   const unsigned below = (1u << lane) - 1u;
   const bool sigmoid = p.scoring == QMOE_GATE_SIGMOID;
   const int e0 = lane * VPT;
-  GateScratch& cand = scratch[warp];
+  unsigned long long* cand = scratch[warp].cand;
   grid_dep_wait();
   grid_dep_launch();
   for (long long m = (long long)blockIdx.x * kGateWarps + warp; m < p.M;
@@ -159,20 +160,20 @@ __global__ void __launch_bounds__(kGateWarps * 32) gate_kernel(const GateArgs p)
       total = warp_sum(total);
     }
     if (sigmoid) {
+      float bias[VPT];
+      if (p.bias) load_run<float, VPT, VEC>(p.bias, e0, p.E, bias);
 #pragma unroll
-      for (int j = 0; j < VPT; ++j)
-        v[j] = v[j] > -INFINITY ? sigmoid_f32(v[j]) : -INFINITY;
-      if (p.bias) {
-#pragma unroll
-        for (int j = 0; j < VPT; ++j)
-          if (e0 + j < p.E) v[j] += p.bias[e0 + j];
+      for (int j = 0; j < VPT; ++j) {
+        const float s = sigmoid_f32(v[j]);
+        v[j] = v[j] > -INFINITY ? (p.bias ? s + bias[j] : s) : -INFINITY;
       }
     }
     uint32_t key[VPT];
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
-      if (!(v[j] > -INFINITY)) v[j] = -INFINITY;
-      key[j] = v[j] > -INFINITY ? order_key(v[j]) : 0u;
+      const bool in = v[j] > -INFINITY;  // not so for NaN
+      key[j] = in ? order_key(v[j]) : 0u;
+      if (!in) v[j] = -INFINITY;
     }
     if (p.group_lanes > 0) {
       // groups of group_lanes whole lanes (a power of two)
@@ -222,39 +223,38 @@ __global__ void __launch_bounds__(kGateWarps * 32) gate_kernel(const GateArgs p)
     for (int j = 0; j < VPT; ++j) best = max(best, key[j]);
     // a bound from below of the top_k-th key
     uint32_t bound = 0, mx = best;
+#pragma unroll 1
     for (int r = 0; r < p.top_k; ++r) {
       bound = __reduce_max_sync(kAll, mx);
-      if (bound == 0u) break;
       if (mx == bound) mx = 0u;
     }
-    if (bound == 0u) bound = 1u;  // every unmasked key
+    bound = max(bound, 1u);  // no lane left: every unmasked key
     int n = 0;
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
       const bool in = key[j] >= bound;
       const unsigned who = __ballot_sync(kAll, in);
       const int at = n + __popc(who & below);
-      if (in && at < 32) {
-        cand.key[at] = key[j];
-        cand.expert[at] = e0 + j;
-      }
+      if (in && at < 32)
+        cand[at] = (unsigned long long)key[j] << 32 | (uint32_t)~(e0 + j);
       n += __popc(who);
     }
     __syncwarp();
     // slot `slot` of the row belongs to this lane, with this expert (and a second one above 32)
     int slot[2] = {-1, -1}, expert[2] = {-1, -1};
     if (n <= 32) {
-      const bool here = lane < n;
-      const uint32_t k = here ? cand.key[lane] : 0u;
-      const int e = here ? cand.expert[lane] : 0x7fffffff;
-      int rank = 0;
-      for (int i = 0; i < n; ++i) {
-        const uint32_t k2 = cand.key[i];
-        rank += k2 > k || (k2 == k && cand.expert[i] < e);
-      }
       // the lanes past the candidates take the slots that are left over, as empty ones
-      slot[0] = here ? rank : lane;
-      if (here) expert[0] = e;
+      if (lane >= n) cand[lane] = 0u;
+      __syncwarp();
+      const unsigned long long mine = cand[lane];
+      int rank = 0;
+#pragma unroll 1
+      for (int i = 0; i < n; i += 4) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) rank += cand[i + k] > mine;
+      }
+      slot[0] = lane < n ? rank : lane;
+      if (lane < n) expert[0] = (int)~(uint32_t)mine;
       slot[1] = lane + 32;
     } else {
       for (int r = 0; r < p.top_k; ++r) {
@@ -440,6 +440,7 @@ cudaError_t gate_vpt(GateArgs p, int num_sms, cudaStream_t stream) {
       p.n_group > 1 && p.group_lanes == 0 ? (size_t)kGateWarps * p.E * sizeof(float) : 0;
   constexpr int N = run_chunk<T, VPT>();
   const bool vec = reinterpret_cast<uintptr_t>(p.logits) % (N * sizeof(T)) == 0 && p.ld % N == 0 &&
+                   reinterpret_cast<uintptr_t>(p.bias) % (run_chunk<float, VPT>() * 4) == 0 &&
                    p.E % N == 0;
   return vec ? launch(gate_kernel<T, VPT, true>, p, smem, num_sms, stream)
              : launch(gate_kernel<T, VPT, false>, p, smem, num_sms, stream);

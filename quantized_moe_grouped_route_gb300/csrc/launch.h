@@ -207,6 +207,7 @@ struct LoraArgs : LoraPlan {
   int* count;  // [tiles] distinct adapters of a tile
   int* bad;    // [tiles] whether an id of the tile is L or more
   int* list;   // [tiles][tile_n] the distinct adapters
+  int* place;  // [tiles][tile_n] each token's adapter's place in the list, -1: none
   void* t;     // [M][2][R] scales[a] * (x . A^T): rounded, and what the rounding left
   float* part; // [tiles * blocks][splits][cg][tile_n][128] partial sums, splits > 1
 };

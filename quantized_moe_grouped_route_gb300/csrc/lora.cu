@@ -96,8 +96,9 @@ __device__ __forceinline__ int list_adapters(const int32_t* __restrict__ ids, in
 
 // What the GEMM needs of the lists, and zeros where it counts; by one block per tile.
 __device__ __forceinline__ void publish_list(const LoraArgs& p, int t, const int* list, int n,
-                                             bool bad) {
+                                             int mine, bool bad) {
   const int tid = threadIdx.x;
+  if (tid < p.tile_n) p.place[(size_t)t * p.tile_n + tid] = mine;
   if (t == 0) {
     if (tid == 0) p.err[0] = 0u;
     for (int i = tid; i < p.n_cnt; i += blockDim.x) p.cnt[i] = 0;
@@ -125,7 +126,7 @@ __global__ void __launch_bounds__(kShrinkMost) lora_shrink_kernel(const LoraArgs
     bool bad;
     const int n =
         list_adapters(p.ids, m0, min(p.tile_n, p.M - m0), p.L, scratch, list, &mine, &bad);
-    publish_list(p, t, list, n, bad);
+    publish_list(p, t, list, n, mine, bad);
     return;
   }
   __shared__ float part[kWarps][8];
@@ -182,7 +183,13 @@ constexpr int kSmemLimit = 232448;
 // Bytes of one step of a CTA's token rows; slots of the builders' operand (two of them
 // each: t rounded, and the rest): four of one warp each for up to 32 rows, else two of two.
 __host__ __device__ constexpr int token_bytes(int tile_n, int cg) { return tile_n / cg * 128; }
-__host__ __device__ constexpr int token_slots(int tile_n, int cg) { return tile_n / cg <= 32 ? 4 : 2; }
+__host__ __device__ constexpr int token_slots(int tile_n, int cg) { return tile_n / cg <= 64 ? 4 : 2; }
+// The builders' copy of t for a CTA's token rows (both values), where it takes up to 16 KB:
+// every row enters one adapter's step, and the steps then build from shared memory what
+// they would each wait for from L2 (48 tokens of 43 adapters: 22 -> see lora_plan).
+__host__ __device__ constexpr int t_copy_bytes(int tile_n, int cg, int R) {
+  return tile_n / cg * R * 4 <= 16384 ? tile_n / cg * R * 4 : 0;
+}
 
 __device__ __forceinline__ void mma_ss(uint32_t cg, uint32_t d, uint64_t a, uint64_t b,
                                        uint32_t idesc, uint32_t accumulate) {
@@ -204,6 +211,9 @@ __device__ __forceinline__ void mma_ss(uint32_t cg, uint32_t d, uint64_t a, uint
 __device__ __forceinline__ uint32_t idesc_16bit(int M, int N, int dtype) {
   return idesc_bf16_f32(M, N) & (dtype == QMOE_DTYPE_BF16 ? ~0u : ~((1u << 7) | (1u << 10)));
 }
+
+// Barrier of the four builder warps.
+__device__ __forceinline__ void builders_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 
 __device__ __forceinline__ void fence_proxy_async() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -285,7 +295,7 @@ __global__ void __launch_bounds__(kShrinkThreads, 1)
   bool bad;
   const int n = list_adapters(p.ids, m0, cols, p.L, scratch, list, &mine, &bad);
   place[threadIdx.x] = mine;
-  if (seg == 0 && blockIdx.y == 0) publish_list(p, t, list, n, bad);
+  if (seg == 0 && blockIdx.y == 0) publish_list(p, t, list, n, mine, bad);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -448,7 +458,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   const int stages = p.stages;
   const int tslots = token_slots(p.tile_n, CG);
   uint8_t* tbuf = smem + stages * stage_bytes;  // [tslots][2][bytes_b]
-  uint8_t* ctrl = tbuf + 2 * tslots * bytes_b;
+  uint8_t* tcopy = tbuf + 2 * tslots * bytes_b;  // [rows_b][2][R]
+  const int copy_bytes = t_copy_bytes(p.tile_n, CG, p.R);
+  uint8_t* ctrl = tcopy + (copy_bytes + 1023) / 1024 * 1024;
   uint64_t* full = reinterpret_cast<uint64_t*>(ctrl);
   uint64_t* empty = full + kMaxStages;
   uint64_t* tfull = empty + kMaxStages;
@@ -458,6 +470,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   uint64_t* drain = acce + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  short* place = reinterpret_cast<short*>(ctrl + 512);  // [rows_b] the tokens' adapters
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = CG == 2 ? cluster_rank() : 0u;
@@ -679,14 +692,27 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     uint32_t step = 0, tph = 1;
     bool ok = true;
     const uint32_t tfull0 = CG == 2 ? peer_addr(smem_u32(tfull), 0) : smem_u32(tfull);
-    for (int i = worker; i < pieces && ok; i += workers) {
+    const T* tsrc = reinterpret_cast<const T*>(p.t);
+    // (after a wait that gave up a warp still meets the others at their barriers)
+    for (int i = worker; i < pieces; i += workers) {
       const Piece c = piece_of(i);
       const int n = adapters(c.tile);
       const int m0 = c.tile * p.tile_n + (int)rank * rows_b;
+      if (c.seg >= n) continue;  // the same for all builders
+      builders_sync();           // the previous unit's rows have been used
+      for (int r = threadIdx.x - 256; r < rows_b; r += 128)
+        place[r] = (short)p.place[(size_t)c.tile * p.tile_n + (int)rank * rows_b + r];
+      if (copy_bytes) {
+        const int quads = p.R / 4;  // 16-byte units of a row's two values
+        for (int u = threadIdx.x - 256; u < rows_b * quads; u += 128)
+          if (m0 + u / quads < p.M)
+            reinterpret_cast<uint4*>(tcopy)[u] =
+                reinterpret_cast<const uint4*>(tsrc + (size_t)m0 * 2 * p.R)[u];
+      }
+      builders_sync();
       for (int d = c.seg; d < n && ok; d += S) {
         for (int h = 0; h < chunks; ++h, ++step) {
           if ((int)(step % tslots) != own) continue;
-          const int id = p.list[(size_t)c.tile * p.tile_n + d];
           const int units = (min(64, p.R - h * 64) + 15) / 16 * 2;  // 16-byte units of a row
           if (!wait(&tempty[own], tph)) {
             ok = false;
@@ -695,10 +721,11 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
           tph ^= 1;
           for (int u = tid; u < rows_b * units; u += group * 32) {
             const int row = u / units, j = u - row * units;
-            const int m = m0 + row, r = h * 64 + j * 8;
+            const int r = h * 64 + j * 8;
             uint4 hi = make_uint4(0u, 0u, 0u, 0u), lo = hi;
-            if (m < p.M && r < p.R && p.ids[m] == id) {
-              const T* src = reinterpret_cast<const T*>(p.t) + (size_t)m * 2 * p.R + r;
+            if (place[row] == d && r < p.R) {
+              const T* src = copy_bytes ? reinterpret_cast<const T*>(tcopy) + row * 2 * p.R + r
+                                        : tsrc + (size_t)(m0 + row) * 2 * p.R + r;
               hi = *reinterpret_cast<const uint4*>(src);
               lo = *reinterpret_cast<const uint4*>(src + p.R);
             }
@@ -919,9 +946,10 @@ cudaError_t run(LoraArgs& p, const LoraMaps& maps, int num_sms, cudaStream_t str
   if (e != cudaSuccess) return e;
   const int stage = kStageA + token_bytes(p.tile_n, p.cg);
   const int tslots = 2 * token_slots(p.tile_n, p.cg) * token_bytes(p.tile_n, p.cg);
-  const int rest = kSmemLimit - 1024 - kCtrl - tslots;
+  const int copy = (t_copy_bytes(p.tile_n, p.cg, p.R) + 1023) / 1024 * 1024;
+  const int rest = kSmemLimit - 1024 - kCtrl - tslots - copy;
   p.stages = rest / stage < kMaxStages ? rest / stage : kMaxStages;
-  const size_t smem = 1024 + kCtrl + (size_t)p.stages * stage + tslots;
+  const size_t smem = 1024 + kCtrl + (size_t)p.stages * stage + tslots + copy;
   auto* k = p.cg == 2 ? lora_gemm_kernel<T, 2> : lora_gemm_kernel<T, 1>;
   e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;

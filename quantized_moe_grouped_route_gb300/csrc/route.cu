@@ -336,26 +336,37 @@ __global__ void __launch_bounds__(kRouteThreads)
   warp_histogram(ids, lo, hi, E, hist + w * E, lane);
   grid_dep_wait();
   grid_dep_launch();
-  // columns of the count table: `shares` threads per expert, each a run of blocks (integer
-  // sums, so their order does not matter)
-  const int shares = E < kRouteThreads ? kRouteThreads / E : 1;
-  for (int i = tid; i < E * shares; i += kRouteThreads) {
-    const int e = i % E, s = i / E;
-    int t = 0, u = 0;
-#pragma unroll 8
-    for (int r = s; r < B; r += shares) {
-      const int c = counts[(size_t)r * E + e];
-      t += c;
-      u += r < b ? c : 0;
+  // columns of the count table, four experts a thread where E allows: `shares` threads per
+  // column, each a run of rows (integer sums, so their order does not matter)
+  auto add_up = [&](auto zero) {
+    using V = decltype(zero);
+    constexpr int kV = sizeof(V) / sizeof(int);
+    const int cols = E / kV;
+    const int shares = cols < kRouteThreads ? kRouteThreads / cols : 1;
+    for (int i = tid; i < cols * shares; i += kRouteThreads) {
+      const int col = i % cols, s = i / cols;
+      int t[kV] = {}, u[kV] = {};
+#pragma unroll 16
+      for (int r = s; r < B; r += shares) {
+        const V v = *reinterpret_cast<const V*>(counts + (size_t)r * E + col * kV);
+        const int* c = reinterpret_cast<const int*>(&v);
+#pragma unroll
+        for (int k = 0; k < kV; ++k) {
+          t[k] += c[k];
+          u[k] += r < b ? c[k] : 0;
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < kV; ++k) {
+        atomicAdd(&all[col * kV + k], t[k]);
+        atomicAdd(&before[col * kV + k], u[k]);
+      }
     }
-    if (shares == 1) {
-      all[e] = t;
-      before[e] = u;
-    } else {
-      atomicAdd(&all[e], t);
-      atomicAdd(&before[e], u);
-    }
-  }
+  };
+  if (E % 4 == 0)
+    add_up(int4{});
+  else
+    add_up(int{});
   __syncthreads();
   const int ept = (E + kRouteThreads - 1) / kRouteThreads;
   int mine = 0;

@@ -170,10 +170,15 @@ __global__ void __launch_bounds__(kTokThreads)
         wk[k] = !has ? 0.f : WEIGHTED ? w[slot0 + k0 + k] : 1.f;
 #pragma unroll
         for (int j = 0; j < kPer; ++j) {
-          v[k][j].raw = R_{};
-          if (has && c0 + 32 * j < chunks)
-            v[k][j].raw = *reinterpret_cast<const R_*>(y + (size_t)pos * ldy +
-                                                       (size_t)(c0 + 32 * j) * N);
+          if constexpr (sizeof(R_) == 16) {
+            const T* at = y + (has ? (size_t)pos * ldy + (size_t)(c0 + 32 * j) * N : 0);
+            v[k][j].raw = load_if(reinterpret_cast<const R_*>(at), has && c0 + 32 * j < chunks);
+          } else {
+            v[k][j].raw = R_{};
+            if (has && c0 + 32 * j < chunks)
+              v[k][j].raw = *reinterpret_cast<const R_*>(y + (size_t)pos * ldy +
+                                                         (size_t)(c0 + 32 * j) * N);
+          }
         }
       }
 #pragma unroll
@@ -288,7 +293,7 @@ cudaError_t sort_copy(const void* x, long long ldx_bytes, const int32_t* pair_po
   const int chunks = (int)(row_bytes / (long long)sizeof(C));
   const long long warps = (long long)M * ((chunks + 255) / 256);
   long long blocks = (warps * 32 + kTokThreads - 1) / kTokThreads;
-  if (blocks > num_sms * 8LL) blocks = num_sms * 8LL;
+  if (blocks > (1 << 22)) blocks = 1 << 22;
   cudaLaunchAttribute attr[1];
   cudaLaunchConfig_t cfg = config(blocks, kTokThreads, stream, attr);
   return cudaLaunchKernelEx(&cfg, sort_copy_kernel<C>, reinterpret_cast<const C*>(x),
@@ -301,8 +306,9 @@ cudaError_t unsort(const TokenArgs& a, int num_sms, cudaStream_t stream) {
   const int chunks = a.H / N;
   const int per_warp = 32 * chunks_per_lane<T, N>();
   const long long warps = (long long)a.M * ((chunks + per_warp - 1) / per_warp);
+  // a block per eight items, so that the last round of blocks is a small share of them
   long long blocks = (warps * 32 + kTokThreads - 1) / kTokThreads;
-  if (blocks > num_sms * 8LL) blocks = num_sms * 8LL;
+  if (blocks > (1 << 22)) blocks = 1 << 22;
   cudaLaunchAttribute attr[1];
   cudaLaunchConfig_t cfg = config(blocks, kTokThreads, stream, attr);
   const T* y = reinterpret_cast<const T*>(a.y);
