@@ -255,36 +255,28 @@ static int check_lora(int M, int K, int N, int R, int L) {
   return QMOE_OK;
 }
 
-// Workspace of qmoe_lora_linear: the error word's block, arrival counters, the tiles'
-// adapter lists, the low-rank activations, partial sums.
+// Workspace of qmoe_lora_linear: the error word's block, the tiles' adapter lists, the
+// low-rank activations (which do not depend on whether there is a w).
 struct LoraLayout {
-  size_t cnt, count, bad, list, place, t, part, total;
-  int n_cnt;
+  size_t count, bad, list, place, t, total;
 };
 
 static LoraLayout lora_layout(const LoraPlan& P, int M, int R) {
   LoraLayout L;
-  const size_t units = (size_t)P.tiles * P.blocks;
-  L.n_cnt = P.splits > 1 ? (int)(units * P.cg * 4) : 0;
-  L.cnt = kWsHeaderBytes;
-  L.count = align_up(L.cnt + 4 * (size_t)L.n_cnt, 256);
+  const size_t tokens = (size_t)P.tiles * P.tile_n;
+  L.count = kWsHeaderBytes;
   L.bad = align_up(L.count + 4 * (size_t)P.tiles, 256);
   L.list = align_up(L.bad + 4 * (size_t)P.tiles, 256);
-  L.place = align_up(L.list + 4 * (size_t)P.tiles * P.tile_n, 256);
-  L.t = align_up(L.place + 4 * (size_t)P.tiles * P.tile_n, 256);
-  L.part = align_up(L.t + 4 * (size_t)M * R, 256);
-  L.total = L.part;
-  if (P.splits > 1) L.total += units * P.splits * P.cg * P.tile_n * 128 * sizeof(float);
+  L.place = align_up(L.list + 4 * tokens, 256);
+  L.t = align_up(L.place + 4 * tokens, 256);
+  L.total = align_up(L.t + 4 * (size_t)M * R, 256);
   return L;
 }
 
-// The larger of the plans with and without w, so that one workspace serves both.
 size_t qmoe_lora_workspace_size(int M, int K, int N, int R, int L) {
   if (check_lora(M, K, N, R, L) != QMOE_OK) return 0;
   if (M == 0) return kWsHeaderBytes;
-  const size_t with_w = lora_layout(lora_plan(M, K, N, R, true), M, R).total;
-  const size_t without = lora_layout(lora_plan(M, K, N, R, false), M, R).total;
-  return with_w > without ? with_w : without;
+  return lora_layout(lora_plan(M, K, N, R, true), M, R).total;
 }
 
 int qmoe_lora_linear(const void* x_dev, int dtype, long long ldx, const void* w_dev,
@@ -326,14 +318,12 @@ int qmoe_lora_linear(const void* x_dev, int dtype, long long ldx, const void* w_
   p.R = R;
   p.L = L;
   p.err = reinterpret_cast<unsigned int*>(ws);
-  p.cnt = reinterpret_cast<int*>(ws + W.cnt);
-  p.n_cnt = W.n_cnt;
   p.count = reinterpret_cast<int*>(ws + W.count);
   p.bad = reinterpret_cast<int*>(ws + W.bad);
   p.list = reinterpret_cast<int*>(ws + W.list);
   p.place = reinterpret_cast<int*>(ws + W.place);
   p.t = ws + W.t;
-  p.part = reinterpret_cast<float*>(ws + W.part);
+  p.wide = chunked(out_dev, N, N, 2, 16);
 
   LoraMaps maps;
   const uint64_t dx[2] = {(uint64_t)K, (uint64_t)M}, sx[1] = {(uint64_t)ldx * 2};

@@ -91,14 +91,15 @@ __device__ __forceinline__ void tmem_dealloc2(uint32_t taddr, uint32_t ncols) {
   asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols)
                : "memory");
 }
-// Arrive once on the barrier at `bar` in both CTAs of the pair when the MMAs issued so
-// far complete.
-__device__ __forceinline__ void tc_commit2_both_if(uint32_t pred, uint32_t bar) {
+// Arrive once on the barrier at `bar` in both CTAs of the pair (bits of `mask`: their ranks
+// in the cluster) when the MMAs issued so far complete.
+__device__ __forceinline__ void tc_commit2_both_if(uint32_t pred, uint32_t bar,
+                                                   uint16_t mask = 3) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b16 m;\n\tsetp.ne.b32 p, %0, 0;\n\tmov.b16 m, 3;\n\t"
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %0, 0;\n\t"
       "@p tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
-      "[%1], m;\n\t}" ::"r"(pred),
-      "r"(bar)
+      "[%1], %2;\n\t}" ::"r"(pred),
+      "r"(bar), "h"(mask)
       : "memory");
 }
 // 2-D tensor copy into this CTA's shared memory whose completion is counted on a

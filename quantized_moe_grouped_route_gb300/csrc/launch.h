@@ -181,12 +181,12 @@ cudaError_t launch_unsort_backward(const TokenArgs& a, int dtype, int chunk, int
                                    cudaStream_t stream);
 
 // lora.cu
-// How a problem is cut: token tiles of tile_n (a multiple of 16, at most 256), units of one
-// tile x 128 * cg rows of w (cg: CTAs per unit), each unit's ksteps steps of 64 of K in
-// `splits` segments; the shrink with plain products (tsplits 0) or on the tensor cores
-// (tsplits its segments of K, chosen at launch).
+// How a problem is cut: token tiles of tile_n (a multiple of 16, at most 240), units of one
+// tile x 128 * cg rows of w (cg: CTAs per unit), each of ksteps steps of 64 of K; the shrink
+// with plain products (tsplits 0) or on the tensor cores (tsplits its segments of K, set at
+// launch).
 struct LoraPlan {
-  int cg, tile_n, tiles, blocks, ksteps, splits, tsplits;
+  int cg, tile_n, tiles, blocks, ksteps, tsplits;
 };
 LoraPlan lora_plan(int M, int K, int N, int R, bool has_w);
 struct LoraArgs : LoraPlan {
@@ -200,16 +200,14 @@ struct LoraArgs : LoraPlan {
   long long ldbase;
   void* out;  // [M][N]
   int M, K, N, R, L;
-  int stages;  // of the GEMM's ring (launch_lora)
+  int wide;    // rows of out move in 16-byte chunks
+  int stages, splits;  // of the GEMM's ring, of a unit's steps (set at launch)
   unsigned int* err;
-  int* cnt;    // arrival counters [tiles * blocks][cg][4], n_cnt in all
-  int n_cnt;
   int* count;  // [tiles] distinct adapters of a tile
   int* bad;    // [tiles] whether an id of the tile is L or more
   int* list;   // [tiles][tile_n] the distinct adapters
   int* place;  // [tiles][tile_n] each token's adapter's place in the list, -1: none
   void* t;     // [M][2][R] scales[a] * (x . A^T): rounded, and what the rounding left
-  float* part; // [tiles * blocks][splits][cg][tile_n][128] partial sums, splits > 1
 };
 struct LoraMaps {
   CUtensorMap x, w, b;  // the GEMM's

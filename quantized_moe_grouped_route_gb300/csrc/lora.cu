@@ -6,7 +6,7 @@
 // many) forms the sums x . A^T in fp32 and lists, for each tile
 // of tokens, the distinct adapters its tokens use.  The second is one GEMM whose
 // contraction runs over K and then over the ranks of the tile's adapters: the MMA's M side
-// is 128 rows of w (or of B[a]), its N side a tile of up to 256 tokens, and for each of
+// is 128 rows of w (or of B[a]), its N side a tile of up to 240 tokens, and for each of
 // the tile's adapters the token operand is t with the rows of other adapters zero.  So the
 // adapters cost a tile (distinct adapters) * ranks more of contraction length, whatever
 // the order of the tokens, and the result is rounded once.
@@ -16,17 +16,20 @@
 // of a contraction that is short, instead of a second rounding of the result's size.  The
 // shrink kernel writes both.
 //
-// GEMM pipeline (a unit is 128 rows of w per CTA x one token tile, its contraction split
-// into S segments when there are fewer units than SMs):
+// GEMM pipeline (a unit is 128 rows of w per CTA x one token tile; when there are fewer
+// units than SMs the contraction is split into S segments, one CTA or pair each in one
+// cluster):
 //   warp 0      TMA producer: steps of 64 of K, [128 rows of w | token rows], then per
 //               adapter and 64 ranks [128 rows of B[a]]
 //   warp 1      MMA issue: 4 x tcgen05.mma kind::f16 per step, fp32 accumulator in TMEM,
 //               two accumulators, so that the epilogue overlaps the next unit
-//   warps 4-7   epilogue: TMEM -> registers -> base, rounding, global stores; with S > 1
-//               the segments' partial sums are added in K order by the last to arrive
-//   warps 8-11  builders: the token operand (both values of t) of the adapter steps, in
-//               slots of their own; one warp (few tokens) or two build a step, so that
-//               several steps are in the making at once
+//   warps 4-7   epilogue: TMEM -> registers -> base, rounding -> a transpose through shared
+//               memory -> 16-byte global stores; with S > 1 each segment's sums stay in its
+//               shared memory, and after a cluster barrier every CTA adds up a share of the
+//               tokens over all segments, in K order
+//   warps 8-15  builders: the token operand (both values of t) of the adapter steps, in
+//               slots of their own; one to four warps (the more, the wider the tile) build a
+//               step, so that several steps are in the making at once
 // Few tokens (one tile): one CTA per unit, w streamed once, HBM bound.  More: CTA pairs
 // (cta_group::2, M = 256), each SM loading half of the token rows, since a 128 x 256 tile
 // fed by one SM alone asks more of its L2 port (96 bytes a clock) than it has.
@@ -46,7 +49,7 @@ namespace {
 // A block per (token, 8 ranks) with a thread per 8 elements of K (up to 1024), so that a
 // single token's latency is about one round trip to memory; the eight sums are reduced in
 // a fixed order.  The blocks before them list the tiles' adapters (one block each) and zero
-// the error word and the arrival counters.
+// the error word.
 constexpr int kShrinkThreads = 256;
 
 // The distinct valid ids of a tile's tokens, in order of first appearance, into list
@@ -94,15 +97,12 @@ __device__ __forceinline__ int list_adapters(const int32_t* __restrict__ ids, in
   return total;
 }
 
-// What the GEMM needs of the lists, and zeros where it counts; by one block per tile.
+// What the GEMM needs of the lists; by one block per tile.
 __device__ __forceinline__ void publish_list(const LoraArgs& p, int t, const int* list, int n,
                                              int mine, bool bad) {
   const int tid = threadIdx.x;
   if (tid < p.tile_n) p.place[(size_t)t * p.tile_n + tid] = mine;
-  if (t == 0) {
-    if (tid == 0) p.err[0] = 0u;
-    for (int i = tid; i < p.n_cnt; i += blockDim.x) p.cnt[i] = 0;
-  }
+  if (t == 0 && tid == 0) p.err[0] = 0u;
   for (int i = tid; i < n; i += blockDim.x) p.list[(size_t)t * p.tile_n + i] = list[i];
   const bool any = __syncthreads_or(bad);
   if (tid == 0) {
@@ -173,22 +173,28 @@ __global__ void __launch_bounds__(kShrinkMost) lora_shrink_kernel(const LoraArgs
 }
 
 // ------------------------------------------------------------------------------- GEMM
-constexpr int kGemmThreads = 384;
+constexpr int kBuilders = 8;  // warps
+constexpr int kGemmThreads = 256 + 32 * kBuilders;
 constexpr int kStageA = 128 * 128;  // 128 rows x 64 elements
 constexpr int kMaxStages = 12;
 constexpr int kAccCols = 256;  // TMEM columns of one accumulator
 constexpr int kCtrl = 1024;
+constexpr int kEpiStage = 4 * 2048;  // transpose tiles of the epilogue warps: 32 tokens x 32 rows
 constexpr int kSmemLimit = 232448;
+constexpr int kMostTokens = 240;  // of a tile: five stages of the ring; 256 leave room for four
+constexpr int kMaxSplits = 8;  // CTAs of a cluster, at most
 
 // Bytes of one step of a CTA's token rows; slots of the builders' operand (two of them
-// each: t rounded, and the rest): four of one warp each for up to 32 rows, else two of two.
+// each: t rounded, and the rest), fewer the wider the tile.
 __host__ __device__ constexpr int token_bytes(int tile_n, int cg) { return tile_n / cg * 128; }
-__host__ __device__ constexpr int token_slots(int tile_n, int cg) { return tile_n / cg <= 64 ? 4 : 2; }
+__host__ __device__ constexpr int token_slots(int tile_n, int cg) {
+  return tile_n / cg <= 48 ? 8 : tile_n / cg <= 64 ? 4 : 2;
+}
 // The builders' copy of t for a CTA's token rows (both values), where it takes up to 16 KB:
 // every row enters one adapter's step, and the steps then build from shared memory what
 // they would each wait for from L2 (48 tokens of 43 adapters: 22 -> see lora_plan).
 __host__ __device__ constexpr int t_copy_bytes(int tile_n, int cg, int R) {
-  return tile_n / cg * R * 4 <= 16384 ? tile_n / cg * R * 4 : 0;
+  return cg == 1 && tile_n * R * 4 <= 16384 ? tile_n * R * 4 : 0;
 }
 
 __device__ __forceinline__ void mma_ss(uint32_t cg, uint32_t d, uint64_t a, uint64_t b,
@@ -212,8 +218,10 @@ __device__ __forceinline__ uint32_t idesc_16bit(int M, int N, int dtype) {
   return idesc_bf16_f32(M, N) & (dtype == QMOE_DTYPE_BF16 ? ~0u : ~((1u << 7) | (1u << 10)));
 }
 
-// Barrier of the four builder warps.
-__device__ __forceinline__ void builders_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+// Barrier of the builder warps.
+__device__ __forceinline__ void builders_sync() {
+  asm volatile("bar.sync 1, %0;" ::"n"(32 * kBuilders) : "memory");
+}
 
 __device__ __forceinline__ void fence_proxy_async() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -461,11 +469,12 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   uint8_t* tcopy = tbuf + 2 * tslots * bytes_b;  // [rows_b][2][R]
   const int copy_bytes = t_copy_bytes(p.tile_n, CG, p.R);
   uint8_t* ctrl = tcopy + (copy_bytes + 1023) / 1024 * 1024;
+  uint8_t* epi_stage = ctrl + kCtrl;
   uint64_t* full = reinterpret_cast<uint64_t*>(ctrl);
   uint64_t* empty = full + kMaxStages;
   uint64_t* tfull = empty + kMaxStages;
-  uint64_t* tempty = tfull + 4;
-  uint64_t* accf = tempty + 4;
+  uint64_t* tempty = tfull + 8;
+  uint64_t* accf = tempty + 8;
   uint64_t* acce = accf + 2;
   uint64_t* drain = acce + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
@@ -473,16 +482,21 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   short* place = reinterpret_cast<short*>(ctrl + 512);  // [rows_b] the tokens' adapters
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t rank = CG == 2 ? cluster_rank() : 0u;
-  const int worker = CG == 2 ? (int)cluster_index() : (int)blockIdx.x;
-  const int workers = CG == 2 ? (int)cluster_count() : (int)gridDim.x;
+  // a cluster: S segments of CG CTAs
+  const int S = p.splits;
+  const bool clustered = CG * S > 1;
+  const uint32_t crank = clustered ? cluster_rank() : 0u;
+  const uint32_t rank = crank % CG, lead_rank = crank - rank;
+  const int seg = (int)crank / CG;
+  const int worker = clustered ? (int)cluster_index() : (int)blockIdx.x;
+  const int workers = clustered ? (int)cluster_count() : (int)gridDim.x;
   if (threadIdx.x == 0) {
     for (int s = 0; s < stages; ++s) {
       mbar_init(smem_u32(&full[s]), 1);
       mbar_init(smem_u32(&empty[s]), 1);
     }
     for (int i = 0; i < tslots; ++i) {
-      mbar_init(smem_u32(&tfull[i]), 4 / tslots * CG);
+      mbar_init(smem_u32(&tfull[i]), kBuilders / tslots * CG);
       mbar_init(smem_u32(&tempty[i]), 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -510,28 +524,14 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   grid_dep_launch();
   tc_fence_before();
   __syncthreads();
-  if (CG == 2) cluster_sync_all();  // the peer's barriers exist before any remote arrival
+  if (clustered) cluster_sync_all();  // the peer's barriers exist before any remote arrival
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
   const int ksteps = p.ksteps;  // of the shared product; 0 without w
   const int chunks = (p.R + 63) / 64;
-  const int S = p.splits;
-  const int pieces = p.tiles * p.blocks * S;
-  // piece = (tile, block, segment), segments of a unit next to each other
-  struct Piece {
-    int tile, block, seg, k0, k1;
-  };
-  auto piece_of = [&](int i) {
-    Piece c;
-    const int u = i / S;
-    c.seg = i - u * S;
-    c.tile = u / p.blocks;
-    c.block = u - c.tile * p.blocks;
-    c.k0 = (int)((long long)ksteps * c.seg / S);
-    c.k1 = (int)((long long)ksteps * (c.seg + 1) / S);
-    return c;
-  };
+  const int units = p.tiles * p.blocks;
+  const int k0 = (int)((long long)ksteps * seg / S), k1 = (int)((long long)ksteps * (seg + 1) / S);
   // bounded waits; the pair's barriers take arrivals from both CTAs
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
     if (CG == 2) return warp_wait_cl(smem_u32(bar), parity, abort_flag, p.err);
@@ -554,18 +554,18 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     uint32_t s = 0, ph = 1;
     bool ok = true;
     // the leader's barriers as seen from this CTA (pair: both CTAs' copies count there)
-    const uint32_t full0 = CG == 2 ? peer_addr(smem_u32(full), 0) : smem_u32(full);
+    const uint32_t full0 = CG == 2 ? peer_addr(smem_u32(full), lead_rank) : smem_u32(full);
     auto next = [&]() {
       if (++s == (uint32_t)stages) {
         s = 0;
         ph ^= 1;
       }
     };
-    for (int i = worker; i < pieces && ok; i += workers) {
-      const Piece c = piece_of(i);
-      const int row = (c.block * CG + (int)rank) * 128;
-      const int m = c.tile * p.tile_n + (int)rank * rows_b;
-      for (int k = c.k0; k < c.k1; ++k) {
+    for (int i = worker; i < units && ok; i += workers) {
+      const int tile = i / p.blocks, block = i - tile * p.blocks;
+      const int row = (block * CG + (int)rank) * 128;
+      const int m = tile * p.tile_n + (int)rank * rows_b;
+      for (int k = k0; k < k1; ++k) {
         if (!wait(&empty[s], ph)) {
           ok = false;
           break;
@@ -582,9 +582,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         }
         next();
       }
-      const int n = ok ? adapters(c.tile) : 0;
-      for (int d = c.seg; d < n && ok; d += S) {
-        const int id = p.list[(size_t)c.tile * p.tile_n + d];
+      const int n = ok ? adapters(tile) : 0;
+      for (int d = seg; d < n && ok; d += S) {
+        const int id = p.list[(size_t)tile * p.tile_n + d];
         for (int h = 0; h < chunks; ++h) {
           if (!wait(&empty[s], ph)) {
             ok = false;
@@ -616,7 +616,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       bool ok = true;
       auto commit = [&](uint64_t* bar) {
         if (CG == 2)
-          tc_commit2_both_if(lead, smem_u32(bar));
+          tc_commit2_both_if(lead, smem_u32(bar), (uint16_t)(3u << lead_rank));
         else
           tc_commit_if(lead, smem_u32(bar));
       };
@@ -626,8 +626,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
           ph ^= 1;
         }
       };
-      for (int i = worker; i < pieces && ok; i += workers, ++local) {
-        const Piece c = piece_of(i);
+      for (int i = worker; i < units && ok; i += workers, ++local) {
         const int ab = local & 1;
         if (!wait(&acce[ab], ((local >> 1) & 1) ^ 1)) {
           ok = false;
@@ -636,7 +635,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         tc_fence_after();
         const uint32_t dst = tmem + ab * kAccCols;
         uint32_t acc = 0;
-        for (int k = c.k0; k < c.k1; ++k) {
+        for (int k = k0; k < k1; ++k) {
           if (!wait(&full[s], ph)) {
             ok = false;
             break;
@@ -652,8 +651,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
           commit(&empty[s]);
           next();
         }
-        const int n = ok ? adapters(c.tile) : 0;
-        for (int d = c.seg; d < n && ok; d += S) {
+        const int n = ok ? adapters(i / p.blocks) : 0;
+        for (int d = seg; d < n && ok; d += S) {
           for (int h = 0; h < chunks; ++h) {
             const int slices = (min(64, p.R - h * 64) + 15) / 16;
             if (!wait(&full[s], ph) || !wait(&tfull[ts], tph)) {
@@ -685,32 +684,32 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   } else if (warp >= 8) {
     // ------------------------------------------------------------------- builders
     // step i goes to the warps of slot i % tslots
-    const int group = 4 / tslots;
+    const int group = kBuilders / tslots;
     const int own = (warp - 8) / group;
     const int tid = (warp - 8) % group * 32 + lane;
     uint8_t* const dst = tbuf + 2 * own * bytes_b;
     uint32_t step = 0, tph = 1;
     bool ok = true;
-    const uint32_t tfull0 = CG == 2 ? peer_addr(smem_u32(tfull), 0) : smem_u32(tfull);
+    const uint32_t tfull0 = CG == 2 ? peer_addr(smem_u32(tfull), lead_rank) : smem_u32(tfull);
     const T* tsrc = reinterpret_cast<const T*>(p.t);
     // (after a wait that gave up a warp still meets the others at their barriers)
-    for (int i = worker; i < pieces; i += workers) {
-      const Piece c = piece_of(i);
-      const int n = adapters(c.tile);
-      const int m0 = c.tile * p.tile_n + (int)rank * rows_b;
-      if (c.seg >= n) continue;  // the same for all builders
+    for (int i = worker; i < units; i += workers) {
+      const int tile = i / p.blocks;
+      const int n = adapters(tile);
+      const int m0 = tile * p.tile_n + (int)rank * rows_b;
+      if (seg >= n) continue;    // the same for all builders
       builders_sync();           // the previous unit's rows have been used
-      for (int r = threadIdx.x - 256; r < rows_b; r += 128)
-        place[r] = (short)p.place[(size_t)c.tile * p.tile_n + (int)rank * rows_b + r];
+      for (int r = threadIdx.x - 256; r < rows_b; r += 32 * kBuilders)
+        place[r] = (short)p.place[(size_t)m0 + r];
       if (copy_bytes) {
         const int quads = p.R / 4;  // 16-byte units of a row's two values
-        for (int u = threadIdx.x - 256; u < rows_b * quads; u += 128)
+        for (int u = threadIdx.x - 256; u < rows_b * quads; u += 32 * kBuilders)
           if (m0 + u / quads < p.M)
             reinterpret_cast<uint4*>(tcopy)[u] =
                 reinterpret_cast<const uint4*>(tsrc + (size_t)m0 * 2 * p.R)[u];
       }
       builders_sync();
-      for (int d = c.seg; d < n && ok; d += S) {
+      for (int d = seg; d < n && ok; d += S) {
         for (int h = 0; h < chunks; ++h, ++step) {
           if ((int)(step % tslots) != own) continue;
           const int units = (min(64, p.R - h * 64) + 15) / 16 * 2;  // 16-byte units of a row
@@ -748,86 +747,74 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   } else if (warp >= 4) {
     // ------------------------------------------------------------------- epilogue
     const int q = warp & 3;
-    const uint32_t acce0 = CG == 2 ? peer_addr(smem_u32(acce), 0) : smem_u32(acce);
+    const uint32_t acce0 = CG == 2 ? peer_addr(smem_u32(acce), lead_rank) : smem_u32(acce);
     uint32_t local = 0;
-    T* out = reinterpret_cast<T*>(p.out);
-    const T* base = reinterpret_cast<const T*>(p.base);
-    grid_dep_wait();  // the counters are the shrink kernel's to clear
-    if (worker == 0 && rank == 0 && warp == 4) {
+    grid_dep_wait();  // the shrink kernel's lists
+    if (worker == 0 && crank == 0 && warp == 4) {
       bool bad = false;
       for (int t = lane; t < p.tiles; t += 32) bad |= p.bad[t] != 0;
       bad = __any_sync(0xffffffffu, bad);
       if (lane == 0 && bad) atomicOr(p.err, QMOE_FLAG_BAD_ID);
     }
-    for (int i = worker; i < pieces; i += workers, ++local) {
-      const Piece c = piece_of(i);
+    T* stage = reinterpret_cast<T*>(epi_stage + q * 2048);  // [32 tokens][32 rows]
+    for (int i = worker; i < units; i += workers, ++local) {
+      const int tile = i / p.blocks, block = i - tile * p.blocks;
       const int ab = local & 1;
-      const int m0 = c.tile * p.tile_n;
+      const int m0 = tile * p.tile_n;
       const int cols = min(p.tile_n, p.M - m0);
-      const int n = (c.block * CG + (int)rank) * 128 + q * 32 + lane;
-      const bool any = c.k1 > c.k0 || p.count[c.tile] > c.seg;
+      const int n0 = (block * CG + (int)rank) * 128 + q * 32;
+      const bool any = k1 > k0 || p.count[tile] > seg;
       if (!wait(&accf[ab], (local >> 1) & 1)) break;
       tc_fence_after();
       const uint32_t tbase = tmem + ((uint32_t)(q * 32) << 16) + ab * kAccCols;
-      auto load = [&](int c0, float (&v)[16]) {
-        if (!any) {
+      for (int c0 = 0; c0 < cols; c0 += 32) {
+        float v[32];
+        if (any) {
+          // (a tile's last 16 columns may be followed by columns of no meaning, within the
+          // accumulator's 256)
+          uint32_t r[2][16];
+          tmem_ld_x16(tbase + c0, r[0]);
+          tmem_ld_x16(tbase + c0 + 16, r[1]);
+          tmem_wait_ld();
+          tmem_ld_ready(r[0]);
+          tmem_ld_ready(r[1]);
 #pragma unroll
-          for (int k = 0; k < 16; ++k) v[k] = 0.f;
-          return;
+          for (int k = 0; k < 32; ++k) v[k] = __uint_as_float(r[k >> 4][k & 15]);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 32; ++k) v[k] = 0.f;
         }
-        uint32_t r[16];
-        tmem_ld_x16(tbase + c0, r);
-        tmem_wait_ld();
-        tmem_ld_ready(r);
+        if (S > 1) {
+          // this segment's sums [token][row], over the ring, which is idle: a CTA of a split
+          // unit has this one unit, and its MMAs are complete
+          float* sums = reinterpret_cast<float*>(smem) + (size_t)c0 * 128 + q * 32 + lane;
 #pragma unroll
-        for (int k = 0; k < 16; ++k) v[k] = __uint_as_float(r[k]);
-      };
-      bool last = true;
-      const size_t slot0 = ((size_t)(i / S) * S * CG + rank) * 128 * p.tile_n;
-      const size_t slot_step = (size_t)CG * 128 * p.tile_n;
-      if (S > 1) {
-        // this segment's sums, [column][row] so that a warp's stores are contiguous
-        float* mine = p.part + slot0 + c.seg * slot_step + q * 32 + lane;
-        for (int c0 = 0; c0 < cols; c0 += 16) {
-          float v[16];
-          load(c0, v);
+          for (int k = 0; k < 32; ++k)
+            if (c0 + k < cols) sums[k * 128] = v[k];
+        } else {
+          if (p.base) {
+            const T* base = reinterpret_cast<const T*>(p.base) + (size_t)(m0 + c0) * p.ldbase + n0;
+            const bool in = n0 + lane < p.N;
 #pragma unroll
-          for (int k = 0; k < 16; ++k)
-            if (c0 + k < cols) mine[(size_t)(c0 + k) * 128] = v[k];
-        }
-        __threadfence();
-        __syncwarp();
-        int old = 0;
-        if (lane == 0) old = atomicAdd(p.cnt + ((size_t)(i / S) * CG + rank) * 4 + q, 1);
-        last = __shfl_sync(0xffffffffu, old, 0) == S - 1;
-        __threadfence();
-      }
-      if (last) {
-        for (int c0 = 0; c0 < cols; c0 += 16) {
-          float v[16];
-          if (S == 1) {
-            load(c0, v);
-          } else {
-#pragma unroll
-            for (int k = 0; k < 16; ++k) v[k] = 0.f;
-#pragma unroll 4
-            for (int g = 0; g < S; ++g) {
-              const float* src = p.part + slot0 + g * slot_step + q * 32 + lane;
-#pragma unroll
-              for (int k = 0; k < 16; ++k)
-                if (c0 + k < cols) v[k] += __ldcg(src + (size_t)(c0 + k) * 128);
-            }
+            for (int k = 0; k < 32; ++k)
+              if (in && c0 + k < cols) v[k] += to_f32(base[(size_t)k * p.ldbase + lane]);
           }
-          if (n < p.N) {
+          __syncwarp();
 #pragma unroll
-            for (int k = 0; k < 16; ++k) {
-              const int m = m0 + c0 + k;
-              if (c0 + k < cols) {
-                float f = v[k];
-                if (base) f += to_f32(base[(size_t)m * p.ldbase + n]);
-                out[(size_t)m * p.N + n] = from_f32<T>(f);
-              }
+          for (int k = 0; k < 32; ++k) stage[k * 32 + lane] = from_f32<T>(v[k]);
+          __syncwarp();
+          T* out = reinterpret_cast<T*>(p.out) + (size_t)(m0 + c0) * p.N + n0;
+          if (p.wide) {
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              const int tok = u * 8 + lane / 4, part = lane % 4 * 8;
+              if (c0 + tok < cols && n0 + part < p.N)
+                *reinterpret_cast<uint4*>(out + (size_t)tok * p.N + part) =
+                    *reinterpret_cast<const uint4*>(stage + tok * 32 + part);
             }
+          } else if (n0 + lane < p.N) {
+            for (int k = 0; k < 32 && c0 + k < cols; ++k)
+              out[(size_t)k * p.N + lane] = stage[k * 32 + lane];
           }
         }
       }
@@ -852,13 +839,48 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
-  if (CG == 2) cluster_sync_all();
+  if (clustered) cluster_sync_all();
   if (warp == 1) {
     tc_fence_after();
     if (CG == 2)
       tmem_dealloc2(tmem, 2 * kAccCols);
     else
       tmem_dealloc(tmem, 2 * kAccCols);
+  }
+  if (S > 1) {
+    // the unit's tokens seg, seg + S, .. over all segments: a warp per token, four rows a
+    // lane, the segments' values in flight together
+    const int tile = worker / p.blocks, block = worker - tile * p.blocks;
+    const int m0 = tile * p.tile_n, cols = min(p.tile_n, p.M - m0);
+    const int n = (block * CG + (int)rank) * 128 + 4 * lane;
+    const uint32_t sums0 = smem_u32(smem) + 16 * lane;
+    for (int c = seg + S * warp; c < cols; c += S * (kGemmThreads / 32)) {
+      float4 v[kMaxSplits];
+#pragma unroll
+      for (int g = 0; g < kMaxSplits; ++g)
+        if (g < S) v[g] = ld_cluster_f32x4(peer_addr(sums0 + c * 512, g * CG + rank));
+      float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int g = 0; g < kMaxSplits; ++g)
+        if (g < S) t.x += v[g].x, t.y += v[g].y, t.z += v[g].z, t.w += v[g].w;
+      float f[4] = {t.x, t.y, t.z, t.w};
+      const T* base = reinterpret_cast<const T*>(p.base) + (size_t)(m0 + c) * p.ldbase + n;
+      T* out = reinterpret_cast<T*>(p.out) + (size_t)(m0 + c) * p.N + n;
+      Pack<T, 4> o;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (p.base && n + e < p.N) f[e] += to_f32(base[e]);
+        o.v[e] = from_f32<T>(f[e]);
+      }
+      if (p.wide && n < p.N) {
+        *reinterpret_cast<uint2*>(out) = o.raw;
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (n + e < p.N) out[e] = o.v[e];
+      }
+    }
+    cluster_sync_all();  // no CTA leaves while its sums may still be read
   }
 }
 
@@ -947,37 +969,47 @@ cudaError_t run(LoraArgs& p, const LoraMaps& maps, int num_sms, cudaStream_t str
   const int stage = kStageA + token_bytes(p.tile_n, p.cg);
   const int tslots = 2 * token_slots(p.tile_n, p.cg) * token_bytes(p.tile_n, p.cg);
   const int copy = (t_copy_bytes(p.tile_n, p.cg, p.R) + 1023) / 1024 * 1024;
-  const int rest = kSmemLimit - 1024 - kCtrl - tslots - copy;
-  p.stages = rest / stage < kMaxStages ? rest / stage : kMaxStages;
-  const size_t smem = 1024 + kCtrl + (size_t)p.stages * stage + tslots + copy;
+  const int other = 1024 + kCtrl + kEpiStage + tslots + copy;
+  const int most = (kSmemLimit - other) / stage;
+  p.stages = most < kMaxStages ? most : kMaxStages;
+  // every plan's shared memory leaves one CTA an SM
+  const size_t smem = other + (size_t)p.stages * stage;
   auto* k = p.cg == 2 ? lora_gemm_kernel<T, 2> : lora_gemm_kernel<T, 1>;
   e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  const long long pieces = (long long)p.tiles * p.blocks * p.splits;
-  const int workers = num_sms / p.cg;
-  cfg.gridDim = dim3((unsigned)((pieces < workers ? (int)pieces : workers) * p.cg));
+  const int units = p.tiles * p.blocks;
+  static std::atomic<int> kept[2][kMaxSplits + 1];
+  auto clusters_of = [&](int splits) {
+    const int size = p.cg * splits;
+    if (size == 1) return num_sms;
+    return resident_clusters(k, size, kGemmThreads, smem, kept[p.cg - 1][splits], num_sms);
+  };
+  // Segments: where every unit's cluster is resident at once and each has 4 steps or more,
+  // as many as there can be
+  p.splits = 1;
+  for (int s = kMaxSplits / p.cg; s > 1 && p.splits == 1; --s)
+    if (4 * s <= p.ksteps && units <= num_sms / (p.cg * s) && units <= clusters_of(s)) p.splits = s;
+  const int held = clusters_of(p.splits);
+  if (held < 1) return cudaErrorInvalidConfiguration;
+  const int size = p.cg * p.splits;
+  cfg.gridDim = dim3((unsigned)((units < held ? units : held) * size));
   cfg.blockDim = dim3(kGemmThreads);
   cfg.dynamicSmemBytes = smem;
-  if (p.cg == 2) {
+  if (size > 1) {
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = 2;
+    attr[1].val.clusterDim.x = size;
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
     cfg.numAttrs = 2;
-    static std::atomic<int> kept;  // every plan's shared memory leaves one CTA an SM
-    const int clusters = resident_clusters(k, 2, kGemmThreads, smem, kept, num_sms);
-    if (clusters < 1) return cudaErrorInvalidConfiguration;
-    if (2 * clusters < (int)cfg.gridDim.x) cfg.gridDim = dim3((unsigned)(2 * clusters));
   }
   return cudaLaunchKernelEx(&cfg, k, maps.x, maps.w, maps.b, p);
 }
 
 }  // namespace
 
-// Tiles, pairs and splits for a problem (SMs of a GB300: the workspace size must not depend
-// on the device).  Up to 128 tokens are one tile and one CTA a unit; more go to CTA pairs,
-// with the tile width whose last round of units leaves the least idle.  A unit is split
-// along K when there are fewer units than workers, into segments of at least 4 steps.
+// Tiles and pairs for a problem (SMs of a GB300: the workspace size must not depend on the
+// device).  Up to 128 tokens are one tile and one CTA a unit; more go to CTA pairs, with the
+// tile width whose last round of units leaves the least idle.
 LoraPlan lora_plan(int M, int K, int N, int R, bool has_w) {
   LoraPlan L;
   const int sms = 152;
@@ -990,7 +1022,7 @@ LoraPlan lora_plan(int M, int K, int N, int R, bool has_w) {
   } else {
     L.cg = 2;
     long long best = -1;
-    for (int tn = 256; tn >= 128; tn -= 16) {
+    for (int tn = kMostTokens; tn >= 128; tn -= 16) {
       const long long tiles = (M + tn - 1) / tn, units = tiles * ((N + 255) / 256);
       const long long rounds = (units + sms / 2 - 1) / (sms / 2);
       const long long cost = rounds * (tn + 16);
@@ -1002,12 +1034,6 @@ LoraPlan lora_plan(int M, int K, int N, int R, bool has_w) {
     }
   }
   L.blocks = (N + 128 * L.cg - 1) / (128 * L.cg);
-  const long long units = (long long)L.tiles * L.blocks;
-  L.splits = 1;
-  if (units * 2 <= sms / L.cg) {
-    L.splits = (int)(sms / L.cg / units);
-    if (L.splits > L.ksteps / 4) L.splits = L.ksteps / 4 > 0 ? L.ksteps / 4 : 1;
-  }
   // the fp32 shrink reads a token's adapter anew for each token: up to 16 MB of such reads
   L.tsplits = (long long)M * R * K * 2 > (16LL << 20) ? 1 : 0;
   return L;
