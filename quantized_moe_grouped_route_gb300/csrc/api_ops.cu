@@ -307,6 +307,7 @@ int qmoe_lora_linear(const void* x_dev, int dtype, long long ldx, const void* w_
   p.x = x_dev;
   p.ldx = ldx;
   p.a = a_dev;
+  p.b = b_dev;
   p.ids = adapter_ids_dev;
   p.scales = scales_dev;
   p.base = base_dev;

@@ -194,6 +194,7 @@ struct LoraArgs : LoraPlan {
   const void* x;  // [M][K], rows ldx elements apart
   long long ldx;
   const void* a;  // [L][R][K]
+  const void* b;  // [L][N][R]
   const int32_t* ids;
   const float* scales;
   const void* base;  // [M][N], rows ldbase elements apart, or NULL

@@ -30,6 +30,14 @@
 //   warps 8-15  builders: the token operand (both values of t) of the adapter steps, in
 //               slots of their own; one to four warps (the more, the wider the tile) build a
 //               step, so that several steps are in the making at once
+// Few tokens of few ranks (VEC: at most 64 tokens, tokens * ranks at most 4096; a decode
+// step's requests with an adapter each) do not take the adapters through the MMA: a step
+// per adapter moves 128 rows of B[a] for one or two tokens, and the tensor copies took 0.24
+// us a step (64-byte rows), 5.3 of the 15.9 us of 48 tokens of 43 adapters.  There warp 2
+// brings in B[a]'s rows, which lie next to each other, as one bulk copy each, while w
+// streams; the builder warps multiply them with t in fp32, and the
+// epilogue adds what they leave in shared memory.
+//
 // Few tokens (one tile): one CTA per unit, w streamed once, HBM bound.  More: CTA pairs
 // (cta_group::2, M = 256), each SM loading half of the token rows, since a 128 x 256 tile
 // fed by one SM alone asks more of its L2 port (96 bytes a clock) than it has.
@@ -195,6 +203,33 @@ __host__ __device__ constexpr int token_slots(int tile_n, int cg) {
 // they would each wait for from L2 (48 tokens of 43 adapters: 22 -> see lora_plan).
 __host__ __device__ constexpr int t_copy_bytes(int tile_n, int cg, int R) {
   return cg == 1 && tile_n * R * 4 <= 16384 ? tile_n * R * 4 : 0;
+}
+
+// VEC: bytes of an adapter's 128 rows of B, and how many adapters are in flight (64 KB at
+// most).  A power of two: step i's slot is i % vec_slots, and the kBuilders / vec_slots warps
+// of a slot take all of its steps, since a wait on a phase's parity cannot tell it from the
+// phase after the next (six slots among eight warps ran into that and timed out).
+constexpr int kVecTokens = 64, kVecTokenRanks = 4096;
+__host__ __device__ constexpr int vec_slot_bytes(int R) { return 128 * R * 2; }
+__host__ __device__ constexpr int vec_slots(int R) { return R <= 32 ? 8 : R <= 64 ? 4 : 2; }
+
+// Bytes of shared memory behind the ring (multiples of 1024 each): the builders' slots, their
+// copy of t, and (VEC) what they leave for the epilogue [tokens][128] in fp32.
+struct Behind {
+  int slots, copy, delta;
+};
+__host__ __device__ constexpr int round_kb(int v) { return (v + 1023) / 1024 * 1024; }
+__host__ __device__ constexpr Behind behind(bool vec, int tile_n, int cg, int R) {
+  Behind b{};
+  if (vec) {
+    b.slots = round_kb(vec_slots(R) * vec_slot_bytes(R));
+    b.copy = round_kb(tile_n * R * 4);
+    b.delta = tile_n * 512;
+  } else {
+    b.slots = 2 * token_slots(tile_n, cg) * token_bytes(tile_n, cg);
+    b.copy = round_kb(t_copy_bytes(tile_n, cg, R));
+  }
+  return b;
 }
 
 __device__ __forceinline__ void mma_ss(uint32_t cg, uint32_t d, uint64_t a, uint64_t b,
@@ -453,7 +488,7 @@ __global__ void __launch_bounds__(kShrinkThreads, 1)
   cluster_sync_all();  // no CTA leaves while its sums may still be read
 }
 
-template <class T, int CG>
+template <class T, int CG, bool VEC>
 __global__ void __launch_bounds__(kGemmThreads, 1)
     lora_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
                      const __grid_constant__ CUtensorMap map_b, const LoraArgs p) {
@@ -464,11 +499,13 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   const int bytes_b = token_bytes(p.tile_n, CG);
   const int stage_bytes = kStageA + bytes_b;
   const int stages = p.stages;
-  const int tslots = token_slots(p.tile_n, CG);
-  uint8_t* tbuf = smem + stages * stage_bytes;  // [tslots][2][bytes_b]
-  uint8_t* tcopy = tbuf + 2 * tslots * bytes_b;  // [rows_b][2][R]
+  const int tslots = VEC ? vec_slots(p.R) : token_slots(p.tile_n, CG);
+  const Behind behind_ring = behind(VEC, p.tile_n, CG, p.R);
+  uint8_t* tbuf = smem + stages * stage_bytes;  // [tslots][2][bytes_b]; VEC [tslots][128][R]
+  uint8_t* tcopy = tbuf + behind_ring.slots;    // [rows_b][2][R]; VEC fp32 [rows_b][R]
   const int copy_bytes = t_copy_bytes(p.tile_n, CG, p.R);
-  uint8_t* ctrl = tcopy + (copy_bytes + 1023) / 1024 * 1024;
+  float* delta = reinterpret_cast<float*>(tcopy + behind_ring.copy);  // VEC [tokens][128]
+  uint8_t* ctrl = tcopy + behind_ring.copy + behind_ring.delta;
   uint8_t* epi_stage = ctrl + kCtrl;
   uint64_t* full = reinterpret_cast<uint64_t*>(ctrl);
   uint64_t* empty = full + kMaxStages;
@@ -477,7 +514,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   uint64_t* accf = tempty + 8;
   uint64_t* acce = accf + 2;
   uint64_t* drain = acce + 2;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  uint64_t* dfull = drain + 1;  // VEC: delta complete (builder warps), read (epilogue warps)
+  uint64_t* dempty = dfull + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(dempty + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   short* place = reinterpret_cast<short*>(ctrl + 512);  // [rows_b] the tokens' adapters
 
@@ -496,9 +535,11 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       mbar_init(smem_u32(&empty[s]), 1);
     }
     for (int i = 0; i < tslots; ++i) {
-      mbar_init(smem_u32(&tfull[i]), kBuilders / tslots * CG);
-      mbar_init(smem_u32(&tempty[i]), 1);
+      mbar_init(smem_u32(&tfull[i]), VEC ? 1 : kBuilders / tslots * CG);
+      mbar_init(smem_u32(&tempty[i]), VEC ? kBuilders / tslots : 1);
     }
+    mbar_init(smem_u32(dfull), kBuilders);
+    mbar_init(smem_u32(dempty), 4);
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&accf[i]), 1);
       mbar_init(smem_u32(&acce[i]), 4 * CG);
@@ -545,6 +586,19 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     waited = true;
     return p.count[tile];
   };
+  // VEC: the tile's adapters (bits: places in its list) that this CTA's tokens seg, seg + S,
+  // .. use; whole warp
+  auto own_adapters = [&](int tile) -> uint64_t {
+    adapters(tile);
+    uint32_t lo = 0, hi = 0;
+    for (int c = seg + S * lane; c < p.tile_n; c += S * 32) {
+      const int at = p.place[(size_t)tile * p.tile_n + c];
+      if (at >= 0) (at < 32 ? lo : hi) |= 1u << (at & 31);
+    }
+    lo = __reduce_or_sync(0xffffffffu, lo);
+    hi = __reduce_or_sync(0xffffffffu, hi);
+    return (uint64_t)hi << 32 | lo;
+  };
 
   if (warp == 0) {
     // ------------------------------------------------------------------ TMA producer
@@ -582,7 +636,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         }
         next();
       }
-      const int n = ok ? adapters(tile) : 0;
+      const int n = ok && !VEC ? adapters(tile) : 0;
       for (int d = seg; d < n && ok; d += S) {
         const int id = p.list[(size_t)tile * p.tile_n + d];
         for (int h = 0; h < chunks; ++h) {
@@ -651,7 +705,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
           commit(&empty[s]);
           next();
         }
-        const int n = ok ? adapters(i / p.blocks) : 0;
+        const int n = ok && !VEC ? adapters(i / p.blocks) : 0;
         for (int d = seg; d < n && ok; d += S) {
           for (int h = 0; h < chunks; ++h) {
             const int slices = (min(64, p.R - h * 64) + 15) / 16;
@@ -680,6 +734,122 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         if (ok) commit(&accf[ab]);
       }
       commit(drain);
+    }
+  } else if (VEC && warp == 2) {
+    // ------------------------------------------------------- VEC: the adapters' rows of B
+    const uint32_t lead = elect_one();
+    const uint64_t pol = l2_policy_evict_last();
+    uint32_t step = 0;
+    bool ok = true;
+    for (int i = worker; i < units && ok; i += workers) {
+      const int tile = i / p.blocks, block = i - tile * p.blocks;
+      const uint32_t bytes = (uint32_t)min(128, p.N - block * 128) * p.R * 2;
+      for (uint64_t left = own_adapters(tile); left && ok; left &= left - 1, ++step) {
+        const int s = step % tslots;
+        const int id = p.list[(size_t)tile * p.tile_n + __ffsll(left) - 1];
+        if (!wait(&tempty[s], ((step / tslots) & 1) ^ 1)) {
+          ok = false;
+          break;
+        }
+        mbar_arrive_expect_tx_if(lead, smem_u32(&tfull[s]), bytes);
+        bulk_g2s_if(lead, smem_u32(tbuf) + s * vec_slot_bytes(p.R),
+                    reinterpret_cast<const T*>(p.b) + ((size_t)id * p.N + block * 128) * p.R, bytes,
+                    smem_u32(&tfull[s]), pol);
+      }
+    }
+    if (!ok) {  // the copies of the last steps may still be landing
+      const unsigned long long t0 = globaltimer_ns();
+      while (globaltimer_ns() - t0 < 2000000ull) {
+      }
+    }
+  } else if (VEC && warp >= 8) {
+    // ------------------------------------------------------------- VEC: t . B^T in fp32
+    // A slot's adapter is one to four warps' work (the more, the longer its rows), a lane
+    // having four to one of the 128 rows: several adapters are in the making, with several
+    // sums a lane in flight (two groups of four warps, a row a thread, took 0.65 us a step).
+    // delta holds this CTA's tokens seg, seg + S, .. one after the other.  A row is read in
+    // 16-byte chunks from a place of its own on, so that eight neighbouring rows' chunks lie
+    // in different banks.
+    const int group = kBuilders / tslots;
+    const int own = (warp - 8) / group;
+    const int rows_lane = 4 / group;
+    const int row0 = (warp - 8) % group * rows_lane * 32 + lane;
+    const int C = p.R / 8;  // chunks of a row
+    // rows after which the chunks' banks repeat: 8 / gcd(C, 8)
+    const int apart = C % 8 == 0 ? 1 : C % 4 == 0 ? 2 : C % 2 == 0 ? 4 : 8;
+    const int turn = lane / apart % C;
+    float* tf = reinterpret_cast<float*>(tcopy);
+    const T* tsrc = reinterpret_cast<const T*>(p.t);
+    const int own_rows = (p.tile_n - seg + S - 1) / S;
+    uint32_t step = 0, dph = 1;
+    bool ok = true;
+    // (after a wait that gave up a warp still meets the others at their barriers)
+    for (int i = worker; i < units; i += workers) {
+      const int tile = i / p.blocks;
+      const int m0 = tile * p.tile_n;
+      const uint64_t used = own_adapters(tile);
+      builders_sync();  // the previous unit's t has been used
+      for (int u = threadIdx.x - 256; u < own_rows * p.R; u += 32 * kBuilders) {
+        const int c = u / p.R * S + seg, r = u % p.R;
+        if (m0 + c < p.M) {
+          const T* src = tsrc + (size_t)(m0 + c) * 2 * p.R + r;
+          tf[u] = to_f32(src[0]) + to_f32(src[p.R]);
+        }
+      }
+      if (ok && !wait(dempty, dph)) ok = false;  // the epilogue has read the previous delta
+      dph ^= 1;
+      for (int u = threadIdx.x - 256; u < own_rows; u += 32 * kBuilders)
+        place[u] = (short)p.place[(size_t)m0 + u * S + seg];
+      builders_sync();
+      // tokens without an adapter
+      for (int c = warp - 8; c < own_rows; c += kBuilders)
+        if (place[c] < 0)
+          reinterpret_cast<float4*>(delta + c * 128)[lane] = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (uint64_t left = used; left && ok; left &= left - 1, ++step) {
+        if ((int)(step % tslots) != own) continue;
+        const int d = __ffsll(left) - 1, s = own;
+        if (!wait(&tfull[s], (step / tslots) & 1)) {
+          ok = false;
+          break;
+        }
+        const uint4* b =
+            reinterpret_cast<const uint4*>(tbuf + s * vec_slot_bytes(p.R)) + row0 * C;
+        for (int c0 = 0; c0 < own_rows; c0 += 32) {
+          const bool hit = c0 + lane < own_rows && place[c0 + lane] == d;
+          for (unsigned who = __ballot_sync(0xffffffffu, hit); who; who &= who - 1) {
+            const int c = c0 + __ffs(who) - 1;
+            const float4* t4 = reinterpret_cast<const float4*>(tf + c * p.R);
+            float acc[4] = {0.f, 0.f, 0.f, 0.f};
+            int j = turn;
+#pragma unroll 2
+            for (int k = 0; k < C; ++k) {
+              const float4 x = t4[2 * j], y = t4[2 * j + 1];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                if (i >= rows_lane) break;
+                Pack<T, 8> v;
+                v.raw = b[i * 32 * C + j];
+                acc[i] = fmaf(to_f32(v.v[0]), x.x, acc[i]);
+                acc[i] = fmaf(to_f32(v.v[1]), x.y, acc[i]);
+                acc[i] = fmaf(to_f32(v.v[2]), x.z, acc[i]);
+                acc[i] = fmaf(to_f32(v.v[3]), x.w, acc[i]);
+                acc[i] = fmaf(to_f32(v.v[4]), y.x, acc[i]);
+                acc[i] = fmaf(to_f32(v.v[5]), y.y, acc[i]);
+                acc[i] = fmaf(to_f32(v.v[6]), y.z, acc[i]);
+                acc[i] = fmaf(to_f32(v.v[7]), y.w, acc[i]);
+              }
+              if (++j == C) j = 0;
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (i < rows_lane) delta[c * 128 + row0 + 32 * i] = acc[i];
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&tempty[s]));
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(dfull));
     }
   } else if (warp >= 8) {
     // ------------------------------------------------------------------- builders
@@ -763,8 +933,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       const int m0 = tile * p.tile_n;
       const int cols = min(p.tile_n, p.M - m0);
       const int n0 = (block * CG + (int)rank) * 128 + q * 32;
-      const bool any = k1 > k0 || p.count[tile] > seg;
+      const bool any = k1 > k0 || (!VEC && p.count[tile] > seg);
       if (!wait(&accf[ab], (local >> 1) & 1)) break;
+      if (VEC && !wait(dfull, local & 1)) break;
       tc_fence_after();
       const uint32_t tbase = tmem + ((uint32_t)(q * 32) << 16) + ab * kAccCols;
       for (int c0 = 0; c0 < cols; c0 += 32) {
@@ -792,6 +963,11 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
           for (int k = 0; k < 32; ++k)
             if (c0 + k < cols) sums[k * 128] = v[k];
         } else {
+          if constexpr (VEC) {
+#pragma unroll
+            for (int k = 0; k < 32; ++k)
+              if (c0 + k < cols) v[k] += delta[(c0 + k) * 128 + q * 32 + lane];
+          }
           if (p.base) {
             const T* base = reinterpret_cast<const T*>(p.base) + (size_t)(m0 + c0) * p.ldbase + n0;
             const bool in = n0 + lane < p.N;
@@ -825,6 +1001,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
           mbar_arrive_remote(acce0 + ab * 8);
         else
           mbar_arrive(smem_u32(&acce[ab]));
+        if (VEC) mbar_arrive(smem_u32(dempty));
       }
     }
   }
@@ -863,6 +1040,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
 #pragma unroll
       for (int g = 0; g < kMaxSplits; ++g)
         if (g < S) t.x += v[g].x, t.y += v[g].y, t.z += v[g].z, t.w += v[g].w;
+      if constexpr (VEC) {
+        const float4 d = reinterpret_cast<const float4*>(delta + c / S * 128)[lane];
+        t.x += d.x, t.y += d.y, t.z += d.z, t.w += d.w;
+      }
       float f[4] = {t.x, t.y, t.z, t.w};
       const T* base = reinterpret_cast<const T*>(p.base) + (size_t)(m0 + c) * p.ldbase + n;
       T* out = reinterpret_cast<T*>(p.out) + (size_t)(m0 + c) * p.N + n;
@@ -967,22 +1148,25 @@ cudaError_t run(LoraArgs& p, const LoraMaps& maps, int num_sms, cudaStream_t str
   }
   if (e != cudaSuccess) return e;
   const int stage = kStageA + token_bytes(p.tile_n, p.cg);
-  const int tslots = 2 * token_slots(p.tile_n, p.cg) * token_bytes(p.tile_n, p.cg);
-  const int copy = (t_copy_bytes(p.tile_n, p.cg, p.R) + 1023) / 1024 * 1024;
-  const int other = 1024 + kCtrl + kEpiStage + tslots + copy;
+  const bool vec = p.cg == 1 && p.tile_n <= kVecTokens && p.tile_n * p.R <= kVecTokenRanks;
+  const Behind more = behind(vec, p.tile_n, p.cg, p.R);
+  const int other = 1024 + kCtrl + kEpiStage + more.slots + more.copy + more.delta;
   const int most = (kSmemLimit - other) / stage;
   p.stages = most < kMaxStages ? most : kMaxStages;
   // every plan's shared memory leaves one CTA an SM
   const size_t smem = other + (size_t)p.stages * stage;
-  auto* k = p.cg == 2 ? lora_gemm_kernel<T, 2> : lora_gemm_kernel<T, 1>;
+  auto* k = p.cg == 2 ? lora_gemm_kernel<T, 2, false>
+            : vec     ? lora_gemm_kernel<T, 1, true>
+                      : lora_gemm_kernel<T, 1, false>;
   e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   const int units = p.tiles * p.blocks;
-  static std::atomic<int> kept[2][kMaxSplits + 1];
+  static std::atomic<int> kept[3][kMaxSplits + 1];
   auto clusters_of = [&](int splits) {
     const int size = p.cg * splits;
     if (size == 1) return num_sms;
-    return resident_clusters(k, size, kGemmThreads, smem, kept[p.cg - 1][splits], num_sms);
+    return resident_clusters(k, size, kGemmThreads, smem, kept[vec ? 2 : p.cg - 1][splits],
+                             num_sms);
   };
   // Segments: where every unit's cluster is resident at once and each has 4 steps or more,
   // as many as there can be

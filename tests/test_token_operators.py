@@ -532,7 +532,8 @@ LORAS = [  # M, K, N, R, L, with w, with base, ids
 LORAS_WIDE = [
     (256, 4096, 96, 24, 40, True, False, "mixed"), (200, 2048, 130, 128, 50, True, False, "mixed"),
     (1100, 1024, 300, 8, 500, True, True, "mixed"), (33, 8192, 64, 64, 9, False, True, "mixed"),
-    (2047, 1096, 512, 48, 11, True, False, "runs"), (700, 968, 200, 128, 3, True, False, "none"),
+    (2047, 1096, 512, 48, 11, True, False, "runs"), (60, 256, 20000, 64, 40, True, True, "mixed"),
+    (31, 512, 160, 128, 31, True, False, "mixed"), (64, 1024, 30000, 16, 60, True, False, "mixed"), (700, 968, 200, 128, 3, True, False, "none"),
 ]
 
 
