@@ -464,16 +464,17 @@ __global__ void __launch_bounds__(kShrinkThreads, 1)
   for (int i = threadIdx.x; i < share * quads; i += kShrinkThreads) {
     const int c = i / quads * p.tsplits + seg, r = i % quads * 4;
     const int at = place[c];
-    if (at < 0 || at / cap % (int)gridDim.y != (int)blockIdx.y) continue;
+    const bool here = at >= 0 && at / cap % (int)gridDim.y == (int)blockIdx.y;
+    const float s = here ? p.scales[list[at]] : 0.f;
     float4 v[kShrinkSegments];
 #pragma unroll
     for (int g = 0; g < kShrinkSegments; ++g)
-      if (g < p.tsplits) v[g] = ld_cluster_f32x4(peer_addr(sums0 + (c * p.R + r) * 4, g));
+      if (g < p.tsplits && here) v[g] = ld_cluster_f32x4(peer_addr(sums0 + (c * p.R + r) * 4, g));
     float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int g = 0; g < kShrinkSegments; ++g)
       if (g < p.tsplits) t.x += v[g].x, t.y += v[g].y, t.z += v[g].z, t.w += v[g].w;
-    const float s = p.scales[list[at]];
+    if (!here) continue;
     const float f[4] = {t.x * s, t.y * s, t.z * s, t.w * s};
     Pack<T, 4> hi, lo;
 #pragma unroll
@@ -586,18 +587,28 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     waited = true;
     return p.count[tile];
   };
-  // VEC: the tile's adapters (bits: places in its list) that this CTA's tokens seg, seg + S,
-  // .. use; whole warp
-  auto own_adapters = [&](int tile) -> uint64_t {
-    adapters(tile);
-    uint32_t lo = 0, hi = 0;
-    for (int c = seg + S * lane; c < p.tile_n; c += S * 32) {
-      const int at = p.place[(size_t)tile * p.tile_n + c];
-      if (at >= 0) (at < 32 ? lo : hi) |= 1u << (at & 31);
+  // VEC: this CTA's tokens seg, seg + S, .. of a tile, numbered 0, 1, .., two a lane; their
+  // ids (-1: none) come from the call's own input, so the rows of B are under way before the
+  // shrink kernel is done.  for_adapters calls body(id, tokens lane, tokens lane + 32 as
+  // ballots) for each distinct id in order of first appearance, until it returns false.
+  const int own_rows = (p.tile_n - seg + S - 1) / S;
+  auto own_id = [&](int tile, int c) -> int {
+    const int m = tile * p.tile_n + c * S + seg;
+    const int id = c < own_rows && m < p.M ? p.ids[m] : -1;
+    return id < p.L ? id : -1;
+  };
+  auto for_adapters = [&](int tile, auto&& body) {
+    const int a = own_id(tile, lane), b = own_id(tile, lane + 32);
+    unsigned left_a = __ballot_sync(0xffffffffu, a >= 0), left_b = __ballot_sync(0xffffffffu, b >= 0);
+    while (left_a | left_b) {
+      const int id = left_a ? __shfl_sync(0xffffffffu, a, __ffs(left_a) - 1)
+                            : __shfl_sync(0xffffffffu, b, __ffs(left_b) - 1);
+      const unsigned in_a = __ballot_sync(0xffffffffu, a == id);
+      const unsigned in_b = __ballot_sync(0xffffffffu, b == id);
+      left_a &= ~in_a;
+      left_b &= ~in_b;
+      if (!body(id, in_a, in_b)) break;
     }
-    lo = __reduce_or_sync(0xffffffffu, lo);
-    hi = __reduce_or_sync(0xffffffffu, hi);
-    return (uint64_t)hi << 32 | lo;
   };
 
   if (warp == 0) {
@@ -744,18 +755,17 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     for (int i = worker; i < units && ok; i += workers) {
       const int tile = i / p.blocks, block = i - tile * p.blocks;
       const uint32_t bytes = (uint32_t)min(128, p.N - block * 128) * p.R * 2;
-      for (uint64_t left = own_adapters(tile); left && ok; left &= left - 1, ++step) {
+      for_adapters(tile, [&](int id, unsigned, unsigned) {
         const int s = step % tslots;
-        const int id = p.list[(size_t)tile * p.tile_n + __ffsll(left) - 1];
-        if (!wait(&tempty[s], ((step / tslots) & 1) ^ 1)) {
-          ok = false;
-          break;
-        }
+        ok = wait(&tempty[s], ((step / tslots) & 1) ^ 1);
+        ++step;
+        if (!ok) return false;
         mbar_arrive_expect_tx_if(lead, smem_u32(&tfull[s]), bytes);
         bulk_g2s_if(lead, smem_u32(tbuf) + s * vec_slot_bytes(p.R),
                     reinterpret_cast<const T*>(p.b) + ((size_t)id * p.N + block * 128) * p.R, bytes,
                     smem_u32(&tfull[s]), pol);
-      }
+        return true;
+      });
     }
     if (!ok) {  // the copies of the last steps may still be landing
       const unsigned long long t0 = globaltimer_ns();
@@ -780,74 +790,69 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     const int turn = lane / apart % C;
     float* tf = reinterpret_cast<float*>(tcopy);
     const T* tsrc = reinterpret_cast<const T*>(p.t);
-    const int own_rows = (p.tile_n - seg + S - 1) / S;
     uint32_t step = 0, dph = 1;
     bool ok = true;
     // (after a wait that gave up a warp still meets the others at their barriers)
     for (int i = worker; i < units; i += workers) {
       const int tile = i / p.blocks;
       const int m0 = tile * p.tile_n;
-      const uint64_t used = own_adapters(tile);
+      adapters(tile);   // t is complete
       builders_sync();  // the previous unit's t has been used
-      for (int u = threadIdx.x - 256; u < own_rows * p.R; u += 32 * kBuilders) {
-        const int c = u / p.R * S + seg, r = u % p.R;
-        if (m0 + c < p.M) {
-          const T* src = tsrc + (size_t)(m0 + c) * 2 * p.R + r;
-          tf[u] = to_f32(src[0]) + to_f32(src[p.R]);
-        }
+      for (int u = threadIdx.x - 256; u < own_rows * C; u += 32 * kBuilders) {
+        const int c = u / C, m = m0 + c * S + seg;
+        if (m >= p.M) break;
+        const T* src = tsrc + (size_t)m * 2 * p.R + u % C * 8;
+        Pack<T, 8> hi, lo;
+        hi.raw = *reinterpret_cast<const uint4*>(src);
+        lo.raw = *reinterpret_cast<const uint4*>(src + p.R);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) tf[u * 8 + e] = to_f32(hi.v[e]) + to_f32(lo.v[e]);
       }
       if (ok && !wait(dempty, dph)) ok = false;  // the epilogue has read the previous delta
       dph ^= 1;
-      for (int u = threadIdx.x - 256; u < own_rows; u += 32 * kBuilders)
-        place[u] = (short)p.place[(size_t)m0 + u * S + seg];
       builders_sync();
       // tokens without an adapter
       for (int c = warp - 8; c < own_rows; c += kBuilders)
-        if (place[c] < 0)
+        if (own_id(tile, c) < 0)
           reinterpret_cast<float4*>(delta + c * 128)[lane] = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (uint64_t left = used; left && ok; left &= left - 1, ++step) {
-        if ((int)(step % tslots) != own) continue;
-        const int d = __ffsll(left) - 1, s = own;
-        if (!wait(&tfull[s], (step / tslots) & 1)) {
-          ok = false;
-          break;
-        }
+      for_adapters(tile, [&](int, unsigned in_a, unsigned in_b) {
+        if ((int)(step++ % tslots) != own || !ok) return true;
+        ok = wait(&tfull[own], ((step - 1) / tslots) & 1);
+        if (!ok) return true;
         const uint4* b =
-            reinterpret_cast<const uint4*>(tbuf + s * vec_slot_bytes(p.R)) + row0 * C;
-        for (int c0 = 0; c0 < own_rows; c0 += 32) {
-          const bool hit = c0 + lane < own_rows && place[c0 + lane] == d;
-          for (unsigned who = __ballot_sync(0xffffffffu, hit); who; who &= who - 1) {
-            const int c = c0 + __ffs(who) - 1;
-            const float4* t4 = reinterpret_cast<const float4*>(tf + c * p.R);
-            float acc[4] = {0.f, 0.f, 0.f, 0.f};
-            int j = turn;
+            reinterpret_cast<const uint4*>(tbuf + own * vec_slot_bytes(p.R)) + row0 * C;
+        for (uint64_t who = (uint64_t)in_b << 32 | in_a; who; who &= who - 1) {
+          const int c = __ffsll(who) - 1;
+          const float4* t4 = reinterpret_cast<const float4*>(tf + c * p.R);
+          float acc[4] = {0.f, 0.f, 0.f, 0.f};
+          int j = turn;
 #pragma unroll 2
-            for (int k = 0; k < C; ++k) {
-              const float4 x = t4[2 * j], y = t4[2 * j + 1];
+          for (int k = 0; k < C; ++k) {
+            const float4 x = t4[2 * j], y = t4[2 * j + 1];
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                if (i >= rows_lane) break;
-                Pack<T, 8> v;
-                v.raw = b[i * 32 * C + j];
-                acc[i] = fmaf(to_f32(v.v[0]), x.x, acc[i]);
-                acc[i] = fmaf(to_f32(v.v[1]), x.y, acc[i]);
-                acc[i] = fmaf(to_f32(v.v[2]), x.z, acc[i]);
-                acc[i] = fmaf(to_f32(v.v[3]), x.w, acc[i]);
-                acc[i] = fmaf(to_f32(v.v[4]), y.x, acc[i]);
-                acc[i] = fmaf(to_f32(v.v[5]), y.y, acc[i]);
-                acc[i] = fmaf(to_f32(v.v[6]), y.z, acc[i]);
-                acc[i] = fmaf(to_f32(v.v[7]), y.w, acc[i]);
-              }
-              if (++j == C) j = 0;
+            for (int i = 0; i < 4; ++i) {
+              if (i >= rows_lane) break;
+              Pack<T, 8> v;
+              v.raw = b[i * 32 * C + j];
+              acc[i] = fmaf(to_f32(v.v[0]), x.x, acc[i]);
+              acc[i] = fmaf(to_f32(v.v[1]), x.y, acc[i]);
+              acc[i] = fmaf(to_f32(v.v[2]), x.z, acc[i]);
+              acc[i] = fmaf(to_f32(v.v[3]), x.w, acc[i]);
+              acc[i] = fmaf(to_f32(v.v[4]), y.x, acc[i]);
+              acc[i] = fmaf(to_f32(v.v[5]), y.y, acc[i]);
+              acc[i] = fmaf(to_f32(v.v[6]), y.z, acc[i]);
+              acc[i] = fmaf(to_f32(v.v[7]), y.w, acc[i]);
             }
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if (i < rows_lane) delta[c * 128 + row0 + 32 * i] = acc[i];
+            if (++j == C) j = 0;
           }
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (i < rows_lane) delta[c * 128 + row0 + 32 * i] = acc[i];
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&tempty[s]));
-      }
+        if (lane == 0) mbar_arrive(smem_u32(&tempty[own]));
+        return true;
+      });
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(dfull));
     }
