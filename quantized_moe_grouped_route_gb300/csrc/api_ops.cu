@@ -306,6 +306,7 @@ int qmoe_lora_linear(const void* x_dev, int dtype, long long ldx, const void* w_
   p.dtype = dtype;
   p.x = x_dev;
   p.ldx = ldx;
+  p.w = w_dev;
   p.a = a_dev;
   p.b = b_dev;
   p.ids = adapter_ids_dev;
@@ -325,29 +326,7 @@ int qmoe_lora_linear(const void* x_dev, int dtype, long long ldx, const void* w_
   p.place = reinterpret_cast<int*>(ws + W.place);
   p.t = ws + W.t;
   p.wide = chunked(out_dev, N, N, 2, 16);
-
-  LoraMaps maps;
-  const uint64_t dx[2] = {(uint64_t)K, (uint64_t)M}, sx[1] = {(uint64_t)ldx * 2};
-  const uint32_t bx[2] = {64, (uint32_t)(p.tile_n / p.cg)};
-  const uint64_t dw[2] = {(uint64_t)K, (uint64_t)N}, sw[1] = {(uint64_t)K * 2};
-  const uint32_t bw[2] = {64, 128};
-  const uint64_t db[3] = {(uint64_t)R, (uint64_t)N, (uint64_t)L};
-  const uint64_t sb[2] = {(uint64_t)R * 2, (uint64_t)N * R * 2};
-  const uint32_t bb[3] = {64, 128, 1};
-  rc = make_tmap16(&maps.x, dtype, x_dev, 2, dx, sx, bx);
-  if (rc == QMOE_OK && w_dev) rc = make_tmap16(&maps.w, dtype, w_dev, 2, dw, sw, bw);
-  if (rc == QMOE_OK && !w_dev) maps.w = maps.x;  // never read
-  if (rc == QMOE_OK) rc = make_tmap16(&maps.b, dtype, b_dev, 3, db, sb, bb);
-  if (rc == QMOE_OK && p.tsplits > 0) {
-    const uint32_t bxs[2] = {64, (uint32_t)p.tile_n};
-    const uint64_t da[3] = {(uint64_t)K, (uint64_t)R, (uint64_t)L};
-    const uint64_t sa[2] = {(uint64_t)K * 2, (uint64_t)K * R * 2};
-    const uint32_t ba[3] = {64, (uint32_t)R, 1};
-    rc = make_tmap16(&maps.xs, dtype, x_dev, 2, dx, sx, bxs);
-    if (rc == QMOE_OK) rc = make_tmap16(&maps.a, dtype, a_dev, 3, da, sa, ba);
-  }
-  if (rc != QMOE_OK) return rc;
-  return cuda_rc(launch_lora(p, maps, sms, reinterpret_cast<cudaStream_t>(stream)));
+  return cuda_rc(launch_lora(p, sms, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

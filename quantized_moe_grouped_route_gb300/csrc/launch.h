@@ -193,6 +193,7 @@ struct LoraArgs : LoraPlan {
   int dtype;
   const void* x;  // [M][K], rows ldx elements apart
   long long ldx;
+  const void* w;  // [N][K] or NULL
   const void* a;  // [L][R][K]
   const void* b;  // [L][N][R]
   const int32_t* ids;
@@ -210,10 +211,6 @@ struct LoraArgs : LoraPlan {
   int* place;  // [tiles][tile_n] each token's adapter's place in the list, -1: none
   void* t;     // [M][2][R] scales[a] * (x . A^T): rounded, and what the rounding left
 };
-struct LoraMaps {
-  CUtensorMap x, w, b;  // the GEMM's
-  CUtensorMap xs, a;    // the tensor-core shrink's
-};
-cudaError_t launch_lora(LoraArgs& p, const LoraMaps& maps, int num_sms, cudaStream_t stream);
+cudaError_t launch_lora(LoraArgs& p, int num_sms, cudaStream_t stream);
 
 }  // namespace qmoe

@@ -42,6 +42,8 @@
 // (cta_group::2, M = 256), each SM loading half of the token rows, since a 128 x 256 tile
 // fed by one SM alone asks more of its L2 port (96 bytes a clock) than it has.
 //
+// Up to four tokens run as plain products, a warp per row of w (lora_gemv_kernel).
+//
 // Every wait is bounded, as in the layer's GEMMs.
 #include <atomic>
 
@@ -1070,6 +1072,105 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   }
 }
 
+// ------------------------------------------------------------------- up to four tokens
+// One, two or four warps (WPR, the more, the longer the row) per row of w: its product with
+// up to MT token rows in fp32, w in 16-byte loads of which a lane has about eight in all, in
+// flight together (one warp a row, 28 loads a lane at K = 7168, took 9.4 us); then the row
+// of each token's B with t.
+// HBM (or L2) bound; at one token the arithmetic is about a third of the stream's time, at
+// four about equal, and there is nothing to set up: the tensor-core kernel spends 5 of its
+// 10.3 us at M = 1, K = 7168, N = 2048 on barriers, TMEM, the cluster and the last sums.
+constexpr int kGemvThreads = 128, kGemvTokens = 4;
+
+template <class T, int MT, int WPR>
+__global__ void __launch_bounds__(kGemvThreads) lora_gemv_kernel(const LoraArgs p) {
+  using P_ = Pack<T, 8>;
+  __shared__ float part[kGemvThreads / 32][MT];
+  grid_dep_launch();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = warp % WPR;
+  const int n = blockIdx.x * (kGemvThreads / 32 / WPR) + warp / WPR;
+  const bool here = n < p.N;  // the warp's row (the others only wait for the shrink kernel)
+  float acc[MT];
+  int id[MT];
+  T bv[MT][4];  // ranks lane, lane + 32, ..
+#pragma unroll
+  for (int m = 0; m < MT; ++m) {
+    acc[m] = 0.f;
+    id[m] = here && sub == 0 && m < p.M ? p.ids[m] : -1;
+    if (id[m] >= p.L) id[m] = -1;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (id[m] >= 0 && lane + 32 * i < p.R)
+        bv[m][i] = reinterpret_cast<const T*>(p.b)[((size_t)id[m] * p.N + n) * p.R + lane + 32 * i];
+  }
+  if (here && p.w) {
+    const uint4* w = reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(p.w) + (size_t)n * p.K);
+    const T* x = reinterpret_cast<const T*>(p.x);
+    const int chunks = p.K / 8;
+    constexpr int kFlight = MT == 1 ? 8 : MT == 2 ? 6 : 4;
+    for (int c0 = sub * 32 + lane; c0 < chunks; c0 += 32 * WPR * kFlight) {
+      P_ wv[kFlight];
+#pragma unroll
+      for (int i = 0; i < kFlight; ++i) {
+        const int c = c0 + 32 * WPR * i;
+        wv[i].raw = load_if(w + c, c < chunks);
+      }
+#pragma unroll
+      for (int i = 0; i < kFlight; ++i) {
+        const int c = c0 + 32 * WPR * i;
+        if (c >= chunks) break;
+        float f[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] = to_f32(wv[i].v[e]);
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          if (m >= p.M) break;
+          P_ xv;
+          xv.raw = reinterpret_cast<const uint4*>(x + m * p.ldx)[c];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) acc[m] = fmaf(f[e], to_f32(xv.v[e]), acc[m]);
+        }
+      }
+    }
+  }
+  grid_dep_wait();  // t
+  if (blockIdx.x == 0 && threadIdx.x == 0 && p.bad[0]) atomicOr(p.err, QMOE_FLAG_BAD_ID);
+#pragma unroll
+  for (int m = 0; m < MT; ++m) {
+    if (id[m] >= 0) {
+      const T* t = reinterpret_cast<const T*>(p.t) + (size_t)m * 2 * p.R + lane;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (lane + 32 * i < p.R)
+          acc[m] = fmaf(to_f32(bv[m][i]), to_f32(t[32 * i]) + to_f32(t[p.R + 32 * i]), acc[m]);
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) acc[m] += __shfl_xor_sync(0xffffffffu, acc[m], o);
+    if (lane == 0) part[warp][m] = acc[m];
+  }
+  __syncthreads();
+  if (here && sub == 0 && lane < MT && lane < p.M) {
+    const int m = lane;
+    float f = 0.f;
+#pragma unroll
+    for (int w = 0; w < WPR; ++w) f += part[warp + w][m];
+    if (p.base) f += to_f32(reinterpret_cast<const T*>(p.base)[m * p.ldbase + n]);
+    reinterpret_cast<T*>(p.out)[(size_t)m * p.N + n] = from_f32<T>(f);
+  }
+}
+
+template <class T, int WPR>
+cudaError_t gemv(const LoraArgs& p, cudaLaunchConfig_t cfg) {
+  constexpr int kRows = kGemvThreads / 32 / WPR;
+  cfg.blockDim = dim3(kGemvThreads);
+  cfg.gridDim = dim3((p.N + kRows - 1) / kRows);
+  cfg.dynamicSmemBytes = 0;
+  auto* k = p.M == 1   ? lora_gemv_kernel<T, 1, WPR>
+            : p.M == 2 ? lora_gemv_kernel<T, 2, WPR>
+                       : lora_gemv_kernel<T, 4, WPR>;
+  return cudaLaunchKernelEx(&cfg, k, p);
+}
+
 // Clusters of `size` CTAs of a kernel that the device holds at once: asked of the runtime
 // once per size and kept (a property of the kernel and the device model).
 template <class K>
@@ -1117,8 +1218,36 @@ int shrink_segments(int tiles, int ksteps, int num_sms) {
   return best;
 }
 
+// Tensor maps: token rows in boxes of `rows`, [N][K] and [L][rows][cols] in boxes of 64
+// columns.
+cudaError_t map_rows(CUtensorMap* map, const LoraArgs& p, const void* base, int cols, int rows,
+                     long long ld, int box_rows) {
+  const uint64_t dims[2] = {(uint64_t)cols, (uint64_t)rows}, strides[1] = {(uint64_t)ld * 2};
+  const uint32_t box[2] = {64, (uint32_t)box_rows};
+  return make_tmap16(map, p.dtype, base, 2, dims, strides, box) == QMOE_OK ? cudaSuccess
+                                                                           : cudaErrorUnknown;
+}
+cudaError_t map_adapters(CUtensorMap* map, const LoraArgs& p, const void* base, int cols, int rows,
+                         int box_rows) {
+  const uint64_t dims[3] = {(uint64_t)cols, (uint64_t)rows, (uint64_t)p.L};
+  const uint64_t strides[2] = {(uint64_t)cols * 2, (uint64_t)rows * cols * 2};
+  const uint32_t box[3] = {64, (uint32_t)box_rows, 1};
+  return make_tmap16(map, p.dtype, base, 3, dims, strides, box) == QMOE_OK ? cudaSuccess
+                                                                           : cudaErrorUnknown;
+}
+cudaError_t shrink_maps(const LoraArgs& p, CUtensorMap* x, CUtensorMap* a) {
+  const cudaError_t e = map_rows(x, p, p.x, p.K, p.M, p.ldx, p.tile_n);
+  return e == cudaSuccess ? map_adapters(a, p, p.a, p.K, p.R, p.R) : e;
+}
+cudaError_t gemm_maps(const LoraArgs& p, CUtensorMap* x, CUtensorMap* w, CUtensorMap* b) {
+  cudaError_t e = map_rows(x, p, p.x, p.K, p.M, p.ldx, p.tile_n / p.cg);
+  if (e == cudaSuccess && p.w) e = map_rows(w, p, p.w, p.K, p.N, p.K, 128);
+  if (!p.w) *w = *x;  // never read
+  return e == cudaSuccess ? map_adapters(b, p, p.b, p.R, p.N, 128) : e;
+}
+
 template <class T>
-cudaError_t run(LoraArgs& p, const LoraMaps& maps, int num_sms, cudaStream_t stream) {
+cudaError_t run(LoraArgs& p, int num_sms, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
   attr[0] = pdl_attribute();
@@ -1148,9 +1277,19 @@ cudaError_t run(LoraArgs& p, const LoraMaps& maps, int num_sms, cudaStream_t str
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
     cfg.numAttrs = 2;
-    e = cudaLaunchKernelEx(&cfg, lora_shrink_mma_kernel<T>, maps.xs, maps.a, p);
+    CUtensorMap map_x, map_a;
+    e = shrink_maps(p, &map_x, &map_a);
+    if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, lora_shrink_mma_kernel<T>, map_x, map_a, p);
     cfg.numAttrs = 1;
   }
+  if (e != cudaSuccess) return e;
+  if (p.M <= kGemvTokens) {
+    return p.K <= 2048   ? gemv<T, 1>(p, cfg)
+           : p.K <= 4096 ? gemv<T, 2>(p, cfg)
+                         : gemv<T, 4>(p, cfg);
+  }
+  CUtensorMap map_x, map_w, map_b;
+  e = gemm_maps(p, &map_x, &map_w, &map_b);
   if (e != cudaSuccess) return e;
   const int stage = kStageA + token_bytes(p.tile_n, p.cg);
   const bool vec = p.cg == 1 && p.tile_n <= kVecTokens && p.tile_n * p.R <= kVecTokenRanks;
@@ -1191,7 +1330,7 @@ cudaError_t run(LoraArgs& p, const LoraMaps& maps, int num_sms, cudaStream_t str
     attr[1].val.clusterDim.z = 1;
     cfg.numAttrs = 2;
   }
-  return cudaLaunchKernelEx(&cfg, k, maps.x, maps.w, maps.b, p);
+  return cudaLaunchKernelEx(&cfg, k, map_x, map_w, map_b, p);
 }
 
 }  // namespace
@@ -1228,9 +1367,9 @@ LoraPlan lora_plan(int M, int K, int N, int R, bool has_w) {
   return L;
 }
 
-cudaError_t launch_lora(LoraArgs& p, const LoraMaps& maps, int num_sms, cudaStream_t stream) {
-  return p.dtype == QMOE_DTYPE_BF16 ? run<__nv_bfloat16>(p, maps, num_sms, stream)
-                                    : run<__half>(p, maps, num_sms, stream);
+cudaError_t launch_lora(LoraArgs& p, int num_sms, cudaStream_t stream) {
+  return p.dtype == QMOE_DTYPE_BF16 ? run<__nv_bfloat16>(p, num_sms, stream)
+                                    : run<__half>(p, num_sms, stream);
 }
 
 }  // namespace qmoe

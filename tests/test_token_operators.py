@@ -533,7 +533,9 @@ LORAS_WIDE = [
     (256, 4096, 96, 24, 40, True, False, "mixed"), (200, 2048, 130, 128, 50, True, False, "mixed"),
     (1100, 1024, 300, 8, 500, True, True, "mixed"), (33, 8192, 64, 64, 9, False, True, "mixed"),
     (2047, 1096, 512, 48, 11, True, False, "runs"), (60, 256, 20000, 64, 40, True, True, "mixed"),
-    (31, 512, 160, 128, 31, True, False, "mixed"), (64, 1024, 30000, 16, 60, True, False, "mixed"), (700, 968, 200, 128, 3, True, False, "none"),
+    (31, 512, 160, 128, 31, True, False, "mixed"), (2, 2056, 77, 128, 2, True, True, "mixed"),
+    (4, 4104, 130, 72, 9, True, False, "mixed"), (3, 1544, 5, 32, 2, False, False, "mixed"),
+    (1, 16384, 40, 64, 3, True, True, "runs"), (64, 1024, 30000, 16, 60, True, False, "mixed"), (700, 968, 200, 128, 3, True, False, "none"),
 ]
 
 
