@@ -269,7 +269,7 @@ static LoraLayout lora_layout(const LoraPlan& P, int M, int R) {
   L.list = align_up(L.bad + 4 * (size_t)P.tiles, 256);
   L.place = align_up(L.list + 4 * tokens, 256);
   L.t = align_up(L.place + 4 * tokens, 256);
-  L.total = align_up(L.t + 4 * (size_t)M * R, 256);
+  L.total = align_up(L.t + 4 * (size_t)M * R * P.tsplits, 256);
   return L;
 }
 
@@ -324,7 +324,7 @@ int qmoe_lora_linear(const void* x_dev, int dtype, long long ldx, const void* w_
   p.bad = reinterpret_cast<int*>(ws + W.bad);
   p.list = reinterpret_cast<int*>(ws + W.list);
   p.place = reinterpret_cast<int*>(ws + W.place);
-  p.t = ws + W.t;
+  p.t = reinterpret_cast<float*>(ws + W.t);
   p.wide = chunked(out_dev, N, N, 2, 16);
   return cuda_rc(launch_lora(p, sms, reinterpret_cast<cudaStream_t>(stream)));
 }

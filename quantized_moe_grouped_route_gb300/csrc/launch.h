@@ -183,10 +183,9 @@ cudaError_t launch_unsort_backward(const TokenArgs& a, int dtype, int chunk, int
 // lora.cu
 // How a problem is cut: token tiles of tile_n (a multiple of 16, at most 240), units of one
 // tile x 128 * cg rows of w (cg: CTAs per unit), each of ksteps steps of 64 of K; the shrink
-// with plain products (tsplits 0) or on the tensor cores (tsplits its segments of K, set at
-// launch).
+// with plain products or on the tensor cores, in tsplits segments of K.
 struct LoraPlan {
-  int cg, tile_n, tiles, blocks, ksteps, tsplits;
+  int cg, tile_n, tiles, blocks, ksteps, tensor_shrink, tsplits;
 };
 LoraPlan lora_plan(int M, int K, int N, int R, bool has_w);
 struct LoraArgs : LoraPlan {
@@ -209,7 +208,7 @@ struct LoraArgs : LoraPlan {
   int* bad;    // [tiles] whether an id of the tile is L or more
   int* list;   // [tiles][tile_n] the distinct adapters
   int* place;  // [tiles][tile_n] each token's adapter's place in the list, -1: none
-  void* t;     // [M][2][R] scales[a] * (x . A^T): rounded, and what the rounding left
+  float* t;    // [tsplits][M][R] scales[a] * (x . A^T) over a segment of K
 };
 cudaError_t launch_lora(LoraArgs& p, int num_sms, cudaStream_t stream);
 

@@ -172,14 +172,37 @@ __global__ void __launch_bounds__(kShrinkMost) lora_shrink_kernel(const LoraArgs
   if (tid < 8) {
     float s = 0.f;
     for (int w = 0; w < (int)(blockDim.x >> 5); ++w) s += part[w][tid];
-    if (id >= 0 && id < p.L) {
-      s *= p.scales[id];
-      T* dst = reinterpret_cast<T*>(p.t) + (size_t)m * 2 * p.R + r0 + tid;
-      const T hi = from_f32<T>(s);
-      dst[0] = hi;
-      dst[p.R] = from_f32<T>(s - to_f32(hi));
-    }
+    if (id >= 0 && id < p.L) p.t[(size_t)m * p.R + r0 + tid] = s * p.scales[id];
   }
+}
+
+// Ranks r .. r + 7 of a token's t, over the shrink's segments of K in order.
+__device__ __forceinline__ void load_t8(const LoraArgs& p, int m, int r, float (&t)[8]) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) t[e] = 0.f;
+  const float* src = p.t + (size_t)m * p.R + r;
+#pragma unroll 4
+  for (int g = 0; g < p.tsplits; ++g) {
+    const float4 a = reinterpret_cast<const float4*>(src + (size_t)g * p.M * p.R)[0];
+    const float4 b = reinterpret_cast<const float4*>(src + (size_t)g * p.M * p.R)[1];
+    t[0] += a.x, t[1] += a.y, t[2] += a.z, t[3] += a.w;
+    t[4] += b.x, t[5] += b.y, t[6] += b.z, t[7] += b.w;
+  }
+}
+// ... as their rounding and what that leaves.
+template <class T>
+__device__ __forceinline__ void load_t8_split(const LoraArgs& p, int m, int r, uint4* hi,
+                                              uint4* lo) {
+  float t[8];
+  load_t8(p, m, r, t);
+  Pack<T, 8> h, l;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    h.v[e] = from_f32<T>(t[e]);
+    l.v[e] = from_f32<T>(t[e] - to_f32(h.v[e]));
+  }
+  *hi = h.raw;
+  *lo = l.raw;
 }
 
 // ------------------------------------------------------------------------------- GEMM
@@ -202,7 +225,7 @@ __host__ __device__ constexpr int token_slots(int tile_n, int cg) {
 }
 // The builders' copy of t for a CTA's token rows (both values), where it takes up to 16 KB:
 // every row enters one adapter's step, and the steps then build from shared memory what
-// they would each wait for from L2 (48 tokens of 43 adapters: 22 -> see lora_plan).
+// they would each wait for from L2.
 __host__ __device__ constexpr int t_copy_bytes(int tile_n, int cg, int R) {
   return cg == 1 && tile_n * R * 4 <= 16384 ? tile_n * R * 4 : 0;
 }
@@ -268,20 +291,16 @@ __device__ __forceinline__ void fence_proxy_async() {
 // A CTA per (token tile, K segment): D[rank of adapter][token] = A[a] . x^T on the tensor
 // cores, with the 128 / R adapters of a pass stacked on the MMA's 128 rows, so that a tile
 // of few adapters (requests one after another) takes one pass over its token rows.  Each
-// token keeps the rows of its own adapter, in shared memory; the segments of a tile are one
-// cluster, whose CTAs then add up a share of the tokens each over all segments, in order.
-// gridDim.y clusters share a tile's passes.
-constexpr int kShrinkStages = 6;
-constexpr int kShrinkSegments = 8;  // CTAs of a cluster, at most
+// token keeps the rows of its own adapter; the GEMM adds up the segments where it takes t
+// up (adding them here, through a cluster's shared memory, cost more than the reads it
+// saved, and 37 tiles of four segments did not fit as clusters: at M = 8192, K = 7168 31 us).
+// gridDim.y CTAs share a tile's passes.
+constexpr int kShrinkMostStages = 6;
+constexpr int kShrinkSegments = 8;  // at most
 __host__ __device__ constexpr int shrink_stage_bytes(int tile_n) { return kStageA + tile_n * 128; }
-// bytes of a CTA's sums [tile_n][R]
-__host__ __device__ constexpr int shrink_sum_bytes(int tile_n, int R) { return tile_n * R * 4; }
-// Stages of the ring beside `other` bytes.  A CTA with one pass writes its sums over the
-// ring, which it no longer needs then; with more, they have a place of their own.
-constexpr int kShrinkBytes = kSmemLimit - 8192;  // less the static shared memory
-__host__ __device__ constexpr int shrink_stages(int tile_n, int other) {
-  const int n = (kShrinkBytes - other) / shrink_stage_bytes(tile_n);
-  return n < kShrinkStages ? n : kShrinkStages;
+__host__ __device__ constexpr int shrink_stages(int tile_n) {
+  const int n = (kSmemLimit - 8192) / shrink_stage_bytes(tile_n);  // less the static memory
+  return n < kShrinkMostStages ? n : kShrinkMostStages;
 }
 
 template <class T>
@@ -294,14 +313,15 @@ __global__ void __launch_bounds__(kShrinkThreads, 1)
   __shared__ ListScratch scratch;
   __shared__ int list[kShrinkThreads];
   __shared__ __align__(16) int place[kShrinkThreads];
-  __shared__ __align__(8) uint64_t full[kShrinkStages], empty[kShrinkStages], accf, acce, drain;
+  __shared__ __align__(8) uint64_t full[kShrinkMostStages], empty[kShrinkMostStages], accf,
+      acce, drain;
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_word;
   volatile int* abort_flag = &abort_word;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int stage_bytes = shrink_stage_bytes(p.tile_n);
+  const int stage_bytes = shrink_stage_bytes(p.tile_n), stages = shrink_stages(p.tile_n);
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kShrinkStages; ++s) {
+    for (int s = 0; s < stages; ++s) {
       mbar_init(smem_u32(&full[s]), 1);
       mbar_init(smem_u32(&empty[s]), 1);
     }
@@ -324,11 +344,10 @@ __global__ void __launch_bounds__(kShrinkThreads, 1)
   const int ksteps = (p.K + 63) / 64;
   const int k0 = (int)((long long)ksteps * seg / p.tsplits);
   const int k1 = (int)((long long)ksteps * (seg + 1) / p.tsplits);
-  const int sum_bytes = shrink_sum_bytes(p.tile_n, p.R);
   const uint64_t pol = l2_policy_evict_last();  // the GEMM reads the token rows next
   // the first token rows are fetched while the list is made (their bytes count on a phase
   // that the adapters' copies have yet to arrive at)
-  const int early = min(shrink_stages(p.tile_n, sum_bytes), k1 - k0);
+  const int early = min(stages, k1 - k0);
   if (warp == 0) {
     __syncwarp();
     const uint32_t lead = elect_one();
@@ -347,10 +366,6 @@ __global__ void __launch_bounds__(kShrinkThreads, 1)
   const uint32_t tmem = tmem_slot;
   const int cap = 128 / p.R;
   const int passes = (n + cap - 1) / cap;
-  const bool once = passes <= (int)(blockIdx.y + gridDim.y);
-  const int stages = shrink_stages(p.tile_n, once ? 0 : sum_bytes);
-  float* sums = reinterpret_cast<float*>(smem + (once ? 0 : kShrinkBytes - sum_bytes));  // [tile_n][R]
-
   if (warp == 0) {
     const uint32_t lead = elect_one();
     uint32_t s = 0, ph = 1;
@@ -427,7 +442,8 @@ __global__ void __launch_bounds__(kShrinkThreads, 1)
       if (!warp_wait(smem_u32(&accf), ph, abort_flag, p.err)) break;
       ph ^= 1;
       tc_fence_after();
-      const int want = slot < cap ? ps * cap + slot : -2;
+      const int want = slot < cap && ps * cap + slot < n ? ps * cap + slot : -2;
+      const float scale = want >= 0 ? p.scales[list[want]] : 0.f;
       for (int c0 = 0; c0 < cols; c0 += 16) {
         uint32_t v[16];
         tmem_ld_x16(tmem + ((uint32_t)(q * 32) << 16) + c0, v);
@@ -438,13 +454,13 @@ __global__ void __launch_bounds__(kShrinkThreads, 1)
         for (int k = 0; k < 4; ++k) at[k] = reinterpret_cast<const int4*>(place + c0)[k];
         tmem_wait_ld();
         tmem_ld_ready(v);
-        float* dst = sums + c0 * p.R + r;
+        float* dst = p.t + ((size_t)seg * p.M + m0 + c0) * p.R + r;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          if (at[k].x == want) dst[(4 * k) * p.R] = __uint_as_float(v[4 * k]);
-          if (at[k].y == want) dst[(4 * k + 1) * p.R] = __uint_as_float(v[4 * k + 1]);
-          if (at[k].z == want) dst[(4 * k + 2) * p.R] = __uint_as_float(v[4 * k + 2]);
-          if (at[k].w == want) dst[(4 * k + 3) * p.R] = __uint_as_float(v[4 * k + 3]);
+          if (at[k].x == want) dst[(4 * k) * p.R] = __uint_as_float(v[4 * k]) * scale;
+          if (at[k].y == want) dst[(4 * k + 1) * p.R] = __uint_as_float(v[4 * k + 1]) * scale;
+          if (at[k].z == want) dst[(4 * k + 2) * p.R] = __uint_as_float(v[4 * k + 2]) * scale;
+          if (at[k].w == want) dst[(4 * k + 3) * p.R] = __uint_as_float(v[4 * k + 3]) * scale;
         }
       }
       tc_fence_before();
@@ -458,37 +474,6 @@ __global__ void __launch_bounds__(kShrinkThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, kAccCols);
   }
-  // the tokens c = seg, seg + segments, .. of this cluster's passes, summed over the segments
-  cluster_sync_all();
-  // (four ranks a thread, the segments' values in flight together)
-  const uint32_t sums0 = smem_u32(sums);
-  const int share = (cols - seg + p.tsplits - 1) / p.tsplits, quads = p.R / 4;
-  for (int i = threadIdx.x; i < share * quads; i += kShrinkThreads) {
-    const int c = i / quads * p.tsplits + seg, r = i % quads * 4;
-    const int at = place[c];
-    const bool here = at >= 0 && at / cap % (int)gridDim.y == (int)blockIdx.y;
-    const float s = here ? p.scales[list[at]] : 0.f;
-    float4 v[kShrinkSegments];
-#pragma unroll
-    for (int g = 0; g < kShrinkSegments; ++g)
-      if (g < p.tsplits && here) v[g] = ld_cluster_f32x4(peer_addr(sums0 + (c * p.R + r) * 4, g));
-    float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-    for (int g = 0; g < kShrinkSegments; ++g)
-      if (g < p.tsplits) t.x += v[g].x, t.y += v[g].y, t.z += v[g].z, t.w += v[g].w;
-    if (!here) continue;
-    const float f[4] = {t.x * s, t.y * s, t.z * s, t.w * s};
-    Pack<T, 4> hi, lo;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      hi.v[e] = from_f32<T>(f[e]);
-      lo.v[e] = from_f32<T>(f[e] - to_f32(hi.v[e]));
-    }
-    uint2* dst = reinterpret_cast<uint2*>(reinterpret_cast<T*>(p.t) + (size_t)(m0 + c) * 2 * p.R + r);
-    dst[0] = hi.raw;
-    dst[p.R / 4] = lo.raw;
-  }
-  cluster_sync_all();  // no CTA leaves while its sums may still be read
 }
 
 template <class T, int CG, bool VEC>
@@ -791,7 +776,6 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     const int apart = C % 8 == 0 ? 1 : C % 4 == 0 ? 2 : C % 2 == 0 ? 4 : 8;
     const int turn = lane / apart % C;
     float* tf = reinterpret_cast<float*>(tcopy);
-    const T* tsrc = reinterpret_cast<const T*>(p.t);
     uint32_t step = 0, dph = 1;
     bool ok = true;
     // (after a wait that gave up a warp still meets the others at their barriers)
@@ -803,12 +787,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       for (int u = threadIdx.x - 256; u < own_rows * C; u += 32 * kBuilders) {
         const int c = u / C, m = m0 + c * S + seg;
         if (m >= p.M) break;
-        const T* src = tsrc + (size_t)m * 2 * p.R + u % C * 8;
-        Pack<T, 8> hi, lo;
-        hi.raw = *reinterpret_cast<const uint4*>(src);
-        lo.raw = *reinterpret_cast<const uint4*>(src + p.R);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) tf[u * 8 + e] = to_f32(hi.v[e]) + to_f32(lo.v[e]);
+        float t[8];
+        load_t8(p, m, u % C * 8, t);
+        reinterpret_cast<float4*>(tf)[2 * u] = make_float4(t[0], t[1], t[2], t[3]);
+        reinterpret_cast<float4*>(tf)[2 * u + 1] = make_float4(t[4], t[5], t[6], t[7]);
       }
       if (ok && !wait(dempty, dph)) ok = false;  // the epilogue has read the previous delta
       dph ^= 1;
@@ -868,7 +850,6 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     uint32_t step = 0, tph = 1;
     bool ok = true;
     const uint32_t tfull0 = CG == 2 ? peer_addr(smem_u32(tfull), lead_rank) : smem_u32(tfull);
-    const T* tsrc = reinterpret_cast<const T*>(p.t);
     // (after a wait that gave up a warp still meets the others at their barriers)
     for (int i = worker; i < units; i += workers) {
       const int tile = i / p.blocks;
@@ -879,11 +860,14 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       for (int r = threadIdx.x - 256; r < rows_b; r += 32 * kBuilders)
         place[r] = (short)p.place[(size_t)m0 + r];
       if (copy_bytes) {
-        const int quads = p.R / 4;  // 16-byte units of a row's two values
-        for (int u = threadIdx.x - 256; u < rows_b * quads; u += 32 * kBuilders)
-          if (m0 + u / quads < p.M)
-            reinterpret_cast<uint4*>(tcopy)[u] =
-                reinterpret_cast<const uint4*>(tsrc + (size_t)m0 * 2 * p.R)[u];
+        const int eights = p.R / 8;
+        for (int u = threadIdx.x - 256; u < rows_b * eights; u += 32 * kBuilders) {
+          const int row = u / eights, r = u % eights * 8;
+          if (m0 + row >= p.M) break;
+          T* dst = reinterpret_cast<T*>(tcopy) + row * 2 * p.R + r;
+          load_t8_split<T>(p, m0 + row, r, reinterpret_cast<uint4*>(dst),
+                           reinterpret_cast<uint4*>(dst + p.R));
+        }
       }
       builders_sync();
       for (int d = seg; d < n && ok; d += S) {
@@ -900,10 +884,13 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             const int r = h * 64 + j * 8;
             uint4 hi = make_uint4(0u, 0u, 0u, 0u), lo = hi;
             if (place[row] == d && r < p.R) {
-              const T* src = copy_bytes ? reinterpret_cast<const T*>(tcopy) + row * 2 * p.R + r
-                                        : tsrc + (size_t)(m0 + row) * 2 * p.R + r;
-              hi = *reinterpret_cast<const uint4*>(src);
-              lo = *reinterpret_cast<const uint4*>(src + p.R);
+              if (copy_bytes) {
+                const T* src = reinterpret_cast<const T*>(tcopy) + row * 2 * p.R + r;
+                hi = *reinterpret_cast<const uint4*>(src);
+                lo = *reinterpret_cast<const uint4*>(src + p.R);
+              } else {
+                load_t8_split<T>(p, m0 + row, r, &hi, &lo);
+              }
             }
             // rows of 128 bytes, 16-byte units swizzled by the row (128-byte swizzle)
             uint8_t* at = dst + row * 128 + ((j ^ (row & 7)) << 4);
@@ -1138,11 +1125,11 @@ __global__ void __launch_bounds__(kGemvThreads) lora_gemv_kernel(const LoraArgs 
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
     if (id[m] >= 0) {
-      const T* t = reinterpret_cast<const T*>(p.t) + (size_t)m * 2 * p.R + lane;
+      // (so few tokens have one segment)
+      const float* t = p.t + (size_t)m * p.R + lane;
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        if (lane + 32 * i < p.R)
-          acc[m] = fmaf(to_f32(bv[m][i]), to_f32(t[32 * i]) + to_f32(t[p.R + 32 * i]), acc[m]);
+        if (lane + 32 * i < p.R) acc[m] = fmaf(to_f32(bv[m][i]), t[32 * i], acc[m]);
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) acc[m] += __shfl_xor_sync(0xffffffffu, acc[m], o);
@@ -1195,29 +1182,6 @@ int resident_clusters(K* kernel, int size, int threads, size_t smem, std::atomic
   return n;
 }
 
-// Segments of K of the tensor-core shrink, one cluster per tile: the count whose rounds of
-// resident clusters take the fewest K steps, a round counting 20 steps for what does not
-// shrink with them (36 clusters of four CTAs are resident, so that 37 tiles of four segments
-// took two rounds and 54 us; of three, see lora_shrink_mma_kernel).
-template <class T>
-int shrink_segments(int tiles, int ksteps, int num_sms) {
-  static std::atomic<int> kept[kShrinkSegments + 1];
-  int best = 1;
-  long long least = -1;
-  for (int s = 1; s <= kShrinkSegments && (s == 1 || s * 4 <= ksteps); ++s) {
-    const int held = s == 1 ? num_sms
-                            : resident_clusters(lora_shrink_mma_kernel<T>, s, kShrinkThreads,
-                                                1024 + kShrinkBytes, kept[s], num_sms);
-    if (held < 1) continue;
-    const long long cost = (long long)((tiles + held - 1) / held) * ((ksteps + s - 1) / s + 20);
-    if (least < 0 || cost < least) {
-      least = cost;
-      best = s;
-    }
-  }
-  return best;
-}
-
 // Tensor maps: token rows in boxes of `rows`, [N][K] and [L][rows][cols] in boxes of 64
 // columns.
 cudaError_t map_rows(CUtensorMap* map, const LoraArgs& p, const void* base, int cols, int rows,
@@ -1255,32 +1219,25 @@ cudaError_t run(LoraArgs& p, int num_sms, cudaStream_t stream) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   cudaError_t e;
-  if (p.tsplits == 0) {
+  if (!p.tensor_shrink) {
     int threads = (p.K / 8 + 31) / 32 * 32;
     threads = threads < kShrinkThreads ? kShrinkThreads : threads > kShrinkMost ? kShrinkMost : threads;
     cfg.blockDim = dim3(threads);
     cfg.gridDim = dim3((unsigned)(p.tiles + (long long)p.M * (p.R / 8)));
     e = cudaLaunchKernelEx(&cfg, lora_shrink_kernel<T>, p);
   } else {
-    e = cudaFuncSetAttribute(lora_shrink_mma_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             1024 + kShrinkBytes);
-    if (e != cudaSuccess) return e;
-    p.tsplits = shrink_segments<T>(p.tiles, (p.K + 63) / 64, num_sms);
     const int ctas = p.tiles * p.tsplits, cap = 128 / p.R;
     const int most = ((p.L < p.tile_n ? p.L : p.tile_n) + cap - 1) / cap;
     const int share = num_sms / ctas < 1 ? 1 : num_sms / ctas;
     cfg.blockDim = dim3(kShrinkThreads);
     cfg.gridDim = dim3(ctas, share < most ? share : most);
-    cfg.dynamicSmemBytes = 1024 + kShrinkBytes;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = p.tsplits;
-    attr[1].val.clusterDim.y = 1;
-    attr[1].val.clusterDim.z = 1;
-    cfg.numAttrs = 2;
+    cfg.dynamicSmemBytes = 1024 + shrink_stages(p.tile_n) * shrink_stage_bytes(p.tile_n);
+    e = cudaFuncSetAttribute(lora_shrink_mma_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)cfg.dynamicSmemBytes);
+    if (e != cudaSuccess) return e;
     CUtensorMap map_x, map_a;
     e = shrink_maps(p, &map_x, &map_a);
     if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, lora_shrink_mma_kernel<T>, map_x, map_a, p);
-    cfg.numAttrs = 1;
   }
   if (e != cudaSuccess) return e;
   if (p.M <= kGemvTokens) {
@@ -1362,8 +1319,15 @@ LoraPlan lora_plan(int M, int K, int N, int R, bool has_w) {
     }
   }
   L.blocks = (N + 128 * L.cg - 1) / (128 * L.cg);
-  // the fp32 shrink reads a token's adapter anew for each token: up to 16 MB of such reads
-  L.tsplits = (long long)M * R * K * 2 > (16LL << 20) ? 1 : 0;
+  // the fp32 shrink reads a token's adapter anew for each token: up to 16 MB of such reads,
+  // and what runs as plain products throughout
+  L.tensor_shrink = M > kGemvTokens && (long long)M * R * K * 2 > (16LL << 20);
+  L.tsplits = 1;
+  if (L.tensor_shrink) {
+    const int most = ksteps / 4 < kShrinkSegments ? ksteps / 4 : kShrinkSegments;
+    const int s = sms / L.tiles < most ? sms / L.tiles : most;
+    L.tsplits = s < 1 ? 1 : s;
+  }
   return L;
 }
 
