@@ -42,7 +42,7 @@
 // (cta_group::2, M = 256), each SM loading half of the token rows, since a 128 x 256 tile
 // fed by one SM alone asks more of its L2 port (96 bytes a clock) than it has.
 //
-// Up to four tokens run as plain products, a warp per row of w (lora_gemv_kernel).
+// One or two tokens run as plain products, warps per row of w (lora_gemv_kernel).
 //
 // Every wait is bounded, as in the layer's GEMMs.
 #include <atomic>
@@ -1059,15 +1059,16 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   }
 }
 
-// ------------------------------------------------------------------- up to four tokens
+// --------------------------------------------------------------------- one or two tokens
 // One, two or four warps (WPR, the more, the longer the row) per row of w: its product with
 // up to MT token rows in fp32, w in 16-byte loads of which a lane has about eight in all, in
 // flight together (one warp a row, 28 loads a lane at K = 7168, took 9.4 us); then the row
 // of each token's B with t.
-// HBM (or L2) bound; at one token the arithmetic is about a third of the stream's time, at
-// four about equal, and there is nothing to set up: the tensor-core kernel spends 5 of its
+// HBM (or L2) bound, and there is nothing to set up: the tensor-core kernel spends 5 of its
 // 10.3 us at M = 1, K = 7168, N = 2048 on barriers, TMEM, the cluster and the last sums.
-constexpr int kGemvThreads = 128, kGemvTokens = 4;
+// Whole calls at K = 7168, N = 2048, R = 16: one token 9.7 us (tensor cores 11.4), two 10.9
+// (11.9), four 16.0 (12.0).
+constexpr int kGemvThreads = 128, kGemvTokens = 2;
 
 template <class T, int MT, int WPR>
 __global__ void __launch_bounds__(kGemvThreads) lora_gemv_kernel(const LoraArgs p) {
@@ -1094,7 +1095,7 @@ __global__ void __launch_bounds__(kGemvThreads) lora_gemv_kernel(const LoraArgs 
     const uint4* w = reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(p.w) + (size_t)n * p.K);
     const T* x = reinterpret_cast<const T*>(p.x);
     const int chunks = p.K / 8;
-    constexpr int kFlight = MT == 1 ? 8 : MT == 2 ? 6 : 4;
+    constexpr int kFlight = MT == 1 ? 8 : 6;
     for (int c0 = sub * 32 + lane; c0 < chunks; c0 += 32 * WPR * kFlight) {
       P_ wv[kFlight];
 #pragma unroll
@@ -1152,9 +1153,7 @@ cudaError_t gemv(const LoraArgs& p, cudaLaunchConfig_t cfg) {
   cfg.blockDim = dim3(kGemvThreads);
   cfg.gridDim = dim3((p.N + kRows - 1) / kRows);
   cfg.dynamicSmemBytes = 0;
-  auto* k = p.M == 1   ? lora_gemv_kernel<T, 1, WPR>
-            : p.M == 2 ? lora_gemv_kernel<T, 2, WPR>
-                       : lora_gemv_kernel<T, 4, WPR>;
+  auto* k = p.M == 1 ? lora_gemv_kernel<T, 1, WPR> : lora_gemv_kernel<T, 2, WPR>;
   return cudaLaunchKernelEx(&cfg, k, p);
 }
 
@@ -1319,8 +1318,9 @@ LoraPlan lora_plan(int M, int K, int N, int R, bool has_w) {
     }
   }
   L.blocks = (N + 128 * L.cg - 1) / (128 * L.cg);
-  // the fp32 shrink reads a token's adapter anew for each token: up to 16 MB of such reads,
-  // and what runs as plain products throughout
+  // the fp32 shrink reads a token's adapter anew for each token: up to 16 MB of such reads
+  // (at 33 MB, M = 256, K = N = 4096, R = 16, a call takes 19.8 us with the tensor cores
+  // and 22.7 without, at 17 MB 18.3 and 17.8), and what runs as plain products throughout
   L.tensor_shrink = M > kGemvTokens && (long long)M * R * K * 2 > (16LL << 20);
   L.tsplits = 1;
   if (L.tensor_shrink) {
