@@ -28,7 +28,7 @@ constexpr int kGateWarps = 4;
 // An unsigned key in the order of the float (both zeros equal); 0 is kept for masked.
 __device__ __forceinline__ uint32_t order_key(float v) {
   const uint32_t u = __float_as_uint(v + 0.0f);
-  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+  return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);  // a negative's bits all turn
 }
 
 // The reciprocal is correctly rounded, so this is 1 / (1 + exp(-l)) to the bit.
@@ -229,18 +229,25 @@ __global__ void __launch_bounds__(kGateWarps * 32) gate_kernel(const GateArgs p)
       if (mx == bound) mx = 0u;
     }
     bound = max(bound, 1u);  // no lane left: every unmasked key
-    int n = 0;
+    // each lane's candidates, at a place after those of the lanes before it
+    int mine_n = 0;
 #pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-      const bool in = key[j] >= bound;
-      const unsigned who = __ballot_sync(kAll, in);
-      const int at = n + __popc(who & below);
-      if (in && at < 32)
-        cand[at] = (unsigned long long)key[j] << 32 | (uint32_t)~(e0 + j);
-      n += __popc(who);
+    for (int j = 0; j < VPT; ++j) mine_n += key[j] >= bound;
+    int at = 0, n = 0;
+#pragma unroll
+    for (int bit = 1; bit <= VPT; bit <<= 1) {
+      const unsigned who = __ballot_sync(kAll, mine_n & bit);
+      at += bit * __popc(who & below);
+      n += bit * __popc(who);
+    }
+    if (n <= 32) {
+#pragma unroll
+      for (int j = 0; j < VPT; ++j)
+        if (key[j] >= bound) cand[at++] = (unsigned long long)key[j] << 32 | (uint32_t)~(e0 + j);
     }
     __syncwarp();
     // slot `slot` of the row belongs to this lane, with this expert (and a second one above 32)
+    const int nslot = p.top_k > 32 ? 2 : 1;
     int slot[2] = {-1, -1}, expert[2] = {-1, -1};
     if (n <= 32) {
       // the lanes past the candidates take the slots that are left over, as empty ones
@@ -282,36 +289,32 @@ __global__ void __launch_bounds__(kGateWarps * 32) gate_kernel(const GateArgs p)
       slot[1] = lane + 32;
     }
     __syncwarp();  // the candidates have been read
-    float s[2] = {0.f, 0.f}, lv[2];
+    float s[2] = {0.f, 0.f}, lv[2] = {-INFINITY, -INFINITY};
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
+      if (i >= nslot) break;
       if (slot[i] >= p.top_k) slot[i] = expert[i] = -1;
-      lv[i] = expert[i] >= 0 ? to_f32(l[expert[i]]) : -INFINITY;
+      if (expert[i] >= 0) lv[i] = to_f32(l[expert[i]]);
     }
+    float divide = 1.f;
     if (sigmoid) {
 #pragma unroll
       for (int i = 0; i < 2; ++i)
-        if (expert[i] >= 0) s[i] = sigmoid_f32(lv[i]);
-      if (p.renormalize) {
-        const float d = warp_sum(s[0] + s[1]) + 1e-20f;
-        s[0] /= d;
-        s[1] /= d;
-      }
+        if (i < nslot && expert[i] >= 0) s[i] = sigmoid_f32(lv[i]);
+      if (p.renormalize) divide = warp_sum(s[0] + s[1]) + 1e-20f;
     } else {
       if (p.renormalize) top = warp_max(fmaxf(lv[0], lv[1]));
 #pragma unroll
       for (int i = 0; i < 2; ++i)
-        if (expert[i] >= 0) s[i] = expf(lv[i] - top);
-      if (p.renormalize) total = warp_sum(s[0] + s[1]);
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-        if (expert[i] >= 0) s[i] /= total;
+        if (i < nslot && expert[i] >= 0) s[i] = expf(lv[i] - top);
+      divide = p.renormalize ? warp_sum(s[0] + s[1]) : total;
     }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
+      if (i >= nslot) break;
       if (slot[i] >= 0) {
         p.ids[m * p.top_k + slot[i]] = expert[i];
-        p.weights[m * p.top_k + slot[i]] = expert[i] >= 0 ? s[i] * p.scale : 0.f;
+        p.weights[m * p.top_k + slot[i]] = expert[i] >= 0 ? s[i] / divide * p.scale : 0.f;
       }
     }
   }
