@@ -338,32 +338,34 @@ __global__ void __launch_bounds__(kGateWarps * 32) gate_backward_kernel(const Ga
   grid_dep_wait();
   grid_dep_launch();
   const bool sigmoid = p.scoring == QMOE_GATE_SIGMOID;
+  const int nslot = p.top_k > 32 ? 2 : 1;  // slots a lane
   for (long long m = (long long)blockIdx.x * kGateWarps + warp; m < p.M;
        m += (long long)gridDim.x * kGateWarps) {
     const T* l = reinterpret_cast<const T*>(p.logits) + m * p.ld;
-    int e[2];
-    float s[2], dw[2], lv[2], d[2];
+    int e[2] = {-1, -1};
+    float s[2] = {0.f, 0.f}, dw[2] = {0.f, 0.f}, lv[2] = {-INFINITY, -INFINITY}, d[2] = {0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
+      if (i >= nslot) break;
       const int r = lane + 32 * i;
       e[i] = r < p.top_k ? p.ids_in[m * p.top_k + r] : -1;
       if ((unsigned)e[i] >= (unsigned)p.E) e[i] = -1;
       dw[i] = e[i] >= 0 ? p.dweights[m * p.top_k + r] : 0.f;
       lv[i] = e[i] >= 0 ? to_f32(l[e[i]]) : -INFINITY;
-      s[i] = d[i] = 0.f;
     }
     float top = 0.f, dense = 0.f;  // dense: what every expert's exp(l - top) is multiplied by
     if (sigmoid) {
 #pragma unroll
       for (int i = 0; i < 2; ++i)
-        if (e[i] >= 0) s[i] = sigmoid_f32(lv[i]);
-      float S = 1.f, inner = 0.f;
+        if (i < nslot && e[i] >= 0) s[i] = sigmoid_f32(lv[i]);
+      float c = p.scale, inner = 0.f;
       if (p.renormalize) {
-        S = warp_sum(s[0] + s[1]) + 1e-20f;
-        inner = warp_sum(s[0] / S * dw[0] + s[1] / S * dw[1]);
+        const float S = warp_sum(s[0] + s[1]) + 1e-20f;
+        inner = warp_sum(s[0] * dw[0] + s[1] * dw[1]) / S;
+        c /= S;
       }
 #pragma unroll
-      for (int i = 0; i < 2; ++i) d[i] = p.scale / S * (dw[i] - inner) * s[i] * (1.f - s[i]);
+      for (int i = 0; i < 2; ++i) d[i] = c * (dw[i] - inner) * s[i] * (1.f - s[i]);
     } else {
       float total = 0.f;
       if (p.renormalize) {
@@ -380,14 +382,14 @@ __global__ void __launch_bounds__(kGateWarps * 32) gate_backward_kernel(const Ga
       }
 #pragma unroll
       for (int i = 0; i < 2; ++i)
-        if (e[i] >= 0) s[i] = expf(lv[i] - top);
+        if (i < nslot && e[i] >= 0) s[i] = expf(lv[i] - top);
       if (p.renormalize) total = warp_sum(s[0] + s[1]);
 #pragma unroll
       for (int i = 0; i < 2; ++i)
-        if (e[i] >= 0) s[i] /= total;
+        if (i < nslot && e[i] >= 0) s[i] /= total;
       const float inner = warp_sum(s[0] * dw[0] + s[1] * dw[1]);
-      const bool any = __any_sync(0xffffffffu, e[0] >= 0 || e[1] >= 0);
-      if (!p.renormalize && any) dense = -p.scale * inner / total;
+      if (!p.renormalize && __any_sync(0xffffffffu, e[0] >= 0 || e[1] >= 0))
+        dense = -p.scale * inner / total;
 #pragma unroll
       for (int i = 0; i < 2; ++i)
         d[i] = p.scale * s[i] * (dw[i] - (p.renormalize ? inner : 0.f));
