@@ -25,8 +25,8 @@ LIBDIR = os.path.join(PKG, "_lib")
 LIB = os.path.join(LIBDIR, "libqmoe.so")
 BINDING = os.path.join(LIBDIR, "qmoe_torch.so")
 
-SOURCES = ["api.cu", "route.cu", "misc.cu", "gemm.cu", "gemm2.cu", "api_ops.cu", "gate.cu", "tokens.cu",
-           "lora.cu"]
+SOURCES = ["api.cu", "route.cu", "misc.cu", "gemm.cu", "gemm2.cu", "api_ops.cu", "gate.cu",
+           "tokens.cu", "lora.cu", "lora_shrink.cu", "lora_gemm.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
