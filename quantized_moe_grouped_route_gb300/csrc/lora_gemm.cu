@@ -140,7 +140,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   grid_dep_launch();
   tc_fence_before();
   __syncthreads();
-  if (clustered) cluster_sync_all();  // the peer's barriers exist before any remote arrival
+  if (CG == 2) cluster_sync_all();  // the peer's barriers exist before any remote arrival
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
@@ -612,34 +612,44 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     const int m0 = tile * p.tile_n, cols = min(p.tile_n, p.M - m0);
     const int n = (block * CG + (int)rank) * 128 + 4 * lane;
     const uint32_t sums0 = smem_u32(smem) + 16 * lane;
-    for (int c = seg + S * warp; c < cols; c += S * (kGemmThreads / 32)) {
-      float4 v[kMaxSplits];
+    constexpr int kAtOnce = 2;  // tokens a warp
+    const int stride = S * (kGemmThreads / 32);
+    for (int c0 = seg + S * warp; c0 < cols; c0 += kAtOnce * stride) {
+      float4 v[kAtOnce][kMaxSplits];
 #pragma unroll
-      for (int g = 0; g < kMaxSplits; ++g)
-        if (g < S) v[g] = ld_cluster_f32x4(peer_addr(sums0 + c * 512, g * CG + rank));
-      float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int u = 0; u < kAtOnce; ++u)
 #pragma unroll
-      for (int g = 0; g < kMaxSplits; ++g)
-        if (g < S) t.x += v[g].x, t.y += v[g].y, t.z += v[g].z, t.w += v[g].w;
-      if constexpr (VEC) {
-        const float4 d = reinterpret_cast<const float4*>(delta + c / S * 128)[lane];
-        t.x += d.x, t.y += d.y, t.z += d.z, t.w += d.w;
-      }
-      float f[4] = {t.x, t.y, t.z, t.w};
-      const T* base = reinterpret_cast<const T*>(p.base) + (size_t)(m0 + c) * p.ldbase + n;
-      T* out = reinterpret_cast<T*>(p.out) + (size_t)(m0 + c) * p.N + n;
-      Pack<T, 4> o;
+        for (int g = 0; g < kMaxSplits; ++g)
+          if (g < S && c0 + u * stride < cols)
+            v[u][g] = ld_cluster_f32x4(peer_addr(sums0 + (c0 + u * stride) * 512, g * CG + rank));
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if (p.base && n + e < p.N) f[e] += to_f32(base[e]);
-        o.v[e] = from_f32<T>(f[e]);
-      }
-      if (p.wide && n < p.N) {
-        *reinterpret_cast<uint2*>(out) = o.raw;
-      } else {
+      for (int u = 0; u < kAtOnce; ++u) {
+        const int c = c0 + u * stride;
+        if (c >= cols) break;
+        float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (n + e < p.N) out[e] = o.v[e];
+        for (int g = 0; g < kMaxSplits; ++g)
+          if (g < S) t.x += v[u][g].x, t.y += v[u][g].y, t.z += v[u][g].z, t.w += v[u][g].w;
+        if constexpr (VEC) {
+          const float4 d = reinterpret_cast<const float4*>(delta + c / S * 128)[lane];
+          t.x += d.x, t.y += d.y, t.z += d.z, t.w += d.w;
+        }
+        float f[4] = {t.x, t.y, t.z, t.w};
+        const T* base = reinterpret_cast<const T*>(p.base) + (size_t)(m0 + c) * p.ldbase + n;
+        T* out = reinterpret_cast<T*>(p.out) + (size_t)(m0 + c) * p.N + n;
+        Pack<T, 4> o;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if (p.base && n + e < p.N) f[e] += to_f32(base[e]);
+          o.v[e] = from_f32<T>(f[e]);
+        }
+        if (p.wide && n < p.N) {
+          *reinterpret_cast<uint2*>(out) = o.raw;
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (n + e < p.N) out[e] = o.v[e];
+        }
       }
     }
     cluster_sync_all();  // no CTA leaves while its sums may still be read
