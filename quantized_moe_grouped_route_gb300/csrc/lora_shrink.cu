@@ -89,14 +89,16 @@ __global__ void __launch_bounds__(kShrinkMost) lora_shrink_kernel(const LoraArgs
     publish_list(p, t, list, n, mine, bad);
     return;
   }
-  __shared__ float part[kWarps][8];
+  __shared__ float part[8][kWarps + 1];
   using P_ = Pack<T, 8>;
   const int groups = p.R / 8;
   const long long it = (long long)blockIdx.x - p.tiles;
   const int m = (int)(it / groups), r0 = (int)(it % groups) * 8;
   const int id = p.ids[m];
+  const bool has = id >= 0 && id < p.L;
+  const float scale = has ? p.scales[id] : 0.f;
   float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  if (id >= 0 && id < p.L) {
+  if (has) {
     const uint4* x = reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(p.x) + m * p.ldx);
     const uint4* a =
         reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(p.a) + ((size_t)id * p.R + r0) * p.K);
@@ -116,13 +118,14 @@ __global__ void __launch_bounds__(kShrinkMost) lora_shrink_kernel(const LoraArgs
   for (int r = 0; r < 8; ++r) {
 #pragma unroll
     for (int o = 16; o; o >>= 1) acc[r] += __shfl_xor_sync(0xffffffffu, acc[r], o);
-    if (lane == 0) part[warp][r] = acc[r];
+    if (lane == 0) part[r][warp] = acc[r];
   }
   __syncthreads();
-  if (tid < 8) {
-    float s = 0.f;
-    for (int w = 0; w < (int)(blockDim.x >> 5); ++w) s += part[w][tid];
-    if (id >= 0 && id < p.L) p.t[(size_t)m * p.R + r0 + tid] = s * p.scales[id];
+  if (warp < 8) {  // a warp per rank: at least 8 warps a block, at most 32
+    float s = lane < (int)(blockDim.x >> 5) ? part[warp][lane] : 0.f;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (lane == 0 && has) p.t[(size_t)m * p.R + r0 + warp] = s * scale;
   }
 }
 
