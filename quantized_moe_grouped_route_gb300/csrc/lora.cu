@@ -54,16 +54,17 @@ namespace {
 
 // --------------------------------------------------------------------- one or two tokens
 // One, two or four warps (WPR, the more, the longer the row) per row of w: its product with
-// up to MT token rows in fp32, w in 16-byte loads of which a lane has about eight in all, in
-// flight together (one warp a row, 28 loads a lane at K = 7168, took 9.4 us); then the row
-// of each token's B with t.  HBM (or L2) bound, and there is nothing to set up: the tensor-core kernel spends 5 of its
-// 10.3 us at M = 1, K = 7168, N = 2048 on barriers, TMEM, the cluster and the last sums.
-// Whole calls at K = 7168, N = 2048, R = 16: one token 9.7 us (tensor cores 11.4), two 10.9
-// (11.9), four 16.0 (12.0).
+// up to MT token rows in fp32, then the row of each token's B with t.  HBM (or L2) bound, and
+// there is nothing to set up: the tensor-core kernel spends 5 of its 10.3 us at M = 1,
+// K = 7168, N = 2048 on barriers, TMEM, the cluster and the last sums.  What hides the loads'
+// latency is warps, not loads a warp: with few registers all rows of that size are resident
+// at once (two loads in flight a lane, 16 blocks an SM: 7.1 us a call; eight loads, 8
+// blocks: 9.6; for two tokens three loads and 8 blocks: 9.7, six: 12.4).  On the tensor cores
+// one token takes 11.4 us, two 11.9, four 12.0 (here 16.0).
 constexpr int kGemvThreads = 128;
 
 template <class T, int MT, int WPR>
-__global__ void __launch_bounds__(kGemvThreads) lora_gemv_kernel(const LoraArgs p) {
+__global__ void __launch_bounds__(kGemvThreads, MT == 1 ? 16 : 8) lora_gemv_kernel(const LoraArgs p) {
   using P_ = Pack<T, 8>;
   __shared__ float part[kGemvThreads / 32][MT];
   grid_dep_launch();
@@ -87,7 +88,7 @@ __global__ void __launch_bounds__(kGemvThreads) lora_gemv_kernel(const LoraArgs 
     const uint4* w = reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(p.w) + (size_t)n * p.K);
     const T* x = reinterpret_cast<const T*>(p.x);
     const int chunks = p.K / 8;
-    constexpr int kFlight = MT == 1 ? 8 : 6;
+    constexpr int kFlight = MT == 1 ? 2 : 3;
     for (int c0 = sub * 32 + lane; c0 < chunks; c0 += 32 * WPR * kFlight) {
       P_ wv[kFlight];
 #pragma unroll
