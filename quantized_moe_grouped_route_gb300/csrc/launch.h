@@ -211,7 +211,7 @@ struct LoraArgs : LoraPlan {
   float* t;    // [tsplits][M][R] scales[a] * (x . A^T) over a segment of K
 };
 cudaError_t launch_lora(LoraArgs& p, int num_sms, cudaStream_t stream);
-// its two steps (the second for more than two tokens): lora_shrink.cu, lora_gemm.cu
+// its two steps (the second for more than eight tokens): lora_shrink.cu, lora_gemm.cu
 cudaError_t launch_lora_shrink(const LoraArgs& p, int num_sms, cudaStream_t stream);
 cudaError_t launch_lora_gemm(LoraArgs& p, int num_sms, cudaStream_t stream);
 

@@ -13,7 +13,6 @@ constexpr int kAccCols = 256;       // TMEM columns of one accumulator
 constexpr int kSmemLimit = 232448;
 constexpr int kMostTokens = 240;    // of a tile: five stages of the GEMM's ring; 256 leave room for four
 constexpr int kShrinkSegments = 8;  // of K in the tensor-core shrink, at most
-constexpr int kGemvTokens = 2;      // that run as plain products
 
 // Ranks r .. r + 7 of a token's t, over the shrink's segments of K in order.
 __device__ __forceinline__ void load_t8(const LoraArgs& p, int m, int r, float (&t)[8]) {

@@ -535,7 +535,10 @@ LORAS_WIDE = [
     (2047, 1096, 512, 48, 11, True, False, "runs"), (60, 256, 20000, 64, 40, True, True, "mixed"),
     (31, 512, 160, 128, 31, True, False, "mixed"), (2, 2056, 77, 128, 2, True, True, "mixed"),
     (4, 4104, 130, 72, 9, True, False, "mixed"), (3, 1544, 5, 32, 2, False, False, "mixed"),
-    (1, 16384, 40, 64, 3, True, True, "runs"), (64, 1024, 30000, 16, 60, True, False, "mixed"), (700, 968, 200, 128, 3, True, False, "none"),
+    (1, 16384, 40, 64, 3, True, True, "runs"), (8, 4104, 77, 128, 9, True, True, "mixed"),
+    (7, 40, 17, 8, 3, True, False, "mixed"), (5, 16400, 31, 24, 2, True, False, "runs"),
+    (8, 8200, 4099, 64, 30, True, False, "mixed"), (6, 2048, 100, 40, 5, False, True, "mixed"),
+    (2, 8192, 48, 128, 2, True, False, "none"), (64, 1024, 30000, 16, 60, True, False, "mixed"), (700, 968, 200, 128, 3, True, False, "none"),
 ]
 
 
