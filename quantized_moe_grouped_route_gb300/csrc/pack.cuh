@@ -60,6 +60,26 @@ __device__ __forceinline__ uint4 load_if(const uint4* p, bool there) {
   return v;
 }
 
+// The same for 8 and 4 bytes; neighbouring rows' chunks share sectors, so they may stay in L1.
+__device__ __forceinline__ uint2 load_if(const uint2* p, bool there) {
+  uint2 v;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %3, 0;\n\tmov.u32 %0, 0;\n\tmov.u32 %1, 0;\n\t"
+      "@p ld.global.v2.u32 {%0, %1}, [%2];\n\t}"
+      : "=&r"(v.x), "=&r"(v.y)
+      : "l"(p), "r"((int)there));
+  return v;
+}
+__device__ __forceinline__ uint32_t load_if(const uint32_t* p, bool there) {
+  uint32_t v;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\tmov.u32 %0, 0;\n\t"
+      "@p ld.global.u32 %0, [%1];\n\t}"
+      : "=&r"(v)
+      : "l"(p), "r"((int)there));
+  return v;
+}
+
 // N consecutive elements of type T, moved in one access.
 template <class T, int N>
 union Pack {

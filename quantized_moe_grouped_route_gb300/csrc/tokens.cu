@@ -171,10 +171,10 @@ __global__ void __launch_bounds__(kTokThreads)
         wk[k] = !has ? 0.f : WEIGHTED ? w[slot0 + k0 + k] : 1.f;
 #pragma unroll
         for (int j = 0; j < kPer; ++j) {
-          if constexpr (sizeof(R_) == 16) {
+          if constexpr (sizeof(R_) >= 4) {
             const T* at = y + (has ? (size_t)pos * ldy + (size_t)(c0 + 32 * j) * N : 0);
             v[k][j].raw = load_if(reinterpret_cast<const R_*>(at), has && c0 + 32 * j < chunks);
-          } else {
+          } else {  // (two bytes: behind a branch 3.8 us for the 1001-wide rows, so 4.8)
             v[k][j].raw = R_{};
             if (has && c0 + 32 * j < chunks)
               v[k][j].raw = *reinterpret_cast<const R_*>(y + (size_t)pos * ldy +
@@ -200,8 +200,16 @@ __global__ void __launch_bounds__(kTokThreads)
   }
 }
 
-// A block per token: its gradient row is read once per eight slots (later reads hit L1),
+template <class T, int N>
+__host__ __device__ constexpr int backward_chunks() {
+  return N == 1 ? 1 : chunks_per_lane<T, N>();
+}
+
+// A block per token: its gradient row is read once per batch of slots (later reads hit L1),
 // each slot's row of y once; the dot products are reduced over the block in a fixed order.
+// A thread takes kPer chunks of each of kBatch slots at a time: several of 4 or 8 bytes
+// (4096 tokens of 1002 fp16, 8 slots: 46.8 -> 30.3 us), one of 16 bytes or of one element
+// (1001: 46.4 us against 60.4).
 template <class T, int N>
 __global__ void __launch_bounds__(kTokThreads)
     unsort_backward_kernel(const T* __restrict__ dout, long long ldd, const T* __restrict__ y,
@@ -212,7 +220,8 @@ __global__ void __launch_bounds__(kTokThreads)
   using R_ = typename P_::raw_t;
   grid_dep_wait();
   grid_dep_launch();
-  constexpr int kBatch = 8, kWarps = kTokThreads / 32;
+  constexpr int kPer = backward_chunks<T, N>(), kBatch = kPer == 1 ? 8 : 4;
+  constexpr int kWarps = kTokThreads / 32;
   __shared__ float part[kWarps][kBatch];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const unsigned P = (unsigned)(M * top_k);
@@ -228,24 +237,41 @@ __global__ void __launch_bounds__(kTokThreads)
         wk[k] = k0 + k < top_k ? w[i] : 0.f;
         acc[k] = 0.f;
       }
-      for (int c = threadIdx.x; c < chunks; c += blockDim.x) {
-        P_ g, v[kBatch];
-        g.raw = *reinterpret_cast<const R_*>(d + (size_t)c * N);
+      for (int c0 = threadIdx.x; c0 < chunks; c0 += kPer * blockDim.x) {
+        P_ g[kPer], v[kBatch][kPer];
 #pragma unroll
-        for (int k = 0; k < kBatch; ++k)
-          if ((unsigned)pos[k] < P)
-            v[k].raw = *reinterpret_cast<const R_*>(y + (size_t)pos[k] * ldy + (size_t)c * N);
+        for (int j = 0; j < kPer; ++j) {
+          const int c = c0 + j * blockDim.x;
+          const bool in = c < chunks;
+          g[j].raw = *reinterpret_cast<const R_*>(d + (in ? (size_t)c * N : 0));
 #pragma unroll
-        for (int k = 0; k < kBatch; ++k) {
-          if ((unsigned)pos[k] >= P) continue;
-          P_ o;
-#pragma unroll
-          for (int i = 0; i < N; ++i) {
-            const float gi = to_f32(g.v[i]);
-            acc[k] = fmaf(gi, to_f32(v[k].v[i]), acc[k]);
-            o.v[i] = from_f32<T>(wk[k] * gi);
+          for (int k = 0; k < kBatch; ++k) {
+            if constexpr (kPer == 1) {
+              if ((unsigned)pos[k] < P)
+                v[k][j].raw = *reinterpret_cast<const R_*>(y + (size_t)pos[k] * ldy + (size_t)c * N);
+            } else {  // an element of row 0 stands in for one that is not there
+              const bool there = in && (unsigned)pos[k] < P;
+              v[k][j].raw =
+                  *reinterpret_cast<const R_*>(y + (there ? (size_t)pos[k] * ldy + (size_t)c * N : 0));
+            }
           }
-          *reinterpret_cast<R_*>(dy + ((size_t)pos[k] * chunks + c) * N) = o.raw;
+        }
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) {
+          const int c = c0 + j * blockDim.x;
+          if (c >= chunks) break;
+#pragma unroll
+          for (int k = 0; k < kBatch; ++k) {
+            if ((unsigned)pos[k] >= P) continue;
+            P_ o;
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+              const float gi = to_f32(g[j].v[i]);
+              acc[k] = fmaf(gi, to_f32(v[k][j].v[i]), acc[k]);
+              o.v[i] = from_f32<T>(wk[k] * gi);
+            }
+            *reinterpret_cast<R_*>(dy + ((size_t)pos[k] * chunks + c) * N) = o.raw;
+          }
         }
       }
 #pragma unroll
@@ -324,7 +350,8 @@ cudaError_t unsort(const TokenArgs& a, int num_sms, cudaStream_t stream) {
 template <class T, int N>
 cudaError_t unsort_backward(const TokenArgs& a, int num_sms, cudaStream_t stream) {
   const int chunks = a.H / N;
-  int threads = (chunks + 31) / 32 * 32;
+  constexpr int kPer = backward_chunks<T, N>();
+  int threads = ((chunks + kPer - 1) / kPer + 31) / 32 * 32;
   if (threads > kTokThreads) threads = kTokThreads;
   long long blocks = a.M;
   if (blocks > num_sms * 64LL) blocks = num_sms * 64LL;
