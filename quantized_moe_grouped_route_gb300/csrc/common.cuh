@@ -354,17 +354,20 @@ __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N) {
          | ((uint32_t)(M >> 4) << 24);          // M / 16
 }
 
-// Shared-memory matrix descriptor for a K-major operand in the 128-byte swizzled
-// layout (rows of 128 bytes, 8-row groups 1024 bytes apart, groups 1024-aligned).
-__device__ __forceinline__ uint64_t sdesc_sw128(uint32_t saddr) {
+// Shared-memory matrix descriptor for a K-major operand in the swizzled layout of its row
+// length: rows of 128, 64 or 32 bytes, groups of 8 rows one after another, and the operand
+// on a boundary of a group's length.
+__device__ __forceinline__ uint64_t sdesc_swizzled(uint32_t saddr, int row_bytes) {
   uint64_t d = 0;
   d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);   // start address
   d |= (uint64_t)1 << 16;                      // leading byte offset (unused here) = 16 B
-  d |= (uint64_t)(1024 >> 4) << 32;            // stride byte offset = 1024 B
+  d |= (uint64_t)(8 * row_bytes >> 4) << 32;   // stride byte offset: a group of 8 rows
   d |= (uint64_t)1 << 46;                      // descriptor version
-  d |= (uint64_t)2 << 61;                      // 128-byte swizzle
+  d |= (uint64_t)(row_bytes == 128 ? 2 : row_bytes == 64 ? 4 : 6) << 61;  // swizzle
   return d;
 }
-
+__device__ __forceinline__ uint64_t sdesc_sw128(uint32_t saddr) {
+  return sdesc_swizzled(saddr, 128);
+}
 
 }  // namespace qmoe

@@ -1,5 +1,6 @@
 // The GEMM of the projection with adapters (lora.cu describes it).
 #include <atomic>
+#include <type_traits>
 
 #include "cluster.cuh"
 #include "lora.cuh"
@@ -10,15 +11,23 @@ namespace {
 constexpr int kBuilders = 8;  // warps
 constexpr int kGemmThreads = 256 + 32 * kBuilders;
 constexpr int kMaxStages = 12;
-constexpr int kCtrl = 1024;
+constexpr int kCtrl = 2048;
 constexpr int kEpiStage = 4 * 2048;  // transpose tiles of the epilogue warps: 32 tokens x 32 rows
 constexpr int kMaxSplits = 8;  // CTAs of a cluster, at most
 
-// Bytes of one step of a CTA's token rows; slots of the builders' operand (two of them
-// each: t rounded, and the rest), fewer the wider the tile.
+// Bytes of one step of a CTA's token rows.
 __host__ __device__ constexpr int token_bytes(int tile_n, int cg) { return tile_n / cg * 128; }
-__host__ __device__ constexpr int token_slots(int tile_n, int cg) {
-  return tile_n / cg <= 48 ? 8 : tile_n / cg <= 64 ? 4 : 2;
+// The builders' operand (two of them a slot: t rounded, and the rest) has rows as long as an
+// adapter's ranks ask for, in the swizzle of that length, so that more adapters are in the
+// making where their steps are short (256 tokens of 64 adapters, K = N = 4096, R = 16: 33.4 us
+// a call, with rows of 128 bytes 38.4; 2047 tokens of a few requests, R = 32: 54.1 and 57.6).
+__host__ __device__ constexpr int t_pitch(int R) { return R <= 16 ? 32 : R <= 32 ? 64 : 128; }
+__host__ __device__ constexpr int t_bytes(int tile_n, int cg, int R) {
+  return tile_n / cg * t_pitch(R);
+}
+__host__ __device__ constexpr int token_slots(int tile_n, int cg, int R) {
+  const int bytes = t_bytes(tile_n, cg, R);
+  return bytes <= 48 * 128 ? 8 : bytes <= 64 * 128 ? 4 : 2;
 }
 // The builders' copy of t for a CTA's token rows (both values), where it takes up to 16 KB:
 // every row enters one adapter's step, and the steps then build from shared memory what
@@ -48,7 +57,7 @@ __host__ __device__ constexpr Behind behind(bool vec, int tile_n, int cg, int R)
     b.copy = round_kb(tile_n * R * 4);
     b.delta = tile_n * 512;
   } else {
-    b.slots = 2 * token_slots(tile_n, cg) * token_bytes(tile_n, cg);
+    b.slots = round_kb(2 * token_slots(tile_n, cg, R) * t_bytes(tile_n, cg, R));
     b.copy = round_kb(t_copy_bytes(tile_n, cg, R));
   }
   return b;
@@ -74,9 +83,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   const int bytes_b = token_bytes(p.tile_n, CG);
   const int stage_bytes = kStageA + bytes_b;
   const int stages = p.stages;
-  const int tslots = VEC ? vec_slots(p.R) : token_slots(p.tile_n, CG);
+  const int tslots = VEC ? vec_slots(p.R) : token_slots(p.tile_n, CG, p.R);
+  const int pitch = t_pitch(p.R), half_slot = t_bytes(p.tile_n, CG, p.R);
   const Behind behind_ring = behind(VEC, p.tile_n, CG, p.R);
-  uint8_t* tbuf = smem + stages * stage_bytes;  // [tslots][2][bytes_b]; VEC [tslots][128][R]
+  uint8_t* tbuf = smem + stages * stage_bytes;  // [tslots][2][rows_b][pitch]; VEC [tslots][128][R]
   uint8_t* tcopy = tbuf + behind_ring.slots;    // [rows_b][2][R]; VEC fp32 [rows_b][R]
   const int copy_bytes = t_copy_bytes(p.tile_n, CG, p.R);
   float* delta = reinterpret_cast<float*>(tcopy + behind_ring.copy);  // VEC [tokens][128]
@@ -94,6 +104,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(dempty + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   short* place = reinterpret_cast<short*>(ctrl + 512);  // [rows_b] the tokens' adapters
+  uint8_t* listed = ctrl + 1024;                        // [kBuilders][128] the builders' lists
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // a cluster: S segments of CG CTAs
@@ -250,7 +261,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       const uint32_t lead = elect_one();
       const uint32_t idesc = idesc_16bit(128 * CG, p.tile_n, p.dtype);
       const uint64_t desc0 = sdesc_sw128(smem_u32(smem));
-      const uint32_t t0 = (uint32_t)(tbuf - smem) >> 4;
+      const uint64_t tdesc0 = sdesc_swizzled(smem_u32(tbuf), pitch);
       uint32_t s = 0, ph = 0, ts = 0, tph = 0, local = 0;
       bool ok = true;
       auto commit = [&](uint64_t* bar) {
@@ -300,7 +311,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             }
             tc_fence_after();
             const uint64_t a = desc0 + ((s * stage_bytes) >> 4);
-            const uint64_t hi = desc0 + t0 + ((2 * ts * bytes_b) >> 4), lo = hi + (bytes_b >> 4);
+            const uint64_t hi = tdesc0 + ((2 * ts * half_slot) >> 4), lo = hi + (half_slot >> 4);
             if (lead)
               for (int j = 0; j < slices; ++j) {
                 mma_ss(CG, dst, a + 2 * j, hi + 2 * j, idesc, acc | (j > 0));
@@ -429,48 +440,76 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     }
   } else if (warp >= 8) {
     // ------------------------------------------------------------------- builders
-    // step i goes to the warps of slot i % tslots
-    const int group = kBuilders / tslots;
-    const int own = (warp - 8) / group;
-    const int tid = (warp - 8) % group * 32 + lane;
-    uint8_t* const dst = tbuf + 2 * own * bytes_b;
-    uint32_t step = 0, tph = 1;
-    bool ok = true;
-    const uint32_t tfull0 = CG == 2 ? peer_addr(smem_u32(tfull), lead_rank) : smem_u32(tfull);
-    // (after a wait that gave up a warp still meets the others at their barriers)
-    for (int i = worker; i < units; i += workers) {
-      const int tile = i / p.blocks;
-      const int n = adapters(tile);
-      const int m0 = tile * p.tile_n + (int)rank * rows_b;
-      if (seg >= n) continue;    // the same for all builders
-      builders_sync();           // the previous unit's rows have been used
-      for (int r = threadIdx.x - 256; r < rows_b; r += 32 * kBuilders)
-        place[r] = (short)p.place[(size_t)m0 + r];
-      if (copy_bytes) {
-        const int eights = p.R / 8;
-        for (int u = threadIdx.x - 256; u < rows_b * eights; u += 32 * kBuilders) {
-          const int row = u / eights, r = u % eights * 8;
-          if (m0 + row >= p.M) break;
-          T* dst = reinterpret_cast<T*>(tcopy) + row * 2 * p.R + r;
-          load_t8_split<T>(p, m0 + row, r, reinterpret_cast<uint4*>(dst),
-                           reinterpret_cast<uint4*>(dst + p.R));
-        }
-      }
-      builders_sync();
-      for (int d = seg; d < n && ok; d += S) {
-        for (int h = 0; h < chunks; ++h, ++step) {
-          if ((int)(step % tslots) != own) continue;
-          const int units = (min(64, p.R - h * 64) + 15) / 16 * 2;  // 16-byte units of a row
-          if (!wait(&tempty[own], tph)) {
-            ok = false;
-            break;
+    // Step i goes to the warps of slot i % tslots, 32 of its rows a warp at a time.  Of a slot
+    // only the rows of the step's adapter are written, and those of the step before it that
+    // it has not are cleared: with an adapter a token a step is a row or two (128 tokens of 64
+    // adapters, K = N = 4096, R = 64: 33.2 us a call, writing whole slots 42.7).  A lane's first
+    // ranks of t are on their way before the slot is free.  This chain of instructions is what
+    // a step costs, hence the row lengths at compile time (R = 128: 124 us, at run time 144).
+    auto build = [&](auto log_units) {
+      const int group = kBuilders / tslots;
+      const int own = (warp - 8) / group, part = (warp - 8) % group;
+      uint8_t* const slot = tbuf + 2 * own * half_slot;
+      constexpr int LG = decltype(log_units)::value, kUnits = 1 << LG;  // of 16 bytes a row
+      constexpr int kWords = LG == 3 ? 2 : LG == 2 ? 3 : 4;  // 32 rows each, by the slots' sizes
+      constexpr int kPitch = 16 << LG;
+      uint8_t* const rows = listed + (warp - 8) * 128;  // this warp's rows of a step
+      unsigned held[kWords] = {};                    // rows in the slot that are not zero,
+      int held_units = 0;                               // and how many units of 16 bytes they have
+      auto row0 = [&](int w) { return 32 * (part + w * group); };
+      // a row's units of 16 bytes, swizzled by the 128-byte line that it is in
+      auto put = [&](int row, int j, uint4 hi, uint4 lo) {
+        uint8_t* at = slot + row * kPitch + ((j ^ (row >> (3 - LG) & (kUnits - 1))) << 4);
+        *reinterpret_cast<uint4*>(at) = hi;
+        *reinterpret_cast<uint4*>(at + half_slot) = lo;
+      };
+      const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+      for (int w = 0; row0(w) < rows_b; ++w)
+        for (int u = lane; u < 32 * kUnits; u += 32)
+          if (row0(w) + u / kUnits < rows_b)
+            put(row0(w) + u / kUnits, u % kUnits, zero, zero);
+      uint32_t step = 0, tph = 1;
+      bool ok = true;
+      const uint32_t tfull0 = CG == 2 ? peer_addr(smem_u32(tfull), lead_rank) : smem_u32(tfull);
+      // (after a wait that gave up a warp still meets the others at their barriers)
+      for (int i = worker; i < units; i += workers) {
+        const int tile = i / p.blocks;
+        const int n = adapters(tile);
+        const int m0 = tile * p.tile_n + (int)rank * rows_b;
+        if (seg >= n) continue;    // the same for all builders
+        builders_sync();           // the previous unit's rows have been used
+        for (int r = threadIdx.x - 256; r < rows_b; r += 32 * kBuilders)
+          place[r] = (short)p.place[(size_t)m0 + r];
+        if (copy_bytes) {
+          const int eights = p.R / 8;
+          for (int u = threadIdx.x - 256; u < rows_b * eights; u += 32 * kBuilders) {
+            const int row = u / eights, r = u % eights * 8;
+            if (m0 + row >= p.M) break;
+            T* dst = reinterpret_cast<T*>(tcopy) + row * 2 * p.R + r;
+            load_t8_split<T>(p, m0 + row, r, reinterpret_cast<uint4*>(dst),
+                             reinterpret_cast<uint4*>(dst + p.R));
           }
-          tph ^= 1;
-          for (int u = tid; u < rows_b * units; u += group * 32) {
-            const int row = u / units, j = u - row * units;
-            const int r = h * 64 + j * 8;
-            uint4 hi = make_uint4(0u, 0u, 0u, 0u), lo = hi;
-            if (place[row] == d && r < p.R) {
+        }
+        builders_sync();
+        for (int d = seg; d < n && ok; d += S) {
+          for (int h = 0; h < chunks; ++h, ++step) {
+            if ((int)(step % tslots) != own) continue;
+            const int units = min(64, p.R - h * 64) / 8;  // of a row, with ranks in them
+            unsigned now[kWords];
+            int found = 0;
+  #pragma unroll
+            for (int w = 0; w < kWords; ++w) {
+              const int row = row0(w) + lane;
+              const bool in = row < rows_b && place[row] == d;
+              now[w] = __ballot_sync(0xffffffffu, in);
+              if (in) rows[found + __popc(now[w] & ((1u << lane) - 1u))] = (uint8_t)row;
+              found += __popc(now[w]);
+            }
+            __syncwarp();
+            found *= kUnits;
+            uint4 hi, lo;
+            auto fetch = [&](int u) {
+              const int row = rows[u / kUnits], r = h * 64 + u % kUnits * 8;
               if (copy_bytes) {
                 const T* src = reinterpret_cast<const T*>(tcopy) + row * 2 * p.R + r;
                 hi = *reinterpret_cast<const uint4*>(src);
@@ -478,23 +517,45 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
               } else {
                 load_t8_split<T>(p, m0 + row, r, &hi, &lo);
               }
+            };
+            const bool mine = lane % kUnits < units;  // (32 is a multiple of kUnits)
+            if (mine && lane < found) fetch(lane);
+            if (!wait(&tempty[own], tph)) {
+              ok = false;
+              break;
             }
-            // rows of 128 bytes, 16-byte units swizzled by the row (128-byte swizzle)
-            uint8_t* at = dst + row * 128 + ((j ^ (row & 7)) << 4);
-            *reinterpret_cast<uint4*>(at) = hi;
-            *reinterpret_cast<uint4*>(at + bytes_b) = lo;
-          }
-          fence_proxy_async();
-          __syncwarp();
-          if (lane == 0) {
-            if (CG == 2 && rank != 0)
-              mbar_arrive_remote(tfull0 + own * 8);
-            else
-              mbar_arrive(smem_u32(&tfull[own]));
+            tph ^= 1;
+  #pragma unroll
+            for (int w = 0; w < kWords; ++w) {
+              unsigned left = held_units > units ? held[w] : held[w] & ~now[w];
+              for (; left; left &= left - 1)
+                if (lane < kUnits) put(row0(w) + __ffs(left) - 1, lane, zero, zero);
+              held[w] = now[w];
+            }
+            held_units = units;
+            __syncwarp();
+            for (int u = lane; mine && u < found; u += 32) {
+              if (u != lane) fetch(u);
+              put(rows[u / kUnits], u % kUnits, hi, lo);
+            }
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) {
+              if (CG == 2 && rank != 0)
+                mbar_arrive_remote(tfull0 + own * 8);
+              else
+                mbar_arrive(smem_u32(&tfull[own]));
+            }
           }
         }
       }
-    }
+    };
+    if (pitch == 32)
+      build(std::integral_constant<int, 1>{});
+    else if (pitch == 64)
+      build(std::integral_constant<int, 2>{});
+    else
+      build(std::integral_constant<int, 3>{});
   } else if (warp >= 4) {
     // ------------------------------------------------------------------- epilogue
     const int q = warp & 3;

@@ -542,9 +542,19 @@ LORAS_WIDE = [
 ]
 
 
+# many adapters a tile, in every length of the tensor-core operand's rows, over several tiles a
+# CTA; ranks that end inside a step of 64, or inside the 16 of an MMA
+LORAS_MANY = [
+    (128, 256, 1100, 16, 90, True, False, "mixed"), (120, 72, 300, 8, 40, True, True, "mixed"),
+    (480, 136, 20000, 72, 30, True, False, "mixed"), (600, 128, 12000, 24, 60, True, False, "mixed"),
+    (400, 128, 16000, 8, 20, True, False, "runs"), (250, 64, 700, 32, 200, False, True, "mixed"),
+    (1000, 64, 9000, 40, 12, True, False, "mixed"), (48, 128, 500, 104, 30, True, False, "mixed"),
+]
+
+
 @gpu
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
-@pytest.mark.parametrize("M,K,N,R,L,with_w,with_base,how", LORAS + LORAS_WIDE)
+@pytest.mark.parametrize("M,K,N,R,L,with_w,with_base,how", LORAS + LORAS_WIDE + LORAS_MANY)
 def test_lora_linear(M, K, N, R, L, with_w, with_base, how, dtype):
     g = _gen(M * 3 + K)
     x = _rows(g, M, K, dtype, pad=8)
@@ -593,6 +603,28 @@ def test_lora_linear(M, K, N, R, L, with_w, with_base, how, dtype):
         inout = base.contiguous()
         q.qmoe_lora_linear(x, w, a, b, ids, s, base=inout, out=inout)
         assert torch.equal(inout, out)
+
+
+@gpu
+@pytest.mark.parametrize("M,R", [(20, 16), (100, 16), (128, 32), (70, 64), (300, 24), (260, 120)])
+def test_lora_token_of_infinities_stays_alone(M, R):
+    """A token whose x A^T is infinite or NaN spoils its own row and no other."""
+    K, N, L = 128, 1500, 12
+    g = _gen(M + R)
+    x = _rows(g, M, K, torch.bfloat16)
+    w = _rows(g, N, K, torch.bfloat16)
+    a, b = _rows(g, L * R, K, torch.bfloat16), _rows(g, L * N, R, torch.bfloat16)
+    s = torch.ones(L, device="cuda")
+    ids = torch.randint(0, L, (M,), generator=g, device="cuda", dtype=torch.int32)
+    args = (w, a.view(L, R, K), b.view(L, N, R), ids, s)
+    good = q.qmoe_lora_linear(x, *args)
+    at = torch.arange(3, M, 7, device="cuda")
+    x[at[::2], 5], x[at[1::2], 5] = math.inf, math.nan
+    out = q.qmoe_lora_linear(x, *args)
+    keep = torch.ones(M, dtype=torch.bool, device="cuda")
+    keep[at] = False
+    assert torch.equal(out[keep], good[keep])
+    assert not torch.isfinite(out[at]).any()
 
 
 @gpu
