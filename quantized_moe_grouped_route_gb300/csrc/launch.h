@@ -181,7 +181,7 @@ cudaError_t launch_unsort_backward(const TokenArgs& a, int dtype, int chunk, int
                                    cudaStream_t stream);
 
 // lora.cu
-// How a problem is cut: token tiles of tile_n (a multiple of 16, at most 240), units of one
+// How a problem is cut: token tiles of tile_n (a multiple of 16, at most 256), units of one
 // tile x 128 * cg rows of w (cg: CTAs per unit), each of ksteps steps of 64 of K; the shrink
 // with plain products or on the tensor cores, in tsplits segments of K.
 struct LoraPlan {

@@ -6,7 +6,7 @@
 // cores for many) forms t in fp32 and lists, for each tile of tokens, the distinct adapters
 // its tokens use.  The second (lora_gemm.cu) is one GEMM whose contraction runs over K and
 // then over the ranks of the tile's adapters: the MMA's M side
-// is 128 rows of w (or of B[a]), its N side a tile of up to 240 tokens, and for each of
+// is 128 rows of w (or of B[a]), its N side a tile of up to 256 tokens, and for each of
 // the tile's adapters the token operand is t with the rows of other adapters zero.  So the
 // adapters cost a tile (distinct adapters) * ranks more of contraction length, whatever
 // the order of the tokens, and the result is rounded once.  (A zero row times an infinity
@@ -274,6 +274,7 @@ LoraPlan lora_plan(int M, int K, int N, int R, bool has_w) {
     for (int tn = kMostTokens; tn >= 128; tn -= 16) {
       const long long tiles = (M + tn - 1) / tn, units = tiles * ((N + 255) / 256);
       const long long rounds = (units + sms / 2 - 1) / (sms / 2);
+      if (rounds > 1 && tn > kMostInRounds) continue;
       const long long cost = rounds * (tn + 16);
       if (best < 0 || cost < best) {
         best = cost;

@@ -497,7 +497,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             const int units = min(64, p.R - h * 64) / 8;  // of a row, with ranks in them
             unsigned now[kWords];
             int found = 0;
-  #pragma unroll
+#pragma unroll
             for (int w = 0; w < kWords; ++w) {
               const int row = row0(w) + lane;
               const bool in = row < rows_b && place[row] == d;
@@ -525,7 +525,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
               break;
             }
             tph ^= 1;
-  #pragma unroll
+#pragma unroll
             for (int w = 0; w < kWords; ++w) {
               unsigned left = held_units > units ? held[w] : held[w] & ~now[w];
               for (; left; left &= left - 1)
@@ -779,10 +779,11 @@ cudaError_t run(LoraArgs& p, int num_sms, cudaStream_t stream) {
     return resident_clusters(k, size, kGemmThreads, smem, kept[vec ? 2 : p.cg - 1][splits],
                              num_sms);
   };
-  // Segments: where every unit's cluster is resident at once and each has 4 steps or more,
-  // as many as there can be
+  // Segments: where every unit's cluster is resident at once, each has 4 steps or more and a
+  // CTA's sums fit over its ring, as many as there can be
   p.splits = 1;
-  for (int s = kMaxSplits / p.cg; s > 1 && p.splits == 1; --s)
+  const bool sums_fit = p.tile_n * 512 <= p.stages * stage;
+  for (int s = sums_fit ? kMaxSplits / p.cg : 1; s > 1 && p.splits == 1; --s)
     if (4 * s <= p.ksteps && units <= num_sms / (p.cg * s) && units <= clusters_of(s)) p.splits = s;
   const int held = clusters_of(p.splits);
   if (held < 1) return cudaErrorInvalidConfiguration;
