@@ -13,32 +13,47 @@ namespace {
 constexpr int kShrinkThreads = 256;
 
 // The distinct valid ids of a tile's tokens, in order of first appearance, into list
-// (shared, one entry per token of the tile); whole block of at least kShrinkThreads.
-// Returns their count; *mine is this thread's token's place in the list (-1: none), *bad
-// whether its id is L or more.
-struct __align__(16) ListScratch {
-  int id[kShrinkThreads], place[kShrinkThreads], warp_count[kShrinkThreads / 32];
+// (shared, one entry per token of the tile); whole block of at least kShrinkThreads, after
+// clear_lists and a barrier.  Returns their count; *mine is this thread's token's place in
+// the list (-1: none), *bad whether any of the tile's ids is L or more.
+//
+// The first token of each id is the least that a table of ids ends up with, whatever order
+// they arrive in; a warp enters each of its ids once.  (Every token against every other one
+// took 2 us more at 240 tokens.)
+constexpr int kTable = 2 * kShrinkThreads;  // entries, a power of two: at most half are taken
+struct ListScratch {
+  int key[kTable], first[kTable];
+  int place[kShrinkThreads], warp_count[kShrinkThreads / 32];
 };
+__device__ __forceinline__ void clear_lists(ListScratch& w) {
+  for (int i = threadIdx.x; i < kTable; i += blockDim.x) {
+    w.key[i] = -1;
+    w.first[i] = kShrinkThreads;
+  }
+}
 __device__ __forceinline__ int list_adapters(const int32_t* __restrict__ ids, int m0, int rows,
                                              int L, ListScratch& w, int* list, int* mine,
                                              bool* bad) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const bool here = tid < kShrinkThreads;
   int id = tid < rows ? ids[m0 + tid] : -1;
-  *bad = id >= L;
-  if (id >= L || id < 0) id = -1;
-  if (here) w.id[tid] = id;
-  __syncthreads();
-  int lead = tid;  // the first token with this id
-  const int4* four = reinterpret_cast<const int4*>(w.id);
-#pragma unroll 4
-  for (int i = (rows - 1) / 4; i >= 0; --i) {  // backwards: the last match found is the first
-    const int4 v = four[i];
-    if (v.w == id) lead = 4 * i + 3;
-    if (v.z == id) lead = 4 * i + 2;
-    if (v.y == id) lead = 4 * i + 1;
-    if (v.x == id) lead = 4 * i;
+  const bool high = id >= L;
+  if (high || id < 0) id = -1;
+  const unsigned same = __match_any_sync(0xffffffffu, id);
+  const int head = __ffs(same) - 1;  // the warp's first token with this id
+  int at = 0;
+  if (id >= 0 && lane == head) {
+    at = (int)((uint32_t)id * 2654435761u >> 16) & (kTable - 1);
+    for (int probe = 0; probe < kTable; ++probe) {  // (no more ids than tokens: a place is found)
+      const int was = atomicCAS(&w.key[at], -1, id);
+      if (was == -1 || was == id) break;
+      at = (at + 1) & (kTable - 1);
+    }
+    atomicMin(&w.first[at], tid);
   }
+  at = __shfl_sync(0xffffffffu, at, head);
+  *bad = __syncthreads_or(high);
+  const int lead = w.first[at];  // the first token with this id
   const bool first = id >= 0 && lead == tid;
   const unsigned mask = __ballot_sync(0xffffffffu, first);
   if (here && lane == 0) w.warp_count[warp] = __popc(mask);
@@ -64,10 +79,9 @@ __device__ __forceinline__ void publish_list(const LoraArgs& p, int t, const int
   if (tid < p.tile_n) p.place[(size_t)t * p.tile_n + tid] = mine;
   if (t == 0 && tid == 0) p.err[0] = 0u;
   for (int i = tid; i < n; i += blockDim.x) p.list[(size_t)t * p.tile_n + i] = list[i];
-  const bool any = __syncthreads_or(bad);
   if (tid == 0) {
     p.count[t] = n;
-    p.bad[t] = any;
+    p.bad[t] = bad;
   }
 }
 
@@ -82,6 +96,8 @@ __global__ void __launch_bounds__(kShrinkMost) lora_shrink_kernel(const LoraArgs
     __shared__ ListScratch scratch;
     __shared__ int list[kShrinkThreads];
     const int t = blockIdx.x, m0 = t * p.tile_n;
+    clear_lists(scratch);
+    __syncthreads();
     int mine;
     bool bad;
     const int n =
@@ -140,7 +156,7 @@ __global__ void __launch_bounds__(kShrinkMost) lora_shrink_kernel(const LoraArgs
 constexpr int kShrinkMostStages = 6;
 __host__ __device__ constexpr int shrink_stage_bytes(int tile_n) { return kStageA + tile_n * 128; }
 __host__ __device__ constexpr int shrink_stages(int tile_n) {
-  const int n = (kSmemLimit - 8192) / shrink_stage_bytes(tile_n);  // less the static memory
+  const int n = (kSmemLimit - 10240) / shrink_stage_bytes(tile_n);  // less the lists
   return n < kShrinkMostStages ? n : kShrinkMostStages;
 }
 
@@ -178,6 +194,8 @@ __global__ void __launch_bounds__(kShrinkThreads, 1)
     tmem_alloc(smem_u32(&tmem_slot), kAccCols);
     tmem_relinquish();
   }
+  clear_lists(scratch);
+  __syncthreads();
   grid_dep_wait();
   grid_dep_launch();
   const int t = blockIdx.x / p.tsplits, seg = blockIdx.x - t * p.tsplits;
@@ -200,11 +218,11 @@ __global__ void __launch_bounds__(kShrinkThreads, 1)
   bool bad;
   const int n = list_adapters(p.ids, m0, cols, p.L, scratch, list, &mine, &bad);
   place[threadIdx.x] = mine;
-  if (seg == 0 && blockIdx.y == 0) publish_list(p, t, list, n, mine, bad);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
+  if (seg == 0 && blockIdx.y == 0) publish_list(p, t, list, n, mine, bad);
   const int cap = 128 / p.R;
   const int passes = (n + cap - 1) / cap;
   if (warp == 0) {

@@ -550,6 +550,7 @@ LORAS_MANY = [
     (400, 128, 16000, 8, 20, True, False, "runs"), (250, 64, 700, 32, 200, False, True, "mixed"),
     (1000, 64, 9000, 40, 12, True, False, "mixed"), (48, 128, 500, 104, 30, True, False, "mixed"),
     (256, 200, 12000, 24, 40, True, True, "mixed"), (1020, 520, 4096, 64, 30, True, False, "mixed"),
+    (250, 16, 70, 8, 5000, True, False, "mixed"),
 ]
 
 
