@@ -29,13 +29,6 @@ __host__ __device__ constexpr int token_slots(int tile_n, int cg, int R) {
   const int bytes = t_bytes(tile_n, cg, R);
   return bytes <= 48 * 128 ? 8 : bytes <= 64 * 128 ? 4 : 2;
 }
-// The builders' copy of t for a CTA's token rows (both values), where it takes up to 16 KB:
-// every row enters one adapter's step, and the steps then build from shared memory what
-// they would each wait for from L2.
-__host__ __device__ constexpr int t_copy_bytes(int tile_n, int cg, int R) {
-  return cg == 1 && tile_n * R * 4 <= 16384 ? tile_n * R * 4 : 0;
-}
-
 // VEC: bytes of an adapter's 128 rows of B, and how many adapters are in flight (64 KB at
 // most).  A power of two: step i's slot is i % vec_slots, and the kBuilders / vec_slots warps
 // of a slot take all of its steps, since a wait on a phase's parity cannot tell it from the
@@ -44,8 +37,8 @@ constexpr int kVecTokens = 64, kVecTokenRanks = 4096;
 __host__ __device__ constexpr int vec_slot_bytes(int R) { return 128 * R * 2; }
 __host__ __device__ constexpr int vec_slots(int R) { return R <= 32 ? 8 : R <= 64 ? 4 : 2; }
 
-// Bytes of shared memory behind the ring (multiples of 1024 each): the builders' slots, their
-// copy of t, and (VEC) what they leave for the epilogue [tokens][128] in fp32.
+// Bytes of shared memory behind the ring (multiples of 1024 each): the builders' slots, and
+// (VEC) their copy of t and what they leave for the epilogue [tokens][128] in fp32.
 struct Behind {
   int slots, copy, delta;
 };
@@ -58,7 +51,6 @@ __host__ __device__ constexpr Behind behind(bool vec, int tile_n, int cg, int R)
     b.delta = tile_n * 512;
   } else {
     b.slots = round_kb(2 * token_slots(tile_n, cg, R) * t_bytes(tile_n, cg, R));
-    b.copy = round_kb(t_copy_bytes(tile_n, cg, R));
   }
   return b;
 }
@@ -87,8 +79,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   const int pitch = t_pitch(p.R), half_slot = t_bytes(p.tile_n, CG, p.R);
   const Behind behind_ring = behind(VEC, p.tile_n, CG, p.R);
   uint8_t* tbuf = smem + stages * stage_bytes;  // [tslots][2][rows_b][pitch]; VEC [tslots][128][R]
-  uint8_t* tcopy = tbuf + behind_ring.slots;    // [rows_b][2][R]; VEC fp32 [rows_b][R]
-  const int copy_bytes = t_copy_bytes(p.tile_n, CG, p.R);
+  uint8_t* tcopy = tbuf + behind_ring.slots;    // VEC: fp32 [rows_b][R]
   float* delta = reinterpret_cast<float*>(tcopy + behind_ring.copy);  // VEC [tokens][128]
   uint8_t* ctrl = tcopy + behind_ring.copy + behind_ring.delta;
   uint8_t* epi_stage = ctrl + kCtrl;
@@ -104,7 +95,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(dempty + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   short* place = reinterpret_cast<short*>(ctrl + 512);  // [rows_b] the tokens' adapters
-  uint8_t* listed = ctrl + 1024;                        // [kBuilders][128] the builders' lists
+  int* counts = reinterpret_cast<int*>(ctrl + 768);     // [kBuilders] the builders' lists of
+  uint8_t* listed = ctrl + 1024;                        // [kBuilders][128] rows
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // a cluster: S segments of CG CTAs
@@ -446,31 +438,72 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     // adapters, K = N = 4096, R = 64: 33.2 us a call, writing whole slots 42.7).  A lane's first
     // ranks of t are on their way before the slot is free.  This chain of instructions is what
     // a step costs, hence the row lengths at compile time (R = 128: 124 us, at run time 144).
+    // A unit of no more steps than slots has its rows written by all builders together: a tile
+    // of one adapter would leave them to the warps of one slot (128 tokens, K = N = 4096,
+    // R = 64: 20.1 us a call, by that slot's 23.3).
     auto build = [&](auto log_units) {
-      const int group = kBuilders / tslots;
-      const int own = (warp - 8) / group, part = (warp - 8) % group;
-      uint8_t* const slot = tbuf + 2 * own * half_slot;
       constexpr int LG = decltype(log_units)::value, kUnits = 1 << LG;  // of 16 bytes a row
       constexpr int kWords = LG == 3 ? 2 : LG == 2 ? 3 : 4;  // 32 rows each, by the slots' sizes
       constexpr int kPitch = 16 << LG;
+      const int group = kBuilders / tslots;
+      const int own = (warp - 8) / group, part = (warp - 8) % group;
+      uint8_t* const own_slot = tbuf + 2 * own * half_slot;
       uint8_t* const rows = listed + (warp - 8) * 128;  // this warp's rows of a step
-      unsigned held[kWords] = {};                    // rows in the slot that are not zero,
+      unsigned held[kWords] = {};                       // rows in the slot that are not zero,
       int held_units = 0;                               // and how many units of 16 bytes they have
       auto row0 = [&](int w) { return 32 * (part + w * group); };
       // a row's units of 16 bytes, swizzled by the 128-byte line that it is in
-      auto put = [&](int row, int j, uint4 hi, uint4 lo) {
+      auto put = [&](uint8_t* slot, int row, int j, uint4 hi, uint4 lo) {
         uint8_t* at = slot + row * kPitch + ((j ^ (row >> (3 - LG) & (kUnits - 1))) << 4);
         *reinterpret_cast<uint4*>(at) = hi;
         *reinterpret_cast<uint4*>(at + half_slot) = lo;
       };
+      auto units_of = [&](int h) { return min(64, p.R - h * 64) / 8; };  // with ranks in them
       const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
       for (int w = 0; row0(w) < rows_b; ++w)
         for (int u = lane; u < 32 * kUnits; u += 32)
           if (row0(w) + u / kUnits < rows_b)
-            put(row0(w) + u / kUnits, u % kUnits, zero, zero);
+            put(own_slot, row0(w) + u / kUnits, u % kUnits, zero, zero);
       uint32_t step = 0, tph = 1;
       bool ok = true;
       const uint32_t tfull0 = CG == 2 ? peer_addr(smem_u32(tfull), lead_rank) : smem_u32(tfull);
+      auto arrive = [&]() {
+        if (lane != 0) return;
+        if (CG == 2 && rank != 0)
+          mbar_arrive_remote(tfull0 + own * 8);
+        else
+          mbar_arrive(smem_u32(&tfull[own]));
+      };
+      unsigned now[kWords];
+      // this warp's rows of adapter d, times the units of a row
+      auto list_rows = [&](int d) -> int {
+        int found = 0;
+#pragma unroll
+        for (int w = 0; w < kWords; ++w) {
+          const int row = row0(w) + lane;
+          const bool in = row < rows_b && place[row] == d;
+          now[w] = __ballot_sync(0xffffffffu, in);
+          if (in) rows[found + __popc(now[w] & ((1u << lane) - 1u))] = (uint8_t)row;
+          found += __popc(now[w]);
+        }
+        __syncwarp();
+        return found * kUnits;
+      };
+      // waits until the slot's previous step has been used and clears what it leaves
+      auto take_slot = [&](int units) {
+        if (!wait(&tempty[own], tph)) return false;
+        tph ^= 1;
+#pragma unroll
+        for (int w = 0; w < kWords; ++w) {
+          unsigned left = held_units > units ? held[w] : held[w] & ~now[w];
+          for (; left; left &= left - 1)
+            if (lane < kUnits) put(own_slot, row0(w) + __ffs(left) - 1, lane, zero, zero);
+          held[w] = now[w];
+        }
+        held_units = units;
+        __syncwarp();
+        return true;
+      };
       // (after a wait that gave up a warp still meets the others at their barriers)
       for (int i = worker; i < units; i += workers) {
         const int tile = i / p.blocks;
@@ -480,72 +513,59 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         builders_sync();           // the previous unit's rows have been used
         for (int r = threadIdx.x - 256; r < rows_b; r += 32 * kBuilders)
           place[r] = (short)p.place[(size_t)m0 + r];
-        if (copy_bytes) {
-          const int eights = p.R / 8;
-          for (int u = threadIdx.x - 256; u < rows_b * eights; u += 32 * kBuilders) {
-            const int row = u / eights, r = u % eights * 8;
-            if (m0 + row >= p.M) break;
-            T* dst = reinterpret_cast<T*>(tcopy) + row * 2 * p.R + r;
-            load_t8_split<T>(p, m0 + row, r, reinterpret_cast<uint4*>(dst),
-                             reinterpret_cast<uint4*>(dst + p.R));
-          }
-        }
         builders_sync();
+        const int steps = (n - seg + S - 1) / S * chunks;
+        if (steps <= tslots) {
+          const int turn = step & (tslots - 1);
+          auto step_of = [&](int slot) { return (slot - turn) & (tslots - 1); };
+          const int j = step_of(own);
+          int found = 0;
+          if (j < steps && ok) {
+            found = list_rows(seg + j / chunks * S);
+            ok = take_slot(units_of(j % chunks));
+          }
+          if (lane == 0) counts[warp - 8] = ok ? found : 0;
+          builders_sync();
+          int ends[kBuilders];
+#pragma unroll
+          for (int o = 0; o < kBuilders; ++o) ends[o] = counts[o] + (o ? ends[o - 1] : 0);
+          for (int v = threadIdx.x - 256; v < ends[kBuilders - 1]; v += 32 * kBuilders) {
+            int o = 0, begin = 0;
+#pragma unroll
+            for (int e = 0; e < kBuilders - 1; ++e)
+              if (v >= ends[e]) o = e + 1, begin = ends[e];
+            const int row = listed[o * 128 + (v - begin) / kUnits], u = (v - begin) % kUnits;
+            const int slot = o / group, h = step_of(slot) % chunks;
+            uint4 hi, lo;
+            if (u >= units_of(h)) continue;
+            load_t8_split<T>(p, m0 + row, h * 64 + u * 8, &hi, &lo);
+            put(tbuf + 2 * slot * half_slot, row, u, hi, lo);
+          }
+          fence_proxy_async();
+          builders_sync();
+          if (j < steps && ok) arrive();
+          step += steps;
+          continue;
+        }
         for (int d = seg; d < n && ok; d += S) {
           for (int h = 0; h < chunks; ++h, ++step) {
-            if ((int)(step % tslots) != own) continue;
-            const int units = min(64, p.R - h * 64) / 8;  // of a row, with ranks in them
-            unsigned now[kWords];
-            int found = 0;
-#pragma unroll
-            for (int w = 0; w < kWords; ++w) {
-              const int row = row0(w) + lane;
-              const bool in = row < rows_b && place[row] == d;
-              now[w] = __ballot_sync(0xffffffffu, in);
-              if (in) rows[found + __popc(now[w] & ((1u << lane) - 1u))] = (uint8_t)row;
-              found += __popc(now[w]);
-            }
-            __syncwarp();
-            found *= kUnits;
+            if ((int)(step & (tslots - 1)) != own) continue;
+            const int found = list_rows(d), units = units_of(h);
             uint4 hi, lo;
             auto fetch = [&](int u) {
-              const int row = rows[u / kUnits], r = h * 64 + u % kUnits * 8;
-              if (copy_bytes) {
-                const T* src = reinterpret_cast<const T*>(tcopy) + row * 2 * p.R + r;
-                hi = *reinterpret_cast<const uint4*>(src);
-                lo = *reinterpret_cast<const uint4*>(src + p.R);
-              } else {
-                load_t8_split<T>(p, m0 + row, r, &hi, &lo);
-              }
+              load_t8_split<T>(p, m0 + rows[u / kUnits], h * 64 + u % kUnits * 8, &hi, &lo);
             };
             const bool mine = lane % kUnits < units;  // (32 is a multiple of kUnits)
             if (mine && lane < found) fetch(lane);
-            if (!wait(&tempty[own], tph)) {
-              ok = false;
-              break;
-            }
-            tph ^= 1;
-#pragma unroll
-            for (int w = 0; w < kWords; ++w) {
-              unsigned left = held_units > units ? held[w] : held[w] & ~now[w];
-              for (; left; left &= left - 1)
-                if (lane < kUnits) put(row0(w) + __ffs(left) - 1, lane, zero, zero);
-              held[w] = now[w];
-            }
-            held_units = units;
-            __syncwarp();
+            ok = take_slot(units);
+            if (!ok) break;
             for (int u = lane; mine && u < found; u += 32) {
               if (u != lane) fetch(u);
-              put(rows[u / kUnits], u % kUnits, hi, lo);
+              put(own_slot, rows[u / kUnits], u % kUnits, hi, lo);
             }
             fence_proxy_async();
             __syncwarp();
-            if (lane == 0) {
-              if (CG == 2 && rank != 0)
-                mbar_arrive_remote(tfull0 + own * 8);
-              else
-                mbar_arrive(smem_u32(&tfull[own]));
-            }
+            arrive();
           }
         }
       }
