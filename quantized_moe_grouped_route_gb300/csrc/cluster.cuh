@@ -78,6 +78,12 @@ __device__ __forceinline__ void cluster_sync_all() {
                    : "memory");
 }
 
+// ... that orders no memory: for what the threads have already had the values of.
+__device__ __forceinline__ void cluster_sync_relaxed() {
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::
+                   : "memory");
+}
+
 // ---------------------------------------------------------------- tcgen05, CTA pair
 __device__ __forceinline__ void tmem_alloc2(uint32_t dst_smem, uint32_t ncols) {
   asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem),
