@@ -29,13 +29,12 @@
 //               shared memory, and after a cluster barrier every CTA adds up a share of the
 //               tokens over all segments, in K order
 //   warps 8-15  builders: the token operand (both values of t) of the adapter steps, in
-//               slots of their own; one to four warps (the more, the wider the tile) build a
-//               step, so that several steps are in the making at once
+//               slots of their own; one to four warps (the more, the longer a slot's rows)
+//               build a step, so that several steps are in the making at once
 //
-// Few tokens of few ranks (VEC: at most 64 tokens, tokens * ranks at most 4096; a decode
-// step's requests with an adapter each) do not take the adapters through the MMA: a step
-// per adapter moves 128 rows of B[a] for one or two tokens, and the tensor copies took 0.24
-// us a step (64-byte rows), 5.3 of the 15.9 us of 48 tokens of 43 adapters.  There warp 2
+// Few tokens of few ranks (VEC: at most 64 tokens, tokens * ranks at most 512 or, where there
+// are adapters enough for one each, 1536: a decode step's requests) do not take the adapters
+// through the MMA, where each is a step for one or two tokens.  There warp 2
 // brings in B[a]'s rows, which lie next to each other, as one bulk copy each, while w
 // streams; the builder warps multiply them with t in fp32, and the epilogue adds what they
 // leave in shared memory.

@@ -29,11 +29,18 @@ __host__ __device__ constexpr int token_slots(int tile_n, int cg, int R) {
   const int bytes = t_bytes(tile_n, cg, R);
   return bytes <= 48 * 128 ? 8 : bytes <= 64 * 128 ? 4 : 2;
 }
+
 // VEC: bytes of an adapter's 128 rows of B, and how many adapters are in flight (64 KB at
 // most).  A power of two: step i's slot is i % vec_slots, and the kBuilders / vec_slots warps
 // of a slot take all of its steps, since a wait on a phase's parity cannot tell it from the
 // phase after the next (six slots among eight warps ran into that and timed out).
-constexpr int kVecTokens = 64, kVecTokenRanks = 4096;
+//
+// Where it is taken: up to 64 tokens and 512 token-ranks, and up to 1536 where there are as many
+// adapters as tokens.  48 tokens, K = 2048, N = 7168, R = 32: 43 adapters 16.7 us a call, with
+// MMAs 17.9; 14 adapters 17.6 and 14.9, a few 16.9 and 13.4.  64 tokens, R = 32: 44 adapters
+// 19.2 and 19.7, a few 22.2 and 13.8.  32 tokens, R = 16: 26 adapters 12.3 and 14.3.
+constexpr int kVecTokens = 64;
+__host__ constexpr int vec_token_ranks(int tokens, int L) { return L >= tokens ? 1536 : 512; }
 __host__ __device__ constexpr int vec_slot_bytes(int R) { return 128 * R * 2; }
 __host__ __device__ constexpr int vec_slots(int R) { return R <= 32 ? 8 : R <= 64 ? 4 : 2; }
 
@@ -782,7 +789,8 @@ cudaError_t run(LoraArgs& p, int num_sms, cudaStream_t stream) {
   cudaError_t e = gemm_maps(p, &map_x, &map_w, &map_b);
   if (e != cudaSuccess) return e;
   const int stage = kStageA + token_bytes(p.tile_n, p.cg);
-  const bool vec = p.cg == 1 && p.tile_n <= kVecTokens && p.tile_n * p.R <= kVecTokenRanks;
+  const bool vec = p.cg == 1 && p.tile_n <= kVecTokens &&
+                   p.tile_n * p.R <= vec_token_ranks(p.M, p.L);
   const Behind more = behind(vec, p.tile_n, p.cg, p.R);
   const int other = 1024 + kCtrl + kEpiStage + more.slots + more.copy + more.delta;
   const int most = (kSmemLimit - other) / stage;

@@ -551,6 +551,10 @@ LORAS_MANY = [
     (1000, 64, 9000, 40, 12, True, False, "mixed"), (48, 128, 500, 104, 30, True, False, "mixed"),
     (256, 200, 12000, 24, 40, True, True, "mixed"), (1020, 520, 4096, 64, 30, True, False, "mixed"),
     (250, 16, 70, 8, 5000, True, False, "mixed"),
+    # few token-ranks, adapters enough for one a token (and not): fp32 products beside w
+    (48, 1024, 300, 32, 64, True, False, "mixed"), (30, 520, 260, 40, 33, True, True, "mixed"),
+    (16, 264, 130, 96, 20, False, True, "mixed"), (64, 264, 512, 24, 64, True, True, "mixed"),
+    (64, 136, 384, 8, 5, True, False, "mixed"), (40, 264, 20000, 32, 50, True, False, "mixed"),
 ]
 
 
