@@ -444,7 +444,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     // it has not are cleared: with an adapter a token a step is a row or two (128 tokens of 64
     // adapters, K = N = 4096, R = 64: 33.2 us a call, writing whole slots 42.7).  A lane's first
     // ranks of t are on their way before the slot is free.  This chain of instructions is what
-    // a step costs, hence the row lengths at compile time (R = 128: 124 us, at run time 144).
+    // a step costs, hence the row lengths at compile time (512 such tokens, R = 128: 124
+    // us, at run time 144).
     // A unit of no more steps than slots has its rows written by all builders together: a tile
     // of one adapter would leave them to the warps of one slot (128 tokens, K = N = 4096,
     // R = 64: 20.1 us a call, by that slot's 23.3).
