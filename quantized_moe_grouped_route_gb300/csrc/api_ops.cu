@@ -258,7 +258,7 @@ static int check_lora(int M, int K, int N, int R, int L) {
 // Workspace of qmoe_lora_linear: the error word's block, the tiles' adapter lists, the
 // low-rank activations (which do not depend on whether there is a w).
 struct LoraLayout {
-  size_t count, bad, list, place, t, total;
+  size_t count, bad, list, place, left, any_left, t, tleft, total;
 };
 
 static LoraLayout lora_layout(const LoraPlan& P, int M, int R) {
@@ -268,8 +268,11 @@ static LoraLayout lora_layout(const LoraPlan& P, int M, int R) {
   L.bad = align_up(L.count + 4 * (size_t)P.tiles, 256);
   L.list = align_up(L.bad + 4 * (size_t)P.tiles, 256);
   L.place = align_up(L.list + 4 * tokens, 256);
-  L.t = align_up(L.place + 4 * tokens, 256);
-  L.total = align_up(L.t + 4 * (size_t)M * R * P.tsplits, 256);
+  L.left = align_up(L.place + 4 * tokens, 256);
+  L.any_left = align_up(L.left + 4 * tokens, 256);
+  L.t = align_up(L.any_left + 4 * (size_t)P.tiles, 256);
+  L.tleft = align_up(L.t + 4 * (size_t)M * R * P.tsplits, 256);
+  L.total = align_up(L.tleft + 4 * (size_t)M * R, 256);
   return L;
 }
 
@@ -325,6 +328,9 @@ int qmoe_lora_linear(const void* x_dev, int dtype, long long ldx, const void* w_
   p.list = reinterpret_cast<int*>(ws + W.list);
   p.place = reinterpret_cast<int*>(ws + W.place);
   p.t = reinterpret_cast<float*>(ws + W.t);
+  p.left = reinterpret_cast<unsigned int*>(ws + W.left);
+  p.any_left = reinterpret_cast<unsigned int*>(ws + W.any_left);
+  p.tleft = reinterpret_cast<float*>(ws + W.tleft);
   p.wide = chunked(out_dev, N, N, 2, 16);
   return cuda_rc(launch_lora(p, sms, reinterpret_cast<cudaStream_t>(stream)));
 }

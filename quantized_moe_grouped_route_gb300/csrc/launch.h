@@ -209,6 +209,10 @@ struct LoraArgs : LoraPlan {
   int* list;   // [tiles][tile_n] the distinct adapters
   int* place;  // [tiles][tile_n] each token's adapter's place in the list, -1: none
   float* t;    // [tsplits][M][R] scales[a] * (x . A^T) over a segment of K
+  // what of t the activation type does not hold, for the GEMM's epilogue (lora.cuh):
+  unsigned int* left;      // [tiles][tile_n] a bit per eight ranks of a token
+  unsigned int* any_left;  // [tiles] whether the tile has any
+  float* tleft;            // [M][R] t of those ranks, over all segments
 };
 cudaError_t launch_lora(LoraArgs& p, int num_sms, cudaStream_t stream);
 // its two steps (the second for more than eight tokens): lora_shrink.cu, lora_gemm.cu

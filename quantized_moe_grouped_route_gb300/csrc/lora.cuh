@@ -2,6 +2,8 @@
 // both operands in shared memory, and the tensor maps.
 #pragma once
 
+#include <type_traits>
+
 #include "common.cuh"
 #include "launch.h"
 #include "pack.cuh"
@@ -30,12 +32,50 @@ __device__ __forceinline__ void load_t8(const LoraArgs& p, int m, int r, float (
     t[4] += b.x, t[5] += b.y, t[6] += b.z, t[7] += b.w;
   }
 }
-// ... as their rounding and what that leaves.
+// Eight elements times t.
 template <class T>
-__device__ __forceinline__ void load_t8_split(const LoraArgs& p, int m, int r, uint4* hi,
+__device__ __forceinline__ float dot8(const uint4& raw, const float4& t0, const float4& t1) {
+  Pack<T, 8> v;
+  v.raw = raw;
+  float f = to_f32(v.v[0]) * t0.x;
+  f = fmaf(to_f32(v.v[1]), t0.y, f);
+  f = fmaf(to_f32(v.v[2]), t0.z, f);
+  f = fmaf(to_f32(v.v[3]), t0.w, f);
+  f = fmaf(to_f32(v.v[4]), t1.x, f);
+  f = fmaf(to_f32(v.v[5]), t1.y, f);
+  f = fmaf(to_f32(v.v[6]), t1.z, f);
+  return fmaf(to_f32(v.v[7]), t1.w, f);
+}
+
+// What two values of T do not hold of a token's t is left to the GEMM's epilogue: its sums over
+// the segments, and a bit per eight ranks.  The CTAs of a tile's units all leave the same.
+__device__ __forceinline__ void leave_t8(const LoraArgs& p, int tile, int m, int r,
+                                         const float (&t)[8]) {
+  float4* dst = reinterpret_cast<float4*>(p.tleft + (size_t)m * p.R + r);
+  dst[0] = make_float4(t[0], t[1], t[2], t[3]);
+  dst[1] = make_float4(t[4], t[5], t[6], t[7]);
+  atomicOr(&p.left[m], 1u << (r / 8));
+  atomicOr(&p.any_left[tile], 1u);
+  __threadfence();
+}
+__device__ __forceinline__ float max_abs(float a, float b) {  // NaN if either is
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(fabsf(a)), "f"(fabsf(b)));
+  return r;
+}
+// Ranks r .. r + 7 of t as their rounding and what that leaves: two values of T whose sum is
+// within 2^-16 of the largest of the eight.  bf16 has the range of fp32, so that holds for
+// every finite t (up to what rounds to infinity).  fp16 would round 65520 and more to infinity
+// and leave minus infinity, and the sum is off by up to 2^-25 (half a subnormal step), so the
+// largest has to be 2^-9 or more.  Eight values out of these ranges, infinities and NaN among
+// them, enter the MMA as zeros and are left to the epilogue.
+template <class T>
+__device__ __forceinline__ void load_t8_split(const LoraArgs& p, int tile, int m, int r, uint4* hi,
                                               uint4* lo) {
   float t[8];
   load_t8(p, m, r, t);
+  const float top = max_abs(max_abs(max_abs(t[0], t[1]), max_abs(t[2], t[3])),
+                            max_abs(max_abs(t[4], t[5]), max_abs(t[6], t[7])));
   Pack<T, 8> h, l;
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
@@ -44,6 +84,72 @@ __device__ __forceinline__ void load_t8_split(const LoraArgs& p, int m, int r, u
   }
   *hi = h.raw;
   *lo = l.raw;
+  const bool fits = std::is_same<T, __half>::value
+                        ? top < 65520.f && (top >= 0x1p-9f || top == 0.f)
+                        : top < 0x1.ffp127f;
+  if (!fits) {
+    *hi = *lo = make_uint4(0u, 0u, 0u, 0u);
+    leave_t8(p, tile, m, r, t);
+  }
+}
+// ... and its products in fp32 with row n of B: of one token,
+template <class T>
+__device__ __forceinline__ float left_products(const LoraArgs& p, int m, int n) {
+  float f = 0.f;
+  unsigned left = __ldcg(&p.left[m]);
+  if (left == 0u || n >= p.N) return f;
+  const T* b = reinterpret_cast<const T*>(p.b) + ((size_t)p.ids[m] * p.N + n) * p.R;
+  const float* t = p.tleft + (size_t)m * p.R;
+  for (; left; left &= left - 1) {
+    const int r = 8 * (__ffs(left) - 1);
+    f += dot8<T>(*reinterpret_cast<const uint4*>(b + r),
+                 __ldcg(reinterpret_cast<const float4*>(t + r)),
+                 __ldcg(reinterpret_cast<const float4*>(t + r) + 1));
+  }
+  return f;
+}
+// and by a warp of `tokens` tokens m0, m0 + 1, .. into v, each lane with a row of its own.  t goes
+// through shared memory (buf, 32 tokens' eight values), a token's values by the lane of its
+// number; the rows of four tokens' B are in flight together.  (With left_products for one token
+// after the other a batch of such tokens took 2370 us where this takes 763: 8192 tokens,
+// K = 7168, N = 2048, R = 64.)
+template <class T>
+__device__ __forceinline__ void add_left(const LoraArgs& p, int m0, int tokens, int n, float4* buf,
+                                         float (&v)[32]) {
+  constexpr unsigned kAll = 0xffffffffu;
+  const int lane = threadIdx.x & 31;
+  const unsigned left = lane < tokens ? __ldcg(&p.left[m0 + lane]) : 0u;
+  const int id = left ? p.ids[m0 + lane] : 0;
+  // tokens with the adapter of the one before them
+  const int before = __shfl_up_sync(kAll, id, 1);
+  const unsigned run = __ballot_sync(kAll, lane > 0 && id == before);
+  const T* b = reinterpret_cast<const T*>(p.b) + (size_t)min(n, p.N - 1) * p.R;
+  for (unsigned units = __reduce_or_sync(kAll, left); units; units &= units - 1) {
+    const int r = 8 * (__ffs(units) - 1);
+    const unsigned who = __ballot_sync(kAll, left >> (r / 8) & 1u);
+    __syncwarp();  // the values before these have been used
+    if (who >> lane & 1u) {
+      const float4* t = reinterpret_cast<const float4*>(p.tleft + (size_t)(m0 + lane) * p.R + r);
+      buf[2 * lane] = __ldcg(t);
+      buf[2 * lane + 1] = __ldcg(t + 1);
+    }
+    __syncwarp();
+    uint4 row[4] = {};
+#pragma unroll
+    for (int k = 0; k < 32; k += 4) {
+      if ((run >> k & 15u) == 15u) {
+        row[0] = row[1] = row[2] = row[3];
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          row[j] = *reinterpret_cast<const uint4*>(
+              b + (size_t)__shfl_sync(kAll, id, k + j) * p.N * p.R + r);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (who >> (k + j) & 1u) v[k + j] += dot8<T>(row[j], buf[2 * (k + j)], buf[2 * (k + j) + 1]);
+    }
+  }
 }
 
 __device__ __forceinline__ void mma_ss(uint32_t cg, uint32_t d, uint64_t a, uint64_t b,

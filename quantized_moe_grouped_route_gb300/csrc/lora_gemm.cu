@@ -546,7 +546,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             const int slot = o / group, h = step_of(slot) % chunks;
             uint4 hi, lo;
             if (u >= units_of(h)) continue;
-            load_t8_split<T>(p, m0 + row, h * 64 + u * 8, &hi, &lo);
+            load_t8_split<T>(p, tile, m0 + row, h * 64 + u * 8, &hi, &lo);
             put(tbuf + 2 * slot * half_slot, row, u, hi, lo);
           }
           fence_proxy_async();
@@ -561,7 +561,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             const int found = list_rows(d), units = units_of(h);
             uint4 hi, lo;
             auto fetch = [&](int u) {
-              load_t8_split<T>(p, m0 + rows[u / kUnits], h * 64 + u % kUnits * 8, &hi, &lo);
+              load_t8_split<T>(p, tile, m0 + rows[u / kUnits], h * 64 + u % kUnits * 8, &hi, &lo);
             };
             const bool mine = lane % kUnits < units;  // (32 is a multiple of kUnits)
             if (mine && lane < found) fetch(lane);
@@ -607,6 +607,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       if (!wait(&accf[ab], (local >> 1) & 1)) break;
       if (VEC && !wait(dfull, local & 1)) break;
       tc_fence_after();
+      // (the builders' word came before the MMAs that the barrier stands for)
+      const bool left = !VEC && S == 1 && __ldcg(&p.any_left[tile]) != 0u;
       const uint32_t tbase = tmem + ((uint32_t)(q * 32) << 16) + ab * kAccCols;
       for (int c0 = 0; c0 < cols; c0 += 32) {
         float v[32];
@@ -637,6 +639,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
 #pragma unroll
             for (int k = 0; k < 32; ++k)
               if (c0 + k < cols) v[k] += delta[(c0 + k) * 128 + q * 32 + lane];
+          } else if (left) {
+            add_left<T>(p, m0 + c0, cols - c0, n0 + lane, reinterpret_cast<float4*>(stage), v);
           }
           if (p.base) {
             const T* base = reinterpret_cast<const T*>(p.base) + (size_t)(m0 + c0) * p.ldbase + n0;
@@ -700,6 +704,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     const int tile = worker / p.blocks, block = worker - tile * p.blocks;
     const int m0 = tile * p.tile_n, cols = min(p.tile_n, p.M - m0);
     const int n = (block * CG + (int)rank) * 128 + 4 * lane;
+    const bool left = !VEC && __ldcg(&p.any_left[tile]) != 0u;
     const uint32_t sums0 = smem_u32(smem) + 16 * lane;
     constexpr int kAtOnce = 2;  // tokens a warp
     const int stride = S * (kGemmThreads / 32);
@@ -724,6 +729,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
           t.x += d.x, t.y += d.y, t.z += d.z, t.w += d.w;
         }
         float f[4] = {t.x, t.y, t.z, t.w};
+        if (!VEC && left)
+          for (int e = 0; e < 4; ++e) f[e] += left_products<T>(p, m0 + c, n + e);
         const T* base = reinterpret_cast<const T*>(p.base) + (size_t)(m0 + c) * p.ldbase + n;
         T* out = reinterpret_cast<T*>(p.out) + (size_t)(m0 + c) * p.N + n;
         Pack<T, 4> o;

@@ -76,12 +76,16 @@ __device__ __forceinline__ int list_adapters(const int32_t* __restrict__ ids, in
 __device__ __forceinline__ void publish_list(const LoraArgs& p, int t, const int* list, int n,
                                              int mine, bool bad) {
   const int tid = threadIdx.x;
-  if (tid < p.tile_n) p.place[(size_t)t * p.tile_n + tid] = mine;
+  if (tid < p.tile_n) {
+    p.place[(size_t)t * p.tile_n + tid] = mine;
+    p.left[(size_t)t * p.tile_n + tid] = 0u;
+  }
   if (t == 0 && tid == 0) p.err[0] = 0u;
   for (int i = tid; i < n; i += blockDim.x) p.list[(size_t)t * p.tile_n + i] = list[i];
   if (tid == 0) {
     p.count[t] = n;
     p.bad[t] = bad;
+    p.any_left[t] = 0u;
   }
 }
 
