@@ -387,8 +387,7 @@ int moe_unsort_tokens_backward(const void* dout_dev, long long ldd, const void* 
  *   w_dev     [N][K], or NULL: no shared product (an adapter beside a projection computed
  *             elsewhere, given as base)
  *   a_dev, b_dev  [L][R][K] and [L][N][R]; an adapter of a lower rank is padded with zeros.
- *             The b of an adapter in use is finite: an infinity or NaN in it can reach other
- *             tokens of the batch (in x, a, w and base it stays with its tokens or columns)
+ *             Infinities and NaN stay with the tokens, adapters and columns that have them
  *   adapter_ids_dev int32 [M]: -1 (or any negative) for a token without an adapter; ids
  *             of L or more count as none and set QMOE_FLAG_BAD_ID
  *   scales_dev fp32 [L]

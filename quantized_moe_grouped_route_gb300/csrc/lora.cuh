@@ -68,10 +68,10 @@ __device__ __forceinline__ float max_abs(float a, float b) {  // NaN if either i
 // every finite t (up to what rounds to infinity).  fp16 would round 65520 and more to infinity
 // and leave minus infinity, and the sum is off by up to 2^-25 (half a subnormal step), so the
 // largest has to be 2^-9 or more.  Eight values out of these ranges, infinities and NaN among
-// them, enter the MMA as zeros and are left to the epilogue.
-template <class T>
+// them, enter the MMA as zeros and are left to the epilogue, which tell() tells.
+template <class T, class F>
 __device__ __forceinline__ void load_t8_split(const LoraArgs& p, int tile, int m, int r, uint4* hi,
-                                              uint4* lo) {
+                                              uint4* lo, F&& tell) {
   float t[8];
   load_t8(p, m, r, t);
   const float top = max_abs(max_abs(max_abs(t[0], t[1]), max_abs(t[2], t[3])),
@@ -87,8 +87,9 @@ __device__ __forceinline__ void load_t8_split(const LoraArgs& p, int tile, int m
   const bool fits = std::is_same<T, __half>::value
                         ? top < 65520.f && (top >= 0x1p-9f || top == 0.f)
                         : top < 0x1.ffp127f;
-  if (!fits) {
+  if (__builtin_expect(!fits, 0)) {
     *hi = *lo = make_uint4(0u, 0u, 0u, 0u);
+    tell();
     leave_t8(p, tile, m, r, t);
   }
 }
@@ -149,6 +150,119 @@ __device__ __forceinline__ void add_left(const LoraArgs& p, int m0, int tokens, 
       for (int j = 0; j < 4; ++j)
         if (who >> (k + j) & 1u) v[k + j] += dot8<T>(row[j], buf[2 * (k + j)], buf[2 * (k + j) + 1]);
     }
+  }
+}
+
+// One m16n8k16 MMA on register fragments, fp32 sums.
+template <class T>
+__device__ __forceinline__ void mma_m16n8k16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                             uint32_t a3, uint32_t b0, uint32_t b1) {
+  if constexpr (std::is_same<T, __nv_bfloat16>::value)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Infinities and NaN in B.  Through the MMA a row of B meets every token of the tile, those of
+// other adapters as zeros, and zero times an infinity is NaN: a row of B that holds one leaves
+// every token's sum infinite or NaN there.  So sums that are not finite have the epilogue look
+// at the tile's adapters, and what such a row of w spoiled is made anew from x, w and the
+// token's own adapter.  Finite weights pay for one comparison a row.
+//
+// Whether any adapter of the tile has an infinity or NaN in row n of its B.
+template <class T>
+__device__ __noinline__ bool spoiled_row(const LoraArgs& p, int tile, int n) {
+  constexpr uint32_t kExponent = std::is_same<T, __half>::value ? 0x7c00u : 0x7f80u;
+  if (n >= p.N) return false;
+  bool bad = false;
+  const int adapters = p.count[tile];
+  for (int d = 0; d < adapters; ++d) {
+    const int id = p.list[(size_t)tile * p.tile_n + d];
+    const uint4* b = reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(p.b) +
+                                                    ((size_t)id * p.N + n) * p.R);
+#pragma unroll 4
+    for (int u = 0; u < p.R / 8; ++u) {
+      const uint4 v = b[u];
+      const uint32_t word[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        bad |= (word[i] & kExponent) == kExponent || (word[i] >> 16 & kExponent) == kExponent;
+    }
+  }
+  return bad;
+}
+// t[m] . B[n] of the token's own adapter.
+template <class T>
+__device__ __noinline__ float own_products(const LoraArgs& p, int m, int n) {
+  const int id = p.ids[m];
+  float f = 0.f;
+  if (id < 0 || id >= p.L) return f;
+  const T* b = reinterpret_cast<const T*>(p.b) + ((size_t)id * p.N + n) * p.R;
+  for (int r = 0; r < p.R; r += 8) {
+    float t[8];
+    load_t8(p, m, r, t);
+    f += dot8<T>(*reinterpret_cast<const uint4*>(b + r), make_float4(t[0], t[1], t[2], t[3]),
+                 make_float4(t[4], t[5], t[6], t[7]));
+  }
+  return f;
+}
+// The results of the rows n0 + i, i a bit of `rows`, for the tokens m0, m0 + step, .. (`tokens` of
+// them), by a warp: MMAs on fragments straight from memory, 32 rows x 32 tokens at a time.
+template <class T>
+__device__ __noinline__ void redo_rows(const LoraArgs& p, unsigned rows, int n0, int m0, int step,
+                                       int tokens) {
+  const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
+  const long long ldx = step * p.ldx;
+  for (int c0 = 0; c0 < tokens; c0 += 32) {
+    float acc[2][4][4] = {};  // 16 rows x 8 tokens each
+    if (p.w) {
+      const T* w = reinterpret_cast<const T*>(p.w) + (size_t)(n0 + g) * p.K + q * 8;
+      const T* x = reinterpret_cast<const T*>(p.x) + m0 * p.ldx + (c0 + g) * ldx + q * 8;
+      const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll 2
+      for (int k = 0; k < p.K; k += 32) {
+        const bool in = k + q * 8 < p.K;
+        uint4 a[4], b[4];  // rows g, g + 8, .. and tokens g, g + 8, ..
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          a[i] = b[i] = zero;
+          if (in && n0 + g + 8 * i < p.N)
+            a[i] = *reinterpret_cast<const uint4*>(w + (size_t)(8 * i) * p.K + k);
+          if (in && c0 + g + 8 * i < tokens)
+            b[i] = *reinterpret_cast<const uint4*>(x + (8 * i) * ldx + k);
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            mma_m16n8k16<T>(acc[i][j], a[2 * i].x, a[2 * i + 1].x, a[2 * i].y, a[2 * i + 1].y,
+                            b[j].x, b[j].y);
+            mma_m16n8k16<T>(acc[i][j], a[2 * i].z, a[2 * i + 1].z, a[2 * i].w, a[2 * i + 1].w,
+                            b[j].z, b[j].w);
+          }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int row = 16 * i + g + 8 * (e >> 1), c = c0 + 8 * j + 2 * q + (e & 1);
+          if (!(rows >> row & 1u) || c >= tokens) continue;
+          const int m = m0 + c * step, n = n0 + row;
+          float f = acc[i][j][e] + own_products<T>(p, m, n);
+          if (p.base) f += to_f32(reinterpret_cast<const T*>(p.base)[m * p.ldbase + n]);
+          reinterpret_cast<T*>(p.out)[(size_t)m * p.N + n] = from_f32<T>(f);
+        }
   }
 }
 

@@ -71,6 +71,54 @@ __device__ __forceinline__ void fence_proxy_async() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
+__device__ __forceinline__ bool all_finite(const float (&f)[4]) {
+  return fabsf(f[0]) < INFINITY && fabsf(f[1]) < INFINITY && fabsf(f[2]) < INFINITY &&
+         fabsf(f[3]) < INFINITY;
+}
+
+// The spoiled rows (lora.cuh) of a CTA's unsplit units, which their epilogues left out; whole CTA.
+template <class T>
+__device__ __noinline__ void redo_units(const LoraArgs& p, int worker, int workers, int cg,
+                                        int rank) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int first = warp >> 2, step = kGemmThreads / 128;
+  for (int i = worker; i < p.tiles * p.blocks; i += workers) {
+    const int tile = i / p.blocks, block = i - tile * p.blocks;
+    const int n0 = (block * cg + rank) * 128 + (warp & 3) * 32, m0 = tile * p.tile_n;
+    const int cols = min(p.tile_n, p.M - m0);
+    const unsigned spoiled = __ballot_sync(0xffffffffu, spoiled_row<T>(p, tile, n0 + lane));
+    if (spoiled && first < cols)
+      redo_rows<T>(p, spoiled, n0, m0 + first, step, (cols - first + step - 1) / step);
+  }
+}
+
+// What a CTA of a split unit left out: four rows n .. n + 3 of a token (n a multiple of 4) with a
+// sum that is not finite.  Rows that are spoiled (lora.cuh) are made anew for all of the CTA's
+// tokens, and the others get their sums.  n0: the CTA's first row; whole CTA.
+template <class T>
+__device__ __noinline__ void finish_odd(const LoraArgs& p, int tile, int n0, int seg, int cg,
+                                        int rank, uint32_t sums) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, S = p.splits;
+  const int m0 = tile * p.tile_n, cols = min(p.tile_n, p.M - m0);
+  const int block = warp & 3, row = 32 * block + lane, n = n0 + row;
+  const int first = seg + S * (warp >> 2), step = S * (kGemmThreads / 128);
+  const unsigned spoiled = __ballot_sync(0xffffffffu, spoiled_row<T>(p, tile, n));
+  const bool left = __ldcg(&p.any_left[tile]) != 0u;
+  for (int c = first; c < cols; c += step) {
+    float f = 0.f;
+    for (int g = 0; g < S; ++g)
+      f += ld_cluster_f32(peer_addr(sums + (c * 128 + row) * 4, g * cg + rank));
+    if (left) f += left_products<T>(p, m0 + c, n);
+    const unsigned bad = __ballot_sync(0xffffffffu, !(fabsf(f) < INFINITY));
+    if ((bad >> (lane & ~3) & 15u) == 0u || n >= p.N || (spoiled >> lane & 1u)) continue;
+    if (p.base) f += to_f32(reinterpret_cast<const T*>(p.base)[(m0 + c) * p.ldbase + n]);
+    reinterpret_cast<T*>(p.out)[(size_t)(m0 + c) * p.N + n] = from_f32<T>(f);
+  }
+  __syncwarp();
+  if (spoiled && first < cols)
+    redo_rows<T>(p, spoiled, n0 + 32 * block, m0 + first, step, (cols - first + step - 1) / step);
+}
+
 template <class T, int CG, bool VEC>
 __global__ void __launch_bounds__(kGemmThreads, 1)
     lora_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
@@ -101,6 +149,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   uint64_t* dempty = dfull + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(dempty + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  volatile int* any_spoiled = abort_flag + 1;  // rows of this CTA's units are left out (below)
+  // whether the builders (of the pair) left any of t to the epilogue, in whichever unit
+  volatile int* any_left = any_spoiled + 1;
   short* place = reinterpret_cast<short*>(ctrl + 512);  // [rows_b] the tokens' adapters
   int* counts = reinterpret_cast<int*>(ctrl + 768);     // [kBuilders] the builders' lists of
   uint8_t* listed = ctrl + 1024;                        // [kBuilders][128] rows
@@ -131,6 +182,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     }
     mbar_init(smem_u32(drain), 1);
     *abort_flag = 0;
+    *any_spoiled = 0;
+    *any_left = 0;
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -482,6 +535,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         else
           mbar_arrive(smem_u32(&tfull[own]));
       };
+      auto tell = [&]() {
+        *any_left = 1;
+        if (CG == 2) st_cluster_u32(peer_addr(smem_u32((const void*)any_left), crank ^ 1u), 1u);
+      };
       unsigned now[kWords];
       // this warp's rows of adapter d, times the units of a row
       auto list_rows = [&](int d) -> int {
@@ -546,7 +603,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             const int slot = o / group, h = step_of(slot) % chunks;
             uint4 hi, lo;
             if (u >= units_of(h)) continue;
-            load_t8_split<T>(p, tile, m0 + row, h * 64 + u * 8, &hi, &lo);
+            load_t8_split<T>(p, tile, m0 + row, h * 64 + u * 8, &hi, &lo, tell);
             put(tbuf + 2 * slot * half_slot, row, u, hi, lo);
           }
           fence_proxy_async();
@@ -561,7 +618,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             const int found = list_rows(d), units = units_of(h);
             uint4 hi, lo;
             auto fetch = [&](int u) {
-              load_t8_split<T>(p, tile, m0 + rows[u / kUnits], h * 64 + u % kUnits * 8, &hi, &lo);
+              load_t8_split<T>(p, tile, m0 + rows[u / kUnits], h * 64 + u % kUnits * 8, &hi, &lo,
+                               tell);
             };
             const bool mine = lane % kUnits < units;  // (32 is a multiple of kUnits)
             if (mine && lane < found) fetch(lane);
@@ -608,66 +666,86 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       if (VEC && !wait(dfull, local & 1)) break;
       tc_fence_after();
       // (the builders' word came before the MMAs that the barrier stands for)
-      const bool left = !VEC && S == 1 && __ldcg(&p.any_left[tile]) != 0u;
+      const bool left = !VEC && S == 1 && *any_left && __ldcg(&p.any_left[tile]) != 0u;
       const uint32_t tbase = tmem + ((uint32_t)(q * 32) << 16) + ab * kAccCols;
-      for (int c0 = 0; c0 < cols; c0 += 32) {
-        float v[32];
-        if (any) {
-          // (a tile's last 16 columns may be followed by columns of no meaning, within the
-          // accumulator's 256)
-          uint32_t r[2][16];
-          tmem_ld_x16(tbase + c0, r[0]);
-          tmem_ld_x16(tbase + c0 + 16, r[1]);
-          tmem_wait_ld();
-          tmem_ld_ready(r[0]);
-          tmem_ld_ready(r[1]);
-#pragma unroll
-          for (int k = 0; k < 32; ++k) v[k] = __uint_as_float(r[k >> 4][k & 15]);
-        } else {
-#pragma unroll
-          for (int k = 0; k < 32; ++k) v[k] = 0.f;
-        }
-        if (S > 1) {
-          // this segment's sums [token][row], over the ring, which is idle: a CTA of a split
-          // unit has this one unit, and its MMAs are complete
-          float* sums = reinterpret_cast<float*>(smem) + (size_t)c0 * 128 + q * 32 + lane;
-#pragma unroll
-          for (int k = 0; k < 32; ++k)
-            if (c0 + k < cols) sums[k * 128] = v[k];
-        } else {
-          if constexpr (VEC) {
-#pragma unroll
-            for (int k = 0; k < 32; ++k)
-              if (c0 + k < cols) v[k] += delta[(c0 + k) * 128 + q * 32 + lane];
-          } else if (left) {
-            add_left<T>(p, m0 + c0, cols - c0, n0 + lane, reinterpret_cast<float4*>(stage), v);
-          }
-          if (p.base) {
-            const T* base = reinterpret_cast<const T*>(p.base) + (size_t)(m0 + c0) * p.ldbase + n0;
-            const bool in = n0 + lane < p.N;
-#pragma unroll
-            for (int k = 0; k < 32; ++k)
-              if (in && c0 + k < cols) v[k] += to_f32(base[(size_t)k * p.ldbase + lane]);
-          }
-          __syncwarp();
-#pragma unroll
-          for (int k = 0; k < 32; ++k) stage[k * 32 + lane] = from_f32<T>(v[k]);
-          __syncwarp();
-          T* out = reinterpret_cast<T*>(p.out) + (size_t)(m0 + c0) * p.N + n0;
-          if (p.wide) {
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-              const int tok = u * 8 + lane / 4, part = lane % 4 * 8;
-              if (c0 + tok < cols && n0 + part < p.N)
-                *reinterpret_cast<uint4*>(out + (size_t)tok * p.N + part) =
-                    *reinterpret_cast<const uint4*>(stage + tok * 32 + part);
-            }
-          } else if (n0 + lane < p.N) {
-            for (int k = 0; k < 32 && c0 + k < cols; ++k)
-              out[(size_t)k * p.N + lane] = stage[k * 32 + lane];
-          }
-        }
+      // the warp's rows that infinities or NaN in some B spoiled (lora.cuh): looked for where the
+      // first token's sum is not finite
+      unsigned spoiled = 0u;
+      if (!VEC && S == 1 && any) {
+        uint32_t first[16];
+        tmem_ld_x16(tbase, first);
+        tmem_wait_ld();
+        tmem_ld_ready(first);
+        if (__builtin_expect(
+                __any_sync(0xffffffffu, !(fabsf(__uint_as_float(first[0])) < INFINITY)), 0))
+          spoiled = __ballot_sync(0xffffffffu, spoiled_row<T>(p, tile, n0 + lane));
       }
+      auto write_tile = [&](auto with_rest) {
+        for (int c0 = 0; c0 < cols; c0 += 32) {
+          float v[32];
+          if (any) {
+            // (a tile's last 16 columns may be followed by columns of no meaning, within the
+            // accumulator's 256)
+            uint32_t r[2][16];
+            tmem_ld_x16(tbase + c0, r[0]);
+            tmem_ld_x16(tbase + c0 + 16, r[1]);
+            tmem_wait_ld();
+            tmem_ld_ready(r[0]);
+            tmem_ld_ready(r[1]);
+#pragma unroll
+            for (int k = 0; k < 32; ++k) v[k] = __uint_as_float(r[k >> 4][k & 15]);
+          } else {
+#pragma unroll
+            for (int k = 0; k < 32; ++k) v[k] = 0.f;
+          }
+          if (S > 1) {
+            // this segment's sums [token][row], over the ring, which is idle: a CTA of a split
+            // unit has this one unit, and its MMAs are complete
+            float* sums = reinterpret_cast<float*>(smem) + (size_t)c0 * 128 + q * 32 + lane;
+#pragma unroll
+            for (int k = 0; k < 32; ++k)
+              if (c0 + k < cols) sums[k * 128] = v[k];
+          } else {
+            if constexpr (VEC) {
+#pragma unroll
+              for (int k = 0; k < 32; ++k)
+                if (c0 + k < cols) v[k] += delta[(c0 + k) * 128 + q * 32 + lane];
+            } else if constexpr (decltype(with_rest)::value) {
+              if (left)
+                add_left<T>(p, m0 + c0, cols - c0, n0 + lane, reinterpret_cast<float4*>(stage), v);
+            }
+            if (p.base) {
+              const T* base = reinterpret_cast<const T*>(p.base) + (size_t)(m0 + c0) * p.ldbase + n0;
+              const bool in = n0 + lane < p.N;
+#pragma unroll
+              for (int k = 0; k < 32; ++k)
+                if (in && c0 + k < cols) v[k] += to_f32(base[(size_t)k * p.ldbase + lane]);
+            }
+            __syncwarp();
+#pragma unroll
+            for (int k = 0; k < 32; ++k) stage[k * 32 + lane] = from_f32<T>(v[k]);
+            __syncwarp();
+            T* out = reinterpret_cast<T*>(p.out) + (size_t)(m0 + c0) * p.N + n0;
+            if (p.wide && !(decltype(with_rest)::value && spoiled)) {
+#pragma unroll
+              for (int u = 0; u < 4; ++u) {
+                const int tok = u * 8 + lane / 4, part = lane % 4 * 8;
+                if (c0 + tok < cols && n0 + part < p.N)
+                  *reinterpret_cast<uint4*>(out + (size_t)tok * p.N + part) =
+                      *reinterpret_cast<const uint4*>(stage + tok * 32 + part);
+              }
+            } else if (n0 + lane < p.N && !(decltype(with_rest)::value && (spoiled >> lane & 1u))) {
+              for (int k = 0; k < 32 && c0 + k < cols; ++k)
+                out[(size_t)k * p.N + lane] = stage[k * 32 + lane];
+            }
+          }
+        }
+      };
+      // (a loop of its own, since its registers cost the usual one 2 %)
+      if (__builtin_expect(!VEC && (left || spoiled != 0u), 0))
+        write_tile(std::true_type{});
+      else
+        write_tile(std::false_type{});
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
@@ -677,6 +755,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
           mbar_arrive(smem_u32(&acce[ab]));
         if (VEC) mbar_arrive(smem_u32(dempty));
       }
+      if (!VEC && spoiled) *any_spoiled = 1;
     }
   }
 
@@ -698,6 +777,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     else
       tmem_dealloc(tmem, 2 * kAccCols);
   }
+  if (!VEC && S == 1 && *any_spoiled) redo_units<T>(p, worker, workers, CG, (int)rank);
   if (S > 1) {
     // the unit's tokens seg, seg + S, .. over all segments: a warp per token, four rows a
     // lane, the segments' values in flight together
@@ -707,6 +787,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     const bool left = !VEC && __ldcg(&p.any_left[tile]) != 0u;
     const uint32_t sums0 = smem_u32(smem) + 16 * lane;
     constexpr int kAtOnce = 2;  // tokens a warp
+    bool odd = false;           // a sum that is not finite: looked at below
     const int stride = S * (kGemmThreads / 32);
     for (int c0 = seg + S * warp; c0 < cols; c0 += kAtOnce * stride) {
       float4 v[kAtOnce][kMaxSplits];
@@ -731,6 +812,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         float f[4] = {t.x, t.y, t.z, t.w};
         if (!VEC && left)
           for (int e = 0; e < 4; ++e) f[e] += left_products<T>(p, m0 + c, n + e);
+        if (!VEC && !all_finite(f)) {
+          odd = true;
+          continue;
+        }
         const T* base = reinterpret_cast<const T*>(p.base) + (size_t)(m0 + c) * p.ldbase + n;
         T* out = reinterpret_cast<T*>(p.out) + (size_t)(m0 + c) * p.N + n;
         Pack<T, 4> o;
@@ -748,6 +833,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         }
       }
     }
+    if (!VEC && __syncthreads_or(odd))
+      finish_odd<T>(p, tile, (block * CG + (int)rank) * 128, seg, CG, (int)rank, smem_u32(smem));
     // No CTA leaves while its sums may still be read.  Every value fetched above has gone into
     // a store by now, so the barrier need not order memory (waiting for those stores took
     // 0.4 to 1 us: 128 tokens, K = N = 4096, R = 16: 16.6 us a call for 17.4).

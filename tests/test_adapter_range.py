@@ -120,3 +120,89 @@ def test_t_of_all_sizes_in_one_token(M, R):
     for w in (None, _randn(g, N, K, std=K ** -0.5).to(dtype)):
         out = q.qmoe_lora_linear(x, w, a, b, ids, s)
         _near(out, x, w, a, b, ids, s)
+
+
+SPOILED = [  # M, K, N, R, L, with w, with base: few tokens, one tile with K split and not, pairs
+    (1, 256, 130, 16, 2, True, False), (7, 512, 130, 16, 3, True, True),
+    (30, 520, 260, 40, 33, True, True), (20, 256, 300, 128, 6, True, False),
+    (100, 64, 200, 24, 6, True, True), (128, 1024, 384, 16, 40, True, False),
+    (70, 136, 203, 64, 4, False, True), (128, 200, 20000, 16, 60, True, False),
+    (200, 264, 515, 8, 9, True, True), (300, 4096, 256, 32, 5, True, False),
+    (1100, 136, 4099, 40, 30, True, False), (2047, 1096, 4096, 16, 8, True, True),
+    (513, 64, 70, 72, 300, False, False),
+]
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("M,K,N,R,L,with_w,with_base", SPOILED)
+def test_adapter_of_infinities_stays_alone(M, K, N, R, L, with_w, with_base, dtype):
+    """Infinities and NaN in one adapter's B reach its own tokens, in their columns, and no
+    other token."""
+    g = _gen(M + N)
+    x = _randn(g, M, K).to(dtype)
+    w = _randn(g, N, K, std=K ** -0.5).to(dtype) if with_w else None
+    a = _randn(g, L * R, K, std=K ** -0.5).to(dtype).view(L, R, K)
+    b = _randn(g, L, N, R, std=R ** -0.5).to(dtype)
+    s = 0.5 + torch.rand(L, generator=g, device="cuda")
+    ids = torch.randint(-1, L, (M,), generator=g, device="cuda", dtype=torch.int32)
+    ids[M // 2] = L - 1
+    base = _randn(g, M, N).to(dtype) if with_base else None
+    good = q.qmoe_lora_linear(x, w, a, b, ids, s, base=base)
+    bad = b.clone()
+    rows = torch.tensor(sorted({0, 3, 33, 64, N // 2, N - 2, N - 1}), device="cuda")
+    values = torch.tensor([math.inf, math.nan, -math.inf], device="cuda")
+    for i, n in enumerate(rows.tolist()):
+        bad[L - 1, n, (5 * i) % R] = values[i % 3]
+    ws = torch.empty(q.qmoe_lora_workspace_size(M, K, N, R, L), dtype=torch.uint8, device="cuda")
+    out = q.qmoe_lora_linear(x, w, a, bad, ids, s, base=base, workspace=ws)
+    assert qmoe.qmoe_read_error(ws) == (qmoe.QMOE_OK, 0)
+    others = ids != L - 1
+    assert others.any() or M == 1
+    assert torch.isfinite(out[others]).all()
+    if others.any():
+        _near(out[others], x[others], w, a, b, ids[others], s,
+              None if base is None else base[others])
+    clean = torch.ones(N, dtype=torch.bool, device="cuda")
+    clean[rows] = False
+    assert torch.equal(out[:, clean], good[:, clean])
+    # its own tokens: an infinity times t, with t's sign
+    mine = (~others).nonzero()[:, 0]
+    t = x[mine].double() @ a[L - 1].double().t()
+    for i, n in enumerate(rows.tolist()):
+        ti = t[:, (5 * i) % R]
+        sure = ti.abs() > 1e-3
+        got, v = out[mine, n], float(values[i % 3])
+        if math.isnan(v):
+            assert torch.isnan(got).all()
+        else:
+            assert torch.equal(got[sure].double(), torch.sign(ti[sure]) * v)
+    again = q.qmoe_lora_linear(x, w, a, bad, ids, s, base=base)
+    assert torch.equal(torch.nan_to_num(out), torch.nan_to_num(again))
+    if with_base:  # in place of the base
+        inout = base.clone()
+        q.qmoe_lora_linear(x, w, a, bad, ids, s, base=inout, out=inout)
+        assert torch.equal(torch.nan_to_num(inout), torch.nan_to_num(out))
+
+
+@gpu
+@pytest.mark.parametrize("M", [100, 300])
+def test_infinities_everywhere(M):
+    """A token of NaN, a row of w of infinities and an adapter of NaN, each in its place."""
+    g = _gen(M)
+    K, N, R, L, dtype = 128, 520, 16, 4, torch.bfloat16
+    x, w = _randn(g, M, K).to(dtype), _randn(g, N, K, std=K ** -0.5).to(dtype)
+    a = _randn(g, L * R, K, std=K ** -0.5).to(dtype).view(L, R, K)
+    b = _randn(g, L, N, R).to(dtype)
+    s = torch.ones(L, device="cuda")
+    ids = torch.arange(M, device="cuda", dtype=torch.int32) % L
+    want = q.qmoe_lora_linear(x, w, a, b, ids, s)
+    x[0, 7], w[5], b[2] = math.nan, math.inf, math.nan
+    a[3] = math.nan
+    out = q.qmoe_lora_linear(x, w, a, b, ids, s)
+    there = (ids < 2)[:, None].expand(M, N).clone()
+    there[0], there[:, 5] = False, False
+    # rows of w beside b's NaN are added up anew, so equal up to rounding
+    assert torch.isfinite(out[there]).all() and not torch.isfinite(out[~there]).any()
+    err = (out.double() - want.double()).abs()[there]
+    assert (err <= 2.0 ** -7 * want.double().abs()[there] + 2.0 ** -10).all()
