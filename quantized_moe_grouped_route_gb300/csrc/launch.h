@@ -92,6 +92,14 @@ constexpr int kMaxSkCtas = 192;
 inline size_t sk_part_bytes() { return (size_t)kMaxSkCtas * 2 * 128 * 16 * sizeof(float); }
 inline size_t sk_cnt_bytes(int max_ctas) { return (size_t)max_ctas * 4 * sizeof(int); }
 
+// Lets a kernel have up to `bytes` of dynamic shared memory.  Always the kernel's most, not the
+// launch's own need: the limit belongs to the kernel in the whole process, and another thread
+// must not find it lowered between its own call here and its launch.
+template <class K>
+cudaError_t allow_smem(K* kernel, int bytes) {
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+}
+
 // Launch attribute that lets a kernel start while the previous kernel on the stream
 // finishes (it must then call grid_dep_wait before reading that kernel's outputs).
 // The forward uses it on every schedule but the wide prefill one, where kernels that

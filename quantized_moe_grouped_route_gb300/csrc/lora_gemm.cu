@@ -895,7 +895,7 @@ cudaError_t run(LoraArgs& p, int num_sms, cudaStream_t stream) {
   auto* k = p.cg == 2 ? lora_gemm_kernel<T, 2, false>
             : vec     ? lora_gemm_kernel<T, 1, true>
                       : lora_gemm_kernel<T, 1, false>;
-  e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  e = allow_smem(k, kSmemLimit);
   if (e != cudaSuccess) return e;
   const int units = p.tiles * p.blocks;
   static std::atomic<int> kept[3][kMaxSplits + 1];

@@ -158,9 +158,10 @@ __global__ void __launch_bounds__(kShrinkMost) lora_shrink_kernel(const LoraArgs
 // saved, and 37 tiles of four segments did not fit as clusters: at M = 8192, K = 7168 31 us).
 // gridDim.y CTAs share a tile's passes.
 constexpr int kShrinkMostStages = 6;
+constexpr int kShrinkRing = kSmemLimit - 10240;  // bytes at most, less the lists
 __host__ __device__ constexpr int shrink_stage_bytes(int tile_n) { return kStageA + tile_n * 128; }
 __host__ __device__ constexpr int shrink_stages(int tile_n) {
-  const int n = (kSmemLimit - 10240) / shrink_stage_bytes(tile_n);  // less the lists
+  const int n = kShrinkRing / shrink_stage_bytes(tile_n);
   return n < kShrinkMostStages ? n : kShrinkMostStages;
 }
 
@@ -364,9 +365,7 @@ cudaError_t run(const LoraArgs& p, int num_sms, cudaStream_t stream) {
   cfg.blockDim = dim3(kShrinkThreads);
   cfg.gridDim = dim3(ctas, share < most ? share : most);
   cfg.dynamicSmemBytes = 1024 + shrink_stages(p.tile_n) * shrink_stage_bytes(p.tile_n);
-  cudaError_t e =
-      cudaFuncSetAttribute(lora_shrink_mma_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           (int)cfg.dynamicSmemBytes);
+  cudaError_t e = allow_smem(lora_shrink_mma_kernel<T>, 1024 + kShrinkRing);
   if (e != cudaSuccess) return e;
   CUtensorMap map_x, map_a;
   e = shrink_maps(p, &map_x, &map_a);

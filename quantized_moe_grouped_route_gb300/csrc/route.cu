@@ -26,6 +26,8 @@ namespace qmoe {
 namespace {
 
 constexpr int kWarps = kRouteThreads / 32;
+constexpr int kMostExperts = 2048;  // of the C ABI
+constexpr int kRouteMostSmem = kWarps * kMostExperts * (int)sizeof(int);  // count tables
 constexpr int kBatch = 8;  // 32-pair steps whose ids a warp loads at once
 
 // Block-wide exclusive scan of one int per thread; returns the exclusive prefix and
@@ -430,11 +432,9 @@ cudaError_t launch_sort_route(const int32_t* ids, int P, int E, int32_t* offsets
   int* gbad = counts + (size_t)blocks * E;
   const size_t smem1 = route_smem_bytes(E), smem2 = smem1 + 2 * (size_t)E * sizeof(int);
   if (smem2 > 48 * 1024) {
-    cudaError_t rc = cudaFuncSetAttribute(sort_count_kernel,
-                                          cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem1);
+    cudaError_t rc = allow_smem(sort_count_kernel, kRouteMostSmem);
     if (rc == cudaSuccess)
-      rc = cudaFuncSetAttribute(sort_place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                (int)smem2);
+      rc = allow_smem(sort_place_kernel, kRouteMostSmem + 2 * kMostExperts * (int)sizeof(int));
     if (rc != cudaSuccess) return rc;
   }
   cudaLaunchConfig_t cfg = {};
@@ -474,8 +474,7 @@ cudaError_t launch_route(const int32_t* ids, int P, int E, int tile_n, int32_t* 
   const size_t smem = route_smem_bytes(E);
   const int blocks = route_blocks(P);
   if (blocks == 1) {
-    cudaError_t rc = cudaFuncSetAttribute(route_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                          (int)smem);
+    cudaError_t rc = allow_smem(route_kernel, kRouteMostSmem);
     if (rc != cudaSuccess) return rc;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1] = {pdl_attribute()};
@@ -490,11 +489,8 @@ cudaError_t launch_route(const int32_t* ids, int P, int E, int tile_n, int32_t* 
   }
   int* gh = reinterpret_cast<int*>(scratch);
   int* gbad = gh + (size_t)blocks * kWarps * E;
-  cudaError_t rc = cudaFuncSetAttribute(route_hist_kernel,
-                                        cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (rc == cudaSuccess)
-    rc = cudaFuncSetAttribute(route_scatter_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              (int)smem);
+  cudaError_t rc = allow_smem(route_hist_kernel, kRouteMostSmem);
+  if (rc == cudaSuccess) rc = allow_smem(route_scatter_kernel, kRouteMostSmem);
   if (rc != cudaSuccess) return rc;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1] = {pdl_attribute()};
