@@ -256,30 +256,31 @@ static int check_lora(int M, int K, int N, int R, int L) {
 }
 
 // Workspace of qmoe_lora_linear: the error word's block, the tiles' adapter lists, the
-// low-rank activations (which do not depend on whether there is a w).
+// low-rank activations.  Each part is as large as any batch of up to M tokens needs (fewer
+// tokens can have more segments of t), so that a workspace made for some batch serves every
+// smaller one.
 struct LoraLayout {
   size_t count, bad, list, place, left, any_left, t, tleft, total;
 };
 
-static LoraLayout lora_layout(const LoraPlan& P, int M, int R) {
+static LoraLayout lora_layout(int M, int K, int R) {
   LoraLayout L;
-  const size_t tokens = (size_t)P.tiles * P.tile_n;
+  const size_t tiles = (size_t)M / kLoraLeastTile + 1, tokens = (size_t)M + kLoraMostTile;
   L.count = kWsHeaderBytes;
-  L.bad = align_up(L.count + 4 * (size_t)P.tiles, 256);
-  L.list = align_up(L.bad + 4 * (size_t)P.tiles, 256);
+  L.bad = align_up(L.count + 4 * tiles, 256);
+  L.list = align_up(L.bad + 4 * tiles, 256);
   L.place = align_up(L.list + 4 * tokens, 256);
   L.left = align_up(L.place + 4 * tokens, 256);
   L.any_left = align_up(L.left + 4 * tokens, 256);
-  L.t = align_up(L.any_left + 4 * (size_t)P.tiles, 256);
-  L.tleft = align_up(L.t + 4 * (size_t)M * R * P.tsplits, 256);
+  L.t = align_up(L.any_left + 4 * tiles, 256);
+  L.tleft = align_up(L.t + 4 * (size_t)R * lora_segment_rows(M, K, R), 256);
   L.total = align_up(L.tleft + 4 * (size_t)M * R, 256);
   return L;
 }
 
 size_t qmoe_lora_workspace_size(int M, int K, int N, int R, int L) {
   if (check_lora(M, K, N, R, L) != QMOE_OK) return 0;
-  if (M == 0) return kWsHeaderBytes;
-  return lora_layout(lora_plan(M, K, N, R, true), M, R).total;
+  return M == 0 ? kWsHeaderBytes : lora_layout(M, K, R).total;
 }
 
 int qmoe_lora_linear(const void* x_dev, int dtype, long long ldx, const void* w_dev,
@@ -304,7 +305,7 @@ int qmoe_lora_linear(const void* x_dev, int dtype, long long ldx, const void* w_
   if (rc != QMOE_OK) return rc;
   LoraArgs p = {};
   static_cast<LoraPlan&>(p) = lora_plan(M, K, N, R, w_dev != nullptr);
-  const LoraLayout W = lora_layout(p, M, R);
+  const LoraLayout W = lora_layout(M, K, R);
   uint8_t* ws = reinterpret_cast<uint8_t*>(workspace_dev);
   p.dtype = dtype;
   p.x = x_dev;

@@ -195,7 +195,11 @@ cudaError_t launch_unsort_backward(const TokenArgs& a, int dtype, int chunk, int
 struct LoraPlan {
   int cg, tile_n, tiles, blocks, ksteps, tensor_shrink, tsplits;
 };
+constexpr int kLoraLeastTile = 128;  // tokens of a tile, of more than one; at most
+constexpr int kLoraMostTile = 256;
 LoraPlan lora_plan(int M, int K, int N, int R, bool has_w);
+// The most M' * tsplits of any plan of M' <= M tokens.
+size_t lora_segment_rows(int M, int K, int R);
 struct LoraArgs : LoraPlan {
   int dtype;
   const void* x;  // [M][K], rows ldx elements apart

@@ -242,12 +242,35 @@ cudaError_t run_few(const LoraArgs& p, cudaStream_t stream) {
 
 }  // namespace
 
-// Tiles and pairs for a problem (SMs of a GB300: the workspace size must not depend on the
-// device).  Up to 128 tokens are one tile and one CTA a unit; more go to CTA pairs, with the
+// SMs of a GB300: the workspace size must not depend on the device.
+constexpr int kPlanSms = 152;
+
+// Whether x . A^T goes through the tensor cores: the fp32 shrink reads a token's adapter anew
+// for each token, so up to 16 MB of such reads (at 33 MB, M = 256, K = N = 4096, R = 16, a call
+// takes 19.8 us with the tensor cores and 22.7 without, at 17 MB 18.3 and 17.8) do not, nor
+// does a single token.
+static bool tensor_shrink(int M, int K, int R) {
+  return M > 1 && (long long)M * R * K * 2 > (16LL << 20);
+}
+// Segments of K in that form, at most.
+static int most_segments(int K) {
+  const int s = (K + 63) / 64 / 4;
+  return s < 1 ? 1 : s < kShrinkSegments ? s : kShrinkSegments;
+}
+
+// A plan has kPlanSms / tiles segments, or one.
+size_t lora_segment_rows(int M, int K, int R) {
+  if (!tensor_shrink(M, K, R)) return M;
+  const size_t rows = (size_t)M * most_segments(K), full = (size_t)kPlanSms * kMostTokens;
+  const size_t split = rows < full ? rows : full;
+  return split > (size_t)M ? split : M;
+}
+
+// Tiles and pairs for a problem.  Up to 128 tokens are one tile and one CTA a unit; more go to CTA pairs, with the
 // tile width whose last round of units leaves the least idle.
 LoraPlan lora_plan(int M, int K, int N, int R, bool has_w) {
   LoraPlan L;
-  const int sms = 152;
+  const int sms = kPlanSms;
   const int ksteps = (K + 63) / 64;
   L.ksteps = has_w ? ksteps : 0;
   if (M <= 128) {
@@ -257,7 +280,7 @@ LoraPlan lora_plan(int M, int K, int N, int R, bool has_w) {
   } else {
     L.cg = 2;
     long long best = -1;
-    for (int tn = kMostTokens; tn >= 128; tn -= 16) {
+    for (int tn = kMostTokens; tn >= kLoraLeastTile; tn -= 16) {
       const long long tiles = (M + tn - 1) / tn, units = tiles * ((N + 255) / 256);
       const long long rounds = (units + sms / 2 - 1) / (sms / 2);
       if (rounds > 1 && tn > kMostInRounds) continue;
@@ -270,14 +293,10 @@ LoraPlan lora_plan(int M, int K, int N, int R, bool has_w) {
     }
   }
   L.blocks = (N + 128 * L.cg - 1) / (128 * L.cg);
-  // the fp32 shrink reads a token's adapter anew for each token: up to 16 MB of such reads
-  // (at 33 MB, M = 256, K = N = 4096, R = 16, a call takes 19.8 us with the tensor cores
-  // and 22.7 without, at 17 MB 18.3 and 17.8), and a single token's
-  L.tensor_shrink = M > 1 && (long long)M * R * K * 2 > (16LL << 20);
+  L.tensor_shrink = tensor_shrink(M, K, R);
   L.tsplits = 1;
   if (L.tensor_shrink) {
-    const int most = ksteps / 4 < kShrinkSegments ? ksteps / 4 : kShrinkSegments;
-    const int s = sms / L.tiles < most ? sms / L.tiles : most;
+    const int most = most_segments(K), s = kPlanSms / L.tiles < most ? kPlanSms / L.tiles : most;
     L.tsplits = s < 1 ? 1 : s;
   }
   return L;

@@ -16,7 +16,7 @@ constexpr int kSmemLimit = 232448;
 // Tokens of a tile.  Up to 240 leave room for five stages of the GEMM's ring, 256 for four:
 // taken where all units then run at once (1024 tokens, K = N = 4096, R = 16: 36.3 us, in two
 // rounds of 208 38.5; 256 tokens of 64 adapters, K = 1024, N = 16384: 42.0 and 56.6).
-constexpr int kMostTokens = 256, kMostInRounds = 240;
+constexpr int kMostTokens = kLoraMostTile, kMostInRounds = 240;
 constexpr int kShrinkSegments = 8;  // of K in the tensor-core shrink, at most
 
 // Ranks r .. r + 7 of a token's t, over the shrink's segments of K in order.

@@ -206,3 +206,17 @@ def test_infinities_everywhere(M):
     assert torch.isfinite(out[there]).all() and not torch.isfinite(out[~there]).any()
     err = (out.double() - want.double()).abs()[there]
     assert (err <= 2.0 ** -7 * want.double().abs()[there] + 2.0 ** -10).all()
+
+
+@pytest.mark.parametrize("K,N,R", [(4096, 4096, 16), (7168, 2048, 64), (2048, 7168, 32), (64, 64, 8),
+                                   (1096, 512, 128), (65536, 131072, 128)])
+def test_workspace_serves_every_smaller_batch(K, N, R):
+    from quantized_moe_grouped_route_gb300 import build
+    build.build()
+    sizes = [q.qmoe_lora_workspace_size(M, K, N, R, 8) for M in range(1, 9000)]
+    assert all(a <= b for a, b in zip(sizes, sizes[1:]))
+    # and of fewer ranks or a shorter K; what it holds is in proportion to the batch
+    for M in (1, 100, 513, 5152, 8192):
+        assert q.qmoe_lora_workspace_size(M, K // 2 // 8 * 8, N, R, 8) <= sizes[M - 1]
+        assert R == 8 or q.qmoe_lora_workspace_size(M, K, N, R - 8, 8) <= sizes[M - 1]
+        assert sizes[M - 1] <= 4 * (9 * M * R + 4 * (M + 256)) + 16 * 256
