@@ -1,0 +1,51 @@
+"""The expert gate where its scores saturate and its choice values are infinite.
+
+Tolerances: u = 2^-24; expf is within 2 ulp (2^-22) for any argument here, a sigmoid and its
+complement within 2^-21 then, and the sums of k positive terms add k u.
+"""
+
+import math
+
+import pytest
+import torch
+
+import quantized_moe_grouped_route_gb300 as q
+
+gpu = pytest.mark.gpu
+U = 2.0 ** -24
+
+
+def _gen(seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return g
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("renorm", [False, True])
+@pytest.mark.parametrize("lo,hi", [(8.0, 16.0), (16.0, 30.0), (-30.0, -16.0), (-12.0, 40.0)])
+def test_sigmoid_gradient_of_confident_logits(lo, hi, renorm, dtype):
+    """s (1 - s) for s next to 1: the complement is not the rounded score's."""
+    M, E, k = 64, 48, 6
+    g = _gen(int(hi))
+    logits = (lo + (hi - lo) * torch.rand(M, E, generator=g, device="cuda")).to(dtype)
+    kw = dict(scoring=q.QMOE_GATE_SIGMOID, renormalize=renorm, scale=2.5)
+    ids, _ = q.moe_gate(logits, k, **kw)
+    dw = torch.randn(M, k, generator=g, device="cuda")
+    dl = q.moe_gate_backward(dw, logits, ids, **kw)
+    l = torch.gather(logits.double(), 1, ids.long())
+    s, rest, d = torch.sigmoid(l), torch.sigmoid(-l), dw.double()
+    inner, size, p = 0.0, d.abs(), s
+    if renorm:
+        p = s / (s.sum(1, keepdim=True) + 1e-20)
+        inner = (p * d).sum(1, keepdim=True)
+        size = size + (p * d.abs()).sum(1, keepdim=True)
+    want = 2.5 * p * rest * (d - inner)
+    got = torch.gather(dl, 1, ids.long()).double()
+    bound = 2.5 * p * rest * size * (4 * 2.0 ** -21 + (k + 8) * U)
+    # what bf16 rounds, and what is below fp32's normal numbers
+    bound = bound + torch.finfo(dtype).eps / 2 * want.abs() + 2.0 ** -126
+    assert ((got - want).abs() <= bound).all(), float(((got - want).abs() / want.abs()).max())
+    assert (got[want.abs() > 2.0 ** -120] != 0).all()
+    assert torch.count_nonzero(dl) <= M * k
