@@ -316,7 +316,8 @@ int qmoe_selftest_timeout(void* workspace_dev, long long limit_ns, void* stream)
  *                takes part in the choice, not in the weights
  *   n_group, topk_group  the experts are n_group equal runs (n_group <= 32 divides E);
  *                only the topk_group best are chosen from, a run counting by its largest
- *                choice value (softmax) or the sum of its two largest (sigmoid);
+ *                choice value (softmax) or the sum of its two largest (sigmoid; NaN, as
+ *                infinity and a masked expert's -infinity give, comes first);
  *                1, 1 for none
  *   renormalize  nonzero: the weights of a token's chosen experts sum to `scale`
  *                (softmax over the chosen; sigmoid scores over their sum + 1e-20);

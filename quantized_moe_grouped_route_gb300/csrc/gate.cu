@@ -31,6 +31,13 @@ __device__ __forceinline__ uint32_t order_key(float v) {
   return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);  // a negative's bits all turn
 }
 
+// ... of a group's score: the sum of an infinite choice value and a masked one is NaN, which
+// comes before all (compared as floats it came before none and none before it, so that one
+// group more than topk_group stayed).
+__device__ __forceinline__ uint32_t group_key(float v) {
+  return v == v ? order_key(v) : 0xffffffffu;
+}
+
 // The reciprocal is correctly rounded, so this is 1 / (1 + exp(-l)) to the bit.
 __device__ __forceinline__ float sigmoid_f32(float l) { return __frcp_rn(1.0f + expf(-l)); }
 
@@ -103,10 +110,10 @@ __device__ __forceinline__ uint32_t best_groups(const float* row, int E, int n_g
     b = fmaxf(lo, fmaxf(b, b2));
   }
   // a group of one expert has no second: it counts by that expert alone
-  const float score = top2 && size > 1 ? a + b : a;
+  const uint32_t score = group_key(top2 && size > 1 ? a + b : a);
   int rank = 0;
   for (int h = 0; h < n_group; ++h) {
-    const float s = __shfl_sync(0xffffffffu, score, h * per);
+    const uint32_t s = __shfl_sync(0xffffffffu, score, h * per);
     rank += s > score || (s == score && h < g);
   }
   const uint32_t lanes = __ballot_sync(0xffffffffu, g < n_group && sub == 0 && rank < topk_group);
@@ -188,11 +195,11 @@ __global__ void __launch_bounds__(kGateWarps * 32) gate_kernel(const GateArgs p)
         b = fmaxf(fminf(a, a2), fmaxf(b, b2));
         a = fmaxf(a, a2);
       }
-      const float score = sigmoid && p.E > p.n_group ? a + b : a;
+      const uint32_t score = group_key(sigmoid && p.E > p.n_group ? a + b : a);
       const int g = lane / p.group_lanes;
       int rank = 0;
       for (int h = 0; h < p.n_group; ++h) {
-        const float s = __shfl_sync(kAll, score, h * p.group_lanes);
+        const uint32_t s = __shfl_sync(kAll, score, h * p.group_lanes);
         rank += s > score || (s == score && h < g);
       }
       if (rank >= p.topk_group) {

@@ -49,3 +49,25 @@ def test_sigmoid_gradient_of_confident_logits(lo, hi, renorm, dtype):
     assert ((got - want).abs() <= bound).all(), float(((got - want).abs() / want.abs()).max())
     assert (got[want.abs() > 2.0 ** -120] != 0).all()
     assert torch.count_nonzero(dl) <= M * k
+
+
+@gpu
+@pytest.mark.parametrize("size", [3, 4, 8, 40])  # groups of whole lanes of a warp, and others
+def test_group_of_an_infinite_bias_and_masked_experts(size):
+    """An infinite choice value beside masked ones: the sum of the two largest is NaN.  The group
+    comes first, and no more than topk_group groups are chosen from."""
+    G = 4
+    l = torch.zeros(3, G * size, device="cuda")
+    bias = torch.zeros(G * size, device="cuda")
+    bias[2 * size] = math.inf
+    l[:, 2 * size + 1:3 * size] = -math.inf
+    l[0, size] = 3.0
+    l[1, :2 * size] = -math.inf
+    l[2, 2 * size] = -math.inf          # the infinite bias masked too
+    kw = dict(scoring=q.QMOE_GATE_SIGMOID, bias=bias, n_group=G)
+    ids, w = q.moe_gate(l, 2, topk_group=1, **kw)
+    assert ids.tolist() == [[2 * size, -1], [2 * size, -1], [0, 1]]
+    assert w.tolist() == [[1.0, 0.0], [1.0, 0.0], [0.5, 0.5]]
+    ids, _ = q.moe_gate(l, 3, topk_group=2, **kw)
+    assert ids.tolist() == [[2 * size, size, size + 1], [2 * size, 3 * size, 3 * size + 1],
+                            [0, 1, 2]]
