@@ -15,7 +15,6 @@
 namespace qmoe {
 namespace {
 
-constexpr int kMaxDevices = 64;
 // Per-device facts looked up once (0 = not yet known); atomics, since several host
 // threads may make their first calls at the same time.
 std::atomic<int> g_num_sms[kMaxDevices];

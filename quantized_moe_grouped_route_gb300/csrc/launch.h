@@ -5,7 +5,29 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 namespace qmoe {
+
+constexpr int kMaxDevices = 64;
+// Positive numbers that are looked up once per device, N of them; atomics, since several host
+// threads may make their first calls at the same time.
+template <int N>
+struct PerDevice {
+  std::atomic<int> kept[kMaxDevices][N] = {};  // 0: not yet known
+  // Number i of a device; look() gives it, or 0 or less if it cannot.
+  template <class F>
+  int get(int dev, int i, F&& look) {
+    if (dev < 0 || dev >= kMaxDevices) return 0;
+    int v = kept[dev][i].load(std::memory_order_relaxed);
+    if (v == 0) {
+      v = look();
+      if (v < 1) return 0;
+      kept[dev][i].store(v, std::memory_order_relaxed);
+    }
+    return v;
+  }
+};
 
 // route.cu
 constexpr int kRouteThreads = 512;

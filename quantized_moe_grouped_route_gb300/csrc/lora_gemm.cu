@@ -1,5 +1,4 @@
 // The GEMM of the projection with adapters (lora.cu describes it).
-#include <atomic>
 #include <type_traits>
 
 #include "cluster.cuh"
@@ -842,28 +841,22 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   }
 }
 
-// Clusters of `size` CTAs of a kernel that the device holds at once: asked of the runtime
-// once per size and kept (a property of the kernel and the device model).
+// Clusters of `size` CTAs of a kernel that the current device holds at once, 0 if it cannot say.
 template <class K>
-int resident_clusters(K* kernel, int size, int threads, size_t smem, std::atomic<int>& kept,
-                      int num_sms) {
-  int n = kept.load(std::memory_order_relaxed);
-  if (n == 0) {
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = size;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.gridDim = dim3(num_sms / size * size);
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1) return 0;
-    kept.store(n, std::memory_order_relaxed);
-  }
-  return n;
+int resident_clusters(K* kernel, int size, int threads, size_t smem, int num_sms) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = size;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.gridDim = dim3(num_sms / size * size);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  return cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess ? n : 0;
 }
 
 cudaError_t gemm_maps(const LoraArgs& p, CUtensorMap* x, CUtensorMap* w, CUtensorMap* b) {
@@ -898,12 +891,18 @@ cudaError_t run(LoraArgs& p, int num_sms, cudaStream_t stream) {
   e = allow_smem(k, kSmemLimit);
   if (e != cudaSuccess) return e;
   const int units = p.tiles * p.blocks;
-  static std::atomic<int> kept[3][kMaxSplits + 1];
+  int dev = -1;
+  e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  // asked of the runtime once per device, kernel and size (devices of one model can have their
+  // SMs in clusters of different sizes)
+  static PerDevice<3 * (kMaxSplits + 1)> clusters;
   auto clusters_of = [&](int splits) {
     const int size = p.cg * splits;
     if (size == 1) return num_sms;
-    return resident_clusters(k, size, kGemmThreads, smem, kept[vec ? 2 : p.cg - 1][splits],
-                             num_sms);
+    return clusters.get(dev, (vec ? 2 : p.cg - 1) * (kMaxSplits + 1) + splits, [&] {
+      return resident_clusters(k, size, kGemmThreads, smem, num_sms);
+    });
   };
   // Segments: where every unit's cluster is resident at once, each has 4 steps or more and a
   // CTA's sums fit over its ring, as many as there can be
