@@ -161,7 +161,7 @@ int moe_sort_tokens(const void* x_dev, int dtype, long long ldx, const int32_t* 
                                     s);
   if (e != cudaSuccess) return QMOE_ERR_CUDA;
   return cuda_rc(launch_sort_copy(x_dev, ldx * es, pair_pos_dev, offsets_dev + E, M, top_k,
-                                  (long long)H * es, chunk.bytes, xs_dev, sms, s));
+                                  (long long)H * es, chunk.bytes, xs_dev, s));
 }
 
 static int unsort_call(const void* y_dev, int dtype, long long ldy, const int32_t* pair_pos_dev,
@@ -191,7 +191,7 @@ static int unsort_call(const void* y_dev, int dtype, long long ldy, const int32_
   Chunk chunk;
   chunk.rows(y_dev, ldy, H, es);
   chunk.rows(out_dev, H, H, es);
-  return cuda_rc(launch_unsort(a, dtype, chunk.bytes / es, sms, reinterpret_cast<cudaStream_t>(stream)));
+  return cuda_rc(launch_unsort(a, dtype, chunk.bytes / es, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 int moe_sort_tokens_backward(const void* dxs_dev, int dtype, long long ld,

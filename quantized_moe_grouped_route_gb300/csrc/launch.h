@@ -185,7 +185,7 @@ cudaError_t launch_gate_backward(const GateArgs& p, int dtype, bool vec, int num
 // their stride and the pointers), zeros from row n_routed[0] on
 cudaError_t launch_sort_copy(const void* x, long long ldx_bytes, const int32_t* pair_pos,
                              const int32_t* n_routed, int M, int top_k, long long row_bytes,
-                             int chunk_bytes, void* xs, int num_sms, cudaStream_t stream);
+                             int chunk_bytes, void* xs, cudaStream_t stream);
 // the same with the route in one launch, at most kSortSmallPairs pairs
 cudaError_t launch_sort_small(const void* x, long long ldx_bytes, const int32_t* ids, int M,
                               int top_k, int E, long long row_bytes, int chunk_bytes, void* xs,
@@ -205,8 +205,7 @@ struct TokenArgs {
 };
 // chunk: elements that move together (1, 2, 4, or for 16-bit types 8), dividing every row,
 // stride and pointer
-cudaError_t launch_unsort(const TokenArgs& a, int dtype, int chunk, int num_sms,
-                          cudaStream_t stream);
+cudaError_t launch_unsort(const TokenArgs& a, int dtype, int chunk, cudaStream_t stream);
 cudaError_t launch_unsort_backward(const TokenArgs& a, int dtype, int chunk, int num_sms,
                                    cudaStream_t stream);
 

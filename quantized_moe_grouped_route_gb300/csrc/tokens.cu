@@ -316,7 +316,7 @@ cudaLaunchConfig_t config(long long blocks, int threads, cudaStream_t stream,
 template <class C>
 cudaError_t sort_copy(const void* x, long long ldx_bytes, const int32_t* pair_pos,
                       const int32_t* n_routed, int M, int top_k, long long row_bytes, void* xs,
-                      int num_sms, cudaStream_t stream) {
+                      cudaStream_t stream) {
   const int chunks = (int)(row_bytes / (long long)sizeof(C));
   const long long warps = (long long)M * ((chunks + 255) / 256);
   long long blocks = (warps * 32 + kTokThreads - 1) / kTokThreads;
@@ -329,7 +329,7 @@ cudaError_t sort_copy(const void* x, long long ldx_bytes, const int32_t* pair_po
 }
 
 template <class T, int N>
-cudaError_t unsort(const TokenArgs& a, int num_sms, cudaStream_t stream) {
+cudaError_t unsort(const TokenArgs& a, cudaStream_t stream) {
   const int chunks = a.H / N;
   const int per_warp = 32 * chunks_per_lane<T, N>();
   const long long warps = (long long)a.M * ((chunks + per_warp - 1) / per_warp);
@@ -367,10 +367,9 @@ cudaError_t unsort_backward(const TokenArgs& a, int num_sms, cudaStream_t stream
 
 cudaError_t launch_sort_copy(const void* x, long long ldx_bytes, const int32_t* pair_pos,
                              const int32_t* n_routed, int M, int top_k, long long row_bytes,
-                             int chunk_bytes, void* xs, int num_sms, cudaStream_t stream) {
+                             int chunk_bytes, void* xs, cudaStream_t stream) {
   auto go = [&](auto c) {
-    return sort_copy<decltype(c)>(x, ldx_bytes, pair_pos, n_routed, M, top_k, row_bytes, xs,
-                                  num_sms, stream);
+    return sort_copy<decltype(c)>(x, ldx_bytes, pair_pos, n_routed, M, top_k, row_bytes, xs, stream);
   };
   return chunk_bytes == 16  ? go(uint4{})
          : chunk_bytes == 8 ? go(uint2{})
@@ -399,19 +398,17 @@ cudaError_t launch_sort_small(const void* x, long long ldx_bytes, const int32_t*
 }
 
 template <class T>
-static cudaError_t unsort_chunk(const TokenArgs& a, int chunk, int num_sms, cudaStream_t stream) {
+static cudaError_t unsort_chunk(const TokenArgs& a, int chunk, cudaStream_t stream) {
   if constexpr (sizeof(T) == 2)
-    if (chunk == 8) return unsort<T, 8>(a, num_sms, stream);
-  return chunk == 4   ? unsort<T, 4>(a, num_sms, stream)
-         : chunk == 2 ? unsort<T, 2>(a, num_sms, stream)
-                      : unsort<T, 1>(a, num_sms, stream);
+    if (chunk == 8) return unsort<T, 8>(a, stream);
+  return chunk == 4 ? unsort<T, 4>(a, stream) : chunk == 2 ? unsort<T, 2>(a, stream)
+                                                           : unsort<T, 1>(a, stream);
 }
 
-cudaError_t launch_unsort(const TokenArgs& a, int dtype, int chunk, int num_sms,
-                          cudaStream_t stream) {
-  if (dtype == QMOE_DTYPE_BF16) return unsort_chunk<__nv_bfloat16>(a, chunk, num_sms, stream);
-  if (dtype == QMOE_DTYPE_FP16) return unsort_chunk<__half>(a, chunk, num_sms, stream);
-  return unsort_chunk<float>(a, chunk, num_sms, stream);
+cudaError_t launch_unsort(const TokenArgs& a, int dtype, int chunk, cudaStream_t stream) {
+  if (dtype == QMOE_DTYPE_BF16) return unsort_chunk<__nv_bfloat16>(a, chunk, stream);
+  if (dtype == QMOE_DTYPE_FP16) return unsort_chunk<__half>(a, chunk, stream);
+  return unsort_chunk<float>(a, chunk, stream);
 }
 
 template <class T>
