@@ -12,6 +12,6 @@ from .qmoe import (  # noqa: F401
     QMOE_W2, QMOE_SCALES_PLAIN, QMOE_SCALES_SWIZZLED_128X4)
 from .operators import (  # noqa: F401
     moe_gate, moe_gate_backward, moe_sort_tokens, moe_sort_tokens_backward, moe_unsort_tokens,
-    moe_unsort_tokens_backward, qmoe_lora_linear, qmoe_lora_workspace_size,
-    qmoe_sort_workspace_size, QMOE_DTYPE_BF16, QMOE_DTYPE_FP16, QMOE_DTYPE_FP32,
-    QMOE_GATE_SIGMOID, QMOE_GATE_SOFTMAX)
+    moe_unsort_tokens_backward, qmoe_default_read_error, qmoe_lora_linear,
+    qmoe_lora_workspace_size, qmoe_sort_workspace_size, QMOE_DTYPE_BF16, QMOE_DTYPE_FP16,
+    QMOE_DTYPE_FP32, QMOE_GATE_SIGMOID, QMOE_GATE_SOFTMAX)

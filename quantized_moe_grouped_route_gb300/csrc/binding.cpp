@@ -18,6 +18,7 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <array>
 #include <initializer_list>
 #include <sstream>
 #include <string>
@@ -80,6 +81,10 @@ int dtype_code(at::ScalarType t) {
   return t == at::kFloat ? QMOE_DTYPE_FP32 : -1;
 }
 
+// Operators whose default workspaces are kept.
+enum Kept { kSort, kLora, kKeptKinds };
+constexpr int kDevices = 64;
+
 // The device of a call: every tensor has to be on the current one.
 struct Call {
   c10::DeviceIndex dev = -1;
@@ -128,11 +133,21 @@ struct Call {
     dense(t, type, name, shape);
     return t;
   }
-  at::Tensor space(PyObject* o, size_t bytes) {
-    if (o == Py_None) return make(at::kByte, {(int64_t)(bytes < 256 ? 256 : bytes)});
+  at::Tensor space(PyObject* o, size_t bytes, Kept which) {
+    if (o == Py_None) {
+      kept(which) = at::Tensor();  // its memory may serve again
+      return make(at::kByte, {(int64_t)(bytes < 256 ? 256 : bytes)});
+    }
     const at::Tensor& t = tensor(o, "workspace");
     dense(t, at::kByte, "workspace", {t.numel()});
     return t;
+  }
+  // The workspace of the last call that brought none, for its error word (one per operator
+  // and device; never destroyed, since that could come after the CUDA context's end).
+  at::Tensor& kept(Kept which) const {
+    static auto* all = new std::array<at::Tensor, kDevices * kKeptKinds>();
+    if (dev < 0 || dev >= kDevices) fail("too many CUDA devices");
+    return (*all)[(size_t)(dev * kKeptKinds + which)];
   }
   // top_k of an [M][top_k] table
   int64_t slots(const at::Tensor& t, const char* name) {
@@ -235,12 +250,14 @@ PyObject* sort_tokens(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (M == 0) offsets.zero_();  // the call itself is a no-op then
     const at::Tensor pair = c.make(at::kInt, {M * k});
     const at::Tensor pos = c.make(at::kInt, {M, k});
-    const at::Tensor ws = c.space(a[4], qmoe_sort_workspace_size(small(M), small(k), (int)E));
+    const at::Tensor ws =
+        c.space(a[4], qmoe_sort_workspace_size(small(M), small(k), (int)E), kSort);
     check_rc("moe_sort_tokens",
              moe_sort_tokens(x.data_ptr(), dtype_code(x.scalar_type()), ldx, i32(ids), small(M),
                              small(H), small(k), (int)E, xs.data_ptr(), i32_out(offsets),
                              i32_out(pair), i32_out(pos), ws.data_ptr(), (size_t)ws.numel(),
                              c.stream()));
+    if (a[4] == Py_None && M > 0) c.kept(kSort) = ws;  // (no tokens: no error word)
     return pack({xs, offsets, pair, pos});
   });
 }
@@ -346,13 +363,36 @@ PyObject* lora_linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
     }
     const at::Tensor out = c.out(a[7], type, "out", {M, N});
     const at::Tensor ws = c.space(
-        a[8], qmoe_lora_workspace_size(small(M), small(K), small(N), small(R), small(L)));
+        a[8], qmoe_lora_workspace_size(small(M), small(K), small(N), small(R), small(L)), kLora);
     check_rc("qmoe_lora_linear",
              qmoe_lora_linear(x.data_ptr(), dtype_code(type), ldx, w, A.data_ptr(), B.data_ptr(),
                               i32(ids), f32(scales), base, ldb, out.data_ptr(), small(M), small(K),
                               small(N), small(R), small(L), ws.data_ptr(), (size_t)ws.numel(),
                               c.stream()));
+    if (a[8] == Py_None && M > 0) c.kept(kLora) = ws;
     return THPVariable_Wrap(out);
+  });
+}
+
+// The kept workspaces of the current device.
+PyObject* default_workspaces(PyObject*, PyObject* const*, Py_ssize_t n) {
+  return guarded(n, 0, [&]() -> PyObject* {
+    Call c;
+    c.dev = c10::cuda::current_device();
+    PyObject* r = PyList_New(0);
+    if (!r) throw Raised{};
+    for (int which = 0; which < kKeptKinds; ++which) {
+      const at::Tensor& t = c.kept((Kept)which);
+      if (!t.defined()) continue;
+      PyObject* o = THPVariable_Wrap(t);
+      const int rc = o ? PyList_Append(r, o) : -1;
+      Py_XDECREF(o);
+      if (rc != 0) {
+        Py_DECREF(r);
+        throw Raised{};
+      }
+    }
+    return r;
   });
 }
 
@@ -371,6 +411,7 @@ PyMethodDef kMethods[] = {FAST(gate),
                           FAST(unsort_tokens),
                           FAST(unsort_tokens_backward),
                           FAST(lora_linear),
+                          FAST(default_workspaces),
                           {"set_error", set_error, METH_O, nullptr},
                           {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "qmoe_torch", nullptr, -1, kMethods,

@@ -6,7 +6,9 @@ Activations are CUDA tensors of bf16, fp16 or fp32 whose rows may lie apart (str
 last dimension 1); outputs are contiguous and allocated unless given.  Calls run on
 ``stream`` (default: the current stream) and never synchronise.  A call's inputs must be
 ready on that stream; what it allocates belongs to that stream.  A tensor that does not fit
-raises ValueError, a refusal of the library QmoeError.
+raises ValueError, a refusal of the library QmoeError.  What a kernel finds (ids out of range,
+an expired wait) is in the error word at the start of a given workspace (qmoe_read_error), of
+calls that were given none in qmoe_default_read_error.
 
 Checks, allocations and the call itself are compiled (csrc/binding.cpp, qmoe_torch.so).
 """
@@ -55,6 +57,18 @@ def _on(stream):
     if not hasattr(stream, "cuda_stream"):
         stream = torch.cuda.ExternalStream(int(stream))
     return torch.cuda.stream(stream)
+
+
+def qmoe_default_read_error(stream=None):
+    """(return code, flags) of the last moe_sort_tokens and the last qmoe_lora_linear call on the
+    current device that were given no workspace, together; their workspaces are kept until the
+    next such call.  Synchronises the stream (default: the current one), on which, or before
+    which, those calls were made."""
+    rc, flags = qmoe.QMOE_OK, 0
+    for workspace in (_module or _native()).default_workspaces():
+        one, found = qmoe.qmoe_read_error(workspace, stream)
+        rc, flags = rc or one, flags | found
+    return rc, flags
 
 
 # ---------------------------------------------------------------------------- gate
