@@ -2,8 +2,10 @@
 the compiled part of operators.py.
 
 Each .cu file is compiled in parallel with nvcc, then linked into
-``quantized_moe_grouped_route_gb300/_lib/libqmoe.so``; the host compiler builds
-``_lib/qmoe_torch.so`` against it, PyTorch and Python.  Runs on a machine without a
+``quantized_moe_grouped_route_gb300/_lib/libqmoe.so``, which needs nothing of PyTorch; the host
+compiler builds ``_lib/qmoe_torch.so`` against it, PyTorch and Python, anew for another
+PyTorch or Python (``_build/qmoe_torch.for`` says which it was built for), and not at all where
+PyTorch has no CUDA (operators.py then says so when it is used).  Runs on a machine without a
 GPU (nvcc cross-compiles).  ``python -m quantized_moe_grouped_route_gb300.build``.
 """
 
@@ -24,6 +26,7 @@ BUILD = os.path.join(PKG, "_build")
 LIBDIR = os.path.join(PKG, "_lib")
 LIB = os.path.join(LIBDIR, "libqmoe.so")
 BINDING = os.path.join(LIBDIR, "qmoe_torch.so")
+BINDING_FOR = os.path.join(BUILD, "qmoe_torch.for")
 
 SOURCES = ["api.cu", "route.cu", "misc.cu", "gemm.cu", "gemm2.cu", "api_ops.cu", "gate.cu",
            "tokens.cu", "lora.cu", "lora_shrink.cu", "lora_gemm.cu"]
@@ -40,6 +43,27 @@ def nvcc() -> str:
 def _inputs_mtime() -> float:
     paths = [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + [os.path.join(INCLUDE, "qmoe.h")]
     return max(os.path.getmtime(p) for p in paths)
+
+
+def _torch_version():
+    """What qmoe_torch.so is built for: PyTorch's and Python's versions; None without a
+    PyTorch that has CUDA."""
+    try:
+        import torch
+    except ImportError:
+        return None
+    return f"{torch.__version__} {sys.version}" if torch.version.cuda else None
+
+
+def _fresh(path: str, newest: float) -> bool:
+    return os.path.exists(path) and os.path.getmtime(path) >= newest
+
+
+def _binding_fresh(version: str, newest: float) -> bool:
+    if not _fresh(BINDING, newest) or not os.path.exists(BINDING_FOR):
+        return False
+    with open(BINDING_FOR) as f:
+        return f.read() == version
 
 
 def _compile_binding() -> str:
@@ -59,7 +83,7 @@ def _compile_binding() -> str:
     return obj
 
 
-def _link_binding(obj: str):
+def _link_binding(obj: str, version: str):
     from torch.utils import cpp_extension
     tmp = BINDING + ".tmp"
     cmd = [os.environ.get("CXX", "g++"), "-shared", "-o", tmp, obj, LIB,
@@ -69,15 +93,29 @@ def _link_binding(obj: str):
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, BINDING)
+    with open(BINDING_FOR, "w") as f:
+        f.write(version)
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     newest = _inputs_mtime()
-    if not force and all(os.path.exists(f) and os.path.getmtime(f) >= newest
-                         for f in (LIB, BINDING)):
+    version = _torch_version()
+    want_lib = force or not _fresh(LIB, newest)
+    want_binding = version is not None and (force or not _binding_fresh(version, newest))
+    if not want_lib and not want_binding:
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     os.makedirs(LIBDIR, exist_ok=True)
+    with concurrent.futures.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        binding = ex.submit(_compile_binding) if want_binding else None
+        if want_lib:
+            _build_lib(ex, verbose, extra_flags)
+        if want_binding:
+            _link_binding(binding.result(), version)
+    return LIB
+
+
+def _build_lib(ex, verbose, extra_flags):
     cc = nvcc()
     common = [*ARCH, "-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE,
               "-I", CSRC, *extra_flags]
@@ -92,10 +130,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
             print(r.stdout, r.stderr, file=sys.stderr)
         return obj
 
-    with concurrent.futures.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        binding = ex.submit(_compile_binding)
-        objs = list(ex.map(compile_one, SOURCES))
-        binding = binding.result()
+    objs = list(ex.map(compile_one, SOURCES))
     tmp = LIB + ".tmp"
     cmd = [cc, *ARCH, "-shared", "-o", tmp, *objs, "-cudart", "static", "-Xlinker",
            "-soname=libqmoe.so"]
@@ -103,8 +138,6 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
-    _link_binding(binding)
-    return LIB
 
 
 if __name__ == "__main__":
