@@ -13,6 +13,7 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/core/GradMode.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -28,6 +29,7 @@
 namespace {
 
 PyObject* g_error = nullptr;  // operators.py's QmoeError
+PyObject* g_graph = nullptr;  // operators.py's _graph
 
 // What a function throws to leave with a Python exception already set.
 struct Raised {};
@@ -79,6 +81,30 @@ int dtype_code(at::ScalarType t) {
   if (t == at::kBFloat16) return QMOE_DTYPE_BF16;
   if (t == at::kHalf) return QMOE_DTYPE_FP16;
   return t == at::kFloat ? QMOE_DTYPE_FP32 : -1;
+}
+
+// Whether autograd has to know of a call on this argument.
+bool needs_gradient(PyObject* o) {
+  return o != Py_None && THPVariable_Check(o) && THPVariable_Unpack(o).requires_grad();
+}
+// The call `name` with n arguments again, from within a node of autograd's graph.
+PyObject* in_graph(const char* name, PyObject* const* a, Py_ssize_t n) {
+  PyObject* args = PyTuple_New(n + 1);
+  if (!args) throw Raised{};
+  PyObject* s = PyUnicode_FromString(name);
+  if (!s) {
+    Py_DECREF(args);
+    throw Raised{};
+  }
+  PyTuple_SET_ITEM(args, 0, s);
+  for (Py_ssize_t i = 0; i < n; ++i) {
+    Py_INCREF(a[i]);
+    PyTuple_SET_ITEM(args, i + 1, a[i]);
+  }
+  PyObject* r = PyObject_Call(g_graph, args, nullptr);
+  Py_DECREF(args);
+  if (!r) throw Raised{};
+  return r;
 }
 
 // Operators whose default workspaces are kept.
@@ -187,6 +213,8 @@ PyObject* guarded(Py_ssize_t given, Py_ssize_t wanted, F&& body) {
 // logits, top_k, scoring, bias, n_group, topk_group, renormalize, scale, ids, weights
 PyObject* gate(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 10, [&]() -> PyObject* {
+    if (c10::GradMode::is_enabled() && needs_gradient(a[0]))
+      return in_graph("gate", a, n);
     Call c;
     const at::Tensor& logits = tensor(a[0], "logits");
     const long long ld = c.rows(logits, "logits");
@@ -237,6 +265,8 @@ PyObject* gate_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
 // x, ids, E, xs, workspace
 PyObject* sort_tokens(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 5, [&]() -> PyObject* {
+    if (c10::GradMode::is_enabled() && needs_gradient(a[0]))
+      return in_graph("sort_tokens", a, n);
     Call c;
     const at::Tensor& x = tensor(a[0], "x");
     const long long ldx = c.rows(x, "x");
@@ -284,6 +314,8 @@ PyObject* sort_tokens_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
 // y, pair_pos, weights, out
 PyObject* unsort_tokens(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 4, [&]() -> PyObject* {
+    if (c10::GradMode::is_enabled() && (needs_gradient(a[0]) || needs_gradient(a[2])))
+      return in_graph("unsort_tokens", a, n);
     Call c;
     const at::Tensor& y = tensor(a[0], "y");
     const at::Tensor& pos = tensor(a[1], "pair_pos");
@@ -334,6 +366,9 @@ PyObject* unsort_tokens_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
 // x, w, lora_a, lora_b, ids, scales, base, out, workspace
 PyObject* lora_linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 9, [&]() -> PyObject* {
+    if (c10::GradMode::is_enabled())
+      for (int i : {0, 1, 2, 3, 5, 6})  // x, w, lora_a, lora_b, scales, base
+        if (needs_gradient(a[i])) return in_graph("lora_linear", a, n);
     Call c;
     const at::Tensor& x = tensor(a[0], "x");
     const at::Tensor& A = tensor(a[2], "lora_a");
@@ -402,6 +437,12 @@ PyObject* set_error(PyObject*, PyObject* cls) {
   Py_RETURN_NONE;
 }
 
+PyObject* set_graph(PyObject*, PyObject* f) {
+  Py_XINCREF(f);
+  Py_XSETREF(g_graph, f);
+  Py_RETURN_NONE;
+}
+
 #define FAST(name) \
   { #name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(name)), METH_FASTCALL, nullptr }
 PyMethodDef kMethods[] = {FAST(gate),
@@ -413,6 +454,7 @@ PyMethodDef kMethods[] = {FAST(gate),
                           FAST(lora_linear),
                           FAST(default_workspaces),
                           {"set_error", set_error, METH_O, nullptr},
+                          {"set_graph", set_graph, METH_O, nullptr},
                           {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "qmoe_torch", nullptr, -1, kMethods,
                        nullptr,              nullptr,      nullptr, nullptr};

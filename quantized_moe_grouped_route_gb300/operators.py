@@ -10,6 +10,11 @@ raises ValueError, a refusal of the library QmoeError.  What a kernel finds (ids
 an expired wait) is in the error word at the start of a given workspace (qmoe_read_error), of
 calls that were given none in qmoe_default_read_error.
 
+Autograd: moe_gate, moe_sort_tokens and moe_unsort_tokens on tensors that require a gradient
+are nodes of its graph, whose backward is the *_backward call of the same name (those calls
+have no derivative of their own); qmoe_lora_linear has none, and a gradient that comes to it
+raises NotImplementedError.  Such a call takes no outputs to write into.
+
 Checks, allocations and the call itself are compiled (csrc/binding.cpp, qmoe_torch.so).
 """
 
@@ -21,6 +26,7 @@ import os
 from typing import Optional
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import qmoe
 from .qmoe import QmoeError
@@ -48,6 +54,7 @@ def _native():
         module = importlib.util.module_from_spec(spec)
         loader.exec_module(module)
         module.set_error(QmoeError)
+        module.set_graph(_graph)
         _module = module
     return _module
 
@@ -69,6 +76,94 @@ def qmoe_default_read_error(stream=None):
         one, found = qmoe.qmoe_read_error(workspace, stream)
         rc, flags = rc or one, flags | found
     return rc, flags
+
+
+# ------------------------------------------------------------------------ autograd
+def _rows(t: torch.Tensor) -> torch.Tensor:
+    """A gradient as the library takes rows: their elements next to each other."""
+    apart = t.stride(0) if t.size(0) > 1 else t.size(1)
+    fits = (t.size(1) < 2 or t.stride(1) == 1) and (apart == 0 or apart >= t.size(1))
+    return t if fits else t.contiguous()
+
+
+class _Gate(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, top_k, scoring, bias, n_group, topk_group, renormalize, scale, ids,
+                weights):
+        ids, weights = _native().gate(logits, top_k, scoring, bias, n_group, topk_group,
+                                      renormalize, scale, ids, weights)
+        ctx.save_for_backward(logits, ids)
+        ctx.how = (scoring, renormalize, scale)
+        ctx.mark_non_differentiable(ids)
+        return ids, weights
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, _, dweights):
+        logits, ids = ctx.saved_tensors
+        dlogits = _native().gate_backward(dweights.contiguous(), logits, ids, *ctx.how, None)
+        return (dlogits,) + 9 * (None,)
+
+
+class _SortTokens(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, ids, E, xs, workspace):
+        xs, *tables = _native().sort_tokens(x, ids, E, xs, workspace)
+        ctx.save_for_backward(tables[2])
+        ctx.mark_non_differentiable(*tables)
+        return (xs, *tables)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dxs, *_):
+        dx = _native().sort_tokens_backward(_rows(dxs), *ctx.saved_tensors, None)
+        return (dx,) + 4 * (None,)
+
+
+class _UnsortTokens(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, y, pair_pos, weights, out):
+        ctx.save_for_backward(y, pair_pos, weights)
+        return _native().unsort_tokens(y, pair_pos, weights, out)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dout):
+        y, pair_pos, weights = ctx.saved_tensors
+        # sorted_pair from its inverse; pairs without a row write past the end
+        P = pair_pos.numel()
+        pos = pair_pos.reshape(-1).long()
+        pos = torch.where((pos >= 0) & (pos < P), pos, P)
+        pairs = torch.arange(P, dtype=torch.int32, device=y.device)
+        sorted_pair = pairs.new_full((P + 1,), -1).scatter_(0, pos, pairs)[:P]
+        dy, dweights = _native().unsort_tokens_backward(_rows(dout), y, sorted_pair, pair_pos,
+                                                        weights, None, None)
+        return dy, None, dweights, None
+
+
+class _LoraLinear(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, *args):
+        return _native().lora_linear(*args)
+
+    @staticmethod
+    def backward(ctx, _):
+        raise NotImplementedError("qmoe_lora_linear has no gradient: call it under torch.no_grad() "
+                                  "or on detached tensors")
+
+
+# of each call the node, and which of its arguments are outputs
+_NODES = {"gate": (_Gate, (8, 9)), "sort_tokens": (_SortTokens, (3,)),
+          "unsort_tokens": (_UnsortTokens, (3,)), "lora_linear": (_LoraLinear, (7,))}
+
+
+def _graph(name, *args):
+    """A call on tensors that require a gradient (the compiled part hands it over)."""
+    node, outputs = _NODES[name]
+    if any(args[i] is not None for i in outputs):
+        raise ValueError("a call on tensors that require a gradient returns new tensors: no "
+                         "output to write into can be given (or call it under torch.no_grad())")
+    return node.apply(*args)
 
 
 # ---------------------------------------------------------------------------- gate
