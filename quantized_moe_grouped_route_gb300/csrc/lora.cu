@@ -39,7 +39,7 @@
 //               build a step, so that several steps are in the making at once
 //
 // Few tokens of few ranks (VEC: at most 64 tokens, tokens * ranks at most 512 or, where there
-// are adapters enough for one each, 1536: a decode step's requests) do not take the adapters
+// are adapters enough for one each, 1024: a decode step's requests) do not take the adapters
 // through the MMA, where each is a step for one or two tokens.  There warp 2
 // brings in B[a]'s rows, which lie next to each other, as one bulk copy each, while w
 // streams; the builder warps multiply them with t in fp32, and the epilogue adds what they

@@ -34,14 +34,19 @@ __host__ __device__ constexpr int token_slots(int tile_n, int cg, int R) {
 // of a slot take all of its steps, since a wait on a phase's parity cannot tell it from the
 // phase after the next (six slots among eight warps ran into that and timed out).
 //
-// Where it is taken: up to 64 tokens and 512 token-ranks, and up to 1536 where there are as many
-// adapters as tokens.  48 tokens, K = 2048, N = 7168, R = 32: 43 adapters 16.7 us a call, with
-// MMAs 17.9; 14 adapters 17.6 and 14.9, a few 16.9 and 13.4.  64 tokens, R = 32: 44 adapters
-// 19.2 and 19.7, a few 22.2 and 13.8.  32 tokens, R = 16: 26 adapters 12.3 and 14.3.
+// Where it is taken: up to 64 tokens and 512 token-ranks, 1024 where at least as many adapters
+// are loaded as there are tokens.  How many of them the tokens use is not known on the host: VEC
+// pays for tokens, MMAs for distinct adapters.  Time of a call against the MMA form's, by the
+// adapters that 16 to 64 tokens of K = N = 4096 and of K = 2048, N = 7168 use:
+//   token-ranks   512          768          1024         1536         2048
+//   one each      0.70 - 0.91  0.79 - 0.81  0.77 - 0.89  0.81 - 0.82  0.82 - 0.98
+//   0.4 a token   0.87 - 0.96  0.92 - 1.01  0.91 - 1.03  0.99 - 1.07  0.97 - 1.16
+//   four          0.96 - 1.07  1.02 - 1.18  0.98 - 1.25  1.16 - 1.31  1.11 - 1.41
+// so 1024 loses least at worst: 1.25 inside, 1 / 0.81 outside.
 constexpr int kVecTokens = 64;
-__host__ constexpr int vec_token_ranks(int tokens, int L) { return L >= tokens ? 1536 : 512; }
+__host__ constexpr int vec_token_ranks(int tokens, int L) { return L >= tokens ? 1024 : 512; }
 __host__ __device__ constexpr int vec_slot_bytes(int R) { return 128 * R * 2; }
-__host__ __device__ constexpr int vec_slots(int R) { return R <= 32 ? 8 : R <= 64 ? 4 : 2; }
+__host__ __device__ constexpr int vec_slots(int R) { return R <= 32 ? 8 : 4; }
 
 // Bytes of shared memory behind the ring (multiples of 1024 each): the builders' slots, and
 // (VEC) their copy of t and what they leave for the epilogue [tokens][128] in fp32.
@@ -410,9 +415,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     }
   } else if (VEC && warp >= 8) {
     // ------------------------------------------------------------- VEC: t . B^T in fp32
-    // A slot's adapter is one to four warps' work (the more, the longer its rows), a lane
-    // having four to one of the 128 rows: several adapters are in the making, with several
-    // sums a lane in flight (two groups of four warps, a row a thread, took 0.65 us a step).
+    // A slot's adapter is one or two warps' work, a lane having four or two of the 128 rows:
+    // several adapters are in the making, with several sums a lane in flight (two groups of four
+    // warps, a row a thread, took 0.65 us a step).
     // delta holds this CTA's tokens seg, seg + S, .. one after the other.  A row is read in
     // 16-byte chunks from a place of its own on, so that eight neighbouring rows' chunks lie
     // in different banks.

@@ -68,6 +68,10 @@ RANGES = [  # M, K, N, R, L, with w, with base: every form of the projection abo
     (128, 1024, 384, 64, 90, False, False), (70, 136, 200, 24, 4, False, True),
     (300, 264, 515, 8, 9, True, False), (1100, 128, 300, 40, 6, False, False),
     (256, 4096, 96, 24, 40, True, False), (600, 2048, 640, 128, 3, True, True),
+    # fp32 products beside w, at the edges of their range
+    (16, 256, 260, 64, 16, True, False), (32, 264, 260, 32, 40, True, True),
+    (64, 1024, 300, 16, 64, False, False), (64, 264, 512, 8, 5, True, False),
+    (32, 264, 260, 40, 40, True, False), (16, 136, 130, 72, 20, True, True),
 ]
 
 
