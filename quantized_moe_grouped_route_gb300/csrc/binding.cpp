@@ -74,6 +74,11 @@ int64_t integer(PyObject* o) {
   if (v == -1 && PyErr_Occurred()) throw Raised{};
   return v;
 }
+int truth(PyObject* o) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) throw Raised{};
+  return v;
+}
 // A size for the C ABI: out of int's range is out of every limit of the library too.
 int small(int64_t v) { return v < -1 ? -1 : v > INT32_MAX ? INT32_MAX : (int)v; }
 
@@ -233,7 +238,7 @@ PyObject* gate(PyObject*, PyObject* const* a, Py_ssize_t n) {
     check_rc("moe_gate",
              moe_gate(logits.data_ptr(), dtype_code(logits.scalar_type()), ld, small(M), small(E),
                       (int)k, small(integer(a[2])), bias, small(integer(a[4])),
-                      small(integer(a[5])), PyObject_IsTrue(a[6]), (float)scale, i32_out(ids),
+                      small(integer(a[5])), truth(a[6]), (float)scale, i32_out(ids),
                       f32(w), c.stream()));
     return pack({ids, w});
   });
@@ -257,7 +262,7 @@ PyObject* gate_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     check_rc("moe_gate_backward",
              moe_gate_backward(f32(dw), logits.data_ptr(), dtype_code(logits.scalar_type()), ld,
                                i32(ids), small(M), small(E), small(k), small(integer(a[3])),
-                               PyObject_IsTrue(a[4]), (float)scale, dl.data_ptr(), c.stream()));
+                               truth(a[4]), (float)scale, dl.data_ptr(), c.stream()));
     return THPVariable_Wrap(dl);
   });
 }

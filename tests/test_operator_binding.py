@@ -162,3 +162,14 @@ def test_what_autograd_cannot_have_is_refused():
     x = t(4, 8, device="cuda", requires_grad=True)
     with pytest.raises(ValueError):  # a call's own refusals stay
         q.moe_gate(x.t()[:, ::2], 2)
+
+
+@gpu
+def test_a_flag_without_a_truth_value():
+    logits = torch.zeros(4, 8, device="cuda")
+    both = torch.tensor([True, False])
+    with pytest.raises(RuntimeError, match="ambiguous"):
+        q.moe_gate(logits, 2, renormalize=both)
+    ids, w = q.moe_gate(logits, 2)
+    with pytest.raises(RuntimeError, match="ambiguous"):
+        q.moe_gate_backward(w, logits, ids, renormalize=both)
