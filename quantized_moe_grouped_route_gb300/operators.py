@@ -5,7 +5,8 @@ low-rank adapters.
 Activations are CUDA tensors of bf16, fp16 or fp32 whose rows may lie apart (stride of the
 last dimension 1); outputs are contiguous and allocated unless given.  Calls run on
 ``stream`` (default: the current stream) and never synchronise.  A call's inputs must be
-ready on that stream; what it allocates belongs to that stream.  A tensor that does not fit
+ready on that stream; what it allocates belongs to that stream (tensors that another stream
+uses too need record_stream, as for torch's own calls).  A tensor that does not fit
 raises ValueError, a refusal of the library QmoeError.  What a kernel finds (ids out of range,
 an expired wait) is in the error word at the start of a given workspace (qmoe_read_error), of
 calls that were given none in qmoe_default_read_error.
