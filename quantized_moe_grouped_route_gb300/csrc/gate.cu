@@ -365,17 +365,21 @@ __global__ void __launch_bounds__(kGateWarps * 32) gate_backward_kernel(const Ga
 #pragma unroll
       for (int i = 0; i < 2; ++i)
         if (i < nslot && e[i] >= 0) s[i] = sigmoid_f32(lv[i]);
-      float total = 1.f, inner = 0.f;
-      if (p.renormalize) {
-        total = warp_sum(s[0] + s[1]) + 1e-20f;
-        inner = warp_sum(s[0] * dw[0] + s[1] * dw[1]) / total;
-      }
       // 1 - s as the score of -l: from the rounded s it keeps no bits where s is next to 1
       // (at l = 10 it was off by 0.1 %, from 17 on it was 0)
+      float rest[2], inner = 0.f;
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
-        if (i < nslot && e[i] >= 0)
-          d[i] = p.scale * (s[i] / total) * sigmoid_f32(-lv[i]) * (dw[i] - inner);
+      for (int i = 0; i < 2; ++i) rest[i] = i < nslot && e[i] >= 0 ? sigmoid_f32(-lv[i]) : 0.f;
+      if (p.renormalize) {
+        // the weights first, as the softmax below: a single expert's is 1 and its gradient 0
+        // (with sum s dw / S something of dw's last bit remained)
+        const float total = warp_sum(s[0] + s[1]) + 1e-20f;
+        s[0] /= total;
+        s[1] /= total;
+        inner = warp_sum(s[0] * dw[0] + s[1] * dw[1]);
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) d[i] = p.scale * s[i] * rest[i] * (dw[i] - inner);
     } else {
       float total = 0.f;
       if (p.renormalize) {

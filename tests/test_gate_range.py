@@ -71,3 +71,21 @@ def test_group_of_an_infinite_bias_and_masked_experts(size):
     ids, _ = q.moe_gate(l, 3, topk_group=2, **kw)
     assert ids.tolist() == [[2 * size, size, size + 1], [2 * size, 3 * size, 3 * size + 1],
                             [0, 1, 2]]
+
+
+@gpu
+@pytest.mark.parametrize("sigmoid", [False, True])
+@pytest.mark.parametrize("masked", [False, True])
+def test_a_single_renormalized_expert_has_no_gradient(sigmoid, masked):
+    """Its weight is `scale` whatever its logit; with masks, rows of top_k 3 with one expert."""
+    g = _gen(9)
+    M, E, k = 500, 40, 3 if masked else 1
+    logits = torch.randn(M, E, generator=g, device="cuda")
+    if masked:
+        one = torch.randint(0, E, (M, 1), generator=g, device="cuda")
+        logits = torch.full_like(logits, -math.inf).scatter_(1, one, logits)
+    kw = dict(scoring=int(sigmoid), renormalize=True, scale=2.5)
+    ids, w = q.moe_gate(logits, k, **kw)
+    assert (w[:, 0] == 2.5).all()
+    dl = q.moe_gate_backward(torch.randn(M, k, generator=g, device="cuda"), logits, ids, **kw)
+    assert torch.count_nonzero(dl) == 0
