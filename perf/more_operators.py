@@ -92,9 +92,10 @@ def draw(rng):
         c = _checkpoint("", M, H, dtype=dtype, pad=rng.choice([0, 0, 8, 3]))
     else:
         first = rng.random() < 0.2  # the norm before a model's first block: nothing to add to
+        forms = ["none", "token", "channel"] + ["full"] * (M > 1)
         c = _norm("", M, H, dtype=dtype, residual=not first, post=not first and rng.random() < 0.7,
                   pre=first or rng.random() < 0.8,
-                  gate="none" if first else rng.choice(["none", "token", "channel", "full"]),
+                  gate="none" if first else rng.choice(forms),
                   sigmoid=rng.random() < 0.5, scale=rng.choice([1.0, 1.0, 0.5]),
                   offset=rng.choice([0.0, 1.0]), pad=rng.choice([0, 0, 8, 3]),
                   direction=rng.choice(["forward", "backward"]))
