@@ -406,6 +406,138 @@ int qmoe_lora_linear(const void* x_dev, int dtype, long long ldx, const void* w_
                      void* out_dev, int M, int K, int N, int R, int L, void* workspace_dev,
                      size_t ws_bytes, void* stream);
 
+/*
+ * ------------------------------------------------------------------------------------
+ * The dense side of a block: the norms around it fused with its gate and residual, the gated
+ * feed-forward block (a shared expert next to the layer's, or a dense layer's), and activation
+ * checkpoints in 8 bits.  Conventions as for the operators above; M < 2^27.
+ */
+
+/* How a block's gate multiplies: as given, or as its sigmoid. */
+#define QMOE_GATING_LINEAR 0
+#define QMOE_GATING_SIGMOID 1
+/* What a gate is given for: each token, each channel, or each element. */
+#define QMOE_GATE_TOKEN 0
+#define QMOE_GATE_CHANNEL 1
+#define QMOE_GATE_FULL 2
+
+/*
+ * qmoe_block_norm — the norm after a block, the block's gate, the residual and the norm before the
+ * next block, in one pass over the rows:
+ *   v[m]      = y[m] * post_rstd[m] * (weight_offset + post_weight)    (v = y without post_weight)
+ *   out[m]    = residual_scale * residual[m] + gate * v[m]             (no residual: the gate's part)
+ *   normed[m] = out[m] * pre_rstd[m] * (weight_offset + pre_weight)
+ *   post_rstd[m] = 1 / sqrt(mean(y[m]^2) + eps), pre_rstd[m] likewise of out[m] before its rounding
+ *   y_dev       [M][H] of `dtype`, rows ldy apart; 1 <= H <= 65536
+ *   residual_dev [M][H], rows ldr apart, or NULL
+ *   gate_dev    of `dtype` or fp32 (gate_dtype), or NULL for 1; gate_form QMOE_GATE_TOKEN: [M],
+ *               elements ldgate apart (0: the same for all); _CHANNEL: [H]; _FULL: [M][H], rows
+ *               ldgate apart.  gating QMOE_GATING_*
+ *   post_weight_dev, pre_weight_dev  [H] of `dtype` or fp32 (weight_dtype); NULL: no such norm
+ *   out_dev     [M][H]; may be residual_dev or y_dev (rows H apart) itself.  NULL where it is not
+ *               wanted, as without residual, gate and post_weight, where it would be y
+ *   normed_dev  [M][H], with pre_weight_dev and only then
+ *   post_rstd_dev, pre_rstd_dev  fp32 [M] or NULL; what the backward pass needs of the norms
+ * Sums are fp32; fp32 rows whose squares' sum passes the range of fp32 give rstd 0.
+ */
+int qmoe_block_norm(const void* y_dev, int dtype, long long ldy, const void* residual_dev,
+                    long long ldr, float residual_scale, const void* gate_dev, int gate_dtype,
+                    int gate_form, long long ldgate, int gating, const void* post_weight_dev,
+                    const void* pre_weight_dev, int weight_dtype, float weight_offset, float eps,
+                    int M, int H, void* out_dev, void* normed_dev, float* post_rstd_dev,
+                    float* pre_rstd_dev, void* stream);
+
+/*
+ * qmoe_block_norm_backward — gradients of qmoe_block_norm, for the same arguments.
+ *   dout_dev, dnormed_dev  [M][H], rows lddout and lddnormed apart: gradients of out and normed;
+ *               dout_dev NULL for none, dnormed_dev with pre_weight_dev and only then
+ *   out_dev     [M][H], rows ldout apart: qmoe_block_norm's out, read with pre_weight_dev alone;
+ *               NULL: it was y (no residual, gate and post_weight)
+ *   post_rstd_dev, pre_rstd_dev  as qmoe_block_norm left them, where it has those norms
+ *   dy_dev      [M][H];  dresidual_dev [M][H] or NULL
+ *   dgate_dev   NULL, or fp32 [M] (_TOKEN), fp32 [H] (_CHANNEL), [M][H] of `dtype` (_FULL): the
+ *               gradient of the gate as given
+ *   dpost_weight_dev, dpre_weight_dev  fp32 [H] or NULL
+ *   workspace_dev >= qmoe_block_norm_backward_workspace_size(M, H) bytes, 256-byte aligned
+ * Outputs overlap no input.  M == 0: sums over tokens are set to 0.
+ */
+size_t qmoe_block_norm_backward_workspace_size(int M, int H);
+int qmoe_block_norm_backward(const void* dout_dev, long long lddout, const void* dnormed_dev,
+                             long long lddnormed, const void* y_dev, int dtype, long long ldy,
+                             const void* out_dev, long long ldout, float residual_scale,
+                             const void* gate_dev, int gate_dtype, int gate_form, long long ldgate,
+                             int gating, const void* post_weight_dev, const void* pre_weight_dev,
+                             int weight_dtype, float weight_offset, const float* post_rstd_dev,
+                             const float* pre_rstd_dev, int M, int H, void* dy_dev,
+                             void* dresidual_dev, void* dgate_dev, float* dpost_weight_dev,
+                             float* dpre_weight_dev, void* workspace_dev, size_t ws_bytes,
+                             void* stream);
+
+/*
+ * qmoe_checkpoint8 — activations in 8 bits: each block of 32 neighbouring columns of a row (the
+ * last may be shorter) has codes within 127 and one scale, the least power of two for which they
+ * are, at least 2^-127:
+ *   x = code * 2^(scale - 127), off by at most half a step; code is rounded to nearest even
+ * Scale 255: a block with an infinity or NaN, all of which is restored as NaN.
+ *   x_dev [M][C] of `dtype`, rows ldx apart, 1 <= C <= 2^20
+ *   codes_dev [M][C], scales_dev [M][ceil(C / 32)]
+ * qmoe_checkpoint8_restore — the values that codes and scales stand for, within the finite range
+ * of `dtype`: out_dev [M][C].
+ */
+int qmoe_checkpoint8(const void* x_dev, int dtype, long long ldx, int M, int C, int8_t* codes_dev,
+                     uint8_t* scales_dev, void* stream);
+int qmoe_checkpoint8_restore(const int8_t* codes_dev, const uint8_t* scales_dev, int dtype, int M,
+                             int C, void* out_dev, void* stream);
+
+/* Activations of the gated feed-forward block. */
+#define QMOE_ACT_SILU 0
+#define QMOE_ACT_GELU 1 /* in its tanh form */
+
+/*
+ * qmoe_gated_ffn — the gated feed-forward block of 16-bit weights:
+ *   [u | g] = x . w13^T,  h = act(min(g, limit)) * clamp(u, -limit, limit),  out = h . w2^T
+ *   x_dev    bf16 or fp16 [M][H], rows ldx apart;  w13_dev [2I][H], rows 0..I-1 up, I..2I-1 gate,
+ *            as the layer's;  w2_dev [H][I];  out_dev [M][H]
+ *   limit    the layer's SwiGLU limit: positive, +infinity for none
+ *   kept_dev, kept_scales_dev  what the backward pass needs of u and g: both NULL for nothing;
+ *            kept_dev alone: [M][2I] of `dtype`, u beside g; both: as qmoe_checkpoint8 has them,
+ *            codes [M][2I] and scales [M][2][ceil(I / 32)], blocks of u and of g counted apart
+ * u, g and h are fp32 sums and products; h is rounded to `dtype`, in which it enters the second
+ * product.  H % 8 == 0, I % 8 == 0, 8 <= H, I <= 65536; x, w13, w2, out and kept are 16-byte
+ * aligned and ldx is a multiple of 8.
+ *   workspace_dev >= qmoe_gated_ffn_workspace_size(M, H, I) bytes, 256-byte aligned, starting with
+ *            the error word
+ */
+size_t qmoe_gated_ffn_workspace_size(int M, int H, int I);
+int qmoe_gated_ffn(const void* x_dev, int dtype, long long ldx, const void* w13_dev,
+                   const void* w2_dev, int activation, float limit, int M, int H, int I,
+                   void* out_dev, void* kept_dev, uint8_t* kept_scales_dev, void* workspace_dev,
+                   size_t ws_bytes, void* stream);
+
+/*
+ * qmoe_gated_ffn_backward — gradients of qmoe_gated_ffn from what it kept:
+ *   dh = dout . w2,  [du | dg] = dh * (h's derivatives),
+ *   dx = [du | dg] . w13,  dw13 = [du | dg]^T . x,  dw2 = dout^T . h
+ *   dout_dev [M][H], rows lddout apart
+ *   x_dev    [M][H], rows ldx apart; or with x_scales_dev its codes and scales (qmoe_checkpoint8,
+ *            ldx = H), where kept_scales_dev is given too and only then
+ *   kept_dev, kept_scales_dev  as qmoe_gated_ffn left them
+ *   dx_dev [M][H], dw13_dev [2I][H], dw2_dev [H][I] of `dtype`; NULL where not wanted
+ * What the clamp holds has no gradient.  h, du and dg are rounded to `dtype`, in which they enter
+ * the products; sums are fp32.  Limits and alignment as above (codes of x: 8 bytes; dout and the
+ * outputs: 16 bytes, lddout a multiple of 8).
+ *   workspace_dev >= qmoe_gated_ffn_backward_workspace_size(M, H, I, 16, or 8 with codes) bytes,
+ *            256-byte aligned, starting with the error word
+ * M == 0: the weights' gradients are set to 0.
+ */
+size_t qmoe_gated_ffn_backward_workspace_size(int M, int H, int I, int checkpoint);
+int qmoe_gated_ffn_backward(const void* dout_dev, int dtype, long long lddout, const void* x_dev,
+                            long long ldx, const uint8_t* x_scales_dev, const void* w13_dev,
+                            const void* w2_dev, const void* kept_dev,
+                            const uint8_t* kept_scales_dev, int activation, float limit, int M,
+                            int H, int I, void* dx_dev, void* dw13_dev, void* dw2_dev,
+                            void* workspace_dev, size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

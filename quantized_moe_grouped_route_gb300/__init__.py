@@ -15,3 +15,8 @@ from .operators import (  # noqa: F401
     moe_unsort_tokens_backward, qmoe_default_read_error, qmoe_lora_linear,
     qmoe_lora_workspace_size, qmoe_sort_workspace_size, QMOE_DTYPE_BF16, QMOE_DTYPE_FP16,
     QMOE_DTYPE_FP32, QMOE_GATE_SIGMOID, QMOE_GATE_SOFTMAX)
+from .block import (  # noqa: F401
+    qmoe_block_norm, qmoe_block_norm_backward, qmoe_checkpoint8, qmoe_checkpoint8_restore,
+    qmoe_gated_ffn, qmoe_gated_ffn_backward, qmoe_gated_ffn_backward_workspace_size,
+    qmoe_gated_ffn_saved, qmoe_gated_ffn_workspace_size, QMOE_ACT_GELU, QMOE_ACT_SILU,
+    QMOE_GATING_LINEAR, QMOE_GATING_SIGMOID)

@@ -4,13 +4,10 @@
 
 #include "common.cuh"
 #include "launch.h"
+#include "rows.h"
 
 namespace qmoe {
 namespace {
-
-int elem_size(int dtype) { return dtype == QMOE_DTYPE_FP32 ? 4 : 2; }
-
-bool known_dtype(int dtype) { return dtype >= QMOE_DTYPE_BF16 && dtype <= QMOE_DTYPE_FP32; }
 
 int check_tokens(int dtype, int M, int H, int top_k) {
   if (!known_dtype(dtype)) return QMOE_ERR_ARG;
@@ -18,28 +15,6 @@ int check_tokens(int dtype, int M, int H, int top_k) {
   if ((long long)M * top_k >= (1LL << 31) / 16) return QMOE_ERR_SHAPE;
   return QMOE_OK;
 }
-
-bool misaligned(const void* p, int bytes) { return (reinterpret_cast<uintptr_t>(p) % bytes) != 0; }
-
-// A stride of 0 stands for the same row throughout.
-bool bad_ld(long long ld, int width) { return ld < width && ld != 0; }
-
-// Whether every row of `rows` (stride ld elements, length H) can move in chunks of `bytes`.
-bool chunked(const void* rows, long long ld, int H, int es, int bytes) {
-  return !misaligned(rows, bytes) && ld * es % bytes == 0 && (long long)H * es % bytes == 0;
-}
-
-int cuda_rc(cudaError_t e) { return e == cudaSuccess ? QMOE_OK : QMOE_ERR_CUDA; }
-
-size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
-
-// Bytes of the widest chunk (at most 16) in which every one of some matrices' rows moves.
-struct Chunk {
-  int bytes = 16;
-  void rows(const void* p, long long ld, int H, int es) {
-    while (bytes > es && !chunked(p, ld, H, es, bytes)) bytes >>= 1;
-  }
-};
 
 }  // namespace
 }  // namespace qmoe

@@ -113,7 +113,7 @@ PyObject* in_graph(const char* name, PyObject* const* a, Py_ssize_t n) {
 }
 
 // Operators whose default workspaces are kept.
-enum Kept { kSort, kLora, kKeptKinds };
+enum Kept { kSort, kLora, kFfn, kFfnBackward, kKeptKinds };
 constexpr int kDevices = 64;
 
 // The device of a call: every tensor has to be on the current one.
@@ -414,6 +414,314 @@ PyObject* lora_linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+bool given(PyObject* o) { return o != Py_None; }
+void* data(const at::Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; }
+double real(PyObject* o) {
+  const double v = PyFloat_AsDouble(o);
+  if (PyErr_Occurred()) throw Raised{};
+  return v;
+}
+PyObject* wrap_or_none(const at::Tensor& t) {
+  if (t.defined()) return THPVariable_Wrap(t);
+  Py_RETURN_NONE;
+}
+PyObject* pack_some(std::initializer_list<at::Tensor> ts) {
+  PyObject* r = PyTuple_New((Py_ssize_t)ts.size());
+  if (!r) throw Raised{};
+  Py_ssize_t i = 0;
+  for (const at::Tensor& t : ts) PyTuple_SET_ITEM(r, i++, wrap_or_none(t));
+  return r;
+}
+
+// What the forward and backward calls of the norms around a block have in common.
+struct Norms {
+  int type = 0, weight_type = 0;
+  int64_t M = 0, H = 0;
+  at::Tensor gate, post, pre;
+  int gate_type = 0, gate_form = 0, gating = 0;
+  long long ldgate = 0;
+
+  // gate, gating, post_weight, pre_weight
+  void take(Call& c, const at::Tensor& y, PyObject* g, PyObject* how, PyObject* post_weight,
+            PyObject* pre_weight) {
+    M = y.size(0), H = y.size(1);
+    type = gate_type = weight_type = dtype_code(y.scalar_type());
+    gating = small(integer(how));
+    if (given(g)) {
+      gate = tensor(g, "gate");
+      gate_type = of_either(y, gate, "gate");
+      if (gate.dim() != 2 || gate.layout() != at::kStrided)
+        fail("gate: need [M][1], [1][H] or [M][H]");
+      const int64_t n = gate.size(0), w = gate.size(1);
+      if (n == M && w == 1) {  // (also of a row of one element)
+        gate_form = QMOE_GATE_TOKEN;
+        c.here(gate, "gate");
+        ldgate = M > 1 ? gate.stride(0) : 1;
+      } else if (n == 1 && w == H) {
+        gate_form = QMOE_GATE_CHANNEL;
+        c.rows(gate, "gate");
+      } else {
+        gate_form = QMOE_GATE_FULL;
+        ldgate = c.rows(gate, "gate", M, H);
+      }
+    }
+    vector(c, y, post_weight, "post_weight", &post);
+    vector(c, y, pre_weight, "pre_weight", &pre);
+    if (post.defined() && pre.defined() && post.scalar_type() != pre.scalar_type())
+      fail("post_weight, pre_weight: need one dtype");
+  }
+  static int of_either(const at::Tensor& y, const at::Tensor& t, const char* name) {
+    if (t.scalar_type() != y.scalar_type() && t.scalar_type() != at::kFloat)
+      fail(std::string(name) + ": need the activations' dtype or fp32");
+    return dtype_code(t.scalar_type());
+  }
+  void vector(Call& c, const at::Tensor& y, PyObject* o, const char* name, at::Tensor* to) {
+    if (!given(o)) return;
+    *to = tensor(o, name);
+    weight_type = of_either(y, *to, name);
+    c.dense(*to, to->scalar_type(), name, {H});
+  }
+};
+
+// y, residual, gate, gating, post_weight, pre_weight, residual_scale, weight_offset, eps, out,
+// normed
+PyObject* block_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 11, [&]() -> PyObject* {
+    if (c10::GradMode::is_enabled())
+      for (int i : {0, 1, 2, 4, 5})
+        if (needs_gradient(a[i])) return in_graph("block_norm", a, n);
+    Call c;
+    const at::Tensor& y = tensor(a[0], "y");
+    const long long ldy = c.rows(y, "y");
+    const at::ScalarType type = y.scalar_type();
+    Norms s;
+    s.take(c, y, a[2], a[3], a[4], a[5]);
+    at::Tensor residual, out, normed, post_rstd, pre_rstd;
+    long long ldr = 0;
+    if (given(a[1])) {
+      residual = tensor(a[1], "residual");
+      ldr = c.rows(residual, "residual", s.M, s.H);
+      if (residual.scalar_type() != type) fail("y, residual: need one dtype");
+    }
+    const bool changes = residual.defined() || s.gate.defined() || s.post.defined();
+    if (!changes && !s.pre.defined()) fail("block_norm: nothing to compute");
+    if (!changes && given(a[9])) fail("out: would be y");
+    if (!s.pre.defined() && given(a[10])) fail("normed: needs pre_weight");
+    if (changes) out = c.out(a[9], type, "out", {s.M, s.H});
+    if (s.pre.defined()) {
+      normed = c.out(a[10], type, "normed", {s.M, s.H});
+      pre_rstd = c.make(at::kFloat, {s.M});
+    }
+    if (s.post.defined()) post_rstd = c.make(at::kFloat, {s.M});
+    check_rc("qmoe_block_norm",
+             qmoe_block_norm(y.data_ptr(), s.type, ldy, data(residual), ldr, (float)real(a[6]),
+                             data(s.gate), s.gate_type, s.gate_form, s.ldgate, s.gating,
+                             data(s.post), data(s.pre), s.weight_type, (float)real(a[7]),
+                             (float)real(a[8]), small(s.M), small(s.H), data(out), data(normed),
+                             static_cast<float*>(data(post_rstd)),
+                             static_cast<float*>(data(pre_rstd)), c.stream()));
+    return pack_some({out, normed, post_rstd, pre_rstd});
+  });
+}
+
+// dout, dnormed, y, out, gate, gating, post_weight, pre_weight, residual_scale, weight_offset,
+// post_rstd, pre_rstd, which of the gradients are wanted: residual, gate, post_weight, pre_weight
+PyObject* block_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 16, [&]() -> PyObject* {
+    Call c;
+    const at::Tensor& y = tensor(a[2], "y");
+    const long long ldy = c.rows(y, "y");
+    const at::ScalarType type = y.scalar_type();
+    Norms s;
+    s.take(c, y, a[4], a[5], a[6], a[7]);
+    at::Tensor dout, dnormed, out, rstd[2], dresidual, dgate, dpost, dpre;
+    long long ldd = 0, ldn = 0, ldo = 0;
+    auto rows = [&](PyObject* o, const char* name, at::Tensor* t, long long* ld) {
+      if (!given(o)) return;
+      *t = tensor(o, name);
+      *ld = c.rows(*t, name, s.M, s.H);
+      if (t->scalar_type() != type) fail(std::string(name) + ": need y's dtype");
+    };
+    rows(a[0], "dout", &dout, &ldd);
+    rows(a[1], "dnormed", &dnormed, &ldn);
+    rows(a[3], "out", &out, &ldo);
+    const char* names[2] = {"post_rstd", "pre_rstd"};
+    for (int i = 0; i < 2; ++i) {
+      if (!given(a[10 + i])) continue;
+      rstd[i] = tensor(a[10 + i], names[i]);
+      c.dense(rstd[i], at::kFloat, names[i], {s.M});
+    }
+    if (!dout.defined() && !dnormed.defined()) fail("dout, dnormed: need one of them");
+    if (s.pre.defined() != dnormed.defined()) fail("dnormed: goes with pre_weight");
+    const at::Tensor dy = c.make(type, {s.M, s.H});
+    if (truth(a[12])) dresidual = c.make(type, {s.M, s.H});
+    if (truth(a[13]) && s.gate.defined())
+      dgate = s.gate_form == QMOE_GATE_FULL ? c.make(type, {s.M, s.H})
+              : s.gate_form == QMOE_GATE_TOKEN ? c.make(at::kFloat, {s.M, 1})
+                                               : c.make(at::kFloat, {1, s.H});
+    if (truth(a[14]) && s.post.defined()) dpost = c.make(at::kFloat, {s.H});
+    if (truth(a[15]) && s.pre.defined()) dpre = c.make(at::kFloat, {s.H});
+    const size_t bytes = qmoe_block_norm_backward_workspace_size(small(s.M), small(s.H));
+    const at::Tensor ws = c.make(at::kByte, {(int64_t)(bytes < 256 ? 256 : bytes)});
+    check_rc("qmoe_block_norm_backward",
+             qmoe_block_norm_backward(
+                 data(dout), ldd, data(dnormed), ldn, y.data_ptr(), s.type, ldy, data(out), ldo,
+                 (float)real(a[8]), data(s.gate), s.gate_type, s.gate_form, s.ldgate, s.gating,
+                 data(s.post), data(s.pre), s.weight_type, (float)real(a[9]),
+                 static_cast<float*>(data(rstd[0])), static_cast<float*>(data(rstd[1])), small(s.M),
+                 small(s.H), dy.data_ptr(), data(dresidual), data(dgate),
+                 static_cast<float*>(data(dpost)), static_cast<float*>(data(dpre)), ws.data_ptr(),
+                 (size_t)ws.numel(), c.stream()));
+    return pack_some({dy, dresidual, dgate, dpost, dpre});
+  });
+}
+
+// x, codes, scales
+PyObject* checkpoint8(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 3, [&]() -> PyObject* {
+    Call c;
+    const at::Tensor& x = tensor(a[0], "x");
+    const long long ldx = c.rows(x, "x");
+    const int64_t M = x.size(0), C = x.size(1);
+    const at::Tensor codes = c.out(a[1], at::kChar, "codes", {M, C});
+    const at::Tensor scales = c.out(a[2], at::kByte, "scales", {M, (C + 31) / 32});
+    check_rc("qmoe_checkpoint8",
+             qmoe_checkpoint8(x.data_ptr(), dtype_code(x.scalar_type()), ldx, small(M), small(C),
+                              static_cast<int8_t*>(codes.data_ptr()),
+                              static_cast<uint8_t*>(scales.data_ptr()), c.stream()));
+    return pack({codes, scales});
+  });
+}
+
+// A checkpoint's codes and scales, `parts` matrices beside each other.
+const int8_t* codes_of(Call& c, const at::Tensor& codes, const at::Tensor& scales, int64_t M,
+                       int64_t C, int parts, const char* name) {
+  c.dense(codes, at::kChar, (std::string(name) + " codes").c_str(), {M, parts * C});
+  c.dense(scales, at::kByte, (std::string(name) + " scales").c_str(), {M, parts * ((C + 31) / 32)});
+  return static_cast<const int8_t*>(codes.data_ptr());
+}
+
+// codes, scales, an empty tensor of the wanted type, out
+PyObject* checkpoint8_restore(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 4, [&]() -> PyObject* {
+    Call c;
+    const at::Tensor& codes = tensor(a[0], "codes");
+    const at::Tensor& scales = tensor(a[1], "scales");
+    if (codes.dim() != 2) fail("codes: need [M][C]");
+    const int64_t M = codes.size(0), C = codes.size(1);
+    const int8_t* p = codes_of(c, codes, scales, M, C, 1, "x");
+    const at::ScalarType type = tensor(a[2], "dtype").scalar_type();
+    if (dtype_code(type) < 0) fail("dtype: need bf16, fp16 or fp32");
+    const at::Tensor out = c.out(a[3], type, "out", {M, C});
+    check_rc("qmoe_checkpoint8_restore",
+             qmoe_checkpoint8_restore(p, static_cast<const uint8_t*>(scales.data_ptr()),
+                                      dtype_code(type), small(M), small(C), out.data_ptr(),
+                                      c.stream()));
+    return THPVariable_Wrap(out);
+  });
+}
+
+// The sizes of a gated feed-forward block by its weights.
+struct Ffn {
+  at::ScalarType type;
+  int64_t H, I;
+  Ffn(Call& c, const at::Tensor& w13, const at::Tensor& w2) {
+    if (w13.dim() != 2 || w2.dim() != 2) fail("w13, w2: need [2I][H] and [H][I]");
+    type = w2.scalar_type();
+    H = w2.size(0), I = w2.size(1);
+    if (type != at::kBFloat16 && type != at::kHalf) fail("w13, w2: need bf16 or fp16");
+    c.dense(w13, type, "w13", {2 * I, H});
+    c.dense(w2, type, "w2", {H, I});
+  }
+  long long rows(Call& c, const at::Tensor& t, const char* name, int64_t M) const {
+    const long long ld = c.rows(t, name, M, H);
+    if (t.scalar_type() != type) fail(std::string(name) + ": need the weights' dtype");
+    return ld;
+  }
+};
+
+// x, w13, w2, activation, limit, what is kept (0: nothing, 16, 8), out, workspace, what a node of
+// autograd's graph keeps (16, 8; 0: this call is none)
+PyObject* gated_ffn(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 9, [&]() -> PyObject* {
+    if (c10::GradMode::is_enabled() && integer(a[8]) != 0)
+      for (int i : {0, 1, 2})  // x, w13, w2
+        if (needs_gradient(a[i])) return in_graph("gated_ffn", a, n);
+    Call c;
+    const at::Tensor& x = tensor(a[0], "x");
+    const at::Tensor& w13 = tensor(a[1], "w13");
+    const at::Tensor& w2 = tensor(a[2], "w2");
+    const Ffn f(c, w13, w2);
+    if (x.dim() != 2) fail("x: need [M][H]");
+    const int64_t M = x.size(0);
+    const long long ldx = f.rows(c, x, "x", M);
+    const int64_t keep = integer(a[5]);
+    at::Tensor kept, scales;
+    if (keep == 16) kept = c.make(f.type, {M, 2 * f.I});
+    if (keep == 8) {
+      kept = c.make(at::kChar, {M, 2 * f.I});
+      scales = c.make(at::kByte, {M, 2 * ((f.I + 31) / 32)});
+    }
+    const at::Tensor out = c.out(a[6], f.type, "out", {M, f.H});
+    const at::Tensor ws =
+        c.space(a[7], qmoe_gated_ffn_workspace_size(small(M), small(f.H), small(f.I)), kFfn);
+    check_rc("qmoe_gated_ffn",
+             qmoe_gated_ffn(x.data_ptr(), dtype_code(f.type), ldx, w13.data_ptr(), w2.data_ptr(),
+                            small(integer(a[3])), (float)real(a[4]), small(M), small(f.H),
+                            small(f.I), out.data_ptr(), data(kept),
+                            static_cast<uint8_t*>(data(scales)), ws.data_ptr(), (size_t)ws.numel(),
+                            c.stream()));
+    if (!given(a[7]) && M > 0) c.kept(kFfn) = ws;
+    if (keep == 0) return THPVariable_Wrap(out);
+    return pack_some({out, kept, scales});
+  });
+}
+
+// dout, x or its codes, x's scales or None, w13, w2, kept, kept's scales or None, activation, limit,
+// which of the gradients are wanted: x, w13, w2; workspace
+PyObject* gated_ffn_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 13, [&]() -> PyObject* {
+    Call c;
+    const at::Tensor& dout = tensor(a[0], "dout");
+    const at::Tensor& x = tensor(a[1], "x");
+    const at::Tensor& w13 = tensor(a[3], "w13");
+    const at::Tensor& w2 = tensor(a[4], "w2");
+    const at::Tensor& kept = tensor(a[5], "kept");
+    const Ffn f(c, w13, w2);
+    if (dout.dim() != 2) fail("dout: need [M][H]");
+    const int64_t M = dout.size(0);
+    const long long ldd = f.rows(c, dout, "dout", M);
+    long long ldx = f.H;
+    at::Tensor xs, ks;
+    if (given(a[2]) != given(a[6])) fail("x, kept: both in 8 bits, or neither");
+    if (given(a[2])) {
+      xs = tensor(a[2], "x scales");
+      ks = tensor(a[6], "kept scales");
+      codes_of(c, x, xs, M, f.H, 1, "x");
+      codes_of(c, kept, ks, M, f.I, 2, "kept");
+    } else {
+      ldx = f.rows(c, x, "x", M);
+      c.dense(kept, f.type, "kept", {M, 2 * f.I});
+    }
+    at::Tensor dx, dw13, dw2;
+    if (truth(a[9])) dx = c.make(f.type, {M, f.H});
+    if (truth(a[10])) dw13 = c.make(f.type, {2 * f.I, f.H});
+    if (truth(a[11])) dw2 = c.make(f.type, {f.H, f.I});
+    const at::Tensor ws = c.space(
+        a[12], qmoe_gated_ffn_backward_workspace_size(small(M), small(f.H), small(f.I),
+                                                      xs.defined() ? 8 : 16), kFfnBackward);
+    check_rc("qmoe_gated_ffn_backward",
+             qmoe_gated_ffn_backward(dout.data_ptr(), dtype_code(f.type), ldd, x.data_ptr(), ldx,
+                                     static_cast<uint8_t*>(data(xs)), w13.data_ptr(), w2.data_ptr(),
+                                     kept.data_ptr(), static_cast<uint8_t*>(data(ks)),
+                                     small(integer(a[7])), (float)real(a[8]), small(M), small(f.H),
+                                     small(f.I), data(dx), data(dw13), data(dw2), ws.data_ptr(),
+                                     (size_t)ws.numel(), c.stream()));
+    if (!given(a[12]) && M > 0) c.kept(kFfnBackward) = ws;
+    return pack_some({dx, dw13, dw2});
+  });
+}
+
 // The kept workspaces of the current device.
 PyObject* default_workspaces(PyObject*, PyObject* const*, Py_ssize_t n) {
   return guarded(n, 0, [&]() -> PyObject* {
@@ -457,6 +765,12 @@ PyMethodDef kMethods[] = {FAST(gate),
                           FAST(unsort_tokens),
                           FAST(unsort_tokens_backward),
                           FAST(lora_linear),
+                          FAST(block_norm),
+                          FAST(block_norm_backward),
+                          FAST(checkpoint8),
+                          FAST(checkpoint8_restore),
+                          FAST(gated_ffn),
+                          FAST(gated_ffn_backward),
                           FAST(default_workspaces),
                           {"set_error", set_error, METH_O, nullptr},
                           {"set_graph", set_graph, METH_O, nullptr},

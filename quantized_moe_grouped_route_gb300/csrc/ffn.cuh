@@ -1,0 +1,54 @@
+// What the kernels of the gated feed-forward block share: the activation and its derivative, and
+// the arithmetic of the gate, the clamp and the product.
+#pragma once
+
+#include "common.cuh"
+#include "launch.h"
+#include "pack.cuh"
+
+namespace qmoe {
+
+// Both activations are g * sigmoid(k(g)): SiLU with k(g) = g, GELU in its tanh form with
+// k(g) = 2 sqrt(2 / pi) (g + 0.044715 g^3), since (1 + tanh z) / 2 = sigmoid(2 z).  expf's and the
+// division's approximations are off by a few 2^-22, far below the rounding of what they enter.
+constexpr float kGeluA = 1.5957691216057308f;  // 2 sqrt(2 / pi)
+constexpr float kGeluB = 0.044715f;
+
+__device__ __forceinline__ float sigmoid_fast(float k) { return __fdividef(1.f, 1.f + __expf(-k)); }
+
+// sigmoid(k(g)) and k'(g).  (Past 64 the sigmoid is 0 or 1: g^3 need not overflow.  NaN stays.)
+template <bool SLOPE>
+__device__ __forceinline__ void act_parts(bool gelu, float g, float* p, float* slope) {
+  if (gelu) {
+    const float c = g > 64.f ? 64.f : g < -64.f ? -64.f : g, c2 = c * c;
+    *p = sigmoid_fast(kGeluA * c * fmaf(kGeluB, c2, 1.f));
+    if (SLOPE) *slope = kGeluA * fmaf(3.f * kGeluB, c2, 1.f);
+  } else {
+    *p = sigmoid_fast(g);
+    if (SLOPE) *slope = 1.f;
+  }
+}
+
+// h = act(min(g, limit)) * clamp(u, -limit, limit); comparisons that leave NaN as it is.
+__device__ __forceinline__ float gated(bool gelu, float limit, float u, float g) {
+  float p, unused;
+  g = g > limit ? limit : g;
+  u = u > limit ? limit : u < -limit ? -limit : u;
+  act_parts<false>(gelu, g, &p, &unused);
+  return g * p * u;
+}
+// ... and its derivatives' products with dh; what the clamp holds has none.
+__device__ __forceinline__ float gated_backward(bool gelu, float limit, float u, float g, float dh,
+                                                float* du, float* dg) {
+  float p, slope;
+  const bool free_g = !(g > limit), free_u = !(fabsf(u) > limit);  // (NaN is not held)
+  g = g > limit ? limit : g;
+  u = u > limit ? limit : u < -limit ? -limit : u;
+  act_parts<true>(gelu, g, &p, &slope);
+  const float a = g * p;
+  *du = free_u ? dh * a : 0.f;
+  *dg = free_g ? dh * u * fmaf(a * (1.f - p), slope, p) : 0.f;
+  return a * u;
+}
+
+}  // namespace qmoe

@@ -1,0 +1,563 @@
+// The products of the gated feed-forward block for many tokens, forward and backward, on the
+// tensor cores: one persistent kernel on CTA pairs whose operands are taken as they lie in memory,
+// rows along the contraction (K) or across it, and whose epilogues do the rest of the block.
+//
+//   up      [u | g] = x . W13^T, h = act(g) u         x: K, W13: K     (W13 [2I][H], rows 0..I-1 up)
+//   plain   out = h . W2^T                            h: K, W2: K      (W2 [H][I])
+//   dh      dh = dout . W2, then du, dg and h again   dout: K, W2: across
+//   plain   dx = [du | dg] . W13                      [du | dg]: K, W13: across
+//   plain   dW13 = [du | dg]^T . x, dW2 = dout^T . h  both across, K are the tokens
+//
+// A tile is 256 rows x tile_n columns of the accumulator, half of the rows in each SM of the pair
+// (tcgen05 cta_group::2, M = 256; each SM loads its own 128 rows of A and half of B's columns, so
+// an operand passes the memory system once a pair).  Steps of 64 of K go through a ring of
+// TMA-loaded stages; two accumulators in TMEM let a tile's epilogue run under the next one's MMAs.
+// The up tile holds tile_n / 2 columns of u beside the same columns of g: one SM loads the rows of
+// W13 for u and the other those for g, and the epilogue finds both of a pair in one TMEM lane.
+// Epilogues write through swizzled staging tiles and TMA stores, which cut at the matrix's edges.
+// Bound by the tensor cores; edges of K, M, N are zeros that the copies fill in.
+#include <type_traits>
+
+#include "checkpoint.cuh"
+#include "cluster.cuh"
+#include "ffn.cuh"
+
+namespace qmoe {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kMaxStages = 12;
+constexpr int kCtrl = 1024;
+constexpr int kAccCols = 256;
+constexpr int kABytes = 128 * 128;  // a stage's A: 128 rows x 64 of K
+constexpr int kStageTile = 4096;    // an epilogue warp's staging tile: 32 rows x 64 columns
+constexpr int kSmemLimit = 232448;
+
+enum class Op { kUp, kPlainNT, kPlainNN, kPlainTN, kDh };
+__host__ __device__ constexpr bool a_across(Op op) { return op == Op::kPlainTN; }
+__host__ __device__ constexpr bool b_across(Op op) {
+  return op == Op::kPlainTN || op == Op::kPlainNN || op == Op::kDh;
+}
+// Staging tiles of an epilogue warp.
+__host__ __device__ constexpr int staging(Op op) { return op == Op::kUp || op == Op::kDh ? 3 : 2; }
+
+struct Maps {
+  CUtensorMap a, b, b2, o, o2, o3;
+};
+
+__device__ __forceinline__ uint64_t l2_policy_normal() {
+  uint64_t p;
+  asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
+  return p;
+}
+__device__ __forceinline__ void fence_proxy_async() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, uint32_t src, int x, int y) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(src), "r"(x), "r"(y)
+               : "memory");
+}
+__device__ __forceinline__ void store_commit() {
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void store_wait_read() {
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void store_wait_all() {
+  asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+}
+
+__device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                         uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, q;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Descriptor of an operand that lies across K: boxes of 64 elements (128 bytes, swizzled) x 64
+// of K.  Eight of K are 1024 bytes apart (stride offset), the next 64 elements a box (leading).
+__device__ __forceinline__ uint64_t sdesc_across(uint32_t saddr) {
+  return (sdesc_sw128(saddr) & ~((uint64_t)0x3fff << 16)) | (uint64_t)(64 * 128 >> 4) << 16;
+}
+
+// 32 values of a lane's row into half `half` of a staging tile (128-byte rows, swizzled as the
+// store's tensor map has it).
+template <class T>
+__device__ __forceinline__ void stage_half(uint8_t* tile, int half, const float (&v)[32]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    Pack<T, 8> p;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) p.v[e] = from_f32<T>(v[8 * j + e]);
+    *reinterpret_cast<uint4*>(tile + lane * 128 + (((half * 4 + j) ^ (lane & 7)) << 4)) = p.raw;
+  }
+}
+
+__device__ __forceinline__ void load_acc32(uint32_t taddr, float (&v)[32]) {
+  uint32_t r[2][16];
+  tmem_ld_x16(taddr, r[0]);
+  tmem_ld_x16(taddr + 16, r[1]);
+  tmem_wait_ld();
+  tmem_ld_ready(r[0]);
+  tmem_ld_ready(r[1]);
+#pragma unroll
+  for (int k = 0; k < 32; ++k) v[k] = __uint_as_float(r[k >> 4][k & 15]);
+}
+
+// A row's 32 values as 8-bit codes and their scale (checkpoint.cuh); n <= 32 of them exist, a
+// multiple of 8.
+__device__ __forceinline__ void save_block(const float (&v)[32], int n, int8_t* codes,
+                                           uint8_t* scale) {
+  uint32_t top = 0;
+#pragma unroll
+  for (int k = 0; k < 32; ++k)
+    if (k < n) top = max(top, __float_as_uint(v[k]) & 0x7fffffffu);
+  const uint32_t byte = ck_byte(top);
+  const float inverse = ck_inverse(byte);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if (8 * j >= n) break;
+    uint32_t w[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      w[i] = 0;
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        w[i] |= (uint32_t)(ck_code(v[8 * j + 4 * i + e], inverse) & 255) << (8 * e);
+    }
+    *reinterpret_cast<uint2*>(codes + 8 * j) = make_uint2(w[0], w[1]);
+  }
+  *scale = (uint8_t)byte;
+}
+
+// A row's 32 kept values of u or g on their way: 16-bit or codes with a scale.
+struct Kept {
+  uint4 raw[4];
+  uint32_t byte;
+};
+template <class T, bool CODES>
+__device__ __forceinline__ void fetch_kept(Kept& k, const FfnGemm& p, int row, int col, int half) {
+  const size_t at = (size_t)row * 2 * p.N + (size_t)half * p.N + col;
+  const bool in = row < p.M;
+  if constexpr (CODES) {
+    const uint8_t* src = reinterpret_cast<const uint8_t*>(p.kept) + at;
+    uint2 v[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      v[j] = load_if(reinterpret_cast<const uint2*>(src + 8 * j), in && col + 8 * j < p.N);
+    k.raw[0] = make_uint4(v[0].x, v[0].y, v[1].x, v[1].y);
+    k.raw[1] = make_uint4(v[2].x, v[2].y, v[3].x, v[3].y);
+    const int blocks = (p.N + kCkBlock - 1) / kCkBlock;
+    k.byte = in && col < p.N ? p.kept_scales[((size_t)row * 2 + half) * blocks + col / kCkBlock] : 0u;
+  } else {
+    const T* src = reinterpret_cast<const T*>(p.kept) + at;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      k.raw[j] = load_if(reinterpret_cast<const uint4*>(src + 8 * j), in && col + 8 * j < p.N);
+  }
+}
+template <class T, bool CODES>
+__device__ __forceinline__ float kept_value(const Kept& k, int i, float value) {
+  const uint32_t w[16] = {k.raw[0].x, k.raw[0].y, k.raw[0].z, k.raw[0].w, k.raw[1].x, k.raw[1].y,
+                          k.raw[1].z, k.raw[1].w, k.raw[2].x, k.raw[2].y, k.raw[2].z, k.raw[2].w,
+                          k.raw[3].x, k.raw[3].y, k.raw[3].z, k.raw[3].w};
+  if constexpr (CODES) {
+    return ck_restore<T>((int)(int8_t)(w[i >> 2] >> (8 * (i & 3)) & 255u), value);
+  } else {
+    Pack<T, 2> v;
+    v.raw = w[i >> 1];
+    return to_f32(v.v[i & 1]);
+  }
+}
+
+// Tile i of a matrix of tiles: groups of eight rows of tiles, a group column by column, so that
+// the tiles in the making at one time share few rows of A and of B (both stay in L2).
+__device__ __forceinline__ void tile_of(const FfnGemm& p, int i, int* tm, int* tn) {
+  const int group = 8 * p.tiles_n, first = i / group * 8;
+  const int rows = min(8, p.tiles_m - first), r = i - first * p.tiles_n;
+  *tn = r / rows;
+  *tm = first + r - *tn * rows;
+}
+
+template <class T, Op OP, bool CODES>
+__global__ void __launch_bounds__(kThreads, 1)
+    ffn_gemm_kernel(const __grid_constant__ Maps maps, const FfnGemm p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  const int rows_b = p.tile_n / 2;  // of this SM's half of B
+  const int stage_bytes = kABytes + rows_b * 128;
+  const int stages = p.stages;
+  uint8_t* epi = smem + stages * stage_bytes;
+  uint8_t* ctrl = epi + 4 * staging(OP) * kStageTile;
+  uint64_t* full = reinterpret_cast<uint64_t*>(ctrl);
+  uint64_t* empty = full + kMaxStages;
+  uint64_t* accf = empty + kMaxStages;
+  uint64_t* acce = accf + 2;
+  uint64_t* drain = acce + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  const int worker = (int)cluster_index(), workers = (int)cluster_count();
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < stages; ++s) {
+      mbar_init(smem_u32(&full[s]), 1);
+      mbar_init(smem_u32(&empty[s]), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&accf[i]), 1);
+      mbar_init(smem_u32(&acce[i]), 8);  // four epilogue warps of each SM
+    }
+    mbar_init(smem_u32(drain), 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    prefetch_tmap(&maps.a);
+    prefetch_tmap(&maps.b);
+    if (OP == Op::kUp) prefetch_tmap(&maps.b2);
+    prefetch_tmap(&maps.o);
+  }
+  if (warp == 1) {
+    tmem_alloc2(smem_u32(tmem_slot), 2 * kAccCols);
+    tmem_relinquish2();
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();  // the peer's barriers exist before any remote arrival
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  grid_dep_wait();  // (all threads: what they read was written by the kernel before)
+  grid_dep_launch();
+  if (p.clear_err && blockIdx.x == 0 && threadIdx.x == 0) *p.err = 0;
+
+  const int units = p.tiles_m * p.tiles_n;
+  const int cols = OP == Op::kUp ? p.tile_n / 2 : p.tile_n;  // of the result, a tile
+  auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+    return warp_wait_cl(smem_u32(bar), parity, abort_flag, p.err);
+  };
+
+  if (warp == 0) {
+    // ------------------------------------------------------------------ TMA producer
+    const uint32_t lead = elect_one();
+    const uint64_t pol = l2_policy_normal();
+    const uint32_t full0 = peer_addr(smem_u32(full), 0);  // the leader's: both SMs' copies count
+    uint32_t s = 0, ph = 1;
+    bool ok = true;
+    for (int i = worker; i < units && ok; i += workers) {
+      int tm, tn;
+      tile_of(p, i, &tm, &tn);
+      const int row = tm * 256 + (int)rank * 128;
+      const int col = OP == Op::kUp ? tn * cols : tn * p.tile_n + (int)rank * rows_b;
+      for (int k = 0; k < p.ksteps; ++k) {
+        if (!wait(&empty[s], ph)) {
+          ok = false;
+          break;
+        }
+        const uint32_t sa = smem_u32(smem) + s * stage_bytes, sb = sa + kABytes;
+        const uint32_t bar = full0 + s * 8;
+        if (rank == 0)
+          mbar_arrive_expect_tx_if(lead, smem_u32(&full[s]), 2u * (uint32_t)stage_bytes);
+        if (a_across(OP)) {
+          tma_load_2d_pair_if(lead, sa, &maps.a, row, k * 64, bar, pol);
+          tma_load_2d_pair_if(lead, sa + 8192, &maps.a, row + 64, k * 64, bar, pol);
+        } else {
+          tma_load_2d_pair_if(lead, sa, &maps.a, k * 64, row, bar, pol);
+        }
+        if (b_across(OP)) {
+          tma_load_2d_pair_if(lead, sb, &maps.b, col, k * 64, bar, pol);
+          if (rows_b > 64) tma_load_2d_pair_if(lead, sb + 8192, &maps.b, col + 64, k * 64, bar, pol);
+        } else {
+          const CUtensorMap* b = OP == Op::kUp && rank != 0 ? &maps.b2 : &maps.b;
+          tma_load_2d_pair_if(lead, sb, b, k * 64, col, bar, pol);
+        }
+        if (++s == (uint32_t)stages) {
+          s = 0;
+          ph ^= 1;
+        }
+      }
+    }
+    if (!ok) {  // the copies of the last steps may still be landing
+      const unsigned long long t0 = globaltimer_ns();
+      while (globaltimer_ns() - t0 < 2000000ull) {
+      }
+    }
+  } else if (warp == 1) {
+    if (rank == 0) {
+      // ------------------------------------------------------------------ MMA issue
+      const uint32_t lead = elect_one();
+      uint32_t idesc = idesc_bf16_f32(256, p.tile_n);
+      if (std::is_same<T, __half>::value) idesc &= ~((1u << 7) | (1u << 10));
+      if (a_across(OP)) idesc |= 1u << 15;
+      if (b_across(OP)) idesc |= 1u << 16;
+      const uint32_t base = smem_u32(smem);
+      const uint64_t a0 = a_across(OP) ? sdesc_across(base) : sdesc_sw128(base);
+      const uint64_t b0 = b_across(OP) ? sdesc_across(base + kABytes) : sdesc_sw128(base + kABytes);
+      // 16 of K further on: 32 bytes of a row, or 16 rows of 128 bytes
+      constexpr uint32_t step_a = a_across(OP) ? 128 : 2, step_b = b_across(OP) ? 128 : 2;
+      uint32_t s = 0, ph = 0, local = 0;
+      bool ok = true;
+      for (int i = worker; i < units && ok; i += workers, ++local) {
+        const int ab = local & 1;
+        if (!wait(&acce[ab], ((local >> 1) & 1) ^ 1)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t dst = tmem + ab * kAccCols;
+        for (int k = 0; k < p.ksteps; ++k) {
+          if (!wait(&full[s], ph)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t off = (s * stage_bytes) >> 4;
+          if (lead) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              mma_pair(dst, a0 + off + step_a * j, b0 + off + step_b * j, idesc, (k > 0) | (j > 0));
+          }
+          tc_commit2_both_if(lead, smem_u32(&empty[s]));
+          if (++s == (uint32_t)stages) {
+            s = 0;
+            ph ^= 1;
+          }
+        }
+        if (ok) tc_commit2_both_if(lead, smem_u32(&accf[ab]));
+      }
+      tc_commit2_both_if(lead, smem_u32(drain));
+    }
+  } else if (warp >= 4) {
+    // ------------------------------------------------------------------- epilogue
+    const int q = warp & 3;
+    const uint32_t acce0 = peer_addr(smem_u32(acce), 0);
+    uint8_t* stage = epi + q * staging(OP) * kStageTile;
+    const uint32_t stage0 = smem_u32(stage);
+    const bool gelu = p.activation == QMOE_ACT_GELU;
+    uint32_t local = 0;
+    int turn = 0;
+    for (int i = worker; i < units; i += workers, ++local) {
+      int tm, tn;
+      tile_of(p, i, &tm, &tn);
+      const int ab = local & 1;
+      const int row0 = tm * 256 + (int)rank * 128 + q * 32, col0 = tn * cols;
+      const int n = min(cols, p.N - col0);  // columns of this tile
+      Kept ku, kg;
+      if constexpr (OP == Op::kDh) {
+        fetch_kept<T, CODES>(ku, p, row0 + lane, col0, 0);
+        fetch_kept<T, CODES>(kg, p, row0 + lane, col0, 1);
+      }
+      if (!wait(&accf[ab], (local >> 1) & 1)) break;
+      tc_fence_after();
+      const uint32_t tbase = tmem + ((uint32_t)(q * 32) << 16) + ab * kAccCols;
+      const bool rows_in = row0 < p.M;
+      for (int c0 = 0; c0 < n; c0 += 64) {
+        // the staging tiles are free again
+        const int t = OP == Op::kUp || OP == Op::kDh ? 0 : turn;
+        turn ^= 1;
+        if (lane == 0) {
+          if (OP == Op::kUp || OP == Op::kDh)
+            store_wait_read<0>();
+          else
+            store_wait_read<1>();
+        }
+        __syncwarp();
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const int c = c0 + 32 * half;
+          float v[32];
+          load_acc32(tbase + c, v);
+          if constexpr (OP == Op::kUp) {
+            float g[32];
+            load_acc32(tbase + p.tile_n / 2 + c, g);
+            if (p.save == 8 && row0 + lane < p.M && c < n) {
+              const int blocks = (p.N + kCkBlock - 1) / kCkBlock;
+              const size_t at = (size_t)(row0 + lane) * 2 * p.N + col0 + c;
+              const size_t sat = (size_t)(row0 + lane) * 2 * blocks + (col0 + c) / kCkBlock;
+              save_block(v, min(32, n - c), p.codes + at, p.scales + sat);
+              save_block(g, min(32, n - c), p.codes + at + p.N, p.scales + sat + blocks);
+            }
+            if (p.save == 16) {
+              stage_half<T>(stage + kStageTile, half, v);
+              stage_half<T>(stage + 2 * kStageTile, half, g);
+            }
+#pragma unroll
+            for (int k = 0; k < 32; ++k) v[k] = gated(gelu, p.limit, v[k], g[k]);
+            stage_half<T>(stage, half, v);
+          } else if constexpr (OP == Op::kDh) {
+            const float su = CODES ? ck_value(ku.byte) : 0.f, sg = CODES ? ck_value(kg.byte) : 0.f;
+            float du[32], dg[32];
+#pragma unroll
+            for (int k = 0; k < 32; ++k)
+              v[k] = gated_backward(gelu, p.limit, kept_value<T, CODES>(ku, k, su),
+                                    kept_value<T, CODES>(kg, k, sg), v[k], &du[k], &dg[k]);
+            if (c + 32 < n) {
+              fetch_kept<T, CODES>(ku, p, row0 + lane, col0 + c + 32, 0);
+              fetch_kept<T, CODES>(kg, p, row0 + lane, col0 + c + 32, 1);
+            }
+            stage_half<T>(stage, half, v);
+            stage_half<T>(stage + kStageTile, half, du);
+            stage_half<T>(stage + 2 * kStageTile, half, dg);
+          } else {
+            stage_half<T>(stage + t * kStageTile, half, v);
+          }
+        }
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0 && rows_in) {
+          tma_store_2d(&maps.o, stage0 + t * kStageTile, col0 + c0, row0);
+          if (OP == Op::kDh || (OP == Op::kUp && p.save == 16)) {
+            tma_store_2d(&maps.o2, stage0 + kStageTile, col0 + c0, row0);
+            tma_store_2d(&maps.o3, stage0 + 2 * kStageTile, col0 + c0, row0);
+          }
+        }
+        if (lane == 0) store_commit();
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (rank != 0)
+          mbar_arrive_remote(acce0 + ab * 8);
+        else
+          mbar_arrive(smem_u32(&acce[ab]));
+      }
+    }
+    if (lane == 0) store_wait_all();
+  }
+
+  // No MMA may still read this SM's shared memory or write its TMEM, and no remote arrival may be
+  // in flight, when it (or its peer) exits.
+  if (warp == 1) drain_wait_cl(smem_u32(drain), 0);
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc2(tmem, 2 * kAccCols);
+  }
+}
+
+// A matrix [rows][cols] whose rows lie ld elements apart, in boxes of 64 columns.
+bool map_of(CUtensorMap* map, int dtype, const void* base, long long rows, int cols, long long ld,
+            int box_rows) {
+  const uint64_t dims[2] = {(uint64_t)cols, (uint64_t)rows}, strides[1] = {(uint64_t)ld * 2};
+  const uint32_t box[2] = {64, (uint32_t)box_rows};
+  return make_tmap16(map, dtype, base, 2, dims, strides, box) == QMOE_OK;
+}
+
+template <class T, Op OP, bool CODES = false>
+cudaError_t run(FfnGemm& p, const Maps& maps, int num_sms, cudaStream_t stream) {
+  auto* k = ffn_gemm_kernel<T, OP, CODES>;
+  const int stage = kABytes + p.tile_n / 2 * 128;
+  const int other = 1024 + kCtrl + 4 * staging(OP) * kStageTile;
+  const int most = (kSmemLimit - other) / stage;
+  p.stages = most < kMaxStages ? most : kMaxStages;
+  const size_t smem = other + (size_t)p.stages * stage;
+  cudaError_t e = allow_smem(k, kSmemLimit);
+  if (e != cudaSuccess) return e;
+  int dev = -1;
+  e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  // asked of the runtime once per device: all plans leave one pair two SMs
+  static PerDevice<1> clusters;
+  const int held = clusters.get(dev, 0, [&] {
+    return resident_clusters(k, 2, kThreads, kSmemLimit, num_sms);
+  });
+  if (held < 1) return cudaErrorInvalidConfiguration;
+  const int units = p.tiles_m * p.tiles_n;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2] = {pdl_attribute()};
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.gridDim = dim3((unsigned)((units < held ? units : held) * 2));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, k, maps, p);
+}
+
+// Columns of a tile: 256, or 128 where that takes less time, a tile of 128 columns taking about
+// 0.55 of a wide one's (its rows of A are loaded for half as many products).
+void cut(FfnGemm& p, int rows, int cols, int num_sms, bool up) {
+  p.tiles_m = (rows + 255) / 256;
+  const int pairs = num_sms / 2;
+  auto tiles_n = [&](int n) { return (cols + (up ? n / 2 : n) - 1) / (up ? n / 2 : n); };
+  auto waves = [&](int n) { return (p.tiles_m * (long long)tiles_n(n) + pairs - 1) / pairs; };
+  p.tile_n = 100 * waves(256) <= 55 * waves(128) ? 256 : 128;
+  p.tiles_n = tiles_n(p.tile_n);
+}
+
+template <class T>
+cudaError_t of_op(const FfnProduct& f, int num_sms, cudaStream_t stream) {
+  FfnGemm p = {};
+  static_cast<FfnProduct&>(p) = f;
+  Maps m = {};
+  bool ok = true;
+  switch (f.op) {
+    case FfnOp::kUp: {  // x [M][H], w13 [2I][H] -> h [M][I] (u, g [M][I] at a pitch of 2I)
+      cut(p, f.M, f.N, num_sms, true);
+      p.ksteps = (f.K + 63) / 64;
+      const T* w = reinterpret_cast<const T*>(f.b);
+      ok = map_of(&m.a, f.dtype, f.a, f.M, f.K, f.lda, 128) &&
+           map_of(&m.b, f.dtype, w, f.N, f.K, f.K, p.tile_n / 2) &&
+           map_of(&m.b2, f.dtype, w + (size_t)f.N * f.K, f.N, f.K, f.K, p.tile_n / 2) &&
+           map_of(&m.o, f.dtype, f.out, f.M, f.N, f.N, 32);
+      m.o2 = m.o3 = m.o;
+      if (f.save == 16) {
+        T* ug = reinterpret_cast<T*>(f.ug);
+        ok = ok && map_of(&m.o2, f.dtype, ug, f.M, f.N, 2LL * f.N, 32) &&
+             map_of(&m.o3, f.dtype, ug + f.N, f.M, f.N, 2LL * f.N, 32);
+      }
+      return ok ? run<T, Op::kUp>(p, m, num_sms, stream) : cudaErrorInvalidValue;
+    }
+    case FfnOp::kDh: {  // dout [M][H], w2 [H][I] -> h, du, dg
+      cut(p, f.M, f.N, num_sms, false);
+      p.ksteps = (f.K + 63) / 64;
+      T* dug = reinterpret_cast<T*>(f.ug);
+      ok = map_of(&m.a, f.dtype, f.a, f.M, f.K, f.lda, 128) &&
+           map_of(&m.b, f.dtype, f.b, f.K, f.N, f.N, 64) &&
+           map_of(&m.o, f.dtype, f.out, f.M, f.N, f.N, 32) &&
+           map_of(&m.o2, f.dtype, dug, f.M, f.N, 2LL * f.N, 32) &&
+           map_of(&m.o3, f.dtype, dug + f.N, f.M, f.N, 2LL * f.N, 32);
+      m.b2 = m.b;
+      if (!ok) return cudaErrorInvalidValue;
+      return f.kept_scales ? run<T, Op::kDh, true>(p, m, num_sms, stream)
+                           : run<T, Op::kDh, false>(p, m, num_sms, stream);
+    }
+    default: {
+      cut(p, f.M, f.N, num_sms, false);
+      p.ksteps = (f.K + 63) / 64;
+      const bool across_a = f.op == FfnOp::kTN, across_b = f.op != FfnOp::kNT;
+      ok = (across_a ? map_of(&m.a, f.dtype, f.a, f.K, f.M, f.lda, 64)
+                     : map_of(&m.a, f.dtype, f.a, f.M, f.K, f.lda, 128)) &&
+           (across_b ? map_of(&m.b, f.dtype, f.b, f.K, f.N, f.ldb, 64)
+                     : map_of(&m.b, f.dtype, f.b, f.N, f.K, f.ldb, p.tile_n / 2)) &&
+           map_of(&m.o, f.dtype, f.out, f.M, f.N, f.N, 32);
+      m.b2 = m.b;
+      m.o2 = m.o3 = m.o;
+      if (!ok) return cudaErrorInvalidValue;
+      if (f.op == FfnOp::kNT) return run<T, Op::kPlainNT>(p, m, num_sms, stream);
+      if (f.op == FfnOp::kNN) return run<T, Op::kPlainNN>(p, m, num_sms, stream);
+      return run<T, Op::kPlainTN>(p, m, num_sms, stream);
+    }
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_ffn_product(const FfnProduct& f, int num_sms, cudaStream_t stream) {
+  return f.dtype == QMOE_DTYPE_BF16 ? of_op<__nv_bfloat16>(f, num_sms, stream)
+                                    : of_op<__half>(f, num_sms, stream);
+}
+
+}  // namespace qmoe

@@ -122,6 +122,24 @@ cudaError_t allow_smem(K* kernel, int bytes) {
   return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
 }
 
+// Clusters of `size` CTAs of a kernel that the current device holds at once, 0 if it cannot say.
+template <class K>
+int resident_clusters(K* kernel, int size, int threads, size_t smem, int num_sms) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = size;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.gridDim = dim3(num_sms / size * size);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  return cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess ? n : 0;
+}
+
 // Launch attribute that lets a kernel start while the previous kernel on the stream
 // finishes (it must then call grid_dep_wait before reading that kernel's outputs).
 // The forward uses it on every schedule but the wide prefill one, where kernels that
@@ -251,5 +269,92 @@ cudaError_t launch_lora(LoraArgs& p, int num_sms, cudaStream_t stream);
 // its two steps (the second for more than eight tokens): lora_shrink.cu, lora_gemm.cu
 cudaError_t launch_lora_shrink(const LoraArgs& p, int num_sms, cudaStream_t stream);
 cudaError_t launch_lora_gemm(LoraArgs& p, int num_sms, cudaStream_t stream);
+
+// norm.cu, norm_backward.cu
+struct NormArgs {
+  int M, H;
+  int threads, units;  // of a row; rows of sums over the tokens (backward)
+  const void* y;       // [M][H], rows ldy elements apart (likewise the others)
+  long long ldy;
+  const void* residual;
+  long long ldr;
+  float residual_scale;
+  const void* gate;
+  int gate_form, gating, gate_fp32;
+  long long ldgate;
+  const void* post_weight;  // [H], NULL: no such norm
+  const void* pre_weight;
+  int weight_fp32;
+  float weight_offset, eps;
+  float* post_rstd;  // [M]
+  float* pre_rstd;
+  void* out;  // forward: outputs, NULL where not wanted
+  void* normed;
+  const void* dout;  // backward: gradients in, and what the forward pass left
+  long long lddout;
+  const void* dnormed;
+  long long lddnormed;
+  const void* out_in;
+  long long ldout;
+  void* dy;  // gradients out, NULL where not wanted
+  void* dresidual;
+  void* dgate;
+  float* dpost_weight;
+  float* dpre_weight;
+  float* partial;  // [units][3][H]
+};
+constexpr int kNormRegisterColumns = 8192;  // whose sums over the tokens stay in registers
+// chunk: elements that move together (1, 2, 4, or for 16-bit types 8), dividing every row, stride
+// and pointer
+cudaError_t launch_norm(const NormArgs& a, int dtype, int chunk, int sms, cudaStream_t stream);
+// Rows of sums that M tokens leave.
+int norm_units(int M, int H);
+cudaError_t launch_norm_backward(const NormArgs& a, int dtype, int chunk, cudaStream_t stream);
+
+// checkpoint.cu
+struct CheckpointArgs {
+  const void* x;  // [M][C], rows ldx elements apart
+  long long ldx;
+  int M, C, blocks;  // of 32 columns, of a row
+  int8_t* codes;     // [M][C]
+  uint8_t* scales;   // [M][blocks]
+  void* out;         // [M][C]
+};
+// x to codes and scales, or (restore) those to out
+cudaError_t launch_checkpoint(const CheckpointArgs& a, int dtype, int chunk, bool restore, int sms,
+                              cudaStream_t stream);
+
+// ffn_gemm.cu: one product of the gated feed-forward block, D [M][N] over K
+enum class FfnOp {
+  kUp,  // a [M][K], b = w13 [2N][K] -> out = h [M][N]
+  kDh,  // a [M][K], b = w2 [K][N], kept u and g -> out = h [M][N], ug = [du | dg] [M][2N]
+  kNT,  // a [M][K], b [N][K]
+  kNN,  // a [M][K], b [K][N]
+  kTN   // a [K][M], b [K][N]
+};
+struct FfnProduct {
+  FfnOp op;
+  int dtype;
+  const void* a;
+  long long lda;
+  const void* b;
+  long long ldb;
+  int M, N, K;
+  void* out;
+  int save;         // kUp: keep u and g in ug (16) or codes and scales (8)
+  void* ug;         // [M][2N]
+  int8_t* codes;    // [M][2N]
+  uint8_t* scales;  // [M][2][blocks of 32 of N]
+  const void* kept;  // kDh: what kUp kept, codes where there are scales
+  const uint8_t* kept_scales;
+  int activation;
+  float limit;
+  unsigned int* err;
+  int clear_err;  // the first product of a call
+};
+struct FfnGemm : FfnProduct {
+  int tile_n, tiles_m, tiles_n, ksteps, stages;
+};
+cudaError_t launch_ffn_product(const FfnProduct& f, int num_sms, cudaStream_t stream);
 
 }  // namespace qmoe

@@ -103,6 +103,19 @@ def _bind(L):
         "qmoe_lora_workspace_size": (sz, [i32, i32, i32, i32, i32]),
         "qmoe_lora_linear": (i32, [P, i32, i64, P, P, P, P, P, P, i64, P, i32, i32, i32, i32, i32,
                                    P, sz, P]),
+        "qmoe_block_norm": (i32, [P, i32, i64, P, i64, f32, P, i32, i32, i64, i32, P, P, i32, f32,
+                                  f32, i32, i32, P, P, P, P, P]),
+        "qmoe_block_norm_backward_workspace_size": (sz, [i32, i32]),
+        "qmoe_block_norm_backward": (i32, [P, i64, P, i64, P, i32, i64, P, i64, f32, P, i32, i32,
+                                           i64, i32, P, P, i32, f32, P, P, i32, i32, P, P, P, P, P,
+                                           P, sz, P]),
+        "qmoe_checkpoint8": (i32, [P, i32, i64, i32, i32, P, P, P]),
+        "qmoe_checkpoint8_restore": (i32, [P, P, i32, i32, i32, P, P]),
+        "qmoe_gated_ffn_workspace_size": (sz, [i32, i32, i32]),
+        "qmoe_gated_ffn": (i32, [P, i32, i64, P, P, i32, f32, i32, i32, i32, P, P, P, P, sz, P]),
+        "qmoe_gated_ffn_backward_workspace_size": (sz, [i32, i32, i32, i32]),
+        "qmoe_gated_ffn_backward": (i32, [P, i32, i64, P, i64, P, P, P, P, P, i32, f32, i32, i32,
+                                          i32, P, P, P, P, sz, P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(L, name)
