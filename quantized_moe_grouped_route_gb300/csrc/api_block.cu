@@ -329,7 +329,12 @@ int qmoe_gated_ffn(const void* x_dev, int dtype, long long ldx, const void* w13_
   up.limit = limit;
   up.err = reinterpret_cast<unsigned int*>(ws);
   up.clear_err = 1;
-  cudaError_t e = launch_ffn_product(up, sms, s);
+  auto launch = [&](const FfnProduct& f) {
+    if (!kept_dev && M <= kFfnStreamTokens) return launch_ffn_stream(f, s);
+    if (!kept_dev && M <= kFfnFewTokens) return launch_ffn_few(f, sms, s);
+    return launch_ffn_product(f, sms, s);
+  };
+  cudaError_t e = launch(up);
   if (e != cudaSuccess) return QMOE_ERR_CUDA;
   FfnProduct down = {};
   down.op = FfnOp::kNT;
@@ -343,7 +348,7 @@ int qmoe_gated_ffn(const void* x_dev, int dtype, long long ldx, const void* w13_
   down.K = I;
   down.out = out_dev;
   down.err = up.err;
-  return cuda_rc(launch_ffn_product(down, sms, s));
+  return cuda_rc(launch(down));
 }
 
 // Workspace of the backward pass: [du | dg], h, and x out of its codes.

@@ -356,5 +356,14 @@ struct FfnGemm : FfnProduct {
   int tile_n, tiles_m, tiles_n, ksteps, stages;
 };
 cudaError_t launch_ffn_product(const FfnProduct& f, int num_sms, cudaStream_t stream);
+// ffn_stream.cu, ffn_few.cu: kUp (nothing kept) and kNT for few tokens, which are the rows of a
+constexpr int kFfnStreamTokens = 8;
+cudaError_t launch_ffn_stream(const FfnProduct& f, cudaStream_t stream);
+struct FfnFew : FfnProduct {
+  int tile_n, tiles, blocks;  // tokens of a tile, tiles, blocks of 128 rows of weights
+  int ksteps, splits, stages, ring_bytes, tmem_cols;
+};
+constexpr int kFfnFewTokens = 128;
+cudaError_t launch_ffn_few(const FfnProduct& f, int num_sms, cudaStream_t stream);
 
 }  // namespace qmoe
