@@ -274,6 +274,8 @@ cudaError_t launch_lora_gemm(LoraArgs& p, int num_sms, cudaStream_t stream);
 struct NormArgs {
   int M, H;
   int threads, units;  // of a row; rows of sums over the tokens (backward)
+  // matrices a row is read from, rows on their way, vectors in shared memory (set at launch)
+  int mats, depth, vectors;
   const void* y;       // [M][H], rows ldy elements apart (likewise the others)
   long long ldy;
   const void* residual;
@@ -303,6 +305,7 @@ struct NormArgs {
   float* dpre_weight;
   float* partial;  // [units][3][H]
 };
+constexpr int kNormRingBytes = 231424;       // of shared memory for rows and vectors, at most
 constexpr int kNormRegisterColumns = 8192;  // whose sums over the tokens stay in registers
 // chunk: elements that move together (1, 2, 4, or for 16-bit types 8), dividing every row, stride
 // and pointer
