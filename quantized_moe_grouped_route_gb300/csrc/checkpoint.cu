@@ -39,6 +39,17 @@ union CodePack {
   __device__ CodePack() {}
 };
 
+// Row and place in it of unit u of `per` a row: no division where all rows are one.
+__device__ __forceinline__ long long row_of(const CheckpointArgs& a, long long u, int per, int* at) {
+  if (a.M == 1) {
+    *at = (int)u;
+    return 0;
+  }
+  const long long row = u < (1LL << 32) ? (uint32_t)u / (uint32_t)per : u / per;
+  *at = (int)(u - row * per);
+  return row;
+}
+
 // Unit u of work: LANES lanes of block u % blocks of row u / blocks.
 template <class T, int VEC>
 __global__ void __launch_bounds__(kThreads) pack_kernel(const CheckpointArgs a) {
@@ -56,8 +67,7 @@ __global__ void __launch_bounds__(kThreads) pack_kernel(const CheckpointArgs a) 
 #pragma unroll
     for (int i = 0; i < kAtOnce; ++i) {
       const long long u = u0 + i * per_cta + threadIdx.x / LANES;
-      row[i] = u / a.blocks;
-      block[i] = (int)(u - row[i] * a.blocks);
+      row[i] = row_of(a, u, a.blocks, &block[i]);
       in[i] = u < units && block[i] * kCkBlock + part * VEC < a.C;
       if (in[i])
         p[i].raw = *reinterpret_cast<const typename Pack<T, VEC>::raw_t*>(
@@ -101,10 +111,10 @@ __global__ void __launch_bounds__(kThreads) restore_kernel(const CheckpointArgs 
     for (int i = 0; i < kAtOnce; ++i) {
       const long long u = u0 + i * kThreads + threadIdx.x;
       if (u >= units) continue;
-      const long long row = u / chunks;
-      const int col = (int)(u - row * chunks) * VEC;
+      int at;
+      const long long row = row_of(a, u, chunks, &at);
       c[i].raw = *reinterpret_cast<const typename Codes<VEC>::type*>(a.codes + u * VEC);
-      byte[i] = a.scales[row * a.blocks + col / kCkBlock];
+      byte[i] = a.scales[row * a.blocks + at / (kCkBlock / VEC)];
     }
 #pragma unroll
     for (int i = 0; i < kAtOnce; ++i) {
@@ -149,8 +159,15 @@ cudaError_t of_chunk(const CheckpointArgs& a, int chunk, bool restore, int sms,
 
 }  // namespace
 
-cudaError_t launch_checkpoint(const CheckpointArgs& a, int dtype, int chunk, bool restore, int sms,
+cudaError_t launch_checkpoint(const CheckpointArgs& args, int dtype, int chunk, bool restore, int sms,
                               cudaStream_t stream) {
+  CheckpointArgs a = args;
+  // rows of whole blocks one behind the other are one row
+  if (a.C % kCkBlock == 0 && (restore || a.ldx == a.C) && (long long)a.M * a.C < (1LL << 31)) {
+    a.C *= a.M;
+    a.blocks *= a.M;
+    a.M = 1;
+  }
   if (dtype == QMOE_DTYPE_BF16) return of_chunk<__nv_bfloat16>(a, chunk, restore, sms, stream);
   if (dtype == QMOE_DTYPE_FP16) return of_chunk<__half>(a, chunk, restore, sms, stream);
   return of_chunk<float>(a, chunk, restore, sms, stream);

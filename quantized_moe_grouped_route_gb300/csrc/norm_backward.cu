@@ -18,7 +18,7 @@ enum { kPost, kPre, kGate };
 // ACC: the sums over the tokens are kept in registers (rows of up to 8192 elements); otherwise in
 // the unit's own rows in memory, which its threads alone touch.  HOW: how rows come in.
 template <class T, int VEC, int NCH, bool ACC, In HOW, bool GATED>
-__global__ void __launch_bounds__(ACC ? 512 : 1024) norm_backward_kernel(const NormArgs a) {
+__global__ void __launch_bounds__(ACC && VEC > 1 ? 512 : 1024) norm_backward_kernel(const NormArgs a) {
   __shared__ float sums[64];
   extern __shared__ __align__(16) uint8_t ring_raw[];
   const int threads = a.threads;
@@ -329,14 +329,16 @@ cudaError_t of_length(NormArgs a, cudaStream_t stream) {
     return a.H <= 16384 ? run<T, V, 16, false, In::kDirect, true>(a, stream)
                         : run<T, V, 64, false, In::kDirect, true>(a, stream);
   }
+  // (single elements cost so many more instructions that eight a thread are enough)
+  constexpr int kElems = VEC == 1 ? 8 : 16;
   constexpr In kHow = VEC * sizeof(T) >= 4 ? In::kOwn : In::kShared;
-  const int row_threads = norm_threads(a.H, VEC, 16), rows = norm_rows(row_threads);
-  const int left = kNormRingBytes - vector_bytes(a.vectors, 16) * row_threads * rows;
-  a.depth = left / stage_bytes<T, VEC, kHow>(a.mats, row_threads, rows, 16, a.H);
+  const int row_threads = norm_threads(a.H, VEC, kElems), rows = norm_rows(row_threads);
+  const int left = kNormRingBytes - vector_bytes(a.vectors, kElems) * row_threads * rows;
+  a.depth = left / stage_bytes<T, VEC, kHow>(a.mats, row_threads, rows, kElems, a.H);
   if (a.depth > 4) a.depth = 4;
-  if (a.depth >= 2) return run<T, VEC, 16, true, kHow, GATED>(a, stream);
+  if (a.depth >= 2) return run<T, VEC, kElems, true, kHow, GATED>(a, stream);
   // (the longest rows of fp32)
-  if constexpr (sizeof(T) == 4) return run<T, VEC, 16, true, In::kDirect, GATED>(a, stream);
+  if constexpr (sizeof(T) == 4) return run<T, VEC, kElems, true, In::kDirect, GATED>(a, stream);
   return cudaErrorInvalidValue;
 }
 
@@ -357,12 +359,12 @@ cudaError_t of_chunk(const NormArgs& a, int chunk, cudaStream_t stream) {
 }  // namespace
 
 int norm_units(int M, int H) {
-  // as many rows in the making as 512 threads an SM have, a thread sixteen elements; and four rows
-  // a unit or more, whose sums are written and read again, where that leaves every SM one
+  // as many rows in the making as 512 threads an SM have, a thread sixteen elements; and two rows a
+  // unit or more, whose sums are written and read again, where that leaves every SM one
   const int threads = norm_threads(H < kNormRegisterColumns ? H : kNormRegisterColumns, 8, 16);
   const int most = 152 * (threads < 512 ? 512 / threads : 1);
-  const int four = (M + 3) / 4, least = M < 152 ? M : 152;
-  const int n = four > least ? four : least;
+  const int two = (M + 1) / 2, least = M < 152 ? M : 152;
+  const int n = two > least ? two : least;
   return n < most ? n : most;
 }
 
