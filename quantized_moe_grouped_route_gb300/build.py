@@ -30,7 +30,8 @@ BINDING_FOR = os.path.join(BUILD, "qmoe_torch.for")
 
 SOURCES = ["api.cu", "route.cu", "misc.cu", "gemm.cu", "gemm2.cu", "api_ops.cu", "gate.cu",
            "tokens.cu", "lora.cu", "lora_shrink.cu", "lora_gemm.cu", "api_block.cu", "norm.cu",
-           "norm_backward.cu", "checkpoint.cu", "ffn_gemm.cu", "ffn_stream.cu", "ffn_few.cu"]
+           "norm_backward.cu", "checkpoint.cu", "ffn_gemm.cu", "ffn_stream.cu", "ffn_few.cu",
+           "ffn_finish.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

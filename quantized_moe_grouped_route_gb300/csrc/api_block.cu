@@ -286,9 +286,16 @@ static bool ffn_shape(int M, int H, int I) {
   return check_ffn(QMOE_DTYPE_BF16, M, H, I, QMOE_ACT_SILU, 1.f) == QMOE_OK;
 }
 
+// Workspaces: the error word's block, the rows between the products, the sums of segments; each as
+// large as any batch of up to M tokens needs.
+static size_t ffn_forward_part(int M, int I) {
+  return kWsHeaderBytes + align_up((size_t)M * I * 2, 256);
+}
+
 size_t qmoe_gated_ffn_workspace_size(int M, int H, int I) {
   if (!ffn_shape(M, H, I)) return 0;
-  return kWsHeaderBytes + align_up((size_t)M * I * 2, 256);
+  const size_t up = ffn_part_bytes(M, 2LL * I), down = ffn_part_bytes(M, H);
+  return ffn_forward_part(M, I) + align_up(up > down ? up : down, 256);
 }
 
 int qmoe_gated_ffn(const void* x_dev, int dtype, long long ldx, const void* w13_dev,
@@ -329,6 +336,7 @@ int qmoe_gated_ffn(const void* x_dev, int dtype, long long ldx, const void* w13_
   up.limit = limit;
   up.err = reinterpret_cast<unsigned int*>(ws);
   up.clear_err = 1;
+  up.part = reinterpret_cast<float*>(ws + ffn_forward_part(M, I));
   auto launch = [&](const FfnProduct& f) {
     if (!kept_dev && M <= kFfnStreamTokens) return launch_ffn_stream(f, s);
     if (!kept_dev && M <= kFfnFewTokens) return launch_ffn_few(f, sms, s);
@@ -348,19 +356,24 @@ int qmoe_gated_ffn(const void* x_dev, int dtype, long long ldx, const void* w13_
   down.K = I;
   down.out = out_dev;
   down.err = up.err;
+  down.part = up.part;
   return cuda_rc(launch(down));
 }
 
-// Workspace of the backward pass: [du | dg], h, and x out of its codes.
+// Workspace of the backward pass: [du | dg], h, x out of its codes, the sums of segments.
 struct FfnBackwardLayout {
-  size_t dug, h, x, total;
+  size_t dug, h, x, part, total;
 };
 static FfnBackwardLayout ffn_backward_layout(int M, int H, int I, bool codes) {
   FfnBackwardLayout L;
   L.dug = kWsHeaderBytes;
   L.h = align_up(L.dug + (size_t)M * I * 4, 256);
   L.x = align_up(L.h + (size_t)M * I * 2, 256);
-  L.total = align_up(L.x + (codes ? (size_t)M * H * 2 : 0), 256);
+  L.part = align_up(L.x + (codes ? (size_t)M * H * 2 : 0), 256);
+  size_t part = 0;
+  for (size_t b : {ffn_part_bytes(M, I), ffn_part_bytes(M, H), ffn_part_bytes(2LL * I, H)})
+    part = b > part ? b : part;
+  L.total = align_up(L.part + part, 256);
   return L;
 }
 
@@ -418,6 +431,7 @@ int qmoe_gated_ffn_backward(const void* dout_dev, int dtype, long long lddout, c
   f.err = reinterpret_cast<unsigned int*>(ws);
   f.activation = activation;
   f.limit = limit;
+  f.part = reinterpret_cast<float*>(ws + L.part);
   auto product = [&](FfnOp op, const void* a, long long lda, const void* b, long long ldb, int m,
                      int n, int k, void* out) {
     f.op = op;

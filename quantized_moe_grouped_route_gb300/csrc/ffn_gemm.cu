@@ -185,7 +185,9 @@ __device__ __forceinline__ void tile_of(const FfnGemm& p, int i, int* tm, int* t
   *tm = first + r - *tn * rows;
 }
 
-template <class T, Op OP, bool CODES>
+// PART: of a tile's K steps one of p.splits segments, whose sums are left in p.part [splits][M][columns]
+// (u's columns before g's) for the kernels of ffn_finish.cu.
+template <class T, Op OP, bool CODES, bool PART>
 __global__ void __launch_bounds__(kThreads, 1)
     ffn_gemm_kernel(const __grid_constant__ Maps maps, const FfnGemm p) {
   extern __shared__ uint8_t smem_raw[];
@@ -237,7 +239,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   grid_dep_launch();
   if (p.clear_err && blockIdx.x == 0 && threadIdx.x == 0) *p.err = 0;
 
-  const int units = p.tiles_m * p.tiles_n;
+  const int units = p.tiles_m * p.tiles_n * (PART ? p.splits : 1);
+  auto tile_of_unit = [&](int i, int* tm, int* tn) { tile_of(p, PART ? i / p.splits : i, tm, tn); };
+  auto first_step = [&](int i) { return PART ? p.ksteps * (i % p.splits) / p.splits : 0; };
+  auto last_step = [&](int i) {
+    return PART ? p.ksteps * (i % p.splits + 1) / p.splits : p.ksteps;
+  };
   const int cols = OP == Op::kUp ? p.tile_n / 2 : p.tile_n;  // of the result, a tile
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
     return warp_wait_cl(smem_u32(bar), parity, abort_flag, p.err);
@@ -252,10 +259,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     for (int i = worker; i < units && ok; i += workers) {
       int tm, tn;
-      tile_of(p, i, &tm, &tn);
+      tile_of_unit(i, &tm, &tn);
       const int row = tm * 256 + (int)rank * 128;
       const int col = OP == Op::kUp ? tn * cols : tn * p.tile_n + (int)rank * rows_b;
-      for (int k = 0; k < p.ksteps; ++k) {
+      const int k1 = last_step(i);
+      for (int k = first_step(i); k < k1; ++k) {
         if (!wait(&empty[s], ph)) {
           ok = false;
           break;
@@ -311,7 +319,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc_fence_after();
         const uint32_t dst = tmem + ab * kAccCols;
-        for (int k = 0; k < p.ksteps; ++k) {
+        const int k0 = first_step(i), k1 = last_step(i);
+        for (int k = k0; k < k1; ++k) {
           if (!wait(&full[s], ph)) {
             ok = false;
             break;
@@ -321,7 +330,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lead) {
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-              mma_pair(dst, a0 + off + step_a * j, b0 + off + step_b * j, idesc, (k > 0) | (j > 0));
+              mma_pair(dst, a0 + off + step_a * j, b0 + off + step_b * j, idesc, (k > k0) | (j > 0));
           }
           tc_commit2_both_if(lead, smem_u32(&empty[s]));
           if (++s == (uint32_t)stages) {
@@ -344,12 +353,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     int turn = 0;
     for (int i = worker; i < units; i += workers, ++local) {
       int tm, tn;
-      tile_of(p, i, &tm, &tn);
+      tile_of_unit(i, &tm, &tn);
       const int ab = local & 1;
       const int row0 = tm * 256 + (int)rank * 128 + q * 32, col0 = tn * cols;
       const int n = min(cols, p.N - col0);  // columns of this tile
       Kept ku, kg;
-      if constexpr (OP == Op::kDh) {
+      if constexpr (OP == Op::kDh && !PART) {
         fetch_kept<T, CODES>(ku, p, row0 + lane, col0, 0);
         fetch_kept<T, CODES>(kg, p, row0 + lane, col0, 1);
       }
@@ -357,7 +366,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
       const uint32_t tbase = tmem + ((uint32_t)(q * 32) << 16) + ab * kAccCols;
       const bool rows_in = row0 < p.M;
-      for (int c0 = 0; c0 < n; c0 += 64) {
+      if constexpr (PART) {
+        // a lane's row in pieces of 128 bytes
+        const int width = OP == Op::kUp ? 2 * p.N : p.N;
+        float* to = p.part + ((size_t)(i % p.splits) * p.M + row0 + lane) * width + col0;
+        for (int half = 0; half < (OP == Op::kUp ? 2 : 1); ++half)
+          for (int c = 0; c < n; c += 32) {
+            float v[32];
+            load_acc32(tbase + half * (p.tile_n / 2) + c, v);
+#pragma unroll
+            for (int k = 0; k < 32; k += 4)
+              if (row0 + lane < p.M && c + k < n)
+                *reinterpret_cast<float4*>(to + half * p.N + c + k) =
+                    make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
+          }
+      }
+      for (int c0 = 0; c0 < (PART ? 0 : n); c0 += 64) {
         // the staging tiles are free again
         const int t = OP == Op::kUp || OP == Op::kDh ? 0 : turn;
         turn ^= 1;
@@ -451,9 +475,9 @@ bool map_of(CUtensorMap* map, int dtype, const void* base, long long rows, int c
   return make_tmap16(map, dtype, base, 2, dims, strides, box) == QMOE_OK;
 }
 
-template <class T, Op OP, bool CODES = false>
-cudaError_t run(FfnGemm& p, const Maps& maps, int num_sms, cudaStream_t stream) {
-  auto* k = ffn_gemm_kernel<T, OP, CODES>;
+template <class T, Op OP, bool CODES, bool PART>
+cudaError_t run_as(FfnGemm& p, const Maps& maps, int num_sms, cudaStream_t stream) {
+  auto* k = ffn_gemm_kernel<T, OP, CODES, PART>;
   const int stage = kABytes + p.tile_n / 2 * 128;
   const int other = 1024 + kCtrl + 4 * staging(OP) * kStageTile;
   const int most = (kSmemLimit - other) / stage;
@@ -470,7 +494,7 @@ cudaError_t run(FfnGemm& p, const Maps& maps, int num_sms, cudaStream_t stream) 
     return resident_clusters(k, 2, kThreads, kSmemLimit, num_sms);
   });
   if (held < 1) return cudaErrorInvalidConfiguration;
-  const int units = p.tiles_m * p.tiles_n;
+  const int units = p.tiles_m * p.tiles_n * (PART ? p.splits : 1);
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2] = {pdl_attribute()};
   attr[1].id = cudaLaunchAttributeClusterDimension;
@@ -486,27 +510,52 @@ cudaError_t run(FfnGemm& p, const Maps& maps, int num_sms, cudaStream_t stream) 
   return cudaLaunchKernelEx(&cfg, k, maps, p);
 }
 
-// Columns of a tile: 256, or 128 where that takes less time, a tile of 128 columns taking about
-// 0.55 of a wide one's (its rows of A are loaded for half as many products).
-void cut(FfnGemm& p, int rows, int cols, int num_sms, bool up) {
-  p.tiles_m = (rows + 255) / 256;
-  const int pairs = num_sms / 2;
-  auto tiles_n = [&](int n) { return (cols + (up ? n / 2 : n) - 1) / (up ? n / 2 : n); };
-  auto waves = [&](int n) { return (p.tiles_m * (long long)tiles_n(n) + pairs - 1) / pairs; };
-  p.tile_n = 100 * waves(256) <= 55 * waves(128) ? 256 : 128;
-  p.tiles_n = tiles_n(p.tile_n);
+template <class T, Op OP, bool CODES = false>
+cudaError_t run(FfnGemm& p, const Maps& maps, int num_sms, cudaStream_t stream) {
+  if (p.splits == 1) return run_as<T, OP, CODES, false>(p, maps, num_sms, stream);
+  constexpr Op kPart = OP == Op::kDh ? Op::kPlainNN : OP;  // the same operands
+  const cudaError_t e = run_as<T, kPart, false, true>(p, maps, num_sms, stream);
+  return e == cudaSuccess ? launch_ffn_finish(p, stream) : e;
+}
+
+// How a product is cut: tiles of 256 or 128 columns, and their K steps into segments where the
+// tiles are far fewer than the pairs of SMs.  By an estimate of the time in units of a step of a
+// wide tile (0.27 us): a step of a tile of 128 columns takes 0.55 (its rows of A are loaded for
+// half as many products), a tile's last epilogue about 8, segments another kernel of about 12 and
+// their sums written and read again (about 5 TB/s).  By the number of pairs of a GB300, so that
+// results are the same on every part.
+void cut(FfnGemm& p) {
+  constexpr int kPairs = 76;
+  const bool up = p.op == FfnOp::kUp;
+  p.tiles_m = (p.M + 255) / 256;
+  p.ksteps = (p.K + 63) / 64;
+  double best = 0;
+  for (int n = 256; n >= 128; n /= 2) {
+    const int cols = up ? n / 2 : n, tiles_n = (p.N + cols - 1) / cols;
+    const long long tiles = (long long)p.tiles_m * tiles_n;
+    for (int s = 1; s <= kFfnMaxSplits && (s == 1 || (tiles * s <= kPairs && p.ksteps >= 4 * s)); ++s) {
+      const double waves = (double)((tiles * s + kPairs - 1) / kPairs);
+      const double steps = (p.ksteps + s - 1) / s * (n == 256 ? 1.0 : 0.55);
+      const double sums = (double)s * p.M * p.N * (up ? 2 : 1) * 8;
+      const double cost = waves * steps + (n == 256 ? 8 : 4) + (s > 1 ? 12 + sums / 1.35e6 : 0);
+      if (best != 0 && cost >= best) continue;
+      best = cost;
+      p.tile_n = n;
+      p.tiles_n = tiles_n;
+      p.splits = s;
+    }
+  }
 }
 
 template <class T>
 cudaError_t of_op(const FfnProduct& f, int num_sms, cudaStream_t stream) {
   FfnGemm p = {};
   static_cast<FfnProduct&>(p) = f;
+  cut(p);
   Maps m = {};
   bool ok = true;
   switch (f.op) {
     case FfnOp::kUp: {  // x [M][H], w13 [2I][H] -> h [M][I] (u, g [M][I] at a pitch of 2I)
-      cut(p, f.M, f.N, num_sms, true);
-      p.ksteps = (f.K + 63) / 64;
       const T* w = reinterpret_cast<const T*>(f.b);
       ok = map_of(&m.a, f.dtype, f.a, f.M, f.K, f.lda, 128) &&
            map_of(&m.b, f.dtype, w, f.N, f.K, f.K, p.tile_n / 2) &&
@@ -521,8 +570,6 @@ cudaError_t of_op(const FfnProduct& f, int num_sms, cudaStream_t stream) {
       return ok ? run<T, Op::kUp>(p, m, num_sms, stream) : cudaErrorInvalidValue;
     }
     case FfnOp::kDh: {  // dout [M][H], w2 [H][I] -> h, du, dg
-      cut(p, f.M, f.N, num_sms, false);
-      p.ksteps = (f.K + 63) / 64;
       T* dug = reinterpret_cast<T*>(f.ug);
       ok = map_of(&m.a, f.dtype, f.a, f.M, f.K, f.lda, 128) &&
            map_of(&m.b, f.dtype, f.b, f.K, f.N, f.N, 64) &&
@@ -535,8 +582,6 @@ cudaError_t of_op(const FfnProduct& f, int num_sms, cudaStream_t stream) {
                            : run<T, Op::kDh, false>(p, m, num_sms, stream);
     }
     default: {
-      cut(p, f.M, f.N, num_sms, false);
-      p.ksteps = (f.K + 63) / 64;
       const bool across_a = f.op == FfnOp::kTN, across_b = f.op != FfnOp::kNT;
       ok = (across_a ? map_of(&m.a, f.dtype, f.a, f.K, f.M, f.lda, 64)
                      : map_of(&m.a, f.dtype, f.a, f.M, f.K, f.lda, 128)) &&

@@ -354,10 +354,21 @@ struct FfnProduct {
   float limit;
   unsigned int* err;
   int clear_err;  // the first product of a call
+  float* part;    // ffn_part_bytes
 };
 struct FfnGemm : FfnProduct {
   int tile_n, tiles_m, tiles_n, ksteps, stages;
+  int splits;  // segments of K
 };
+// Bytes of the sums of segments of a product with `rows` x `columns` of them, or fewer rows: as
+// many tiles as there are pairs of SMs are the most, and as many segments.
+constexpr int kFfnMaxSplits = 16;
+inline size_t ffn_part_bytes(long long rows, long long columns) {
+  const long long most = 76LL * 256 * 256 * 4, all = kFfnMaxSplits * rows * columns * 4;
+  return (size_t)(all < most ? all : most);
+}
+// ffn_finish.cu: the segments' sums added up, and what a tile's epilogue does
+cudaError_t launch_ffn_finish(const FfnGemm& p, cudaStream_t stream);
 cudaError_t launch_ffn_product(const FfnProduct& f, int num_sms, cudaStream_t stream);
 // ffn_stream.cu, ffn_few.cu: kUp (nothing kept) and kNT for few tokens, which are the rows of a
 constexpr int kFfnStreamTokens = 8;

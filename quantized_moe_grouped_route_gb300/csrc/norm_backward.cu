@@ -282,9 +282,11 @@ __global__ void __launch_bounds__(ACC && VEC > 1 ? 512 : 1024) norm_backward_ker
 }
 
 // dst[h] = sum over the units of their sum number `which`, 32 columns a CTA.
-__global__ void __launch_bounds__(1024) norm_sums_kernel(const float* partial, int units, int H,
-                                                         float* post, float* pre, float* gate) {
-  __shared__ float part[32][33];
+constexpr int kSumWarps = 8;
+__global__ void __launch_bounds__(kSumWarps * 32) norm_sums_kernel(const float* partial, int units,
+                                                                   int H, float* post, float* pre,
+                                                                   float* gate) {
+  __shared__ float part[kSumWarps][32];
   float* dst = blockIdx.y == kPost ? post : blockIdx.y == kPre ? pre : gate;
   grid_dep_wait();
   if (!dst) return;
@@ -294,14 +296,14 @@ __global__ void __launch_bounds__(1024) norm_sums_kernel(const float* partial, i
   if (h < H) {
     const float* src = partial + (size_t)blockIdx.y * H + h;
 #pragma unroll 8
-    for (int u = slice; u < units; u += 32) s += src[(size_t)u * 3 * H];
+    for (int u = slice; u < units; u += kSumWarps) s += src[(size_t)u * 3 * H];
   }
   part[slice][lane] = s;
   __syncthreads();
   if (slice != 0 || h >= H) return;
   s = 0.f;
 #pragma unroll
-  for (int i = 0; i < 32; ++i) s += part[i][lane];
+  for (int i = 0; i < kSumWarps; ++i) s += part[i][lane];
   dst[h] = s;
 }
 
@@ -385,7 +387,7 @@ cudaError_t launch_norm_backward(const NormArgs& args, int dtype, int chunk, cud
   float* post = a.post_weight ? a.dpost_weight : nullptr;
   float* pre = a.pre_weight ? a.dpre_weight : nullptr;
   if (!gate && !post && !pre) return cudaSuccess;
-  return launch_pdl(norm_sums_kernel, dim3((a.H + 31) / 32, 3), 1024, 0, stream,
+  return launch_pdl(norm_sums_kernel, dim3((a.H + 31) / 32, 3), kSumWarps * 32, 0, stream,
                 (const float*)a.partial, a.units, a.H, post, pre, gate);
 }
 
