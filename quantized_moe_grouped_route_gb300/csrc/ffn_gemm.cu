@@ -43,7 +43,15 @@ __host__ __device__ constexpr int staging(Op op) { return op == Op::kUp || op ==
 
 struct Maps {
   CUtensorMap a, b, b2, o, o2, o3;
+  CUtensorMap a_edge, b_edge, b2_edge;  // the operands in boxes of a last block's rows
 };
+
+// A matrix's last block of `box` rows is copied in a box of its own number of rows: rows that a copy
+// has to fill in cost it several times what rows of the matrix do (1 token by boxes of 128 rows: 182 us
+// a call where 512 tokens took 43).  What is left in shared memory beyond reaches rows and columns of
+// the accumulator that are not written; along K zeros are filled in up to the 16 of an MMA.
+__host__ __device__ constexpr int last_rows(int rows, int box) { return (rows + box - 1) % box + 1; }
+__host__ __device__ constexpr int last_deep(int depth) { return (last_rows(depth, 64) + 15) / 16 * 16; }
 
 __device__ __forceinline__ uint64_t l2_policy_normal() {
   uint64_t p;
@@ -225,6 +233,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     prefetch_tmap(&maps.b);
     if (OP == Op::kUp) prefetch_tmap(&maps.b2);
     prefetch_tmap(&maps.o);
+    prefetch_tmap(&maps.a_edge);
+    prefetch_tmap(&maps.b_edge);
   }
   if (warp == 1) {
     tmem_alloc2(smem_u32(tmem_slot), 2 * kAccCols);
@@ -260,30 +270,70 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = worker; i < units && ok; i += workers) {
       int tm, tn;
       tile_of_unit(i, &tm, &tn);
+      // this SM's rows of A and columns of B: where they begin and how many there are
+      auto rows_a = [&](int r) { return max(0, min(128, p.M - tm * 256 - r * 128)); };
+      auto cols_b = [&](int r) {
+        return max(0, min(rows_b, p.N - (OP == Op::kUp ? tn * cols : tn * p.tile_n + r * rows_b)));
+      };
       const int row = tm * 256 + (int)rank * 128;
       const int col = OP == Op::kUp ? tn * cols : tn * p.tile_n + (int)rank * rows_b;
-      const int k1 = last_step(i);
-      for (int k = first_step(i); k < k1; ++k) {
+      const int na = rows_a((int)rank), nb = cols_b((int)rank);
+      // of the pair's two SMs (a tile whose second half is whole is whole)
+      const bool whole = rows_a(1) == 128 && cols_b(1) == rows_b;
+      const int k0 = first_step(i), k1 = last_step(i);
+      // steps of whole boxes, one copy an operand (two across K): the issue is what paces a step
+      const int k_whole = whole ? min(k1, p.K / 64) : k0;
+      for (int k = k0; k < k1; ++k) {
         if (!wait(&empty[s], ph)) {
           ok = false;
           break;
         }
         const uint32_t sa = smem_u32(smem) + s * stage_bytes, sb = sa + kABytes;
         const uint32_t bar = full0 + s * 8;
-        if (rank == 0)
-          mbar_arrive_expect_tx_if(lead, smem_u32(&full[s]), 2u * (uint32_t)stage_bytes);
-        if (a_across(OP)) {
-          tma_load_2d_pair_if(lead, sa, &maps.a, row, k * 64, bar, pol);
-          tma_load_2d_pair_if(lead, sa + 8192, &maps.a, row + 64, k * 64, bar, pol);
+        if (k < k_whole) {
+          if (rank == 0)
+            mbar_arrive_expect_tx_if(lead, smem_u32(&full[s]), 2u * (uint32_t)stage_bytes);
+          if (a_across(OP)) {
+            tma_load_2d_pair_if(lead, sa, &maps.a, row, k * 64, bar, pol);
+            tma_load_2d_pair_if(lead, sa + 8192, &maps.a, row + 64, k * 64, bar, pol);
+          } else {
+            tma_load_2d_pair_if(lead, sa, &maps.a, k * 64, row, bar, pol);
+          }
+          if (b_across(OP)) {
+            tma_load_2d_pair_if(lead, sb, &maps.b, col, k * 64, bar, pol);
+            if (rows_b > 64)
+              tma_load_2d_pair_if(lead, sb + 8192, &maps.b, col + 64, k * 64, bar, pol);
+          } else {
+            const CUtensorMap* b = OP == Op::kUp && rank != 0 ? &maps.b2 : &maps.b;
+            tma_load_2d_pair_if(lead, sb, b, k * 64, col, bar, pol);
+          }
         } else {
-          tma_load_2d_pair_if(lead, sa, &maps.a, k * 64, row, bar, pol);
-        }
-        if (b_across(OP)) {
-          tma_load_2d_pair_if(lead, sb, &maps.b, col, k * 64, bar, pol);
-          if (rows_b > 64) tma_load_2d_pair_if(lead, sb + 8192, &maps.b, col + 64, k * 64, bar, pol);
-        } else {
-          const CUtensorMap* b = OP == Op::kUp && rank != 0 ? &maps.b2 : &maps.b;
-          tma_load_2d_pair_if(lead, sb, b, k * 64, col, bar, pol);
+          const bool deep = k < p.K / 64;  // a whole step of K
+          const int depth = deep ? 64 : last_deep(p.K);
+          if (rank == 0) {
+            uint32_t rows = 0;  // of 128 bytes, of both SMs
+            for (int r = 0; r < 2; ++r)
+              rows += (a_across(OP) ? (rows_a(r) + 63) / 64 * depth : rows_a(r)) +
+                      (b_across(OP) ? (cols_b(r) + 63) / 64 * depth : cols_b(r));
+            mbar_arrive_expect_tx_if(lead, smem_u32(&full[s]), rows * 128u);
+          }
+          if (a_across(OP)) {
+            for (int c = 0; c < na; c += 64)
+              tma_load_2d_pair_if(lead, sa + c * 128, deep ? &maps.a : &maps.a_edge, row + c, k * 64,
+                                  bar, pol);
+          } else if (na > 0) {
+            tma_load_2d_pair_if(lead, sa, na == 128 ? &maps.a : &maps.a_edge, k * 64, row, bar, pol);
+          }
+          if (b_across(OP)) {
+            for (int c = 0; c < nb; c += 64)
+              tma_load_2d_pair_if(lead, sb + c * 128, deep ? &maps.b : &maps.b_edge, col + c, k * 64,
+                                  bar, pol);
+          } else if (nb > 0) {
+            const bool second = OP == Op::kUp && rank != 0;
+            const CUtensorMap* b = nb == rows_b ? (second ? &maps.b2 : &maps.b)
+                                                : (second ? &maps.b2_edge : &maps.b_edge);
+            tma_load_2d_pair_if(lead, sb, b, k * 64, col, bar, pol);
+          }
         }
         if (++s == (uint32_t)stages) {
           s = 0;
@@ -327,9 +377,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           tc_fence_after();
           const uint32_t off = (s * stage_bytes) >> 4;
-          if (lead) {
+          if (k < p.K / 64) {
+            if (lead) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
+              for (int j = 0; j < 4; ++j)
+                mma_pair(dst, a0 + off + step_a * j, b0 + off + step_b * j, idesc, (k > k0) | (j > 0));
+            }
+          } else if (lead) {  // the slices of 16 that there are
+            for (int j = 0; j < (p.K - k * 64 + 15) / 16; ++j)
               mma_pair(dst, a0 + off + step_a * j, b0 + off + step_b * j, idesc, (k > k0) | (j > 0));
           }
           tc_commit2_both_if(lead, smem_u32(&empty[s]));
@@ -560,6 +615,10 @@ cudaError_t of_op(const FfnProduct& f, int num_sms, cudaStream_t stream) {
       ok = map_of(&m.a, f.dtype, f.a, f.M, f.K, f.lda, 128) &&
            map_of(&m.b, f.dtype, w, f.N, f.K, f.K, p.tile_n / 2) &&
            map_of(&m.b2, f.dtype, w + (size_t)f.N * f.K, f.N, f.K, f.K, p.tile_n / 2) &&
+           map_of(&m.a_edge, f.dtype, f.a, f.M, f.K, f.lda, last_rows(f.M, 128)) &&
+           map_of(&m.b_edge, f.dtype, w, f.N, f.K, f.K, last_rows(f.N, p.tile_n / 2)) &&
+           map_of(&m.b2_edge, f.dtype, w + (size_t)f.N * f.K, f.N, f.K, f.K,
+                  last_rows(f.N, p.tile_n / 2)) &&
            map_of(&m.o, f.dtype, f.out, f.M, f.N, f.N, 32);
       m.o2 = m.o3 = m.o;
       if (f.save == 16) {
@@ -573,10 +632,13 @@ cudaError_t of_op(const FfnProduct& f, int num_sms, cudaStream_t stream) {
       T* dug = reinterpret_cast<T*>(f.ug);
       ok = map_of(&m.a, f.dtype, f.a, f.M, f.K, f.lda, 128) &&
            map_of(&m.b, f.dtype, f.b, f.K, f.N, f.N, 64) &&
+           map_of(&m.a_edge, f.dtype, f.a, f.M, f.K, f.lda, last_rows(f.M, 128)) &&
+           map_of(&m.b_edge, f.dtype, f.b, f.K, f.N, f.N, last_deep(f.K)) &&
            map_of(&m.o, f.dtype, f.out, f.M, f.N, f.N, 32) &&
            map_of(&m.o2, f.dtype, dug, f.M, f.N, 2LL * f.N, 32) &&
            map_of(&m.o3, f.dtype, dug + f.N, f.M, f.N, 2LL * f.N, 32);
       m.b2 = m.b;
+      m.b2_edge = m.b_edge;
       if (!ok) return cudaErrorInvalidValue;
       return f.kept_scales ? run<T, Op::kDh, true>(p, m, num_sms, stream)
                            : run<T, Op::kDh, false>(p, m, num_sms, stream);
@@ -587,8 +649,14 @@ cudaError_t of_op(const FfnProduct& f, int num_sms, cudaStream_t stream) {
                      : map_of(&m.a, f.dtype, f.a, f.M, f.K, f.lda, 128)) &&
            (across_b ? map_of(&m.b, f.dtype, f.b, f.K, f.N, f.ldb, 64)
                      : map_of(&m.b, f.dtype, f.b, f.N, f.K, f.ldb, p.tile_n / 2)) &&
+           (across_a ? map_of(&m.a_edge, f.dtype, f.a, f.K, f.M, f.lda, last_deep(f.K))
+                     : map_of(&m.a_edge, f.dtype, f.a, f.M, f.K, f.lda, last_rows(f.M, 128))) &&
+           (across_b ? map_of(&m.b_edge, f.dtype, f.b, f.K, f.N, f.ldb, last_deep(f.K))
+                     : map_of(&m.b_edge, f.dtype, f.b, f.N, f.K, f.ldb,
+                              last_rows(f.N, p.tile_n / 2))) &&
            map_of(&m.o, f.dtype, f.out, f.M, f.N, f.N, 32);
       m.b2 = m.b;
+      m.b2_edge = m.b_edge;
       m.o2 = m.o3 = m.o;
       if (!ok) return cudaErrorInvalidValue;
       if (f.op == FfnOp::kNT) return run<T, Op::kPlainNT>(p, m, num_sms, stream);
