@@ -98,7 +98,7 @@ int make_tmap_rows(CUtensorMap* map, const void* base, int rows, int cols, int b
 }  // namespace
 
 int make_tmap16(CUtensorMap* map, int dtype, const void* base, int rank, const uint64_t* dims,
-                const uint64_t* strides, const uint32_t* box) {
+                const uint64_t* strides, const uint32_t* box, int swizzle) {
   auto fn = encode_fn();
   if (!fn) return QMOE_ERR_CUDA;
   cuuint64_t d[3], st[2];
@@ -108,8 +108,8 @@ int make_tmap16(CUtensorMap* map, int dtype, const void* base, int rank, const u
   const CUresult r = fn(
       map, dtype == QMOE_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
       (cuuint32_t)rank, const_cast<void*>(base), d, st, bx, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-      CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+      swizzle == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+      CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? QMOE_OK : QMOE_ERR_CUDA;
 }
 

@@ -25,12 +25,13 @@
 namespace qmoe {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kEpiWarps = 8;  // two a lane quarter of TMEM, 32 columns in turn
+constexpr int kThreads = 128 + 32 * kEpiWarps;
 constexpr int kMaxStages = 12;
 constexpr int kCtrl = 1024;
 constexpr int kAccCols = 256;
 constexpr int kABytes = 128 * 128;  // a stage's A: 128 rows x 64 of K
-constexpr int kStageTile = 4096;    // an epilogue warp's staging tile: 32 rows x 64 columns
+constexpr int kStageTile = 2048;    // an epilogue warp's staging tile: 32 rows x 32 columns
 constexpr int kSmemLimit = 232448;
 
 enum class Op { kUp, kPlainNT, kPlainNN, kPlainTN, kDh };
@@ -93,20 +94,33 @@ __device__ __forceinline__ uint64_t sdesc_across(uint32_t saddr) {
   return (sdesc_sw128(saddr) & ~((uint64_t)0x3fff << 16)) | (uint64_t)(64 * 128 >> 4) << 16;
 }
 
-// 32 values of a lane's row into half `half` of a staging tile (128-byte rows, swizzled as the
+// 16 values of a lane's row into half `half` of a staging tile (64-byte rows, swizzled as the
 // store's tensor map has it).
 template <class T>
-__device__ __forceinline__ void stage_half(uint8_t* tile, int half, const float (&v)[32]) {
+__device__ __forceinline__ void stage_half(uint8_t* tile, int half, const float* v) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
+  for (int j = 0; j < 2; ++j) {
     Pack<T, 8> p;
 #pragma unroll
     for (int e = 0; e < 8; ++e) p.v[e] = from_f32<T>(v[8 * j + e]);
-    *reinterpret_cast<uint4*>(tile + lane * 128 + (((half * 4 + j) ^ (lane & 7)) << 4)) = p.raw;
+    *reinterpret_cast<uint4*>(tile + lane * 64 + (((half * 2 + j) ^ (lane >> 1 & 3)) << 4)) = p.raw;
   }
 }
+template <class T>
+__device__ __forceinline__ void stage_row(uint8_t* tile, const float (&v)[32]) {
+  stage_half<T>(tile, 0, v);
+  stage_half<T>(tile, 1, v + 16);
+}
 
+__device__ __forceinline__ void load_acc16(uint32_t taddr, float (&v)[16]) {
+  uint32_t r[16];
+  tmem_ld_x16(taddr, r);
+  tmem_wait_ld();
+  tmem_ld_ready(r);
+#pragma unroll
+  for (int k = 0; k < 16; ++k) v[k] = __uint_as_float(r[k]);
+}
 __device__ __forceinline__ void load_acc32(uint32_t taddr, float (&v)[32]) {
   uint32_t r[2][16];
   tmem_ld_x16(taddr, r[0]);
@@ -205,7 +219,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int stage_bytes = kABytes + rows_b * 128;
   const int stages = p.stages;
   uint8_t* epi = smem + stages * stage_bytes;
-  uint8_t* ctrl = epi + 4 * staging(OP) * kStageTile;
+  uint8_t* ctrl = epi + kEpiWarps * staging(OP) * kStageTile;
   uint64_t* full = reinterpret_cast<uint64_t*>(ctrl);
   uint64_t* empty = full + kMaxStages;
   uint64_t* accf = empty + kMaxStages;
@@ -224,7 +238,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&accf[i]), 1);
-      mbar_init(smem_u32(&acce[i]), 8);  // four epilogue warps of each SM
+      mbar_init(smem_u32(&acce[i]), 2 * kEpiWarps);  // of both SMs
     }
     mbar_init(smem_u32(drain), 1);
     *abort_flag = 0;
@@ -399,9 +413,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp >= 4) {
     // ------------------------------------------------------------------- epilogue
-    const int q = warp & 3;
+    const int q = warp & 3, first_col = 32 * ((warp - 4) >> 2);
+    constexpr int kApart = 32 * (kEpiWarps / 4);  // a warp's columns
     const uint32_t acce0 = peer_addr(smem_u32(acce), 0);
-    uint8_t* stage = epi + q * staging(OP) * kStageTile;
+    uint8_t* stage = epi + (warp - 4) * staging(OP) * kStageTile;
     const uint32_t stage0 = smem_u32(stage);
     const bool gelu = p.activation == QMOE_ACT_GELU;
     uint32_t local = 0;
@@ -414,89 +429,92 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int n = min(cols, p.N - col0);  // columns of this tile
       Kept ku, kg;
       if constexpr (OP == Op::kDh && !PART) {
-        fetch_kept<T, CODES>(ku, p, row0 + lane, col0, 0);
-        fetch_kept<T, CODES>(kg, p, row0 + lane, col0, 1);
+        fetch_kept<T, CODES>(ku, p, row0 + lane, col0 + first_col, 0);
+        fetch_kept<T, CODES>(kg, p, row0 + lane, col0 + first_col, 1);
       }
       if (!wait(&accf[ab], (local >> 1) & 1)) break;
       tc_fence_after();
       const uint32_t tbase = tmem + ((uint32_t)(q * 32) << 16) + ab * kAccCols;
       const bool rows_in = row0 < p.M;
-      if constexpr (PART) {
-        // a lane's row in pieces of 128 bytes
-        const int width = OP == Op::kUp ? 2 * p.N : p.N;
-        float* to = p.part + ((size_t)(i % p.splits) * p.M + row0 + lane) * width + col0;
-        for (int half = 0; half < (OP == Op::kUp ? 2 : 1); ++half)
-          for (int c = 0; c < n; c += 32) {
+      for (int c = first_col; c < n; c += kApart) {
+        if constexpr (PART) {
+          // a lane's row in pieces of 128 bytes
+          const int width = OP == Op::kUp ? 2 * p.N : p.N;
+          float* to = p.part + ((size_t)(i % p.splits) * p.M + row0 + lane) * width + col0 + c;
+#pragma unroll
+          for (int half = 0; half < (OP == Op::kUp ? 2 : 1); ++half) {
             float v[32];
             load_acc32(tbase + half * (p.tile_n / 2) + c, v);
 #pragma unroll
             for (int k = 0; k < 32; k += 4)
               if (row0 + lane < p.M && c + k < n)
-                *reinterpret_cast<float4*>(to + half * p.N + c + k) =
+                *reinterpret_cast<float4*>(to + half * p.N + k) =
                     make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
           }
-      }
-      for (int c0 = 0; c0 < (PART ? 0 : n); c0 += 64) {
-        // the staging tiles are free again
-        const int t = OP == Op::kUp || OP == Op::kDh ? 0 : turn;
-        turn ^= 1;
-        if (lane == 0) {
-          if (OP == Op::kUp || OP == Op::kDh)
-            store_wait_read<0>();
-          else
-            store_wait_read<1>();
-        }
-        __syncwarp();
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const int c = c0 + 32 * half;
-          float v[32];
-          load_acc32(tbase + c, v);
+        } else {
+          // the staging tiles are free again
+          const int t = OP == Op::kUp || OP == Op::kDh ? 0 : turn;
+          turn ^= 1;
+          if (lane == 0) {
+            if (OP == Op::kUp || OP == Op::kDh)
+              store_wait_read<0>();
+            else
+              store_wait_read<1>();
+          }
+          __syncwarp();
           if constexpr (OP == Op::kUp) {
-            float g[32];
+            float u[32], g[32];
+            load_acc32(tbase + c, u);
             load_acc32(tbase + p.tile_n / 2 + c, g);
-            if (p.save == 8 && row0 + lane < p.M && c < n) {
+            if (p.save == 8 && row0 + lane < p.M) {
               const int blocks = (p.N + kCkBlock - 1) / kCkBlock;
               const size_t at = (size_t)(row0 + lane) * 2 * p.N + col0 + c;
               const size_t sat = (size_t)(row0 + lane) * 2 * blocks + (col0 + c) / kCkBlock;
-              save_block(v, min(32, n - c), p.codes + at, p.scales + sat);
+              save_block(u, min(32, n - c), p.codes + at, p.scales + sat);
               save_block(g, min(32, n - c), p.codes + at + p.N, p.scales + sat + blocks);
             }
             if (p.save == 16) {
-              stage_half<T>(stage + kStageTile, half, v);
-              stage_half<T>(stage + 2 * kStageTile, half, g);
+              stage_row<T>(stage + kStageTile, u);
+              stage_row<T>(stage + 2 * kStageTile, g);
             }
 #pragma unroll
-            for (int k = 0; k < 32; ++k) v[k] = gated(gelu, p.limit, v[k], g[k]);
-            stage_half<T>(stage, half, v);
+            for (int k = 0; k < 32; ++k) u[k] = gated(gelu, p.limit, u[k], g[k]);
+            stage_row<T>(stage, u);
           } else if constexpr (OP == Op::kDh) {
             const float su = CODES ? ck_value(ku.byte) : 0.f, sg = CODES ? ck_value(kg.byte) : 0.f;
-            float du[32], dg[32];
 #pragma unroll
-            for (int k = 0; k < 32; ++k)
-              v[k] = gated_backward(gelu, p.limit, kept_value<T, CODES>(ku, k, su),
-                                    kept_value<T, CODES>(kg, k, sg), v[k], &du[k], &dg[k]);
-            if (c + 32 < n) {
-              fetch_kept<T, CODES>(ku, p, row0 + lane, col0 + c + 32, 0);
-              fetch_kept<T, CODES>(kg, p, row0 + lane, col0 + c + 32, 1);
+            for (int half = 0; half < 2; ++half) {
+              float v[16], du[16], dg[16];
+              load_acc16(tbase + c + 16 * half, v);
+#pragma unroll
+              for (int k = 0; k < 16; ++k)
+                v[k] = gated_backward(gelu, p.limit, kept_value<T, CODES>(ku, 16 * half + k, su),
+                                      kept_value<T, CODES>(kg, 16 * half + k, sg), v[k], &du[k],
+                                      &dg[k]);
+              stage_half<T>(stage, half, v);
+              stage_half<T>(stage + kStageTile, half, du);
+              stage_half<T>(stage + 2 * kStageTile, half, dg);
             }
-            stage_half<T>(stage, half, v);
-            stage_half<T>(stage + kStageTile, half, du);
-            stage_half<T>(stage + 2 * kStageTile, half, dg);
+            if (c + kApart < n) {
+              fetch_kept<T, CODES>(ku, p, row0 + lane, col0 + c + kApart, 0);
+              fetch_kept<T, CODES>(kg, p, row0 + lane, col0 + c + kApart, 1);
+            }
           } else {
-            stage_half<T>(stage + t * kStageTile, half, v);
+            float v[32];
+            load_acc32(tbase + c, v);
+            stage_row<T>(stage + t * kStageTile, v);
           }
-        }
-        fence_proxy_async();
-        __syncwarp();
-        if (lane == 0 && rows_in) {
-          tma_store_2d(&maps.o, stage0 + t * kStageTile, col0 + c0, row0);
-          if (OP == Op::kDh || (OP == Op::kUp && p.save == 16)) {
-            tma_store_2d(&maps.o2, stage0 + kStageTile, col0 + c0, row0);
-            tma_store_2d(&maps.o3, stage0 + 2 * kStageTile, col0 + c0, row0);
+          fence_proxy_async();
+          __syncwarp();
+          if (lane == 0 && rows_in) {
+            tma_store_2d(&maps.o, stage0 + t * kStageTile, col0 + c, row0);
+            if (OP == Op::kDh || (OP == Op::kUp && p.save == 16)) {
+              tma_store_2d(&maps.o2, stage0 + kStageTile, col0 + c, row0);
+              tma_store_2d(&maps.o3, stage0 + 2 * kStageTile, col0 + c, row0);
+            }
           }
+          if (lane == 0) store_commit();
         }
-        if (lane == 0) store_commit();
       }
       tc_fence_before();
       __syncwarp();
@@ -522,7 +540,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// A matrix [rows][cols] whose rows lie ld elements apart, in boxes of 64 columns.
+// A matrix [rows][cols] whose rows lie ld elements apart, in boxes of 64 columns, or in the
+// epilogue's staging tiles.
+bool map_out(CUtensorMap* map, int dtype, const void* base, long long rows, int cols, long long ld) {
+  const uint64_t dims[2] = {(uint64_t)cols, (uint64_t)rows}, strides[1] = {(uint64_t)ld * 2};
+  const uint32_t box[2] = {32, 32};
+  return make_tmap16(map, dtype, base, 2, dims, strides, box, 64) == QMOE_OK;
+}
 bool map_of(CUtensorMap* map, int dtype, const void* base, long long rows, int cols, long long ld,
             int box_rows) {
   const uint64_t dims[2] = {(uint64_t)cols, (uint64_t)rows}, strides[1] = {(uint64_t)ld * 2};
@@ -534,7 +558,7 @@ template <class T, Op OP, bool CODES, bool PART>
 cudaError_t run_as(FfnGemm& p, const Maps& maps, int num_sms, cudaStream_t stream) {
   auto* k = ffn_gemm_kernel<T, OP, CODES, PART>;
   const int stage = kABytes + p.tile_n / 2 * 128;
-  const int other = 1024 + kCtrl + 4 * staging(OP) * kStageTile;
+  const int other = 1024 + kCtrl + kEpiWarps * staging(OP) * kStageTile;
   const int most = (kSmemLimit - other) / stage;
   p.stages = most < kMaxStages ? most : kMaxStages;
   const size_t smem = other + (size_t)p.stages * stage;
@@ -619,12 +643,12 @@ cudaError_t of_op(const FfnProduct& f, int num_sms, cudaStream_t stream) {
            map_of(&m.b_edge, f.dtype, w, f.N, f.K, f.K, last_rows(f.N, p.tile_n / 2)) &&
            map_of(&m.b2_edge, f.dtype, w + (size_t)f.N * f.K, f.N, f.K, f.K,
                   last_rows(f.N, p.tile_n / 2)) &&
-           map_of(&m.o, f.dtype, f.out, f.M, f.N, f.N, 32);
+           map_out(&m.o, f.dtype, f.out, f.M, f.N, f.N);
       m.o2 = m.o3 = m.o;
       if (f.save == 16) {
         T* ug = reinterpret_cast<T*>(f.ug);
-        ok = ok && map_of(&m.o2, f.dtype, ug, f.M, f.N, 2LL * f.N, 32) &&
-             map_of(&m.o3, f.dtype, ug + f.N, f.M, f.N, 2LL * f.N, 32);
+        ok = ok && map_out(&m.o2, f.dtype, ug, f.M, f.N, 2LL * f.N) &&
+             map_out(&m.o3, f.dtype, ug + f.N, f.M, f.N, 2LL * f.N);
       }
       return ok ? run<T, Op::kUp>(p, m, num_sms, stream) : cudaErrorInvalidValue;
     }
@@ -634,9 +658,9 @@ cudaError_t of_op(const FfnProduct& f, int num_sms, cudaStream_t stream) {
            map_of(&m.b, f.dtype, f.b, f.K, f.N, f.N, 64) &&
            map_of(&m.a_edge, f.dtype, f.a, f.M, f.K, f.lda, last_rows(f.M, 128)) &&
            map_of(&m.b_edge, f.dtype, f.b, f.K, f.N, f.N, last_deep(f.K)) &&
-           map_of(&m.o, f.dtype, f.out, f.M, f.N, f.N, 32) &&
-           map_of(&m.o2, f.dtype, dug, f.M, f.N, 2LL * f.N, 32) &&
-           map_of(&m.o3, f.dtype, dug + f.N, f.M, f.N, 2LL * f.N, 32);
+           map_out(&m.o, f.dtype, f.out, f.M, f.N, f.N) &&
+           map_out(&m.o2, f.dtype, dug, f.M, f.N, 2LL * f.N) &&
+           map_out(&m.o3, f.dtype, dug + f.N, f.M, f.N, 2LL * f.N);
       m.b2 = m.b;
       m.b2_edge = m.b_edge;
       if (!ok) return cudaErrorInvalidValue;
@@ -654,7 +678,7 @@ cudaError_t of_op(const FfnProduct& f, int num_sms, cudaStream_t stream) {
            (across_b ? map_of(&m.b_edge, f.dtype, f.b, f.K, f.N, f.ldb, last_deep(f.K))
                      : map_of(&m.b_edge, f.dtype, f.b, f.N, f.K, f.ldb,
                               last_rows(f.N, p.tile_n / 2))) &&
-           map_of(&m.o, f.dtype, f.out, f.M, f.N, f.N, 32);
+           map_out(&m.o, f.dtype, f.out, f.M, f.N, f.N);
       m.b2 = m.b;
       m.b2_edge = m.b_edge;
       m.o2 = m.o3 = m.o;

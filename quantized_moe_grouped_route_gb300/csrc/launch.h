@@ -57,10 +57,10 @@ cudaError_t launch_sort_route(const int32_t* ids, int P, int E, int32_t* offsets
 // api.cu
 // SM count of the current device; QMOE_ERR_ARCH unless it runs sm_103a code
 int device_info(int* num_sms);
-// Tensor map of 16-bit elements (QMOE_DTYPE_BF16 or _FP16), 128-byte swizzle, zeros out of
+// Tensor map of 16-bit elements (QMOE_DTYPE_BF16 or _FP16), 128- or 64-byte swizzle, zeros out of
 // bounds; strides in bytes, of all dimensions but the innermost
 int make_tmap16(CUtensorMap* map, int dtype, const void* base, int rank, const uint64_t* dims,
-                const uint64_t* strides, const uint32_t* box);
+                const uint64_t* strides, const uint32_t* box, int swizzle = 128);
 
 // misc.cu
 // scale_layout: QMOE_SCALES_PLAIN, _SWIZZLED_128X4 or _PACKED_U32
