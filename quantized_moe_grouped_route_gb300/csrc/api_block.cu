@@ -2,6 +2,8 @@
 // activation checkpoints): argument checks, workspace layout and launches.
 #include <math.h>
 
+#include <utility>
+
 #include "common.cuh"
 #include "launch.h"
 #include "rows.h"
@@ -362,18 +364,21 @@ int qmoe_gated_ffn(const void* x_dev, int dtype, long long ldx, const void* w13_
 
 // Workspace of the backward pass: [du | dg], h, x out of its codes, the sums of segments.
 struct FfnBackwardLayout {
-  size_t dug, h, x, part, total;
+  size_t dug, h, x, part[3], total;
 };
 static FfnBackwardLayout ffn_backward_layout(int M, int H, int I, bool codes) {
   FfnBackwardLayout L;
   L.dug = kWsHeaderBytes;
   L.h = align_up(L.dug + (size_t)M * I * 4, 256);
   L.x = align_up(L.h + (size_t)M * I * 2, 256);
-  L.part = align_up(L.x + (codes ? (size_t)M * H * 2 : 0), 256);
-  size_t part = 0;
+  L.part[0] = align_up(L.x + (codes ? (size_t)M * H * 2 : 0), 256);
+  // of [du | dg] and h, then of any three of the others
+  size_t most = 0;
   for (size_t b : {ffn_part_bytes(M, I), ffn_part_bytes(M, H), ffn_part_bytes(2LL * I, H)})
-    part = b > part ? b : part;
-  L.total = align_up(L.part + part, 256);
+    most = b > most ? b : most;
+  L.part[1] = align_up(L.part[0] + most, 256);
+  L.part[2] = align_up(L.part[1] + most, 256);
+  L.total = align_up(L.part[2] + most, 256);
   return L;
 }
 
@@ -431,33 +436,40 @@ int qmoe_gated_ffn_backward(const void* dout_dev, int dtype, long long lddout, c
   f.err = reinterpret_cast<unsigned int*>(ws);
   f.activation = activation;
   f.limit = limit;
-  f.part = reinterpret_cast<float*>(ws + L.part);
+  int parts = 0;
   auto product = [&](FfnOp op, const void* a, long long lda, const void* b, long long ldb, int m,
                      int n, int k, void* out) {
-    f.op = op;
-    f.a = a;
-    f.lda = lda;
-    f.b = b;
-    f.ldb = ldb;
-    f.M = m;
-    f.N = n;
-    f.K = k;
-    f.out = out;
-    return launch_ffn_product(f, sms, s);
+    FfnProduct g = f;
+    g.op = op;
+    g.a = a;
+    g.lda = lda;
+    g.b = b;
+    g.ldb = ldb;
+    g.M = m;
+    g.N = n;
+    g.K = k;
+    g.out = out;
+    g.part = reinterpret_cast<float*>(ws + L.part[parts++]);
+    return g;
   };
-  f.ug = ws + L.dug;
-  f.kept = kept_dev;
-  f.kept_scales = kept_scales_dev;
-  f.clear_err = 1;
-  cudaError_t e = product(FfnOp::kDh, dout_dev, lddout, w2_dev, I, M, I, H, ws + L.h);
-  f.clear_err = 0;
-  if (e == cudaSuccess && dx_dev)
-    e = product(FfnOp::kNN, ws + L.dug, 2LL * I, w13_dev, H, M, H, 2 * I, dx_dev);
-  if (e == cudaSuccess && dw13_dev)
-    e = product(FfnOp::kTN, ws + L.dug, 2LL * I, x, codes ? H : ldx, 2 * I, H, M, dw13_dev);
-  if (e == cudaSuccess && dw2_dev)
-    e = product(FfnOp::kTN, dout_dev, lddout, ws + L.h, I, H, I, M, dw2_dev);
-  return cuda_rc(e);
+  FfnProduct dh = product(FfnOp::kDh, dout_dev, lddout, w2_dev, I, M, I, H, ws + L.h);
+  parts = 0;  // (its segments' sums have been used when the others' are written)
+  dh.ug = ws + L.dug;
+  dh.kept = kept_dev;
+  dh.kept_scales = kept_scales_dev;
+  dh.clear_err = 1;
+  const cudaError_t e = launch_ffn_product(dh, sms, s);
+  if (e != cudaSuccess) return QMOE_ERR_CUDA;
+  FfnProduct rest[3];
+  int n = 0;
+  if (dx_dev) rest[n++] = product(FfnOp::kNN, ws + L.dug, 2LL * I, w13_dev, H, M, H, 2 * I, dx_dev);
+  if (dw13_dev)
+    rest[n++] = product(FfnOp::kTN, ws + L.dug, 2LL * I, x, codes ? H : ldx, 2 * I, H, M, dw13_dev);
+  if (dw2_dev) rest[n++] = product(FfnOp::kTN, dout_dev, lddout, ws + L.h, I, H, I, M, dw2_dev);
+  // the longest K first, so that the launch ends with short tiles
+  for (int i = 1; i < n; ++i)
+    for (int j = i; j > 0 && rest[j].K > rest[j - 1].K; --j) std::swap(rest[j], rest[j - 1]);
+  return cuda_rc(launch_ffn_products(rest, n, sms, s));
 }
 
 }  // extern "C"

@@ -34,18 +34,23 @@ constexpr int kABytes = 128 * 128;  // a stage's A: 128 rows x 64 of K
 constexpr int kStageTile = 2048;    // an epilogue warp's staging tile: 32 rows x 32 columns
 constexpr int kSmemLimit = 232448;
 
-enum class Op { kUp, kPlainNT, kPlainNN, kPlainTN, kDh };
-__host__ __device__ constexpr bool a_across(Op op) { return op == Op::kPlainTN; }
-__host__ __device__ constexpr bool b_across(Op op) {
-  return op == Op::kPlainTN || op == Op::kPlainNN || op == Op::kDh;
-}
+// kMany: up to three products of their own sizes and operands' lie in one launch, plain epilogues.
+enum class Op { kUp, kDh, kMany };
+constexpr int kMost = 3;
 // Staging tiles of an epilogue warp.
-__host__ __device__ constexpr int staging(Op op) { return op == Op::kUp || op == Op::kDh ? 3 : 2; }
+__host__ __device__ constexpr int staging(Op op) { return op == Op::kMany ? 2 : 3; }
 
 struct Maps {
   CUtensorMap a, b, b2, o, o2, o3;
   CUtensorMap a_edge, b_edge, b2_edge;  // the operands in boxes of a last block's rows
 };
+template <int N>
+struct Launch {
+  int count, stages, stage_bytes;
+  FfnGemm p[N];
+  Maps maps[N];
+};
+constexpr int problems(Op op) { return op == Op::kMany ? kMost : 1; }
 
 // A matrix's last block of `box` rows is copied in a box of its own number of rows: rows that a copy
 // has to fill in cost it several times what rows of the matrix do (1 token by boxes of 128 rows: 182 us
@@ -206,18 +211,36 @@ __device__ __forceinline__ void tile_of(const FfnGemm& p, int i, int* tm, int* t
   *tn = r / rows;
   *tm = first + r - *tn * rows;
 }
+// Unit i of a launch: a tile of one of its products, and of K the segment `seg`.
+struct Unit {
+  int problem, tm, tn, seg, k0, k1;
+};
+template <int N>
+__device__ __forceinline__ Unit unit_of(const Launch<N>& L, int i) {
+  Unit u;
+  u.problem = 0;
+#pragma unroll
+  for (int j = 1; j < N; ++j)
+    if (j < L.count && i >= L.p[j].first) u.problem = j;
+  const FfnGemm& p = L.p[u.problem];
+  i -= p.first;
+  const int tile = i / p.splits;
+  u.seg = i - tile * p.splits;
+  u.k0 = (int)((long long)p.ksteps * u.seg / p.splits);
+  u.k1 = (int)((long long)p.ksteps * (u.seg + 1) / p.splits);
+  tile_of(p, tile, &u.tm, &u.tn);
+  return u;
+}
 
-// PART: of a tile's K steps one of p.splits segments, whose sums are left in p.part [splits][M][columns]
-// (u's columns before g's) for the kernels of ffn_finish.cu.
+// A product whose K is cut into segments leaves each segment's sums in p.part [splits][M][columns]
+// (u's columns before g's) for the kernels of ffn_finish.cu; PART: whether kUp's and kDh's does.
 template <class T, Op OP, bool CODES, bool PART>
 __global__ void __launch_bounds__(kThreads, 1)
-    ffn_gemm_kernel(const __grid_constant__ Maps maps, const FfnGemm p) {
+    ffn_gemm_kernel(const __grid_constant__ Launch<problems(OP)> L) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
-  const int rows_b = p.tile_n / 2;  // of this SM's half of B
-  const int stage_bytes = kABytes + rows_b * 128;
-  const int stages = p.stages;
+  const int stage_bytes = L.stage_bytes, stages = L.stages;
   uint8_t* epi = smem + stages * stage_bytes;
   uint8_t* ctrl = epi + kEpiWarps * staging(OP) * kStageTile;
   uint64_t* full = reinterpret_cast<uint64_t*>(ctrl);
@@ -227,6 +250,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* drain = acce + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  unsigned int* const err = L.p[0].err;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
@@ -243,12 +267,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(smem_u32(drain), 1);
     *abort_flag = 0;
     fence_mbar_init();
-    prefetch_tmap(&maps.a);
-    prefetch_tmap(&maps.b);
-    if (OP == Op::kUp) prefetch_tmap(&maps.b2);
-    prefetch_tmap(&maps.o);
-    prefetch_tmap(&maps.a_edge);
-    prefetch_tmap(&maps.b_edge);
+    for (int j = 0; j < L.count; ++j) {
+      prefetch_tmap(&L.maps[j].a);
+      prefetch_tmap(&L.maps[j].b);
+      if (OP == Op::kUp) prefetch_tmap(&L.maps[j].b2);
+      prefetch_tmap(&L.maps[j].o);
+    }
   }
   if (warp == 1) {
     tmem_alloc2(smem_u32(tmem_slot), 2 * kAccCols);
@@ -261,17 +285,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *tmem_slot;
   grid_dep_wait();  // (all threads: what they read was written by the kernel before)
   grid_dep_launch();
-  if (p.clear_err && blockIdx.x == 0 && threadIdx.x == 0) *p.err = 0;
+  if (L.p[0].clear_err && blockIdx.x == 0 && threadIdx.x == 0) *err = 0;
 
-  const int units = p.tiles_m * p.tiles_n * (PART ? p.splits : 1);
-  auto tile_of_unit = [&](int i, int* tm, int* tn) { tile_of(p, PART ? i / p.splits : i, tm, tn); };
-  auto first_step = [&](int i) { return PART ? p.ksteps * (i % p.splits) / p.splits : 0; };
-  auto last_step = [&](int i) {
-    return PART ? p.ksteps * (i % p.splits + 1) / p.splits : p.ksteps;
+  const FfnGemm& last = L.p[L.count - 1];
+  const int units = last.first + last.tiles_m * last.tiles_n * last.splits;
+  // the operands' lie
+  auto a_across = [&](const FfnGemm& p) { return OP == Op::kMany && p.op == FfnOp::kTN; };
+  auto b_across = [&](const FfnGemm& p) {
+    return OP == Op::kDh || (OP == Op::kMany && p.op != FfnOp::kNT);
   };
-  const int cols = OP == Op::kUp ? p.tile_n / 2 : p.tile_n;  // of the result, a tile
+  // columns of the result, a tile
+  auto tile_cols = [&](const FfnGemm& p) { return OP == Op::kUp ? p.tile_n / 2 : p.tile_n; };
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-    return warp_wait_cl(smem_u32(bar), parity, abort_flag, p.err);
+    return warp_wait_cl(smem_u32(bar), parity, abort_flag, err);
   };
 
   if (warp == 0) {
@@ -282,22 +308,26 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t s = 0, ph = 1;
     bool ok = true;
     for (int i = worker; i < units && ok; i += workers) {
-      int tm, tn;
-      tile_of_unit(i, &tm, &tn);
-      // this SM's rows of A and columns of B: where they begin and how many there are
-      auto rows_a = [&](int r) { return max(0, min(128, p.M - tm * 256 - r * 128)); };
-      auto cols_b = [&](int r) {
-        return max(0, min(rows_b, p.N - (OP == Op::kUp ? tn * cols : tn * p.tile_n + r * rows_b)));
+      const Unit u = unit_of(L, i);
+      const FfnGemm& p = L.p[u.problem];
+      const Maps& maps = L.maps[u.problem];
+      const bool across_a = a_across(p), across_b = b_across(p);
+      const int rows_b = p.tile_n / 2, K = p.K;
+      const uint32_t bytes = 2u * (kABytes + rows_b * 128);  // of a whole step, both SMs
+      // an SM's rows of A and columns of B: where they begin and how many there are
+      auto rows_a = [&](int r) { return max(0, min(128, p.M - u.tm * 256 - r * 128)); };
+      auto begin_b = [&](int r) {
+        return OP == Op::kUp ? u.tn * rows_b : u.tn * p.tile_n + r * rows_b;
       };
-      const int row = tm * 256 + (int)rank * 128;
-      const int col = OP == Op::kUp ? tn * cols : tn * p.tile_n + (int)rank * rows_b;
+      auto cols_b = [&](int r) { return max(0, min(rows_b, p.N - begin_b(r))); };
+      const int row = u.tm * 256 + (int)rank * 128, col = begin_b((int)rank);
       const int na = rows_a((int)rank), nb = cols_b((int)rank);
-      // of the pair's two SMs (a tile whose second half is whole is whole)
-      const bool whole = rows_a(1) == 128 && cols_b(1) == rows_b;
-      const int k0 = first_step(i), k1 = last_step(i);
-      // steps of whole boxes, one copy an operand (two across K): the issue is what paces a step
-      const int k_whole = whole ? min(k1, p.K / 64) : k0;
-      for (int k = k0; k < k1; ++k) {
+      const bool second = OP == Op::kUp && rank != 0;  // the SM with the rows of g
+      const CUtensorMap* const map_b = second ? &maps.b2 : &maps.b;
+      // steps of whole boxes (a tile whose second half is whole is whole), one copy an operand, two
+      // across K: the issue is what paces a step
+      const int k_whole = rows_a(1) == 128 && cols_b(1) == rows_b ? min(u.k1, K / 64) : u.k0;
+      for (int k = u.k0; k < u.k1; ++k) {
         if (!wait(&empty[s], ph)) {
           ok = false;
           break;
@@ -305,47 +335,42 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t sa = smem_u32(smem) + s * stage_bytes, sb = sa + kABytes;
         const uint32_t bar = full0 + s * 8;
         if (k < k_whole) {
-          if (rank == 0)
-            mbar_arrive_expect_tx_if(lead, smem_u32(&full[s]), 2u * (uint32_t)stage_bytes);
-          if (a_across(OP)) {
+          if (rank == 0) mbar_arrive_expect_tx_if(lead, smem_u32(&full[s]), bytes);
+          if (across_a) {
             tma_load_2d_pair_if(lead, sa, &maps.a, row, k * 64, bar, pol);
             tma_load_2d_pair_if(lead, sa + 8192, &maps.a, row + 64, k * 64, bar, pol);
           } else {
             tma_load_2d_pair_if(lead, sa, &maps.a, k * 64, row, bar, pol);
           }
-          if (b_across(OP)) {
-            tma_load_2d_pair_if(lead, sb, &maps.b, col, k * 64, bar, pol);
-            if (rows_b > 64)
-              tma_load_2d_pair_if(lead, sb + 8192, &maps.b, col + 64, k * 64, bar, pol);
+          if (across_b) {
+            tma_load_2d_pair_if(lead, sb, map_b, col, k * 64, bar, pol);
+            if (rows_b > 64) tma_load_2d_pair_if(lead, sb + 8192, map_b, col + 64, k * 64, bar, pol);
           } else {
-            const CUtensorMap* b = OP == Op::kUp && rank != 0 ? &maps.b2 : &maps.b;
-            tma_load_2d_pair_if(lead, sb, b, k * 64, col, bar, pol);
+            tma_load_2d_pair_if(lead, sb, map_b, k * 64, col, bar, pol);
           }
         } else {
-          const bool deep = k < p.K / 64;  // a whole step of K
-          const int depth = deep ? 64 : last_deep(p.K);
+          const bool deep = k < K / 64;  // a whole step of K
+          const int depth = deep ? 64 : last_deep(K);
           if (rank == 0) {
             uint32_t rows = 0;  // of 128 bytes, of both SMs
             for (int r = 0; r < 2; ++r)
-              rows += (a_across(OP) ? (rows_a(r) + 63) / 64 * depth : rows_a(r)) +
-                      (b_across(OP) ? (cols_b(r) + 63) / 64 * depth : cols_b(r));
+              rows += (across_a ? (rows_a(r) + 63) / 64 * depth : rows_a(r)) +
+                      (across_b ? (cols_b(r) + 63) / 64 * depth : cols_b(r));
             mbar_arrive_expect_tx_if(lead, smem_u32(&full[s]), rows * 128u);
           }
-          if (a_across(OP)) {
+          if (across_a) {
             for (int c = 0; c < na; c += 64)
               tma_load_2d_pair_if(lead, sa + c * 128, deep ? &maps.a : &maps.a_edge, row + c, k * 64,
                                   bar, pol);
           } else if (na > 0) {
             tma_load_2d_pair_if(lead, sa, na == 128 ? &maps.a : &maps.a_edge, k * 64, row, bar, pol);
           }
-          if (b_across(OP)) {
+          if (across_b) {
             for (int c = 0; c < nb; c += 64)
               tma_load_2d_pair_if(lead, sb + c * 128, deep ? &maps.b : &maps.b_edge, col + c, k * 64,
                                   bar, pol);
           } else if (nb > 0) {
-            const bool second = OP == Op::kUp && rank != 0;
-            const CUtensorMap* b = nb == rows_b ? (second ? &maps.b2 : &maps.b)
-                                                : (second ? &maps.b2_edge : &maps.b_edge);
+            const CUtensorMap* b = nb == rows_b ? map_b : second ? &maps.b2_edge : &maps.b_edge;
             tma_load_2d_pair_if(lead, sb, b, k * 64, col, bar, pol);
           }
         }
@@ -364,18 +389,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (rank == 0) {
       // ------------------------------------------------------------------ MMA issue
       const uint32_t lead = elect_one();
-      uint32_t idesc = idesc_bf16_f32(256, p.tile_n);
-      if (std::is_same<T, __half>::value) idesc &= ~((1u << 7) | (1u << 10));
-      if (a_across(OP)) idesc |= 1u << 15;
-      if (b_across(OP)) idesc |= 1u << 16;
       const uint32_t base = smem_u32(smem);
-      const uint64_t a0 = a_across(OP) ? sdesc_across(base) : sdesc_sw128(base);
-      const uint64_t b0 = b_across(OP) ? sdesc_across(base + kABytes) : sdesc_sw128(base + kABytes);
-      // 16 of K further on: 32 bytes of a row, or 16 rows of 128 bytes
-      constexpr uint32_t step_a = a_across(OP) ? 128 : 2, step_b = b_across(OP) ? 128 : 2;
       uint32_t s = 0, ph = 0, local = 0;
       bool ok = true;
       for (int i = worker; i < units && ok; i += workers, ++local) {
+        const Unit u = unit_of(L, i);
+        const FfnGemm& p = L.p[u.problem];
+        const bool across_a = a_across(p), across_b = b_across(p);
+        uint32_t idesc = idesc_bf16_f32(256, p.tile_n);
+        if (std::is_same<T, __half>::value) idesc &= ~((1u << 7) | (1u << 10));
+        idesc |= (across_a ? 1u << 15 : 0u) | (across_b ? 1u << 16 : 0u);
+        const uint64_t a0 = across_a ? sdesc_across(base) : sdesc_sw128(base);
+        const uint64_t b0 = across_b ? sdesc_across(base + kABytes) : sdesc_sw128(base + kABytes);
+        // 16 of K further on: 32 bytes of a row, or 16 rows of 128 bytes
+        const uint32_t step_a = across_a ? 128 : 2, step_b = across_b ? 128 : 2;
+        const int k0 = u.k0, whole = p.K / 64;
         const int ab = local & 1;
         if (!wait(&acce[ab], ((local >> 1) & 1) ^ 1)) {
           ok = false;
@@ -383,15 +411,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc_fence_after();
         const uint32_t dst = tmem + ab * kAccCols;
-        const int k0 = first_step(i), k1 = last_step(i);
-        for (int k = k0; k < k1; ++k) {
+        for (int k = k0; k < u.k1; ++k) {
           if (!wait(&full[s], ph)) {
             ok = false;
             break;
           }
           tc_fence_after();
           const uint32_t off = (s * stage_bytes) >> 4;
-          if (k < p.K / 64) {
+          if (k < whole) {
             if (lead) {
 #pragma unroll
               for (int j = 0; j < 4; ++j)
@@ -418,14 +445,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t acce0 = peer_addr(smem_u32(acce), 0);
     uint8_t* stage = epi + (warp - 4) * staging(OP) * kStageTile;
     const uint32_t stage0 = smem_u32(stage);
-    const bool gelu = p.activation == QMOE_ACT_GELU;
+    const bool gelu = L.p[0].activation == QMOE_ACT_GELU;
     uint32_t local = 0;
     int turn = 0;
     for (int i = worker; i < units; i += workers, ++local) {
-      int tm, tn;
-      tile_of_unit(i, &tm, &tn);
-      const int ab = local & 1;
-      const int row0 = tm * 256 + (int)rank * 128 + q * 32, col0 = tn * cols;
+      const Unit unit = unit_of(L, i);
+      const FfnGemm& p = L.p[unit.problem];
+      const Maps& maps = L.maps[unit.problem];
+      const bool part = OP == Op::kMany ? p.splits > 1 : PART;
+      const int ab = local & 1, cols = tile_cols(p);
+      const int row0 = unit.tm * 256 + (int)rank * 128 + q * 32, col0 = unit.tn * cols;
       const int n = min(cols, p.N - col0);  // columns of this tile
       Kept ku, kg;
       if constexpr (OP == Op::kDh && !PART) {
@@ -437,10 +466,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t tbase = tmem + ((uint32_t)(q * 32) << 16) + ab * kAccCols;
       const bool rows_in = row0 < p.M;
       for (int c = first_col; c < n; c += kApart) {
-        if constexpr (PART) {
+        if (part) {
           // a lane's row in pieces of 128 bytes
           const int width = OP == Op::kUp ? 2 * p.N : p.N;
-          float* to = p.part + ((size_t)(i % p.splits) * p.M + row0 + lane) * width + col0 + c;
+          float* to = p.part + ((size_t)unit.seg * p.M + row0 + lane) * width + col0 + c;
 #pragma unroll
           for (int half = 0; half < (OP == Op::kUp ? 2 : 1); ++half) {
             float v[32];
@@ -451,7 +480,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 *reinterpret_cast<float4*>(to + half * p.N + k) =
                     make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
           }
-        } else {
+        } else if constexpr (!PART) {
           // the staging tiles are free again
           const int t = OP == Op::kUp || OP == Op::kDh ? 0 : turn;
           turn ^= 1;
@@ -555,13 +584,19 @@ bool map_of(CUtensorMap* map, int dtype, const void* base, long long rows, int c
 }
 
 template <class T, Op OP, bool CODES, bool PART>
-cudaError_t run_as(FfnGemm& p, const Maps& maps, int num_sms, cudaStream_t stream) {
+cudaError_t run_as(Launch<problems(OP)>& L, int num_sms, cudaStream_t stream) {
   auto* k = ffn_gemm_kernel<T, OP, CODES, PART>;
-  const int stage = kABytes + p.tile_n / 2 * 128;
+  int tile_n = 0, units = 0;
+  for (int j = 0; j < L.count; ++j) {
+    FfnGemm& p = L.p[j];
+    p.first = units;
+    units += p.tiles_m * p.tiles_n * p.splits;
+    if (p.tile_n > tile_n) tile_n = p.tile_n;
+  }
+  L.stage_bytes = kABytes + tile_n / 2 * 128;
   const int other = 1024 + kCtrl + kEpiWarps * staging(OP) * kStageTile;
-  const int most = (kSmemLimit - other) / stage;
-  p.stages = most < kMaxStages ? most : kMaxStages;
-  const size_t smem = other + (size_t)p.stages * stage;
+  const int most = (kSmemLimit - other) / L.stage_bytes;
+  L.stages = most < kMaxStages ? most : kMaxStages;
   cudaError_t e = allow_smem(k, kSmemLimit);
   if (e != cudaSuccess) return e;
   int dev = -1;
@@ -573,7 +608,6 @@ cudaError_t run_as(FfnGemm& p, const Maps& maps, int num_sms, cudaStream_t strea
     return resident_clusters(k, 2, kThreads, kSmemLimit, num_sms);
   });
   if (held < 1) return cudaErrorInvalidConfiguration;
-  const int units = p.tiles_m * p.tiles_n * (PART ? p.splits : 1);
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2] = {pdl_attribute()};
   attr[1].id = cudaLaunchAttributeClusterDimension;
@@ -582,32 +616,32 @@ cudaError_t run_as(FfnGemm& p, const Maps& maps, int num_sms, cudaStream_t strea
   attr[1].val.clusterDim.z = 1;
   cfg.gridDim = dim3((unsigned)((units < held ? units : held) * 2));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
+  cfg.dynamicSmemBytes = other + (size_t)L.stages * L.stage_bytes;
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, k, maps, p);
+  e = cudaLaunchKernelEx(&cfg, k, L);
+  for (int j = 0; j < L.count && e == cudaSuccess; ++j)
+    if (L.p[j].splits > 1) e = launch_ffn_finish(L.p[j], stream);
+  return e;
 }
 
-template <class T, Op OP, bool CODES = false>
-cudaError_t run(FfnGemm& p, const Maps& maps, int num_sms, cudaStream_t stream) {
-  if (p.splits == 1) return run_as<T, OP, CODES, false>(p, maps, num_sms, stream);
-  constexpr Op kPart = OP == Op::kDh ? Op::kPlainNN : OP;  // the same operands
-  const cudaError_t e = run_as<T, kPart, false, true>(p, maps, num_sms, stream);
-  return e == cudaSuccess ? launch_ffn_finish(p, stream) : e;
+template <class T, Op OP, bool CODES>
+cudaError_t run(Launch<problems(OP)>& L, int num_sms, cudaStream_t stream) {
+  if constexpr (OP != Op::kMany)
+    if (L.p[0].splits > 1) return run_as<T, OP, false, true>(L, num_sms, stream);
+  return run_as<T, OP, CODES, false>(L, num_sms, stream);
 }
 
-// How a product is cut: tiles of 256 or 128 columns, and their K steps into segments where the
-// tiles are far fewer than the pairs of SMs.  By an estimate of the time in units of a step of a
-// wide tile (0.27 us): a step of a tile of 128 columns takes 0.55 (its rows of A are loaded for
-// half as many products), a tile's last epilogue about 8, segments another kernel of about 12 and
-// their sums written and read again (about 5 TB/s).  By the number of pairs of a GB300, so that
-// results are the same on every part.
-void cut(FfnGemm& p) {
-  constexpr int kPairs = 76;
+constexpr int kPairs = 76;  // of SMs of a GB300: results are the same on every part
+
+// How a product alone in its launch is cut: tiles of 256 or 128 columns, and their K steps into
+// segments where the tiles are far fewer than the pairs of SMs.  By an estimate of the time in units
+// of a step of a wide tile (0.27 us): a step of a tile of 128 columns takes 0.55 (its rows of A are
+// loaded for half as many products), a tile's last epilogue about 8, segments another kernel of
+// about 12 and their sums written and read again (about 5 TB/s).
+void cut_alone(FfnGemm& p) {
   const bool up = p.op == FfnOp::kUp;
-  p.tiles_m = (p.M + 255) / 256;
-  p.ksteps = (p.K + 63) / 64;
   double best = 0;
   for (int n = 256; n >= 128; n /= 2) {
     const int cols = up ? n / 2 : n, tiles_n = (p.N + cols - 1) / cols;
@@ -626,75 +660,104 @@ void cut(FfnGemm& p) {
   }
 }
 
-template <class T>
-cudaError_t of_op(const FfnProduct& f, int num_sms, cudaStream_t stream) {
-  FfnGemm p = {};
-  static_cast<FfnProduct&>(p) = f;
-  cut(p);
-  Maps m = {};
-  bool ok = true;
-  switch (f.op) {
-    case FfnOp::kUp: {  // x [M][H], w13 [2I][H] -> h [M][I] (u, g [M][I] at a pitch of 2I)
-      const T* w = reinterpret_cast<const T*>(f.b);
-      ok = map_of(&m.a, f.dtype, f.a, f.M, f.K, f.lda, 128) &&
-           map_of(&m.b, f.dtype, w, f.N, f.K, f.K, p.tile_n / 2) &&
-           map_of(&m.b2, f.dtype, w + (size_t)f.N * f.K, f.N, f.K, f.K, p.tile_n / 2) &&
-           map_of(&m.a_edge, f.dtype, f.a, f.M, f.K, f.lda, last_rows(f.M, 128)) &&
-           map_of(&m.b_edge, f.dtype, w, f.N, f.K, f.K, last_rows(f.N, p.tile_n / 2)) &&
-           map_of(&m.b2_edge, f.dtype, w + (size_t)f.N * f.K, f.N, f.K, f.K,
-                  last_rows(f.N, p.tile_n / 2)) &&
-           map_out(&m.o, f.dtype, f.out, f.M, f.N, f.N);
-      m.o2 = m.o3 = m.o;
-      if (f.save == 16) {
-        T* ug = reinterpret_cast<T*>(f.ug);
-        ok = ok && map_out(&m.o2, f.dtype, ug, f.M, f.N, 2LL * f.N) &&
-             map_out(&m.o3, f.dtype, ug + f.N, f.M, f.N, 2LL * f.N);
-      }
-      return ok ? run<T, Op::kUp>(p, m, num_sms, stream) : cudaErrorInvalidValue;
-    }
-    case FfnOp::kDh: {  // dout [M][H], w2 [H][I] -> h, du, dg
-      T* dug = reinterpret_cast<T*>(f.ug);
-      ok = map_of(&m.a, f.dtype, f.a, f.M, f.K, f.lda, 128) &&
-           map_of(&m.b, f.dtype, f.b, f.K, f.N, f.N, 64) &&
-           map_of(&m.a_edge, f.dtype, f.a, f.M, f.K, f.lda, last_rows(f.M, 128)) &&
-           map_of(&m.b_edge, f.dtype, f.b, f.K, f.N, f.N, last_deep(f.K)) &&
-           map_out(&m.o, f.dtype, f.out, f.M, f.N, f.N) &&
-           map_out(&m.o2, f.dtype, dug, f.M, f.N, 2LL * f.N) &&
-           map_out(&m.o3, f.dtype, dug + f.N, f.M, f.N, 2LL * f.N);
-      m.b2 = m.b;
-      m.b2_edge = m.b_edge;
-      if (!ok) return cudaErrorInvalidValue;
-      return f.kept_scales ? run<T, Op::kDh, true>(p, m, num_sms, stream)
-                           : run<T, Op::kDh, false>(p, m, num_sms, stream);
-    }
-    default: {
-      const bool across_a = f.op == FfnOp::kTN, across_b = f.op != FfnOp::kNT;
-      ok = (across_a ? map_of(&m.a, f.dtype, f.a, f.K, f.M, f.lda, 64)
-                     : map_of(&m.a, f.dtype, f.a, f.M, f.K, f.lda, 128)) &&
-           (across_b ? map_of(&m.b, f.dtype, f.b, f.K, f.N, f.ldb, 64)
-                     : map_of(&m.b, f.dtype, f.b, f.N, f.K, f.ldb, p.tile_n / 2)) &&
-           (across_a ? map_of(&m.a_edge, f.dtype, f.a, f.K, f.M, f.lda, last_deep(f.K))
-                     : map_of(&m.a_edge, f.dtype, f.a, f.M, f.K, f.lda, last_rows(f.M, 128))) &&
-           (across_b ? map_of(&m.b_edge, f.dtype, f.b, f.K, f.N, f.ldb, last_deep(f.K))
-                     : map_of(&m.b_edge, f.dtype, f.b, f.N, f.K, f.ldb,
-                              last_rows(f.N, p.tile_n / 2))) &&
-           map_out(&m.o, f.dtype, f.out, f.M, f.N, f.N);
-      m.b2 = m.b;
-      m.b2_edge = m.b_edge;
-      m.o2 = m.o3 = m.o;
-      if (!ok) return cudaErrorInvalidValue;
-      if (f.op == FfnOp::kNT) return run<T, Op::kPlainNT>(p, m, num_sms, stream);
-      if (f.op == FfnOp::kNN) return run<T, Op::kPlainNN>(p, m, num_sms, stream);
-      return run<T, Op::kPlainTN>(p, m, num_sms, stream);
-    }
+// Products that share a launch: narrow tiles where wide ones are fewer than two for each pair of SMs,
+// and K in segments where a tile has more steps than twice a pair's share of all of them.
+void cut_together(FfnGemm* p, int count) {
+  auto tiles = [&](int j, int n) { return (long long)p[j].tiles_m * ((p[j].N + n - 1) / n); };
+  long long wide = 0;
+  double steps = 0;
+  for (int j = 0; j < count; ++j) wide += tiles(j, 256);
+  for (int j = 0; j < count; ++j) {
+    p[j].tile_n = wide >= 2 * kPairs ? 256 : 128;
+    p[j].tiles_n = (p[j].N + p[j].tile_n - 1) / p[j].tile_n;
+    steps += (double)tiles(j, p[j].tile_n) * p[j].ksteps;
   }
+  const double share = steps / kPairs;
+  for (int j = 0; j < count; ++j) {
+    const long long n = tiles(j, p[j].tile_n);
+    int s = 1;
+    while (s < kFfnMaxSplits && p[j].ksteps > 2 * s * (share > 16 ? share : 16) &&
+           n * (s + 1) <= kPairs && p[j].ksteps >= 4 * (s + 1))
+      ++s;
+    p[j].splits = s;
+  }
+}
+
+// The tensor maps of a product.
+template <class T>
+bool maps_of(const FfnGemm& p, Maps* m) {
+  const bool across_a = p.op == FfnOp::kTN;
+  const bool across_b = p.op == FfnOp::kTN || p.op == FfnOp::kNN || p.op == FfnOp::kDh;
+  bool ok = across_a ? map_of(&m->a, p.dtype, p.a, p.K, p.M, p.lda, 64) &&
+                           map_of(&m->a_edge, p.dtype, p.a, p.K, p.M, p.lda, last_deep(p.K))
+                     : map_of(&m->a, p.dtype, p.a, p.M, p.K, p.lda, 128) &&
+                           map_of(&m->a_edge, p.dtype, p.a, p.M, p.K, p.lda, last_rows(p.M, 128));
+  const int half = p.tile_n / 2, edge = last_rows(p.N, half);
+  ok = ok && (across_b ? map_of(&m->b, p.dtype, p.b, p.K, p.N, p.ldb, 64) &&
+                             map_of(&m->b_edge, p.dtype, p.b, p.K, p.N, p.ldb, last_deep(p.K))
+                       : map_of(&m->b, p.dtype, p.b, p.N, p.K, p.ldb, half) &&
+                             map_of(&m->b_edge, p.dtype, p.b, p.N, p.K, p.ldb, edge));
+  m->b2 = m->b;
+  m->b2_edge = m->b_edge;
+  if (p.op == FfnOp::kUp) {  // w13's rows for g
+    const T* g = reinterpret_cast<const T*>(p.b) + (size_t)p.N * p.ldb;
+    ok = ok && map_of(&m->b2, p.dtype, g, p.N, p.K, p.ldb, half) &&
+         map_of(&m->b2_edge, p.dtype, g, p.N, p.K, p.ldb, edge);
+  }
+  ok = ok && map_out(&m->o, p.dtype, p.out, p.M, p.N, p.N);
+  m->o2 = m->o3 = m->o;
+  if (p.op == FfnOp::kDh || (p.op == FfnOp::kUp && p.save == 16)) {  // at a pitch of both halves
+    T* ug = reinterpret_cast<T*>(p.ug);
+    ok = ok && map_out(&m->o2, p.dtype, ug, p.M, p.N, 2LL * p.N) &&
+         map_out(&m->o3, p.dtype, ug + p.N, p.M, p.N, 2LL * p.N);
+  }
+  return ok;
+}
+
+void prepare(FfnGemm& p, const FfnProduct& f) {
+  static_cast<FfnProduct&>(p) = f;
+  p.tiles_m = (f.M + 255) / 256;
+  p.ksteps = (f.K + 63) / 64;
+}
+
+template <class T>
+cudaError_t one(const FfnProduct& f, int num_sms, cudaStream_t stream) {
+  Launch<1> L = {};
+  L.count = 1;
+  prepare(L.p[0], f);
+  cut_alone(L.p[0]);
+  if (!maps_of<T>(L.p[0], &L.maps[0])) return cudaErrorInvalidValue;
+  if (f.op == FfnOp::kUp) return run<T, Op::kUp, false>(L, num_sms, stream);
+  return f.kept_scales ? run<T, Op::kDh, true>(L, num_sms, stream)
+                       : run<T, Op::kDh, false>(L, num_sms, stream);
+}
+
+template <class T>
+cudaError_t many(const FfnProduct* f, int count, int num_sms, cudaStream_t stream) {
+  Launch<kMost> L = {};
+  L.count = count;
+  for (int j = 0; j < count; ++j) prepare(L.p[j], f[j]);
+  if (count == 1)
+    cut_alone(L.p[0]);
+  else
+    cut_together(L.p, count);
+  for (int j = 0; j < count; ++j)
+    if (!maps_of<T>(L.p[j], &L.maps[j])) return cudaErrorInvalidValue;
+  return run<T, Op::kMany, false>(L, num_sms, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_ffn_product(const FfnProduct& f, int num_sms, cudaStream_t stream) {
-  return f.dtype == QMOE_DTYPE_BF16 ? of_op<__nv_bfloat16>(f, num_sms, stream)
-                                    : of_op<__half>(f, num_sms, stream);
+  if (f.op != FfnOp::kUp && f.op != FfnOp::kDh) return launch_ffn_products(&f, 1, num_sms, stream);
+  return f.dtype == QMOE_DTYPE_BF16 ? one<__nv_bfloat16>(f, num_sms, stream)
+                                    : one<__half>(f, num_sms, stream);
+}
+
+cudaError_t launch_ffn_products(const FfnProduct* f, int count, int num_sms, cudaStream_t stream) {
+  if (count < 1 || count > kMost) return cudaErrorInvalidValue;
+  return f[0].dtype == QMOE_DTYPE_BF16 ? many<__nv_bfloat16>(f, count, num_sms, stream)
+                                       : many<__half>(f, count, num_sms, stream);
 }
 
 }  // namespace qmoe

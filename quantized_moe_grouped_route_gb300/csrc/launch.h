@@ -359,6 +359,7 @@ struct FfnProduct {
 struct FfnGemm : FfnProduct {
   int tile_n, tiles_m, tiles_n, ksteps, stages;
   int splits;  // segments of K
+  int first;   // of its launch's units
 };
 // Bytes of the sums of segments of a product with `rows` x `columns` of them, or fewer rows: as
 // many tiles as there are pairs of SMs are the most, and as many segments.
@@ -370,6 +371,8 @@ inline size_t ffn_part_bytes(long long rows, long long columns) {
 // ffn_finish.cu: the segments' sums added up, and what a tile's epilogue does
 cudaError_t launch_ffn_finish(const FfnGemm& p, cudaStream_t stream);
 cudaError_t launch_ffn_product(const FfnProduct& f, int num_sms, cudaStream_t stream);
+// ... and up to three plain ones of one type in one launch, the longest K first
+cudaError_t launch_ffn_products(const FfnProduct* f, int count, int num_sms, cudaStream_t stream);
 // ffn_stream.cu, ffn_few.cu: kUp (nothing kept) and kNT for few tokens, which are the rows of a
 constexpr int kFfnStreamTokens = 8;
 cudaError_t launch_ffn_stream(const FfnProduct& f, cudaStream_t stream);
