@@ -294,6 +294,20 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto b_across = [&](const FfnGemm& p) {
     return OP == Op::kDh || (OP == Op::kMany && p.op != FfnOp::kNT);
   };
+  // f with the lie of both operands as constants
+  auto by_lie = [&](bool across_a, bool across_b, auto&& f) {
+    if constexpr (OP == Op::kUp) {
+      f(std::false_type{}, std::false_type{});
+    } else if constexpr (OP == Op::kDh) {
+      f(std::false_type{}, std::true_type{});
+    } else if (across_a) {
+      f(std::true_type{}, std::true_type{});
+    } else if (across_b) {
+      f(std::false_type{}, std::true_type{});
+    } else {
+      f(std::false_type{}, std::false_type{});
+    }
+  };
   // columns of the result, a tile
   auto tile_cols = [&](const FfnGemm& p) { return OP == Op::kUp ? p.tile_n / 2 : p.tile_n; };
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
@@ -327,58 +341,63 @@ __global__ void __launch_bounds__(kThreads, 1)
       // steps of whole boxes (a tile whose second half is whole is whole), one copy an operand, two
       // across K: the issue is what paces a step
       const int k_whole = rows_a(1) == 128 && cols_b(1) == rows_b ? min(u.k1, K / 64) : u.k0;
-      for (int k = u.k0; k < u.k1; ++k) {
-        if (!wait(&empty[s], ph)) {
-          ok = false;
-          break;
-        }
-        const uint32_t sa = smem_u32(smem) + s * stage_bytes, sb = sa + kABytes;
-        const uint32_t bar = full0 + s * 8;
-        if (k < k_whole) {
-          if (rank == 0) mbar_arrive_expect_tx_if(lead, smem_u32(&full[s]), bytes);
-          if (across_a) {
-            tma_load_2d_pair_if(lead, sa, &maps.a, row, k * 64, bar, pol);
-            tma_load_2d_pair_if(lead, sa + 8192, &maps.a, row + 64, k * 64, bar, pol);
+      auto steps = [&](auto lie_a, auto lie_b) {
+        constexpr bool kA = decltype(lie_a)::value, kB = decltype(lie_b)::value;
+        for (int k = u.k0; k < u.k1; ++k) {
+          if (!wait(&empty[s], ph)) {
+            ok = false;
+            break;
+          }
+          const uint32_t sa = smem_u32(smem) + s * stage_bytes, sb = sa + kABytes;
+          const uint32_t bar = full0 + s * 8;
+          if (k < k_whole) {
+            if (rank == 0) mbar_arrive_expect_tx_if(lead, smem_u32(&full[s]), bytes);
+            if constexpr (kA) {
+              tma_load_2d_pair_if(lead, sa, &maps.a, row, k * 64, bar, pol);
+              tma_load_2d_pair_if(lead, sa + 8192, &maps.a, row + 64, k * 64, bar, pol);
+            } else {
+              tma_load_2d_pair_if(lead, sa, &maps.a, k * 64, row, bar, pol);
+            }
+            if constexpr (kB) {
+              tma_load_2d_pair_if(lead, sb, map_b, col, k * 64, bar, pol);
+              if (rows_b > 64) tma_load_2d_pair_if(lead, sb + 8192, map_b, col + 64, k * 64, bar, pol);
+            } else {
+              tma_load_2d_pair_if(lead, sb, map_b, k * 64, col, bar, pol);
+            }
           } else {
-            tma_load_2d_pair_if(lead, sa, &maps.a, k * 64, row, bar, pol);
+            const bool deep = k < K / 64;  // a whole step of K
+            const int depth = deep ? 64 : last_deep(K);
+            if (rank == 0) {
+              uint32_t rows = 0;  // of 128 bytes, of both SMs
+              for (int r = 0; r < 2; ++r)
+                rows += (kA ? (rows_a(r) + 63) / 64 * depth : rows_a(r)) +
+                        (kB ? (cols_b(r) + 63) / 64 * depth : cols_b(r));
+              mbar_arrive_expect_tx_if(lead, smem_u32(&full[s]), rows * 128u);
+            }
+            if constexpr (kA) {
+              for (int c = 0; c < na; c += 64)
+                tma_load_2d_pair_if(lead, sa + c * 128, deep ? &maps.a : &maps.a_edge, row + c, k * 64,
+                                    bar, pol);
+            } else {
+              if (na > 0)
+                tma_load_2d_pair_if(lead, sa, na == 128 ? &maps.a : &maps.a_edge, k * 64, row, bar, pol);
+            }
+            if constexpr (kB) {
+              for (int c = 0; c < nb; c += 64)
+                tma_load_2d_pair_if(lead, sb + c * 128, deep ? &maps.b : &maps.b_edge, col + c, k * 64,
+                                    bar, pol);
+            } else {
+              const CUtensorMap* b = nb == rows_b ? map_b : second ? &maps.b2_edge : &maps.b_edge;
+              if (nb > 0) tma_load_2d_pair_if(lead, sb, b, k * 64, col, bar, pol);
+            }
           }
-          if (across_b) {
-            tma_load_2d_pair_if(lead, sb, map_b, col, k * 64, bar, pol);
-            if (rows_b > 64) tma_load_2d_pair_if(lead, sb + 8192, map_b, col + 64, k * 64, bar, pol);
-          } else {
-            tma_load_2d_pair_if(lead, sb, map_b, k * 64, col, bar, pol);
-          }
-        } else {
-          const bool deep = k < K / 64;  // a whole step of K
-          const int depth = deep ? 64 : last_deep(K);
-          if (rank == 0) {
-            uint32_t rows = 0;  // of 128 bytes, of both SMs
-            for (int r = 0; r < 2; ++r)
-              rows += (across_a ? (rows_a(r) + 63) / 64 * depth : rows_a(r)) +
-                      (across_b ? (cols_b(r) + 63) / 64 * depth : cols_b(r));
-            mbar_arrive_expect_tx_if(lead, smem_u32(&full[s]), rows * 128u);
-          }
-          if (across_a) {
-            for (int c = 0; c < na; c += 64)
-              tma_load_2d_pair_if(lead, sa + c * 128, deep ? &maps.a : &maps.a_edge, row + c, k * 64,
-                                  bar, pol);
-          } else if (na > 0) {
-            tma_load_2d_pair_if(lead, sa, na == 128 ? &maps.a : &maps.a_edge, k * 64, row, bar, pol);
-          }
-          if (across_b) {
-            for (int c = 0; c < nb; c += 64)
-              tma_load_2d_pair_if(lead, sb + c * 128, deep ? &maps.b : &maps.b_edge, col + c, k * 64,
-                                  bar, pol);
-          } else if (nb > 0) {
-            const CUtensorMap* b = nb == rows_b ? map_b : second ? &maps.b2_edge : &maps.b_edge;
-            tma_load_2d_pair_if(lead, sb, b, k * 64, col, bar, pol);
+          if (++s == (uint32_t)stages) {
+            s = 0;
+            ph ^= 1;
           }
         }
-        if (++s == (uint32_t)stages) {
-          s = 0;
-          ph ^= 1;
-        }
-      }
+      };
+      by_lie(across_a, across_b, steps);
     }
     if (!ok) {  // the copies of the last steps may still be landing
       const unsigned long long t0 = globaltimer_ns();
@@ -401,8 +420,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         idesc |= (across_a ? 1u << 15 : 0u) | (across_b ? 1u << 16 : 0u);
         const uint64_t a0 = across_a ? sdesc_across(base) : sdesc_sw128(base);
         const uint64_t b0 = across_b ? sdesc_across(base + kABytes) : sdesc_sw128(base + kABytes);
-        // 16 of K further on: 32 bytes of a row, or 16 rows of 128 bytes
-        const uint32_t step_a = across_a ? 128 : 2, step_b = across_b ? 128 : 2;
         const int k0 = u.k0, whole = p.K / 64;
         const int ab = local & 1;
         if (!wait(&acce[ab], ((local >> 1) & 1) ^ 1)) {
@@ -411,29 +428,35 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc_fence_after();
         const uint32_t dst = tmem + ab * kAccCols;
-        for (int k = k0; k < u.k1; ++k) {
-          if (!wait(&full[s], ph)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t off = (s * stage_bytes) >> 4;
-          if (k < whole) {
-            if (lead) {
+        auto steps = [&](auto lie_a, auto lie_b) {
+          // 16 of K further on: 32 bytes of a row, or 16 rows of 128 bytes
+          constexpr uint32_t step_a = decltype(lie_a)::value ? 128 : 2;
+          constexpr uint32_t step_b = decltype(lie_b)::value ? 128 : 2;
+          for (int k = k0; k < u.k1; ++k) {
+            if (!wait(&full[s], ph)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint32_t off = (s * stage_bytes) >> 4;
+            if (k < whole) {
+              if (lead) {
 #pragma unroll
-              for (int j = 0; j < 4; ++j)
+                for (int j = 0; j < 4; ++j)
+                  mma_pair(dst, a0 + off + step_a * j, b0 + off + step_b * j, idesc, (k > k0) | (j > 0));
+              }
+            } else if (lead) {  // the slices of 16 that there are
+              for (int j = 0; j < (p.K - k * 64 + 15) / 16; ++j)
                 mma_pair(dst, a0 + off + step_a * j, b0 + off + step_b * j, idesc, (k > k0) | (j > 0));
             }
-          } else if (lead) {  // the slices of 16 that there are
-            for (int j = 0; j < (p.K - k * 64 + 15) / 16; ++j)
-              mma_pair(dst, a0 + off + step_a * j, b0 + off + step_b * j, idesc, (k > k0) | (j > 0));
+            tc_commit2_both_if(lead, smem_u32(&empty[s]));
+            if (++s == (uint32_t)stages) {
+              s = 0;
+              ph ^= 1;
+            }
           }
-          tc_commit2_both_if(lead, smem_u32(&empty[s]));
-          if (++s == (uint32_t)stages) {
-            s = 0;
-            ph ^= 1;
-          }
-        }
+        };
+        by_lie(across_a, across_b, steps);
         if (ok) tc_commit2_both_if(lead, smem_u32(&accf[ab]));
       }
       tc_commit2_both_if(lead, smem_u32(drain));
