@@ -660,9 +660,10 @@ constexpr int kPairs = 76;  // of SMs of a GB300: results are the same on every 
 
 // How a product alone in its launch is cut: tiles of 256 or 128 columns, and their K steps into
 // segments where the tiles are far fewer than the pairs of SMs.  By an estimate of the time in units
-// of a step of a wide tile (0.27 us): a step of a tile of 128 columns takes 0.55 (its rows of A are
-// loaded for half as many products), a tile's last epilogue about 8, segments another kernel of
-// about 12 and their sums written and read again (about 5 TB/s).
+// of a step of a wide tile (0.27 us): a step of a tile of 128 columns takes 0.75 (its operands come at
+// the rate at which L2 feeds an SM), a tile's last epilogue about 8, segments another kernel of about
+// 12 and their sums written and read again in L2.  (3000 tokens, H = 7168, I = 2048: 166 us a call,
+// with 0.55 182; backward of 1023 tokens, 4096 x 1000: 66 us, without segments in its first product 74.)
 void cut_alone(FfnGemm& p) {
   const bool up = p.op == FfnOp::kUp;
   double best = 0;
@@ -671,9 +672,9 @@ void cut_alone(FfnGemm& p) {
     const long long tiles = (long long)p.tiles_m * tiles_n;
     for (int s = 1; s <= kFfnMaxSplits && (s == 1 || (tiles * s <= kPairs && p.ksteps >= 4 * s)); ++s) {
       const double waves = (double)((tiles * s + kPairs - 1) / kPairs);
-      const double steps = (p.ksteps + s - 1) / s * (n == 256 ? 1.0 : 0.55);
+      const double steps = (p.ksteps + s - 1) / s * (n == 256 ? 1.0 : 0.75);
       const double sums = (double)s * p.M * p.N * (up ? 2 : 1) * 8;
-      const double cost = waves * steps + (n == 256 ? 8 : 4) + (s > 1 ? 12 + sums / 1.35e6 : 0);
+      const double cost = waves * steps + (n == 256 ? 8 : 4) + (s > 1 ? 12 + sums / 2.7e6 : 0);
       if (best != 0 && cost >= best) continue;
       best = cost;
       p.tile_n = n;
