@@ -21,7 +21,7 @@ constexpr int kMaxStages = 8;
 constexpr int kCtrl = 1024;
 constexpr int kWeightBytes = 128 * 128;  // a stage's 128 rows x 64 of K
 constexpr int kSmemHalf = 115712, kSmemLimit = 232448;  // two CTAs an SM, one
-constexpr int kMaxSplits = 8;
+constexpr int kMaxSplits = 4;
 
 struct Maps {
   CUtensorMap x, w, w2;
@@ -228,10 +228,12 @@ cudaError_t run(const FfnProduct& f, int num_sms, cudaStream_t stream) {
   p.ksteps = (f.K + 63) / 64;
   p.tmem_cols = p.tile_n <= 32 ? 32 : p.tile_n <= 64 ? 64 : p.tile_n <= 128 ? 128 : 256;
   const int units = p.tiles * p.blocks, stage = kWeightBytes + p.tile_n * 128;
-  // segments of four steps or more, as many as leave two CTAs an SM at most
+  // Segments of two steps or more, four at most, as many as there are SMs for: more of them cost
+  // the adding up what they save (128 tokens, 4096 x 1536: 19.2 us a call, by up to eight segments and
+  // two CTAs an SM 22.0, by two segments 26.2).
   p.splits = 1;
-  while (p.splits < kMaxSplits && units * (p.splits + 1) <= 2 * num_sms &&
-         p.ksteps >= 4 * (p.splits + 1))
+  while (p.splits < kMaxSplits && units * (p.splits + 1) <= num_sms &&
+         p.ksteps >= 2 * (p.splits + 1))
     ++p.splits;
   const int limit = p.tile_n <= 128 ? kSmemHalf : kSmemLimit, other = 1024 + kCtrl;
   const int most = (limit - other) / stage;

@@ -281,8 +281,9 @@ __global__ void __launch_bounds__(ACC && VEC > 1 ? 512 : 1024) norm_backward_ker
   }
 }
 
-// dst[h] = sum over the units of their sum number `which`, 32 columns a CTA.
-constexpr int kSumWarps = 8;
+// dst[h] = sum over the units of their sum number `which`, 32 columns a CTA, a warp every kSumWarps
+// units (few columns have few CTAs, so many units have many warps).
+template <int kSumWarps>
 __global__ void __launch_bounds__(kSumWarps * 32) norm_sums_kernel(const float* partial, int units,
                                                                    int H, float* post, float* pre,
                                                                    float* gate) {
@@ -362,9 +363,10 @@ cudaError_t of_chunk(const NormArgs& a, int chunk, cudaStream_t stream) {
 
 int norm_units(int M, int H) {
   // as many rows in the making as 512 threads an SM have, a thread sixteen elements; and two rows a
-  // unit or more, whose sums are written and read again, where that leaves every SM one
+  // unit or more, whose sums are written and read again, where that leaves every SM one (of the
+  // shortest rows fewer: there the sums of the units are what takes time)
   const int threads = norm_threads(H < kNormRegisterColumns ? H : kNormRegisterColumns, 8, 16);
-  const int most = 152 * (threads < 512 ? 512 / threads : 1);
+  const int most = 152 * (threads >= 512 ? 1 : threads >= 64 ? 512 / threads : 8);
   const int two = (M + 1) / 2, least = M < 152 ? M : 152;
   const int n = two > least ? two : least;
   return n < most ? n : most;
@@ -387,8 +389,10 @@ cudaError_t launch_norm_backward(const NormArgs& args, int dtype, int chunk, cud
   float* post = a.post_weight ? a.dpost_weight : nullptr;
   float* pre = a.pre_weight ? a.dpre_weight : nullptr;
   if (!gate && !post && !pre) return cudaSuccess;
-  return launch_pdl(norm_sums_kernel, dim3((a.H + 31) / 32, 3), kSumWarps * 32, 0, stream,
-                (const float*)a.partial, a.units, a.H, post, pre, gate);
+  const bool wide = a.units > 256;
+  return launch_pdl(wide ? norm_sums_kernel<32> : norm_sums_kernel<8>, dim3((a.H + 31) / 32, 3),
+                    wide ? 1024 : 256, 0, stream, (const float*)a.partial, a.units, a.H, post, pre,
+                    gate);
 }
 
 }  // namespace qmoe
