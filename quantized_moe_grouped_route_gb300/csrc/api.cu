@@ -101,6 +101,14 @@ int make_tmap16(CUtensorMap* map, int dtype, const void* base, int rank, const u
                 const uint64_t* strides, const uint32_t* box, int swizzle) {
   auto fn = encode_fn();
   if (!fn) return QMOE_ERR_CUDA;
+  // The driver's encoder wants a current context, which a thread has none of before its first call
+  // of the runtime that needs one (a thread's own context is left as it is).
+  auto current = ctx_current_fn();
+  CUcontext ctx = nullptr;
+  int dev = 0;
+  if (!current || current(&ctx) != CUDA_SUCCESS) return QMOE_ERR_CUDA;
+  if (!ctx && (cudaGetDevice(&dev) != cudaSuccess || cudaSetDevice(dev) != cudaSuccess))
+    return QMOE_ERR_CUDA;
   cuuint64_t d[3], st[2];
   cuuint32_t bx[3], estr[3] = {1, 1, 1};
   for (int i = 0; i < rank; ++i) d[i] = dims[i], bx[i] = box[i];
