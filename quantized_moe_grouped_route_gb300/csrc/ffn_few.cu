@@ -8,10 +8,9 @@
 // every CTA the tokens seg, seg + S, ..; the order of the sums is fixed.  Bound by the stream of the
 // weights; two CTAs fit an SM, so that the second product's first weights are already on their way
 // while the first product ends (its launch is programmatic, and only the tokens' copies wait).
-#include <type_traits>
-
 #include "cluster.cuh"
 #include "ffn.cuh"
+#include "mma.cuh"
 
 namespace qmoe {
 namespace {
@@ -26,15 +25,6 @@ constexpr int kMaxSplits = 4;
 struct Maps {
   CUtensorMap x, w, w2;
 };
-
-__device__ __forceinline__ void mma_one(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                        uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, q;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
 
 template <class T, bool UP>
 __global__ void __launch_bounds__(kThreads) ffn_few_kernel(const __grid_constant__ Maps maps,
@@ -126,8 +116,7 @@ __global__ void __launch_bounds__(kThreads) ffn_few_kernel(const __grid_constant
   } else if (warp == 1) {
     // ------------------------------------------------------------------ MMA issue
     const uint32_t lead = elect_one();
-    uint32_t idesc = idesc_bf16_f32(128, p.tile_n);
-    if (std::is_same<T, __half>::value) idesc &= ~((1u << 7) | (1u << 10));
+    const uint32_t idesc = idesc_16bit(128, p.tile_n, p.dtype);
     const uint64_t desc0 = sdesc_sw128(smem_u32(smem));
     int s = 0;
     uint32_t ph = 0;
@@ -138,7 +127,7 @@ __global__ void __launch_bounds__(kThreads) ffn_few_kernel(const __grid_constant
       if (lead) {
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          mma_one(tmem, a + 2 * j, a + (kWeightBytes >> 4) + 2 * j, idesc, (k > k0) | (j > 0));
+          mma_ss(1, tmem, a + 2 * j, a + (kWeightBytes >> 4) + 2 * j, idesc, (k > k0) | (j > 0));
       }
       tc_commit_if(lead, smem_u32(&empty[s]));
       if (++s == stages) {

@@ -21,6 +21,7 @@
 #include "checkpoint.cuh"
 #include "cluster.cuh"
 #include "ffn.cuh"
+#include "mma.cuh"
 
 namespace qmoe {
 namespace {
@@ -64,9 +65,6 @@ __device__ __forceinline__ uint64_t l2_policy_normal() {
   asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
   return p;
 }
-__device__ __forceinline__ void fence_proxy_async() {
-  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-}
 __device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, uint32_t src, int x, int y) {
   asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
                    reinterpret_cast<uint64_t>(map)),
@@ -82,15 +80,6 @@ __device__ __forceinline__ void store_wait_read() {
 }
 __device__ __forceinline__ void store_wait_all() {
   asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
-}
-
-__device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                         uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, q;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
-      : "memory");
 }
 
 // Descriptor of an operand that lies across K: boxes of 64 elements (128 bytes, swizzled) x 64
@@ -415,8 +404,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const Unit u = unit_of(L, i);
         const FfnGemm& p = L.p[u.problem];
         const bool across_a = a_across(p), across_b = b_across(p);
-        uint32_t idesc = idesc_bf16_f32(256, p.tile_n);
-        if (std::is_same<T, __half>::value) idesc &= ~((1u << 7) | (1u << 10));
+        uint32_t idesc = idesc_16bit(256, p.tile_n, p.dtype);
         idesc |= (across_a ? 1u << 15 : 0u) | (across_b ? 1u << 16 : 0u);
         const uint64_t a0 = across_a ? sdesc_across(base) : sdesc_sw128(base);
         const uint64_t b0 = across_b ? sdesc_across(base + kABytes) : sdesc_sw128(base + kABytes);
@@ -443,11 +431,11 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (lead) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                  mma_pair(dst, a0 + off + step_a * j, b0 + off + step_b * j, idesc, (k > k0) | (j > 0));
+                  mma_ss(2, dst, a0 + off + step_a * j, b0 + off + step_b * j, idesc, (k > k0) | (j > 0));
               }
             } else if (lead) {  // the slices of 16 that there are
               for (int j = 0; j < (p.K - k * 64 + 15) / 16; ++j)
-                mma_pair(dst, a0 + off + step_a * j, b0 + off + step_b * j, idesc, (k > k0) | (j > 0));
+                mma_ss(2, dst, a0 + off + step_a * j, b0 + off + step_b * j, idesc, (k > k0) | (j > 0));
             }
             tc_commit2_both_if(lead, smem_u32(&empty[s]));
             if (++s == (uint32_t)stages) {

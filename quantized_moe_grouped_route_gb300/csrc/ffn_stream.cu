@@ -6,9 +6,8 @@
 // The warps of a CTA take parts of K of the same rows, added up in shared memory in their order.
 // The first product's 16 rows are eight of u and the same eight of g: a lane ends up with both, and
 // h = act(g) u is made where they are.
-#include <type_traits>
-
 #include "ffn.cuh"
+#include "mma.cuh"
 
 namespace qmoe {
 namespace {
@@ -18,23 +17,6 @@ namespace {
 // eight 18.3, sixteen with seven (one CTA an SM) 21.6.
 constexpr int kWarps = 16;
 constexpr int kAhead = 4;
-
-template <class T>
-__device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                          uint32_t a3, uint32_t b0, uint32_t b1) {
-  if constexpr (std::is_same<T, __nv_bfloat16>::value)
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-        "{%8, %9}, {%0, %1, %2, %3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-  else
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-        "{%8, %9}, {%0, %1, %2, %3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
 
 // UP: rows 8 b .. 8 b + 7 of u and of g, b the CTA; else rows 16 b .. 16 b + 15.
 template <class T, bool UP>
@@ -75,8 +57,8 @@ __global__ void __launch_bounds__(kWarps * 32) ffn_stream_kernel(const FfnProduc
     }
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
-      mma_16816<T>(c, a0[i].x, a1[i].x, a0[i].y, a1[i].y, b[i].x, b[i].y);
-      mma_16816<T>(c, a0[i].z, a1[i].z, a0[i].w, a1[i].w, b[i].z, b[i].w);
+      mma_m16n8k16<T>(c, a0[i].x, a1[i].x, a0[i].y, a1[i].y, b[i].x, b[i].y);
+      mma_m16n8k16<T>(c, a0[i].z, a1[i].z, a0[i].w, a1[i].w, b[i].z, b[i].w);
       weights(s + kAhead, i);
     }
   }

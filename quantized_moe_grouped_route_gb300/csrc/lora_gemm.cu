@@ -71,10 +71,6 @@ __device__ __forceinline__ void builders_sync() {
   asm volatile("bar.sync 1, %0;" ::"n"(32 * kBuilders) : "memory");
 }
 
-__device__ __forceinline__ void fence_proxy_async() {
-  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-}
-
 __device__ __forceinline__ bool all_finite(const float (&f)[4]) {
   return fabsf(f[0]) < INFINITY && fabsf(f[1]) < INFINITY && fabsf(f[2]) < INFINITY &&
          fabsf(f[3]) < INFINITY;
