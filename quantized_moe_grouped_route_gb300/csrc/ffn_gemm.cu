@@ -159,6 +159,19 @@ struct Kept {
   uint4 raw[4];
   uint32_t byte;
 };
+// 16 bytes, or zeros.  (Two lie in a sector, so they may stay in L1: past it each would fetch the sector,
+// twice the bytes through L2's ports, which the operands need: 8192 tokens, H = 7168, I = 2048, the
+// kernel 172 us, past L1 183.)
+__device__ __forceinline__ uint4 load_l1_if(const uint4* p, bool there) {
+  uint4 v;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+      "mov.u32 %0, 0;\n\tmov.u32 %1, 0;\n\tmov.u32 %2, 0;\n\tmov.u32 %3, 0;\n\t"
+      "@p ld.global.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
+      : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)
+      : "l"(p), "r"((int)there));
+  return v;
+}
 template <class T, bool CODES>
 __device__ __forceinline__ void fetch_kept(Kept& k, const FfnGemm& p, int row, int col, int half) {
   const size_t at = (size_t)row * 2 * p.N + (size_t)half * p.N + col;
@@ -177,7 +190,7 @@ __device__ __forceinline__ void fetch_kept(Kept& k, const FfnGemm& p, int row, i
     const T* src = reinterpret_cast<const T*>(p.kept) + at;
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      k.raw[j] = load_if(reinterpret_cast<const uint4*>(src + 8 * j), in && col + 8 * j < p.N);
+      k.raw[j] = load_l1_if(reinterpret_cast<const uint4*>(src + 8 * j), in && col + 8 * j < p.N);
   }
 }
 template <class T, bool CODES>
