@@ -45,6 +45,6 @@ def test_gradients(example, checkpoint):
     ref = (out - want.double()).square().mean()
     ref.backward()
     tol = 2.0 ** -4 if checkpoint == 8 else 2.0 ** -5
-    assert abs(float(loss) - float(ref)) <= tol * float(ref)
+    assert abs(float(loss) - float(ref.detach())) <= tol * float(ref.detach())
     for k, t in grads.items():
         assert (t.double() - v[k].grad).norm() <= tol * v[k].grad.norm(), k
