@@ -23,6 +23,7 @@
 #include "checkpoint.cuh"
 #include "cluster.cuh"
 #include "ffn.cuh"
+#include "ffn_tiles.h"
 #include "mma.cuh"
 
 namespace qmoe {
@@ -54,13 +55,6 @@ struct Launch {
   Maps maps[N];
 };
 constexpr int problems(Op op) { return op == Op::kMany ? kMost : 1; }
-
-// A matrix's last block of `box` rows is copied in a box of its own number of rows: rows that a copy
-// has to fill in cost it several times what rows of the matrix do (1 token by boxes of 128 rows: 182 us
-// a call where 512 tokens took 43).  What is left in shared memory beyond reaches rows and columns of
-// the accumulator that are not written; along K zeros are filled in up to the 16 of an MMA.
-__host__ __device__ constexpr int last_rows(int rows, int box) { return (rows + box - 1) % box + 1; }
-__host__ __device__ constexpr int last_deep(int depth) { return (last_rows(depth, 64) + 15) / 16 * 16; }
 
 __device__ __forceinline__ uint64_t l2_policy_normal() {
   uint64_t p;
@@ -332,19 +326,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool across_a = a_across(p), across_b = b_across(p);
       const int rows_b = p.tile_n / 2, K = p.K;
       const uint32_t bytes = 2u * (kABytes + rows_b * 128);  // of a whole step, both SMs
-      // an SM's rows of A and columns of B: where they begin and how many there are
-      auto rows_a = [&](int r) { return max(0, min(128, p.M - u.tm * 256 - r * 128)); };
-      auto begin_b = [&](int r) {
-        return OP == Op::kUp ? u.tn * rows_b : u.tn * p.tile_n + r * rows_b;
-      };
-      auto cols_b = [&](int r) { return max(0, min(rows_b, p.N - begin_b(r))); };
-      const int row = u.tm * 256 + (int)rank * 128, col = begin_b((int)rank);
-      const int na = rows_a((int)rank), nb = cols_b((int)rank);
+      const Share shares[2] = {share_of(p.M, p.N, p.tile_n, OP == Op::kUp, u.tm, u.tn, 0),
+                               share_of(p.M, p.N, p.tile_n, OP == Op::kUp, u.tm, u.tn, 1)};
+      const Share own = rank == 0 ? shares[0] : shares[1];
+      const int row = own.row, col = own.col, na = own.rows, nb = own.cols;
       const bool second = OP == Op::kUp && rank != 0;  // the SM with the rows of g
       const CUtensorMap* const map_b = second ? &maps.b2 : &maps.b;
       // steps of whole boxes (a tile whose second half is whole is whole), one copy an operand, two
       // across K: the issue is what paces a step
-      const int k_whole = rows_a(1) == 128 && cols_b(1) == rows_b ? min(u.k1, K / 64) : u.k0;
+      const int k_whole =
+          shares[1].rows == 128 && shares[1].cols == rows_b ? min(u.k1, K / 64) : u.k0;
       auto steps = [&](auto lie_a, auto lie_b) {
         constexpr bool kA = decltype(lie_a)::value, kB = decltype(lie_b)::value;
         for (int k = u.k0; k < u.k1; ++k) {
@@ -373,9 +364,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int depth = deep ? 64 : last_deep(K);
             if (rank == 0) {
               uint32_t rows = 0;  // of 128 bytes, of both SMs
+#pragma unroll
               for (int r = 0; r < 2; ++r)
-                rows += (kA ? (rows_a(r) + 63) / 64 * depth : rows_a(r)) +
-                        (kB ? (cols_b(r) + 63) / 64 * depth : cols_b(r));
+                rows += (kA ? (shares[r].rows + 63) / 64 * depth : shares[r].rows) +
+                        (kB ? (shares[r].cols + 63) / 64 * depth : shares[r].cols);
               mbar_arrive_expect_tx_if(lead, smem_u32(&full[s]), rows * 128u);
             }
             if constexpr (kA) {
