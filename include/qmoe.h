@@ -500,8 +500,9 @@ int qmoe_checkpoint8_restore(const int8_t* codes_dev, const uint8_t* scales_dev,
  *            as the layer's;  w2_dev [H][I];  out_dev [M][H]
  *   limit    the layer's SwiGLU limit: positive, +infinity for none
  *   kept_dev, kept_scales_dev  what the backward pass needs of u and g: both NULL for nothing;
- *            kept_dev alone: [M][2I] of `dtype`, u beside g; both: as qmoe_checkpoint8 has them,
- *            codes [M][2I] and scales [M][2][ceil(I / 32)], blocks of u and of g counted apart
+ *            kept_dev alone: [M][2I] of `dtype`, u beside g, finite ones within its finite range;
+ *            both: as qmoe_checkpoint8 has them, codes [M][2I] and scales [M][2][ceil(I / 32)],
+ *            blocks of u and of g counted apart
  * u, g and h are fp32 sums and products; h is rounded to `dtype`, in which it enters the second
  * product.  H % 8 == 0, I % 8 == 0, 8 <= H, I <= 65536; x, w13, w2, out and kept are 16-byte
  * aligned and ldx is a multiple of 8.

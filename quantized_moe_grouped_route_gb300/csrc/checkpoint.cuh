@@ -43,6 +43,12 @@ template <>
 __device__ __forceinline__ float finite_max<float>() {
   return __uint_as_float(0x7f7fffffu);
 }
+// v within T's finite range; infinities and NaN stay.
+template <class T>
+__device__ __forceinline__ float within(float v) {
+  const float most = finite_max<T>();
+  return fabsf(v) < __uint_as_float(0x7f800000u) ? fminf(fmaxf(v, -most), most) : v;
+}
 // The value of a code within T's finite range (a block's largest can round up past it).
 template <class T>
 __device__ __forceinline__ float ck_restore(int code, float value) {

@@ -77,8 +77,11 @@ __global__ void __launch_bounds__(kThreads) ffn_finish_kernel(const FfnGemm p) {
       }
       if (!in) continue;
       if (p.save == 16) {
-        store8<T>(p.ug, kept, f);
-        store8<T>(p.ug, kept + p.N, g);
+        float a[8], b[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) a[e] = within<T>(f[e]), b[e] = within<T>(g[e]);
+        store8<T>(p.ug, kept, a);
+        store8<T>(p.ug, kept + p.N, b);
       }
 #pragma unroll
       for (int e = 0; e < 8; ++e) f[e] = gated(gelu, p.limit, f[e], g[e]);

@@ -102,6 +102,15 @@ __device__ __forceinline__ void stage_row(uint8_t* tile, const float (&v)[32]) {
   stage_half<T>(tile, 0, v);
   stage_half<T>(tile, 1, v + 16);
 }
+// ... of u or g, which is kept within T's finite range: a gate past it is open or closed, where an
+// infinity's product with sigmoid's 0 would leave NaN.
+template <class T>
+__device__ __forceinline__ void stage_kept(uint8_t* tile, const float (&v)[32]) {
+  float f[32];
+#pragma unroll
+  for (int k = 0; k < 32; ++k) f[k] = within<T>(v[k]);
+  stage_row<T>(tile, f);
+}
 
 __device__ __forceinline__ void load_acc16(uint32_t taddr, float (&v)[16]) {
   uint32_t r[16];
@@ -521,8 +530,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               save_block(g, min(32, n - c), p.codes + at + p.N, p.scales + sat + blocks);
             }
             if (p.save == 16) {
-              stage_row<T>(stage + kStageTile, u);
-              stage_row<T>(stage + 2 * kStageTile, g);
+              stage_kept<T>(stage + kStageTile, u);
+              stage_kept<T>(stage + 2 * kStageTile, g);
             }
 #pragma unroll
             for (int k = 0; k < 32; ++k) u[k] = gated(gelu, p.limit, u[k], g[k]);

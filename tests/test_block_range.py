@@ -9,9 +9,42 @@ import torch
 import quantized_moe_grouped_route_gb300 as q
 from quantized_moe_grouped_route_gb300 import qmoe
 from tests import test_block_operators as ops
-from tests.test_block_operators import _ffn_inputs, _gen, _rows
+from tests.test_block_operators import ACTS, _ffn_grads, _ffn_inputs, _gen, _near, _rows
 
 pytestmark = pytest.mark.gpu
+
+
+# --------------------------------------------------------- pre-activations past fp16's range
+@pytest.mark.parametrize("M,H", [(5, 64), (5, 4096), (200, 64), (700, 72)])
+@pytest.mark.parametrize("kind", ["silu", "gelu"])
+def test_kept_values_past_fp16(M, H, kind):
+    """g of -100000 closes its gate and u of 100000 stays finite times an h that is: the forward pass
+    is finite, and so are the gradients.  A finite u or g that fp16 has not is kept as its largest."""
+    I, dt = 520, torch.float16
+    x, w13, w2 = _ffn_inputs(M, H, I, dt)
+    x[:, 0] = 400.0
+    w13[:, 0] = 0.0
+    w13[I + 3, 0] = w13[I + 17, 0] = -250.0  # g = -100000: h = 0
+    w13[9, 0], w13[I + 9] = 250.0, 0.0  # u = 100000, g = 0: h = 0 too, dg = u dh / 2
+    w2[:, 9] *= 2.0 ** -12  # (so that fp16 has dg)
+    how = dict(activation=ACTS[kind])
+    out, (kept,) = q.qmoe_gated_ffn_saved(x, w13, w2, **how)
+    assert torch.isfinite(out).all() and torch.isfinite(kept).all()
+    ug = x.double() @ w13.double().t()
+    want = ug.clamp(-65504, 65504)
+    assert (kept[:, [9, I + 3, I + 17]].double() == want[:, [9, I + 3, I + 17]]).all()
+    dout = _rows(_gen(M), M, H, dt)
+    got = q.qmoe_gated_ffn_backward(dout, x, w13, w2, (kept,), **how)
+    u, g = kept[:, :I].double(), kept[:, I:].double()
+    ref = _ffn_grads(kind, math.inf, dout, x, w13, w2, u, g, dt)
+    for name, t in zip(("dx", "dw13", "dw2"), got):
+        r, bound = ref[name]
+        fits = r.abs() + bound < 65504  # (what fp16 has)
+        _near(torch.where(fits, t.double(), 0.0), torch.where(fits, r, 0.0), bound, name)
+    # a true infinity stays one
+    x[0, 0] = math.inf
+    out, (kept,) = q.qmoe_gated_ffn_saved(x, w13, w2, **how)
+    assert kept[0, 9] == math.inf and not torch.isfinite(out[0]).any()
 
 
 # ------------------------------------------------------ plans that only large sizes take
