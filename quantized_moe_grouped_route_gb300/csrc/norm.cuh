@@ -220,12 +220,18 @@ struct RowSum {
   }
 };
 
-// The gate's value and its derivative in what is given.
+// The gate's value, and its value and derivative in what is given.
 __device__ __forceinline__ float gate_value(const NormArgs& a, float g) {
   return a.gating == QMOE_GATING_SIGMOID ? 1.f / (1.f + expf(-g)) : g;
 }
-__device__ __forceinline__ float gate_slope(const NormArgs& a, float value) {
-  return a.gating == QMOE_GATING_SIGMOID ? value * (1.f - value) : 1.f;
+// A sigmoid s(g)'s derivative is s(g) s(-g), and s(-g) = e^-g s(g): above 0, where 1 - s(g) loses its
+// digits, by that product.
+__device__ __forceinline__ float gate_parts(const NormArgs& a, float g, float* slope) {
+  *slope = 1.f;
+  if (a.gating != QMOE_GATING_SIGMOID) return g;
+  const float e = expf(-g), s = 1.f / (1.f + e);
+  *slope = s * (g > 0.f ? e * s : 1.f - s);
+  return s;
 }
 
 // Vectors over a row's columns (weights, a channel's gate) that each thread keeps for its own

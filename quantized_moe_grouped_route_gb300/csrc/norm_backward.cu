@@ -1,7 +1,7 @@
 // Gradients of the norms after and before a block (norm.cu).  With x^ = out * pre_rstd and
 // y^ = y * post_rstd, w the weights with their offset, <a, b> the mean over a row's elements:
 //   g = dout + pre_rstd * (dnormed w_pre - x^ <dnormed w_pre, x^>)       dpre = sum_m dnormed x^
-//   dresidual = residual_scale * g,   dgate = g v (summed over what shares a gate),  v = y^ w_post
+//   dresidual = residual_scale * g,   dgate = slope g v (g v summed over what shares a gate),  v = y^ w_post
 //   d = gate * g,   dy = post_rstd * (d w_post - y^ <d w_post, y^>)       dpost = sum_m d y^
 // One pass over the rows: four are read and two written a token.  The sums over the tokens stay in
 // the registers of the threads that own the columns; each CTA (or warp) goes through many rows
@@ -181,11 +181,11 @@ __global__ void __launch_bounds__(ACC && VEC > 1 ? 512 : 1024) norm_backward_ker
       put(a.dresidual, row, f);
     }
     // a token's gate, or 1
-    float gate1 = 1.f;
+    float gate1 = 1.f, slope1 = 1.f;
     if (form == QMOE_GATE_TOKEN) {
       float one[1];
       load_either<T, 1>(a.gate, a.gate_fp32, row * a.ldgate, one);
-      gate1 = gate_value(a, one[0]);
+      gate1 = gate_parts(a, one[0], &slope1);
     }
     const bool summed = post || (form == QMOE_GATE_TOKEN && a.dgate);
     float s = 0.f;
@@ -194,9 +194,11 @@ __global__ void __launch_bounds__(ACC && VEC > 1 ? 512 : 1024) norm_backward_ker
       float dg[kElems];
 #pragma unroll
       for (int k = 0; k < NCH; ++k) {
-        float f[VEC], w[VEC], y[VEC];
-        if (per_channel) {
+        float f[VEC], slope[VEC], w[VEC], y[VEC];
+        if (per_channel) {  // (its slope is one for all tokens: norm_sums_kernel multiplies by it)
           vector(kGate, k, f);
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) slope[e] = 1.f;
         } else {
           if (full_t) {
             chunk(GATED ? 4 : 0, k, f);
@@ -206,14 +208,14 @@ __global__ void __launch_bounds__(ACC && VEC > 1 ? 512 : 1024) norm_backward_ker
             if (in[k]) load_either<T, VEC>(a.gate, true, row * a.ldgate + col[k], f);
           }
 #pragma unroll
-          for (int e = 0; e < VEC; ++e) f[e] = gate_value(a, f[e]);
+          for (int e = 0; e < VEC; ++e) f[e] = gate_parts(a, f[e], &slope[e]);
         }
         if (post) vector(kPost, k, w);
         chunk(3, k, y);
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
           const int i = k * VEC + e;
-          dg[i] = g[i] * gate_slope(a, f[e]) * (y[e] * rstd) * (post ? w[e] : 1.f);
+          dg[i] = g[i] * slope[e] * (y[e] * rstd) * (post ? w[e] : 1.f);
           g[i] *= f[e];
         }
         if (per_channel) {
@@ -249,7 +251,7 @@ __global__ void __launch_bounds__(ACC && VEC > 1 ? 512 : 1024) norm_backward_ker
       s = row_sum(s);
     }
     if (form == QMOE_GATE_TOKEN && a.dgate && tid == 0)
-      reinterpret_cast<float*>(a.dgate)[row] = s * gate_slope(a, gate1);
+      reinterpret_cast<float*>(a.dgate)[row] = s * slope1;
     if (GATED) {
 #pragma unroll
       for (int i = 0; i < kElems; ++i) g[i] *= gate1;
@@ -285,22 +287,25 @@ __global__ void __launch_bounds__(ACC && VEC > 1 ? 512 : 1024) norm_backward_ker
 }
 
 // dst[h] = sum over the units of their sum number `which`, 32 columns a CTA, a warp every kSumWarps
-// units (few columns have few CTAs, so many units have many warps).
-template <int kSumWarps>
-__global__ void __launch_bounds__(kSumWarps * 32) norm_sums_kernel(const float* partial, int units,
-                                                                   int H, float* post, float* pre,
-                                                                   float* gate) {
+// units (few columns have few CTAs, so many units have many warps).  A channel's gate: times its
+// slope.
+template <class T, int kSumWarps>
+__global__ void __launch_bounds__(kSumWarps * 32) norm_sums_kernel(const NormArgs a) {
   __shared__ float part[kSumWarps][32];
-  float* dst = blockIdx.y == kPost ? post : blockIdx.y == kPre ? pre : gate;
+  const int which = blockIdx.y, H = a.H;
+  const bool channel = a.gate && a.gate_form == QMOE_GATE_CHANNEL;
+  float* dst = which == kPost  ? (a.post_weight ? a.dpost_weight : nullptr)
+               : which == kPre ? (a.pre_weight ? a.dpre_weight : nullptr)
+                               : (channel ? reinterpret_cast<float*>(a.dgate) : nullptr);
   grid_dep_wait();
   if (!dst) return;
   const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
   const int h = blockIdx.x * 32 + lane;
   float s = 0.f;
   if (h < H) {
-    const float* src = partial + (size_t)blockIdx.y * H + h;
+    const float* src = a.partial + (size_t)which * H + h;
 #pragma unroll 8
-    for (int u = slice; u < units; u += kSumWarps) s += src[(size_t)u * 3 * H];
+    for (int u = slice; u < a.units; u += kSumWarps) s += src[(size_t)u * 3 * H];
   }
   part[slice][lane] = s;
   __syncthreads();
@@ -308,7 +313,20 @@ __global__ void __launch_bounds__(kSumWarps * 32) norm_sums_kernel(const float* 
   s = 0.f;
 #pragma unroll
   for (int i = 0; i < kSumWarps; ++i) s += part[i][lane];
+  if (which == kGate) {
+    float one[1], slope;
+    load_either<T, 1>(a.gate, a.gate_fp32, h, one);
+    gate_parts(a, one[0], &slope);
+    s *= slope;
+  }
   dst[h] = s;
+}
+
+template <class T>
+cudaError_t sums(const NormArgs& a, cudaStream_t stream) {
+  const bool wide = a.units > 256;
+  return launch_pdl(wide ? norm_sums_kernel<T, 32> : norm_sums_kernel<T, 8>, dim3((a.H + 31) / 32, 3),
+                    wide ? 1024 : 256, 0, stream, a);
 }
 
 template <class T, int VEC, int ELEMS, bool ACC, In HOW, bool GATED>
@@ -387,15 +405,12 @@ cudaError_t launch_norm_backward(const NormArgs& args, int dtype, int chunk, cud
                   : dtype == QMOE_DTYPE_FP16 ? of_chunk<__half>(a, chunk, stream)
                                              : of_chunk<float>(a, chunk, stream);
   if (e != cudaSuccess) return e;
-  float* gate = a.gate && a.gate_form == QMOE_GATE_CHANNEL ? reinterpret_cast<float*>(a.dgate)
-                                                           : nullptr;
-  float* post = a.post_weight ? a.dpost_weight : nullptr;
-  float* pre = a.pre_weight ? a.dpre_weight : nullptr;
-  if (!gate && !post && !pre) return cudaSuccess;
-  const bool wide = a.units > 256;
-  return launch_pdl(wide ? norm_sums_kernel<32> : norm_sums_kernel<8>, dim3((a.H + 31) / 32, 3),
-                    wide ? 1024 : 256, 0, stream, (const float*)a.partial, a.units, a.H, post, pre,
-                    gate);
+  const bool gate = a.gate && a.gate_form == QMOE_GATE_CHANNEL && a.dgate;
+  if (!gate && !(a.post_weight && a.dpost_weight) && !(a.pre_weight && a.dpre_weight))
+    return cudaSuccess;
+  return dtype == QMOE_DTYPE_BF16   ? sums<__nv_bfloat16>(a, stream)
+         : dtype == QMOE_DTYPE_FP16 ? sums<__half>(a, stream)
+                                    : sums<float>(a, stream);
 }
 
 }  // namespace qmoe

@@ -9,9 +9,46 @@ import torch
 import quantized_moe_grouped_route_gb300 as q
 from quantized_moe_grouped_route_gb300 import qmoe
 from tests import test_block_operators as ops
-from tests.test_block_operators import ACTS, _ffn_grads, _ffn_inputs, _gen, _near, _rows
+from tests.test_block_operators import (ACTS, ROUND, U, _case, _ffn_grads, _ffn_inputs, _gen, _near,
+                                        _norm_call, _norm_inputs, _rows)
 
 pytestmark = pytest.mark.gpu
+
+
+# ------------------------------------------------------------------- gates far from 0
+def _norm_backward(c, s, out, dout, dn, post, pre, **kw):
+    return q.qmoe_block_norm_backward(
+        dout, dn, s["y"], out=out, residual=c["residual"], gate=s["gate"],
+        gating=int(c["sigmoid"]), post_weight=s["post"], pre_weight=s["pre"], post_rstd=post,
+        pre_rstd=pre, residual_scale=c["scale"], weight_offset=c["offset"], **kw)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("form", ["token", "channel", "full"])
+@pytest.mark.parametrize("M,H", [(40, 264), (3, 33), (2, 8200)])
+def test_gradient_of_a_saturated_gate(M, H, form, dtype):
+    """sigmoid(l) of l from -60 to 60: its slope is sigmoid(l) sigmoid(-l), which 1 - sigmoid(l) has
+    no digits for past 17.  A sigmoid by exp and a division is within a few u, the slope a product of
+    two; the terms' own errors are those of a gate of 1 (whose slope is 1), so they scale with it."""
+    c = _case(M, H, dtype, gate=form, pre=False, sigmoid=True)
+    s = _norm_inputs(c, 5)
+    s["gate"] = torch.linspace(-60, 60, s["gate"].numel(), device="cuda").view_as(s["gate"]).to(dtype)
+    out, _, post, pre = _norm_call(c, s)
+    dout = _rows(_gen(1), M, H, dtype)
+    got = _norm_backward(c, s, out, dout, None, post, pre)[2]
+    l = s["gate"].double()
+    slope = torch.sigmoid(l) * torch.sigmoid(-l)
+    unit = s["y"].double() * post.double()[:, None] * s["post"].double()
+    each = dout.double() * unit
+    if form == "full":
+        ref, bound = each * slope, 32 * U * each.abs() * slope
+    else:
+        dim, n = (1, H) if form == "token" else (0, M)
+        ref = each.sum(dim, keepdim=True) * slope
+        bound = (n + 32) * U * each.abs().sum(dim, keepdim=True) * slope
+    k = got.dtype
+    # (slopes of 60 are 2^-86, far above the least normal numbers)
+    _near(got, ref, bound + ROUND[k] * (ref.abs() + bound), "dgate")
 
 
 # --------------------------------------------------------- pre-activations past fp16's range
