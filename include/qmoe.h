@@ -420,6 +420,8 @@ int qmoe_lora_linear(const void* x_dev, int dtype, long long ldx, const void* w_
 #define QMOE_GATE_TOKEN 0
 #define QMOE_GATE_CHANNEL 1
 #define QMOE_GATE_FULL 2
+/* Added to QMOE_GATE_FULL in the backward call: the gate's gradient is of gate_dtype. */
+#define QMOE_GATE_OWN_GRADIENT 16
 
 /*
  * qmoe_block_norm — the norm after a block, the block's gate, the residual and the norm before the
@@ -455,8 +457,8 @@ int qmoe_block_norm(const void* y_dev, int dtype, long long ldy, const void* res
  *               NULL: it was y (no residual, gate and post_weight)
  *   post_rstd_dev, pre_rstd_dev  as qmoe_block_norm left them, where it has those norms
  *   dy_dev      [M][H];  dresidual_dev [M][H] or NULL
- *   dgate_dev   NULL, or fp32 [M] (_TOKEN), fp32 [H] (_CHANNEL), [M][H] of `dtype` (_FULL): the
- *               gradient of the gate as given
+ *   dgate_dev   NULL, or fp32 [M] (_TOKEN), fp32 [H] (_CHANNEL), [M][H] of `dtype` (_FULL) or of
+ *               gate_dtype (_FULL + QMOE_GATE_OWN_GRADIENT): the gradient of the gate as given
  *   dpost_weight_dev, dpre_weight_dev  fp32 [H] or NULL
  *   workspace_dev >= qmoe_block_norm_backward_workspace_size(M, H) bytes, 256-byte aligned
  * Outputs overlap no input.  M == 0: sums over tokens are set to 0.

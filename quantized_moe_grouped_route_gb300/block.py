@@ -56,7 +56,7 @@ class _BlockNorm(torch.autograd.Function):
         grads = _native().block_norm_backward(
             None if dout is None else _rows(dout), None if dnormed is None else _rows(dnormed), y,
             out, gate, gating, post_weight, pre_weight, residual_scale, weight_offset, post_rstd,
-            pre_rstd, need[1], need[2], need[4], need[5])
+            pre_rstd, need[1], need[2], need[4], need[5], True)
         dy, dresidual, dgate, dpost, dpre = grads
         return dy, dresidual, dgate, None, dpost, dpre, None, None, None, None, None
 
@@ -128,21 +128,27 @@ def qmoe_block_norm_backward(dout: Optional[torch.Tensor], dnormed: Optional[tor
                              pre_weight: Optional[torch.Tensor] = None,
                              post_rstd: Optional[torch.Tensor] = None,
                              pre_rstd: Optional[torch.Tensor] = None, residual_scale: float = 1.0,
-                             weight_offset: float = 0.0, stream=None):
+                             weight_offset: float = 0.0,
+                             gate_grad_dtype: Optional[torch.dtype] = None, stream=None):
     """Gradients of qmoe_block_norm from those of its out and normed (dnormed with pre_weight and
     only then), for what it was given and returned (out: needed with pre_weight; None where it
     would be y); residual: whether its gradient is wanted.  Returns (dy, dresidual, dgate,
     dpost_weight, dpre_weight), None for what there is not; the weights' and a token's or channel's
-    gate's gradients are fp32."""
+    gate's gradients are fp32, a full gate's is of y's dtype, or of the gate's own where
+    gate_grad_dtype says so (as autograd has it)."""
     if stream is not None:
         with _on(stream):
             return qmoe_block_norm_backward(
                 dout, dnormed, y, out=out, residual=residual, gate=gate, gating=gating,
                 post_weight=post_weight, pre_weight=pre_weight, post_rstd=post_rstd,
-                pre_rstd=pre_rstd, residual_scale=residual_scale, weight_offset=weight_offset)
+                pre_rstd=pre_rstd, residual_scale=residual_scale, weight_offset=weight_offset,
+                gate_grad_dtype=gate_grad_dtype)
+    own = gate_grad_dtype is not None and gate_grad_dtype != y.dtype
+    if own and (gate is None or gate_grad_dtype != gate.dtype):
+        raise ValueError(f"gate_grad_dtype: need y's or the gate's dtype, got {gate_grad_dtype}")
     return (operators._module or _native()).block_norm_backward(
         dout, dnormed, y, out, gate, gating, post_weight, pre_weight, residual_scale, weight_offset,
-        post_rstd, pre_rstd, residual, True, True, True)
+        post_rstd, pre_rstd, residual, True, True, True, own)
 
 
 # ---------------------------------------------------------------- checkpoints in 8 bits

@@ -136,6 +136,11 @@ int qmoe_block_norm_backward(const void* dout_dev, long long lddout, const void*
                              void* dresidual_dev, void* dgate_dev, float* dpost_weight_dev,
                              float* dpre_weight_dev, void* workspace_dev, size_t ws_bytes,
                              void* stream) {
+  int dgate_dtype = dtype;  // of a full gate's
+  if (gate_form == QMOE_GATE_FULL + QMOE_GATE_OWN_GRADIENT) {
+    gate_form = QMOE_GATE_FULL;
+    dgate_dtype = gate_dtype;
+  }
   const Gate g = {gate_dev, gate_dtype, gate_form, ldgate, gating};
   int rc = check_norm(dtype, M, H, g, post_weight_dev, pre_weight_dev, weight_dtype, residual_scale,
                       weight_offset);
@@ -170,7 +175,8 @@ int qmoe_block_norm_backward(const void* dout_dev, long long lddout, const void*
     return QMOE_ERR_ARG;
   if (misaligned(dout_dev, es) || misaligned(dnormed_dev, es) || misaligned(y_dev, es) ||
       misaligned(out_dev, es) || misaligned(dy_dev, es) || misaligned(dresidual_dev, es) ||
-      misaligned(dgate_dev, gate_form == QMOE_GATE_FULL ? es : 4) || misaligned(post_rstd_dev, 4) ||
+      misaligned(dgate_dev, gate_form == QMOE_GATE_FULL ? elem_size(dgate_dtype) : 4) ||
+      misaligned(post_rstd_dev, 4) ||
       misaligned(pre_rstd_dev, 4) || misaligned(workspace_dev, 256))
     return QMOE_ERR_ARG;
   if (ws_bytes < qmoe_block_norm_backward_workspace_size(M, H)) return QMOE_ERR_WORKSPACE;
@@ -204,6 +210,7 @@ int qmoe_block_norm_backward(const void* dout_dev, long long lddout, const void*
   a.dy = dy_dev;
   a.dresidual = dresidual_dev;
   a.dgate = dgate_dev;
+  a.dgate_fp32 = dgate_dtype == QMOE_DTYPE_FP32;
   a.dpost_weight = dpost_weight_dev;
   a.dpre_weight = dpre_weight_dev;
   a.partial = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(workspace_dev) + kWsHeaderBytes);
@@ -214,9 +221,12 @@ int qmoe_block_norm_backward(const void* dout_dev, long long lddout, const void*
   if (out_dev) chunk.rows(out_dev, ldout, H, es);
   chunk.rows(dy_dev, H, H, es);
   if (dresidual_dev) chunk.rows(dresidual_dev, H, H, es);
-  if (dgate_dev && gate_form == QMOE_GATE_FULL) chunk.rows(dgate_dev, H, H, es);
-  return cuda_rc(launch_norm_backward(
-      a, dtype, norm_chunk(dtype, H, g, post_weight_dev, pre_weight_dev, weight_dtype, chunk), s));
+  const bool dgate_rows = dgate_dev && gate_form == QMOE_GATE_FULL;
+  if (dgate_rows && dgate_dtype == dtype) chunk.rows(dgate_dev, H, H, es);
+  int n = norm_chunk(dtype, H, g, post_weight_dev, pre_weight_dev, weight_dtype, chunk);
+  if (dgate_rows)  // (n divides H)
+    while (n > 1 && misaligned(dgate_dev, vector_bytes(n, elem_size(dgate_dtype)))) n >>= 1;
+  return cuda_rc(launch_norm_backward(a, dtype, n, s));
 }
 
 static int check_checkpoint(int dtype, int M, int C) {

@@ -525,9 +525,10 @@ PyObject* block_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
 }
 
 // dout, dnormed, y, out, gate, gating, post_weight, pre_weight, residual_scale, weight_offset,
-// post_rstd, pre_rstd, which of the gradients are wanted: residual, gate, post_weight, pre_weight
+// post_rstd, pre_rstd, which of the gradients are wanted: residual, gate, post_weight, pre_weight;
+// whether a full gate's is of the gate's type (else of y's)
 PyObject* block_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded(n, 16, [&]() -> PyObject* {
+  return guarded(n, 17, [&]() -> PyObject* {
     Call c;
     const at::Tensor& y = tensor(a[2], "y");
     const long long ldy = c.rows(y, "y");
@@ -555,8 +556,9 @@ PyObject* block_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (s.pre.defined() != dnormed.defined()) fail("dnormed: goes with pre_weight");
     const at::Tensor dy = c.make(type, {s.M, s.H});
     if (truth(a[12])) dresidual = c.make(type, {s.M, s.H});
+    const bool own = s.gate_form == QMOE_GATE_FULL && truth(a[16]);
     if (truth(a[13]) && s.gate.defined())
-      dgate = s.gate_form == QMOE_GATE_FULL ? c.make(type, {s.M, s.H})
+      dgate = s.gate_form == QMOE_GATE_FULL ? c.make(own ? s.gate.scalar_type() : type, {s.M, s.H})
               : s.gate_form == QMOE_GATE_TOKEN ? c.make(at::kFloat, {s.M, 1})
                                                : c.make(at::kFloat, {1, s.H});
     if (truth(a[14]) && s.post.defined()) dpost = c.make(at::kFloat, {s.H});
@@ -566,10 +568,11 @@ PyObject* block_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     check_rc("qmoe_block_norm_backward",
              qmoe_block_norm_backward(
                  data(dout), ldd, data(dnormed), ldn, y.data_ptr(), s.type, ldy, data(out), ldo,
-                 (float)real(a[8]), data(s.gate), s.gate_type, s.gate_form, s.ldgate, s.gating,
-                 data(s.post), data(s.pre), s.weight_type, (float)real(a[9]),
-                 static_cast<float*>(data(rstd[0])), static_cast<float*>(data(rstd[1])), small(s.M),
-                 small(s.H), dy.data_ptr(), data(dresidual), data(dgate),
+                 (float)real(a[8]), data(s.gate), s.gate_type,
+                 s.gate_form + (own ? QMOE_GATE_OWN_GRADIENT : 0), s.ldgate, s.gating, data(s.post),
+                 data(s.pre), s.weight_type, (float)real(a[9]), static_cast<float*>(data(rstd[0])),
+                 static_cast<float*>(data(rstd[1])), small(s.M), small(s.H), dy.data_ptr(),
+                 data(dresidual), data(dgate),
                  static_cast<float*>(data(dpost)), static_cast<float*>(data(dpre)), ws.data_ptr(),
                  (size_t)ws.numel(), c.stream()));
     return pack_some({dy, dresidual, dgate, dpost, dpre});

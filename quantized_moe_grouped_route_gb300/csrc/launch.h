@@ -301,6 +301,7 @@ struct NormArgs {
   void* dy;  // gradients out, NULL where not wanted
   void* dresidual;
   void* dgate;
+  int dgate_fp32;  // of a full gate
   float* dpost_weight;
   float* dpre_weight;
   float* partial;  // [units][3][H]

@@ -95,6 +95,21 @@ __global__ void __launch_bounds__(ACC && VEC > 1 ? 512 : 1024) norm_backward_ker
       if (in[k]) *reinterpret_cast<raw_t*>(to + col[k]) = o.raw;
     }
   };
+  // ... to a matrix of fp32 beside 16-bit ones
+  auto put_fp32 = [&](void* base, int row, const float (&f)[kElems]) {
+    constexpr int kPart = VEC < 4 ? VEC : 4;
+    float* to = reinterpret_cast<float*>(base) + (size_t)row * a.H;
+#pragma unroll
+    for (int k = 0; k < NCH; ++k)
+#pragma unroll
+      for (int i = 0; i < VEC; i += kPart) {
+        Pack<float, kPart> o;
+#pragma unroll
+        for (int e = 0; e < kPart; ++e) o.v[e] = f[k * VEC + i + e];
+        if (in[k])
+          *reinterpret_cast<typename Pack<float, kPart>::raw_t*>(to + col[k] + i) = o.raw;
+      }
+  };
   // the matrices that a row is read from
   const int own_row = rows == 1 ? 0 : threadIdx.x >> 5;
   RowsIn<T, VEC, NCH, HOW, kMats> in_rows;
@@ -225,7 +240,12 @@ __global__ void __launch_bounds__(ACC && VEC > 1 ? 512 : 1024) norm_backward_ker
           add(GATED ? kGate : 0, k, p);
         }
       }
-      if (form == QMOE_GATE_FULL && a.dgate) put(a.dgate, row, dg);
+      if (form == QMOE_GATE_FULL && a.dgate) {
+        if (sizeof(T) == 2 && a.dgate_fp32)
+          put_fp32(a.dgate, row, dg);
+        else
+          put(a.dgate, row, dg);
+      }
     }
     if (summed) {
       const float by = GATED ? gate1 : 1.f;

@@ -51,6 +51,34 @@ def test_gradient_of_a_saturated_gate(M, H, form, dtype):
     _near(got, ref, bound + ROUND[k] * (ref.abs() + bound), "dgate")
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("M,H,pad", [(9, 256, 0), (33, 1001, 3), (2, 8200, 0), (400, 72, 0)])
+def test_a_full_gate_of_fp32_gets_its_gradient_in_fp32(M, H, pad, dtype):
+    """Values held in fp32 reach an fp32 gate unrounded: also those past fp16's largest number and
+    under its least."""
+    c = _case(M, H, dtype, gate="full", fp32=True, pre=False, pad=pad)
+    s = _norm_inputs(c, 6)
+    leaf = s["gate"].clone().requires_grad_(True)
+    out, _, post, pre = _norm_call(c, dict(s, gate=leaf))
+    dout = _rows(_gen(1), M, H, dtype, pad)
+    dout[0], dout[1] = 60000.0, 2.0 ** -24  # times v: past 65504 and under 2^-24 in some columns
+    out.backward(dout)
+    v = s["y"].double() * post.double()[:, None] * s["post"].double()
+    ref = dout.double() * v
+    assert ref.abs().max() > 65504 and leaf.grad.dtype == torch.float32
+    bound = 32 * U * ref.abs()
+    _near(leaf.grad, ref, bound, "dgate")
+    # the explicit call: in the activations' type, or the gate's by asking
+    own = _norm_backward(c, s, out.detach(), dout, None, post, pre, gate_grad_dtype=torch.float32)
+    assert torch.equal(own[2], leaf.grad)
+    plain = _norm_backward(c, s, out.detach(), dout, None, post, pre)
+    assert plain[2].dtype == dtype and torch.equal(plain[2], own[2].to(dtype))
+    for a, b in zip(own, plain):
+        assert a is own[2] or (a is None and b is None) or torch.equal(a, b)
+    with pytest.raises(ValueError):
+        _norm_backward(c, s, out.detach(), dout, None, post, pre, gate_grad_dtype=torch.float64)
+
+
 # --------------------------------------------------------- pre-activations past fp16's range
 @pytest.mark.parametrize("M,H", [(5, 64), (5, 4096), (200, 64), (700, 72)])
 @pytest.mark.parametrize("kind", ["silu", "gelu"])
