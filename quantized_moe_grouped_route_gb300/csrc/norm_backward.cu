@@ -85,7 +85,22 @@ __global__ void __launch_bounds__(ACC && VEC > 1 ? 512 : 1024) norm_backward_ker
       }
     }
   };
-  auto put = [&](void* base, int row, const float (&f)[kElems]) {
+  auto put = [&](void* base, int row, const float (&f)[kElems], bool fp32 = false) {
+    if (sizeof(T) == 2 && fp32) {  // (a gate's gradient beside 16-bit rows)
+      constexpr int kPart = VEC < 4 ? VEC : 4;
+      float* to = reinterpret_cast<float*>(base) + (size_t)row * a.H + tid * VEC;
+#pragma unroll
+      for (int k = 0; k < NCH; ++k)
+#pragma unroll
+        for (int i = 0; i < VEC; i += kPart) {
+          Pack<float, kPart> o;
+#pragma unroll
+          for (int e = 0; e < kPart; ++e) o.v[e] = f[k * VEC + i + e];
+          if (in[k])
+            *reinterpret_cast<typename Pack<float, kPart>::raw_t*>(to + k * threads * VEC + i) = o.raw;
+        }
+      return;
+    }
     T* to = reinterpret_cast<T*>(base) + (size_t)row * a.H;
 #pragma unroll
     for (int k = 0; k < NCH; ++k) {
@@ -94,21 +109,6 @@ __global__ void __launch_bounds__(ACC && VEC > 1 ? 512 : 1024) norm_backward_ker
       for (int e = 0; e < VEC; ++e) o.v[e] = from_f32<T>(f[k * VEC + e]);
       if (in[k]) *reinterpret_cast<raw_t*>(to + col[k]) = o.raw;
     }
-  };
-  // ... to a matrix of fp32 beside 16-bit ones
-  auto put_fp32 = [&](void* base, int row, const float (&f)[kElems]) {
-    constexpr int kPart = VEC < 4 ? VEC : 4;
-    float* to = reinterpret_cast<float*>(base) + (size_t)row * a.H;
-#pragma unroll
-    for (int k = 0; k < NCH; ++k)
-#pragma unroll
-      for (int i = 0; i < VEC; i += kPart) {
-        Pack<float, kPart> o;
-#pragma unroll
-        for (int e = 0; e < kPart; ++e) o.v[e] = f[k * VEC + i + e];
-        if (in[k])
-          *reinterpret_cast<typename Pack<float, kPart>::raw_t*>(to + col[k] + i) = o.raw;
-      }
   };
   // the matrices that a row is read from
   const int own_row = rows == 1 ? 0 : threadIdx.x >> 5;
@@ -209,11 +209,12 @@ __global__ void __launch_bounds__(ACC && VEC > 1 ? 512 : 1024) norm_backward_ker
       float dg[kElems];
 #pragma unroll
       for (int k = 0; k < NCH; ++k) {
-        float f[VEC], slope[VEC], w[VEC], y[VEC];
+        float f[VEC], w[VEC], y[VEC];
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) w[e] = 1.f;
+        if (post) vector(kPost, k, w);
         if (per_channel) {  // (its slope is one for all tokens: norm_sums_kernel multiplies by it)
           vector(kGate, k, f);
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) slope[e] = 1.f;
         } else {
           if (full_t) {
             chunk(GATED ? 4 : 0, k, f);
@@ -223,14 +224,17 @@ __global__ void __launch_bounds__(ACC && VEC > 1 ? 512 : 1024) norm_backward_ker
             if (in[k]) load_either<T, VEC>(a.gate, true, row * a.ldgate + col[k], f);
           }
 #pragma unroll
-          for (int e = 0; e < VEC; ++e) f[e] = gate_parts(a, f[e], &slope[e]);
+          for (int e = 0; e < VEC; ++e) {
+            float slope;
+            f[e] = gate_parts(a, f[e], &slope);
+            w[e] *= slope;
+          }
         }
-        if (post) vector(kPost, k, w);
         chunk(3, k, y);
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
           const int i = k * VEC + e;
-          dg[i] = g[i] * slope[e] * (y[e] * rstd) * (post ? w[e] : 1.f);
+          dg[i] = g[i] * (y[e] * rstd) * w[e];
           g[i] *= f[e];
         }
         if (per_channel) {
@@ -240,12 +244,7 @@ __global__ void __launch_bounds__(ACC && VEC > 1 ? 512 : 1024) norm_backward_ker
           add(GATED ? kGate : 0, k, p);
         }
       }
-      if (form == QMOE_GATE_FULL && a.dgate) {
-        if (sizeof(T) == 2 && a.dgate_fp32)
-          put_fp32(a.dgate, row, dg);
-        else
-          put(a.dgate, row, dg);
-      }
+      if (form == QMOE_GATE_FULL && a.dgate) put(a.dgate, row, dg, a.dgate_fp32 != 0);
     }
     if (summed) {
       const float by = GATED ? gate1 : 1.f;
@@ -321,8 +320,9 @@ __global__ void __launch_bounds__(kSumWarps * 32) norm_sums_kernel(const NormArg
   if (!dst) return;
   const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
   const int h = blockIdx.x * 32 + lane;
-  float s = 0.f;
+  float s = 0.f, gate[1] = {0.f}, slope = 1.f;
   if (h < H) {
+    if (which == kGate && slice == 0) load_either<T, 1>(a.gate, a.gate_fp32, h, gate);
     const float* src = a.partial + (size_t)which * H + h;
 #pragma unroll 8
     for (int u = slice; u < a.units; u += kSumWarps) s += src[(size_t)u * 3 * H];
@@ -333,13 +333,8 @@ __global__ void __launch_bounds__(kSumWarps * 32) norm_sums_kernel(const NormArg
   s = 0.f;
 #pragma unroll
   for (int i = 0; i < kSumWarps; ++i) s += part[i][lane];
-  if (which == kGate) {
-    float one[1], slope;
-    load_either<T, 1>(a.gate, a.gate_fp32, h, one);
-    gate_parts(a, one[0], &slope);
-    s *= slope;
-  }
-  dst[h] = s;
+  if (which == kGate) gate_parts(a, gate[0], &slope);
+  dst[h] = s * slope;
 }
 
 template <class T>
