@@ -13,10 +13,12 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/core/AutogradState.h>
 #include <c10/core/GradMode.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
+#include <torch/csrc/autograd/forward_grad.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <array>
@@ -200,11 +202,26 @@ PyObject* pack(std::initializer_list<at::Tensor> ts) {
   return r;
 }
 
+// No call has a derivative in forward mode: a tangent is refused, not dropped.
+bool carries_tangent(PyObject* const* a, Py_ssize_t n) {
+  if (!c10::AutogradState::get_tls_state().get_fw_grad_mode() ||
+      !torch::autograd::ForwardADLevel::try_get_by_idx(0))
+    return false;
+  for (Py_ssize_t i = 0; i < n; ++i)
+    if (THPVariable_Check(a[i]) && THPVariable_Unpack(a[i])._fw_grad(0).defined()) return true;
+  return false;
+}
+
 template <class F>
-PyObject* guarded(Py_ssize_t given, Py_ssize_t wanted, F&& body) {
+PyObject* guarded(PyObject* const* a, Py_ssize_t given, Py_ssize_t wanted, F&& body) {
   HANDLE_TH_ERRORS
   if (given != wanted) {
     PyErr_SetString(PyExc_TypeError, "wrong number of arguments");
+    return nullptr;
+  }
+  if (carries_tangent(a, given)) {
+    PyErr_SetString(PyExc_NotImplementedError,
+                    "no derivative in forward mode: call it on tensors without a tangent");
     return nullptr;
   }
   try {
@@ -217,7 +234,7 @@ PyObject* guarded(Py_ssize_t given, Py_ssize_t wanted, F&& body) {
 
 // logits, top_k, scoring, bias, n_group, topk_group, renormalize, scale, ids, weights
 PyObject* gate(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded(n, 10, [&]() -> PyObject* {
+  return guarded(a, n, 10, [&]() -> PyObject* {
     if (c10::GradMode::is_enabled() && needs_gradient(a[0]))
       return in_graph("gate", a, n);
     Call c;
@@ -246,7 +263,7 @@ PyObject* gate(PyObject*, PyObject* const* a, Py_ssize_t n) {
 
 // dweights, logits, ids, scoring, renormalize, scale, dlogits
 PyObject* gate_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded(n, 7, [&]() -> PyObject* {
+  return guarded(a, n, 7, [&]() -> PyObject* {
     Call c;
     const at::Tensor& logits = tensor(a[1], "logits");
     const long long ld = c.rows(logits, "logits");
@@ -269,7 +286,7 @@ PyObject* gate_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
 
 // x, ids, E, xs, workspace
 PyObject* sort_tokens(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded(n, 5, [&]() -> PyObject* {
+  return guarded(a, n, 5, [&]() -> PyObject* {
     if (c10::GradMode::is_enabled() && needs_gradient(a[0]))
       return in_graph("sort_tokens", a, n);
     Call c;
@@ -299,7 +316,7 @@ PyObject* sort_tokens(PyObject*, PyObject* const* a, Py_ssize_t n) {
 
 // dxs, pair_pos, dx
 PyObject* sort_tokens_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded(n, 3, [&]() -> PyObject* {
+  return guarded(a, n, 3, [&]() -> PyObject* {
     Call c;
     const at::Tensor& y = tensor(a[0], "dxs");
     const at::Tensor& pos = tensor(a[1], "pair_pos");
@@ -318,7 +335,7 @@ PyObject* sort_tokens_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
 
 // y, pair_pos, weights, out
 PyObject* unsort_tokens(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded(n, 4, [&]() -> PyObject* {
+  return guarded(a, n, 4, [&]() -> PyObject* {
     if (c10::GradMode::is_enabled() && (needs_gradient(a[0]) || needs_gradient(a[2])))
       return in_graph("unsort_tokens", a, n);
     Call c;
@@ -341,7 +358,7 @@ PyObject* unsort_tokens(PyObject*, PyObject* const* a, Py_ssize_t n) {
 
 // dout, y, sorted_pair, pair_pos, weights, dy, dweights
 PyObject* unsort_tokens_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded(n, 7, [&]() -> PyObject* {
+  return guarded(a, n, 7, [&]() -> PyObject* {
     Call c;
     const at::Tensor& dout = tensor(a[0], "dout");
     const at::Tensor& y = tensor(a[1], "y");
@@ -370,7 +387,7 @@ PyObject* unsort_tokens_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
 
 // x, w, lora_a, lora_b, ids, scales, base, out, workspace
 PyObject* lora_linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded(n, 9, [&]() -> PyObject* {
+  return guarded(a, n, 9, [&]() -> PyObject* {
     if (c10::GradMode::is_enabled())
       for (int i : {0, 1, 2, 3, 5, 6})  // x, w, lora_a, lora_b, scales, base
         if (needs_gradient(a[i])) return in_graph("lora_linear", a, n);
@@ -486,7 +503,7 @@ struct Norms {
 // y, residual, gate, gating, post_weight, pre_weight, residual_scale, weight_offset, eps, out,
 // normed
 PyObject* block_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded(n, 11, [&]() -> PyObject* {
+  return guarded(a, n, 11, [&]() -> PyObject* {
     if (c10::GradMode::is_enabled())
       for (int i : {0, 1, 2, 4, 5})
         if (needs_gradient(a[i])) return in_graph("block_norm", a, n);
@@ -528,7 +545,7 @@ PyObject* block_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
 // post_rstd, pre_rstd, which of the gradients are wanted: residual, gate, post_weight, pre_weight;
 // whether a full gate's is of the gate's type (else of y's)
 PyObject* block_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded(n, 17, [&]() -> PyObject* {
+  return guarded(a, n, 17, [&]() -> PyObject* {
     Call c;
     const at::Tensor& y = tensor(a[2], "y");
     const long long ldy = c.rows(y, "y");
@@ -581,7 +598,7 @@ PyObject* block_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
 
 // x, codes, scales
 PyObject* checkpoint8(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded(n, 3, [&]() -> PyObject* {
+  return guarded(a, n, 3, [&]() -> PyObject* {
     Call c;
     const at::Tensor& x = tensor(a[0], "x");
     const long long ldx = c.rows(x, "x");
@@ -606,7 +623,7 @@ const int8_t* codes_of(Call& c, const at::Tensor& codes, const at::Tensor& scale
 
 // codes, scales, an empty tensor of the wanted type, out
 PyObject* checkpoint8_restore(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded(n, 4, [&]() -> PyObject* {
+  return guarded(a, n, 4, [&]() -> PyObject* {
     Call c;
     const at::Tensor& codes = tensor(a[0], "codes");
     const at::Tensor& scales = tensor(a[1], "scales");
@@ -646,7 +663,7 @@ struct Ffn {
 // x, w13, w2, activation, limit, what is kept (0: nothing, 16, 8), out, workspace, what a node of
 // autograd's graph keeps (16, 8; 0: this call is none)
 PyObject* gated_ffn(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded(n, 9, [&]() -> PyObject* {
+  return guarded(a, n, 9, [&]() -> PyObject* {
     if (c10::GradMode::is_enabled() && integer(a[8]) != 0)
       for (int i : {0, 1, 2})  // x, w13, w2
         if (needs_gradient(a[i])) return in_graph("gated_ffn", a, n);
@@ -683,7 +700,7 @@ PyObject* gated_ffn(PyObject*, PyObject* const* a, Py_ssize_t n) {
 // dout, x or its codes, x's scales or None, w13, w2, kept, kept's scales or None, activation, limit,
 // which of the gradients are wanted: x, w13, w2; workspace
 PyObject* gated_ffn_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded(n, 13, [&]() -> PyObject* {
+  return guarded(a, n, 13, [&]() -> PyObject* {
     Call c;
     const at::Tensor& dout = tensor(a[0], "dout");
     const at::Tensor& x = tensor(a[1], "x");
@@ -726,8 +743,8 @@ PyObject* gated_ffn_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
 }
 
 // The kept workspaces of the current device.
-PyObject* default_workspaces(PyObject*, PyObject* const*, Py_ssize_t n) {
-  return guarded(n, 0, [&]() -> PyObject* {
+PyObject* default_workspaces(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(a, n, 0, [&]() -> PyObject* {
     Call c;
     c.dev = c10::cuda::current_device();
     PyObject* r = PyList_New(0);
