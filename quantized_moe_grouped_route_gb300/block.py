@@ -6,8 +6,9 @@ Tensors, streams, workspaces and errors as in operators.py.  A matrix's rows may
 gated feed-forward block wants them 16-byte aligned.
 
 Autograd: qmoe_block_norm and qmoe_gated_ffn on tensors that require a gradient are nodes of its
-graph, whose backward is the *_backward call of the same name (those calls, qmoe_gated_ffn_saved
-and the checkpoints have no derivative of their own).  Such a call takes no outputs to write into.
+graph, whose backward is the *_backward call of the same name (those calls and the checkpoints have
+no derivative of their own).  qmoe_gated_ffn_saved leaves the backward pass to its caller: a gradient
+that comes to its output raises NotImplementedError.  Such a call takes no outputs to write into.
 A backward pass that is captured into a CUDA graph must find no eager graph of the same leaves
 alive: PyTorch would have it wait for the eager one's stream, which a capture cannot.
 """
@@ -80,6 +81,19 @@ class _GatedFfn(torch.autograd.Function):
         return (dx, dw13, dw2) + 6 * (None,)
 
 
+class _GatedFfnSaved(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, *args):
+        out, *kept = _native().gated_ffn(*args)
+        ctx.mark_non_differentiable(*(t for t in kept if t is not None))
+        return (out, *kept)
+
+    @staticmethod
+    def backward(ctx, *_):
+        raise NotImplementedError("qmoe_gated_ffn_saved leaves the backward pass to its caller: call it "
+                                  "under torch.no_grad() or on detached tensors, or qmoe_gated_ffn")
+
+
 def _aligned(t: torch.Tensor) -> torch.Tensor:
     """A gradient as the gated block takes rows: 16-byte aligned, and each its own."""
     t = _rows(t)
@@ -89,7 +103,8 @@ def _aligned(t: torch.Tensor) -> torch.Tensor:
 
 
 # of each call the node, and which of its arguments are outputs
-operators._NODES.update({"block_norm": (_BlockNorm, (9, 10)), "gated_ffn": (_GatedFfn, (6,))})
+operators._NODES.update({"block_norm": (_BlockNorm, (9, 10)), "gated_ffn": (_GatedFfn, (6,)),
+                         "gated_ffn_saved": (_GatedFfnSaved, (6,))})
 
 
 # --------------------------------------------------------------- norms around a block
@@ -211,7 +226,9 @@ def qmoe_gated_ffn_saved(x: torch.Tensor, w13: torch.Tensor, w2: torch.Tensor, *
                          workspace: Optional[torch.Tensor] = None, stream=None):
     """qmoe_gated_ffn that also returns what its backward pass needs: (out, saved).  checkpoint 16:
     saved = (u beside g [M][2I],), and x itself is needed too; 8: (codes and scales of u beside
-    g, codes and scales of x), without x."""
+    g, codes and scales of x), without x.  The backward pass is the caller's
+    (qmoe_gated_ffn_backward): outside torch.no_grad(), on tensors that require a gradient, a
+    gradient that comes to out raises."""
     if stream is not None:
         with _on(stream):
             return qmoe_gated_ffn_saved(x, w13, w2, activation=activation, limit=limit,

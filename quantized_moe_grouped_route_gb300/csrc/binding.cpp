@@ -661,12 +661,13 @@ struct Ffn {
 };
 
 // x, w13, w2, activation, limit, what is kept (0: nothing, 16, 8), out, workspace, what a node of
-// autograd's graph keeps (16, 8; 0: this call is none)
+// autograd's graph keeps (16, 8; 0: its backward pass is its caller's)
 PyObject* gated_ffn(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(a, n, 9, [&]() -> PyObject* {
-    if (c10::GradMode::is_enabled() && integer(a[8]) != 0)
+    if (c10::GradMode::is_enabled())
       for (int i : {0, 1, 2})  // x, w13, w2
-        if (needs_gradient(a[i])) return in_graph("gated_ffn", a, n);
+        if (needs_gradient(a[i]))
+          return in_graph(integer(a[8]) != 0 ? "gated_ffn" : "gated_ffn_saved", a, n);
     Call c;
     const at::Tensor& x = tensor(a[0], "x");
     const at::Tensor& w13 = tensor(a[1], "w13");

@@ -56,3 +56,26 @@ def test_tangents_are_refused(name):
             with guard, pytest.raises(NotImplementedError):
                 call(dual)
     call(t)
+
+
+@pytest.mark.parametrize("bits", [16, 8])
+@pytest.mark.parametrize("which", range(3))
+def test_the_saved_form_has_no_gradient_and_says_so(which, bits):
+    """Its backward pass is its caller's: a gradient that comes to its output raises, as
+    qmoe_lora_linear's does, and is not lost."""
+    args = [torch.randn(s, **KW) for s in ((5, 64), (48, 64), (64, 24))]
+    want, kept = q.qmoe_gated_ffn_saved(*args, checkpoint=bits)
+    assert not want.requires_grad
+    args[which].requires_grad_(True)
+    out, saved = q.qmoe_gated_ffn_saved(*args, checkpoint=bits)
+    assert torch.equal(out, want) and out.requires_grad
+    assert not any(t.requires_grad for t in saved)
+    for a, b in zip(saved, kept):
+        assert torch.equal(a, b)
+    with pytest.raises(NotImplementedError):
+        out.sum().backward()
+    with pytest.raises(ValueError):
+        q.qmoe_gated_ffn_saved(*args, checkpoint=bits, out=torch.empty_like(want))
+    with torch.no_grad():
+        out, _ = q.qmoe_gated_ffn_saved(*args, checkpoint=bits, out=torch.empty_like(want))
+    assert torch.equal(out, want) and not out.requires_grad
