@@ -120,7 +120,10 @@ constexpr int kDevices = 64;
 
 // The device of a call: every tensor has to be on the current one.
 struct Call {
+  static constexpr int kMostOutputs = 4;
   c10::DeviceIndex dev = -1;
+  c10::TensorImpl* into[kMostOutputs];  // given outputs
+  int written = 0;
   void here(const at::Tensor& t, const char* name) {
     if (t.is_cuda()) {
       if (dev < 0) dev = c10::cuda::current_device();
@@ -164,7 +167,20 @@ struct Call {
     if (o == Py_None) return make(type, shape);
     const at::Tensor& t = tensor(o, name);
     dense(t, type, name, shape);
+    // its history would stand for values that are no longer there
+    if (c10::GradMode::is_enabled() && t.requires_grad())
+      fail(std::string(name) + ": an output to write into cannot require a gradient (or call it "
+                               "under torch.no_grad())");
+    if (written == kMostOutputs) fail("too many outputs");
+    into[written++] = t.unsafeGetTensorImpl();
     return t;
+  }
+  // The library's answer to the call; where it was taken, autograd is told of the outputs that were
+  // written into, so that a node that has kept one of them does not take it for what it was.
+  void answer(const char* fn, int rc) {
+    check_rc(fn, rc);
+    for (int i = 0; i < written; ++i)
+      if (!into[i]->is_inference()) into[i]->bump_version();
   }
   at::Tensor space(PyObject* o, size_t bytes, Kept which) {
     if (o == Py_None) {
@@ -252,7 +268,7 @@ PyObject* gate(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (k < 1 || k > 64) check_rc("moe_gate", QMOE_ERR_SHAPE);
     const at::Tensor ids = c.out(a[8], at::kInt, "topk_ids", {M, k});
     const at::Tensor w = c.out(a[9], at::kFloat, "topk_weights", {M, k});
-    check_rc("moe_gate",
+    c.answer("moe_gate",
              moe_gate(logits.data_ptr(), dtype_code(logits.scalar_type()), ld, small(M), small(E),
                       (int)k, small(integer(a[2])), bias, small(integer(a[4])),
                       small(integer(a[5])), truth(a[6]), (float)scale, i32_out(ids),
@@ -276,7 +292,7 @@ PyObject* gate_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const double scale = PyFloat_AsDouble(a[5]);
     if (PyErr_Occurred()) throw Raised{};
     const at::Tensor dl = c.out(a[6], logits.scalar_type(), "dlogits", {M, E});
-    check_rc("moe_gate_backward",
+    c.answer("moe_gate_backward",
              moe_gate_backward(f32(dw), logits.data_ptr(), dtype_code(logits.scalar_type()), ld,
                                i32(ids), small(M), small(E), small(k), small(integer(a[3])),
                                truth(a[4]), (float)scale, dl.data_ptr(), c.stream()));
@@ -304,7 +320,7 @@ PyObject* sort_tokens(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const at::Tensor pos = c.make(at::kInt, {M, k});
     const at::Tensor ws =
         c.space(a[4], qmoe_sort_workspace_size(small(M), small(k), (int)E), kSort);
-    check_rc("moe_sort_tokens",
+    c.answer("moe_sort_tokens",
              moe_sort_tokens(x.data_ptr(), dtype_code(x.scalar_type()), ldx, i32(ids), small(M),
                              small(H), small(k), (int)E, xs.data_ptr(), i32_out(offsets),
                              i32_out(pair), i32_out(pos), ws.data_ptr(), (size_t)ws.numel(),
@@ -326,7 +342,7 @@ PyObject* sort_tokens_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int64_t H = y.size(1);
     if (y.size(0) != M * k) fail_shape("dxs", {M * k, H}, y.sizes());
     const at::Tensor dx = c.out(a[2], y.scalar_type(), "dx", {M, H});
-    check_rc("moe_sort_tokens_backward",
+    c.answer("moe_sort_tokens_backward",
              moe_sort_tokens_backward(y.data_ptr(), dtype_code(y.scalar_type()), ld, i32(pos),
                                       small(M), small(H), small(k), dx.data_ptr(), c.stream()));
     return THPVariable_Wrap(dx);
@@ -349,7 +365,7 @@ PyObject* unsort_tokens(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int64_t H = y.size(1);
     if (y.size(0) != M * k) fail_shape("y", {M * k, H}, y.sizes());
     const at::Tensor out = c.out(a[3], y.scalar_type(), "out", {M, H});
-    check_rc("moe_unsort_tokens",
+    c.answer("moe_unsort_tokens",
              moe_unsort_tokens(y.data_ptr(), dtype_code(y.scalar_type()), ld, i32(pos), f32(w),
                                small(M), small(H), small(k), out.data_ptr(), c.stream()));
     return THPVariable_Wrap(out);
@@ -376,7 +392,7 @@ PyObject* unsort_tokens_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (dout.scalar_type() != y.scalar_type()) fail("dout, y: need one dtype");
     const at::Tensor dy = c.out(a[5], y.scalar_type(), "dy", {M * k, H});
     const at::Tensor dw = c.out(a[6], at::kFloat, "dweights", {M, k});
-    check_rc("moe_unsort_tokens_backward",
+    c.answer("moe_unsort_tokens_backward",
              moe_unsort_tokens_backward(dout.data_ptr(), ldd, y.data_ptr(), ldy,
                                         dtype_code(y.scalar_type()), i32(pair), i32(pos), f32(w),
                                         small(M), small(H), small(k), dy.data_ptr(), f32(dw),
@@ -421,7 +437,7 @@ PyObject* lora_linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const at::Tensor out = c.out(a[7], type, "out", {M, N});
     const at::Tensor ws = c.space(
         a[8], qmoe_lora_workspace_size(small(M), small(K), small(N), small(R), small(L)), kLora);
-    check_rc("qmoe_lora_linear",
+    c.answer("qmoe_lora_linear",
              qmoe_lora_linear(x.data_ptr(), dtype_code(type), ldx, w, A.data_ptr(), B.data_ptr(),
                               i32(ids), f32(scales), base, ldb, out.data_ptr(), small(M), small(K),
                               small(N), small(R), small(L), ws.data_ptr(), (size_t)ws.numel(),
@@ -530,7 +546,7 @@ PyObject* block_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
       pre_rstd = c.make(at::kFloat, {s.M});
     }
     if (s.post.defined()) post_rstd = c.make(at::kFloat, {s.M});
-    check_rc("qmoe_block_norm",
+    c.answer("qmoe_block_norm",
              qmoe_block_norm(y.data_ptr(), s.type, ldy, data(residual), ldr, (float)real(a[6]),
                              data(s.gate), s.gate_type, s.gate_form, s.ldgate, s.gating,
                              data(s.post), data(s.pre), s.weight_type, (float)real(a[7]),
@@ -582,7 +598,7 @@ PyObject* block_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (truth(a[15]) && s.pre.defined()) dpre = c.make(at::kFloat, {s.H});
     const size_t bytes = qmoe_block_norm_backward_workspace_size(small(s.M), small(s.H));
     const at::Tensor ws = c.make(at::kByte, {(int64_t)(bytes < 256 ? 256 : bytes)});
-    check_rc("qmoe_block_norm_backward",
+    c.answer("qmoe_block_norm_backward",
              qmoe_block_norm_backward(
                  data(dout), ldd, data(dnormed), ldn, y.data_ptr(), s.type, ldy, data(out), ldo,
                  (float)real(a[8]), data(s.gate), s.gate_type,
@@ -605,7 +621,7 @@ PyObject* checkpoint8(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int64_t M = x.size(0), C = x.size(1);
     const at::Tensor codes = c.out(a[1], at::kChar, "codes", {M, C});
     const at::Tensor scales = c.out(a[2], at::kByte, "scales", {M, (C + 31) / 32});
-    check_rc("qmoe_checkpoint8",
+    c.answer("qmoe_checkpoint8",
              qmoe_checkpoint8(x.data_ptr(), dtype_code(x.scalar_type()), ldx, small(M), small(C),
                               static_cast<int8_t*>(codes.data_ptr()),
                               static_cast<uint8_t*>(scales.data_ptr()), c.stream()));
@@ -633,7 +649,7 @@ PyObject* checkpoint8_restore(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const at::ScalarType type = tensor(a[2], "dtype").scalar_type();
     if (dtype_code(type) < 0) fail("dtype: need bf16, fp16 or fp32");
     const at::Tensor out = c.out(a[3], type, "out", {M, C});
-    check_rc("qmoe_checkpoint8_restore",
+    c.answer("qmoe_checkpoint8_restore",
              qmoe_checkpoint8_restore(p, static_cast<const uint8_t*>(scales.data_ptr()),
                                       dtype_code(type), small(M), small(C), out.data_ptr(),
                                       c.stream()));
@@ -686,7 +702,7 @@ PyObject* gated_ffn(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const at::Tensor out = c.out(a[6], f.type, "out", {M, f.H});
     const at::Tensor ws =
         c.space(a[7], qmoe_gated_ffn_workspace_size(small(M), small(f.H), small(f.I)), kFfn);
-    check_rc("qmoe_gated_ffn",
+    c.answer("qmoe_gated_ffn",
              qmoe_gated_ffn(x.data_ptr(), dtype_code(f.type), ldx, w13.data_ptr(), w2.data_ptr(),
                             small(integer(a[3])), (float)real(a[4]), small(M), small(f.H),
                             small(f.I), out.data_ptr(), data(kept),
@@ -731,7 +747,7 @@ PyObject* gated_ffn_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const at::Tensor ws = c.space(
         a[12], qmoe_gated_ffn_backward_workspace_size(small(M), small(f.H), small(f.I),
                                                       xs.defined() ? 8 : 16), kFfnBackward);
-    check_rc("qmoe_gated_ffn_backward",
+    c.answer("qmoe_gated_ffn_backward",
              qmoe_gated_ffn_backward(dout.data_ptr(), dtype_code(f.type), ldd, x.data_ptr(), ldx,
                                      static_cast<uint8_t*>(data(xs)), w13.data_ptr(), w2.data_ptr(),
                                      kept.data_ptr(), static_cast<uint8_t*>(data(ks)),

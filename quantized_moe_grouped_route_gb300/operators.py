@@ -14,8 +14,10 @@ calls that were given none in qmoe_default_read_error.
 Autograd: moe_gate, moe_sort_tokens and moe_unsort_tokens on tensors that require a gradient
 are nodes of its graph, whose backward is the *_backward call of the same name (those calls
 have no derivative of their own); qmoe_lora_linear has none, and a gradient that comes to it
-raises NotImplementedError.  Such a call takes no outputs to write into.  None has a derivative in
-forward mode: a tensor that carries a tangent raises NotImplementedError, grad mode or not.
+raises NotImplementedError.  Such a call takes no outputs to write into.  An output that is given
+counts as changed in place (a node that has kept it raises) and may itself require a gradient under
+torch.no_grad() alone.  None has a derivative in forward mode: a tensor that carries a tangent
+raises NotImplementedError, grad mode or not.
 
 Checks, allocations and the call itself are compiled (csrc/binding.cpp, qmoe_torch.so).
 """

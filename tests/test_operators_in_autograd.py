@@ -6,6 +6,7 @@ import torch
 import torch.autograd.forward_ad as fw
 
 import quantized_moe_grouped_route_gb300 as q
+from quantized_moe_grouped_route_gb300 import qmoe
 
 pytestmark = pytest.mark.gpu
 
@@ -79,3 +80,58 @@ def test_the_saved_form_has_no_gradient_and_says_so(which, bits):
     with torch.no_grad():
         out, _ = q.qmoe_gated_ffn_saved(*args, checkpoint=bits, out=torch.empty_like(want))
     assert torch.equal(out, want) and not out.requires_grad
+
+
+@pytest.mark.parametrize("name", ["norm", "norm_normed", "checkpoint", "restore", "ffn", "lora", "gate",
+                                  "sort", "unsort"])
+def test_an_output_that_autograd_has_saved(name):
+    """A tensor that a node keeps for its backward pass and a call then writes into: the backward pass
+    raises, as after any operation in place, in place of a gradient of other values."""
+    t = torch.ones
+    ids = torch.zeros(4, 2, dtype=torch.int32, device="cuda")
+    pos = torch.arange(8, dtype=torch.int32, device="cuda").view(4, 2)
+    x, w = t(4, 64, **KW), t(64, **KW)
+    one = torch.zeros(4, dtype=torch.int32, device="cuda")
+    codes, scales = q.qmoe_checkpoint8(x)
+    into = {"gate": t(4, 2, device="cuda"), "sort": t(8, 64, **KW), "checkpoint": codes}.get(
+        name, t(4, 64, **KW))
+    calls = {
+        "norm": lambda o: q.qmoe_block_norm(x, residual=o, post_weight=w, out=o),
+        "norm_normed": lambda o: q.qmoe_block_norm(x, pre_weight=w, normed=o),
+        "checkpoint": lambda o: q.qmoe_checkpoint8(x, codes=o),
+        "restore": lambda o: q.qmoe_checkpoint8_restore(codes, scales, out=o),
+        "ffn": lambda o: q.qmoe_gated_ffn(x, t(48, 64, **KW), t(64, 24, **KW), out=o),
+        "lora": lambda o: q.qmoe_lora_linear(x, None, t(1, 8, 64, **KW), t(1, 64, 8, **KW), one,
+                                             t(1, device="cuda"), base=o, out=o),
+        "gate": lambda o: q.moe_gate(x, 2, topk_weights=o),
+        "sort": lambda o: q.moe_sort_tokens(x, ids, 3, xs=o),
+        "unsort": lambda o: q.moe_unsort_tokens(t(8, 64, **KW), pos, t(4, 2, device="cuda"), out=o),
+    }
+    call = calls[name]
+    leaf = torch.ones(into.shape, device="cuda", requires_grad=True)
+    product = leaf * into  # keeps `into`
+    call(into)
+    with pytest.raises(RuntimeError, match="inplace"):
+        product.sum().backward()
+    # (a refused call has written nothing)
+    product, version = leaf * into, into._version
+    with pytest.raises((ValueError, qmoe.QmoeError)):
+        call(into[1:])
+    assert into._version == version
+    product.sum().backward()
+    with torch.inference_mode():  # tensors without a version
+        call(torch.ones_like(into))
+
+
+def test_an_output_that_requires_a_gradient():
+    """What would take the place of its history's values is refused, but under torch.no_grad()."""
+    x, w = torch.randn(4, 64, **KW), torch.randn(64, **KW)
+    leaf = torch.ones(4, 64, **KW).requires_grad_(True)
+    for out in (leaf, leaf * 2):
+        with pytest.raises(ValueError):
+            q.qmoe_block_norm(x, post_weight=w, out=out)
+        with pytest.raises(ValueError):
+            q.qmoe_block_norm(x, pre_weight=w, normed=out)
+        with torch.no_grad():
+            assert torch.equal(q.qmoe_block_norm(x, post_weight=w, out=out)[0],
+                               q.qmoe_block_norm(x, post_weight=w)[0])
