@@ -516,6 +516,12 @@ int qmoe_gated_ffn(const void* x_dev, int dtype, long long ldx, const void* w13_
                    const void* w2_dev, int activation, float limit, int M, int H, int I,
                    void* out_dev, void* kept_dev, uint8_t* kept_scales_dev, void* workspace_dev,
                    size_t ws_bytes, void* stream);
+/* ... with the error word at error_dev (4 bytes, 4-byte aligned) in place of the workspace's start,
+ * so that the workspace need not outlast the call for it. */
+int qmoe_gated_ffn_error_at(const void* x_dev, int dtype, long long ldx, const void* w13_dev,
+                            const void* w2_dev, int activation, float limit, int M, int H, int I,
+                            void* out_dev, void* kept_dev, uint8_t* kept_scales_dev,
+                            void* workspace_dev, size_t ws_bytes, uint32_t* error_dev, void* stream);
 
 /*
  * qmoe_gated_ffn_backward — gradients of qmoe_gated_ffn from what it kept:
@@ -540,6 +546,14 @@ int qmoe_gated_ffn_backward(const void* dout_dev, int dtype, long long lddout, c
                             const uint8_t* kept_scales_dev, int activation, float limit, int M,
                             int H, int I, void* dx_dev, void* dw13_dev, void* dw2_dev,
                             void* workspace_dev, size_t ws_bytes, void* stream);
+/* ... with the error word at error_dev, as above. */
+int qmoe_gated_ffn_backward_error_at(const void* dout_dev, int dtype, long long lddout,
+                                     const void* x_dev, long long ldx, const uint8_t* x_scales_dev,
+                                     const void* w13_dev, const void* w2_dev, const void* kept_dev,
+                                     const uint8_t* kept_scales_dev, int activation, float limit,
+                                     int M, int H, int I, void* dx_dev, void* dw13_dev, void* dw2_dev,
+                                     void* workspace_dev, size_t ws_bytes, uint32_t* error_dev,
+                                     void* stream);
 
 #ifdef __cplusplus
 }

@@ -314,12 +314,24 @@ int qmoe_gated_ffn(const void* x_dev, int dtype, long long ldx, const void* w13_
                    const void* w2_dev, int activation, float limit, int M, int H, int I,
                    void* out_dev, void* kept_dev, uint8_t* kept_scales_dev, void* workspace_dev,
                    size_t ws_bytes, void* stream) {
+  return qmoe_gated_ffn_error_at(x_dev, dtype, ldx, w13_dev, w2_dev, activation, limit, M, H, I,
+                                 out_dev, kept_dev, kept_scales_dev, workspace_dev, ws_bytes,
+                                 reinterpret_cast<uint32_t*>(workspace_dev), stream);
+}
+
+int qmoe_gated_ffn_error_at(const void* x_dev, int dtype, long long ldx, const void* w13_dev,
+                            const void* w2_dev, int activation, float limit, int M, int H, int I,
+                            void* out_dev, void* kept_dev, uint8_t* kept_scales_dev,
+                            void* workspace_dev, size_t ws_bytes, uint32_t* error_dev,
+                            void* stream) {
   int rc = check_ffn(dtype, M, H, I, activation, limit);
   if (rc != QMOE_OK) return rc;
   if (ldx < H || ldx % 8) return QMOE_ERR_SHAPE;
   if (kept_scales_dev && !kept_dev) return QMOE_ERR_ARG;
   if (M == 0) return QMOE_OK;
-  if (!x_dev || !w13_dev || !w2_dev || !out_dev || !workspace_dev) return QMOE_ERR_ARG;
+  if (!x_dev || !w13_dev || !w2_dev || !out_dev || !workspace_dev || !error_dev ||
+      misaligned(error_dev, 4))
+    return QMOE_ERR_ARG;
   if (misaligned(x_dev, 16) || misaligned(w13_dev, 16) || misaligned(w2_dev, 16) ||
       misaligned(out_dev, 16) || misaligned(kept_dev, 16) || misaligned(workspace_dev, 256))
     return QMOE_ERR_ARG;
@@ -346,7 +358,7 @@ int qmoe_gated_ffn(const void* x_dev, int dtype, long long ldx, const void* w13_
   up.scales = kept_scales_dev;
   up.activation = activation;
   up.limit = limit;
-  up.err = reinterpret_cast<unsigned int*>(ws);
+  up.err = error_dev;
   up.clear_err = 1;
   up.part = reinterpret_cast<float*>(ws + ffn_forward_part(M, I));
   auto launch = [&](const FfnProduct& f) {
@@ -403,6 +415,19 @@ int qmoe_gated_ffn_backward(const void* dout_dev, int dtype, long long lddout, c
                             const uint8_t* kept_scales_dev, int activation, float limit, int M,
                             int H, int I, void* dx_dev, void* dw13_dev, void* dw2_dev,
                             void* workspace_dev, size_t ws_bytes, void* stream) {
+  return qmoe_gated_ffn_backward_error_at(
+      dout_dev, dtype, lddout, x_dev, ldx, x_scales_dev, w13_dev, w2_dev, kept_dev, kept_scales_dev,
+      activation, limit, M, H, I, dx_dev, dw13_dev, dw2_dev, workspace_dev, ws_bytes,
+      reinterpret_cast<uint32_t*>(workspace_dev), stream);
+}
+
+int qmoe_gated_ffn_backward_error_at(const void* dout_dev, int dtype, long long lddout,
+                                     const void* x_dev, long long ldx, const uint8_t* x_scales_dev,
+                                     const void* w13_dev, const void* w2_dev, const void* kept_dev,
+                                     const uint8_t* kept_scales_dev, int activation, float limit,
+                                     int M, int H, int I, void* dx_dev, void* dw13_dev, void* dw2_dev,
+                                     void* workspace_dev, size_t ws_bytes, uint32_t* error_dev,
+                                     void* stream) {
   int rc = check_ffn(dtype, M, H, I, activation, limit);
   if (rc != QMOE_OK) return rc;
   if ((x_scales_dev == nullptr) != (kept_scales_dev == nullptr)) return QMOE_ERR_ARG;
@@ -423,7 +448,9 @@ int qmoe_gated_ffn_backward(const void* dout_dev, int dtype, long long lddout, c
     }
     return QMOE_OK;
   }
-  if (!dout_dev || !x_dev || !w13_dev || !w2_dev || !kept_dev || !workspace_dev) return QMOE_ERR_ARG;
+  if (!dout_dev || !x_dev || !w13_dev || !w2_dev || !kept_dev || !workspace_dev || !error_dev ||
+      misaligned(error_dev, 4))
+    return QMOE_ERR_ARG;
   if (misaligned(dout_dev, 16) || misaligned(x_dev, codes ? 8 : 16) || misaligned(w13_dev, 16) ||
       misaligned(w2_dev, 16) || misaligned(kept_dev, 16) || misaligned(workspace_dev, 256))
     return QMOE_ERR_ARG;
@@ -443,7 +470,7 @@ int qmoe_gated_ffn_backward(const void* dout_dev, int dtype, long long lddout, c
   }
   FfnProduct f = {};
   f.dtype = dtype;
-  f.err = reinterpret_cast<unsigned int*>(ws);
+  f.err = error_dev;
   f.activation = activation;
   f.limit = limit;
   int parts = 0;

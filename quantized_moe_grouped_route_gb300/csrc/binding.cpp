@@ -191,12 +191,18 @@ struct Call {
     dense(t, at::kByte, "workspace", {t.numel()});
     return t;
   }
-  // The workspace of the last call that brought none, for its error word (one per operator
+  // What has the error word of the last call that brought no workspace (one per operator
   // and device; never destroyed, since that could come after the CUDA context's end).
   at::Tensor& kept(Kept which) const {
     static auto* all = new std::array<at::Tensor, kDevices * kKeptKinds>();
     if (dev < 0 || dev >= kDevices) fail("too many CUDA devices");
     return (*all)[(size_t)(dev * kKeptKinds + which)];
+  }
+  // Where a call without a workspace has its error word, kept until the next such call: the start
+  // of its workspace, but of one past 1 MiB, which is not to be held for that, a word of its own.
+  static constexpr int64_t kMostHeld = 1 << 20;
+  at::Tensor error_word(const at::Tensor& ws) {
+    return ws.numel() <= kMostHeld ? ws : make(at::kByte, {256});
   }
   // top_k of an [M][top_k] table
   int64_t slots(const at::Tensor& t, const char* name) {
@@ -702,13 +708,14 @@ PyObject* gated_ffn(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const at::Tensor out = c.out(a[6], f.type, "out", {M, f.H});
     const at::Tensor ws =
         c.space(a[7], qmoe_gated_ffn_workspace_size(small(M), small(f.H), small(f.I)), kFfn);
+    const at::Tensor error = given(a[7]) ? ws : c.error_word(ws);
     c.answer("qmoe_gated_ffn",
-             qmoe_gated_ffn(x.data_ptr(), dtype_code(f.type), ldx, w13.data_ptr(), w2.data_ptr(),
-                            small(integer(a[3])), (float)real(a[4]), small(M), small(f.H),
-                            small(f.I), out.data_ptr(), data(kept),
-                            static_cast<uint8_t*>(data(scales)), ws.data_ptr(), (size_t)ws.numel(),
-                            c.stream()));
-    if (!given(a[7]) && M > 0) c.kept(kFfn) = ws;
+             qmoe_gated_ffn_error_at(
+                 x.data_ptr(), dtype_code(f.type), ldx, w13.data_ptr(), w2.data_ptr(),
+                 small(integer(a[3])), (float)real(a[4]), small(M), small(f.H), small(f.I),
+                 out.data_ptr(), data(kept), static_cast<uint8_t*>(data(scales)), ws.data_ptr(),
+                 (size_t)ws.numel(), static_cast<uint32_t*>(error.data_ptr()), c.stream()));
+    if (!given(a[7]) && M > 0) c.kept(kFfn) = error;
     if (keep == 0) return THPVariable_Wrap(out);
     return pack_some({out, kept, scales});
   });
@@ -747,14 +754,15 @@ PyObject* gated_ffn_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const at::Tensor ws = c.space(
         a[12], qmoe_gated_ffn_backward_workspace_size(small(M), small(f.H), small(f.I),
                                                       xs.defined() ? 8 : 16), kFfnBackward);
+    const at::Tensor error = given(a[12]) ? ws : c.error_word(ws);
     c.answer("qmoe_gated_ffn_backward",
-             qmoe_gated_ffn_backward(dout.data_ptr(), dtype_code(f.type), ldd, x.data_ptr(), ldx,
-                                     static_cast<uint8_t*>(data(xs)), w13.data_ptr(), w2.data_ptr(),
-                                     kept.data_ptr(), static_cast<uint8_t*>(data(ks)),
-                                     small(integer(a[7])), (float)real(a[8]), small(M), small(f.H),
-                                     small(f.I), data(dx), data(dw13), data(dw2), ws.data_ptr(),
-                                     (size_t)ws.numel(), c.stream()));
-    if (!given(a[12]) && M > 0) c.kept(kFfnBackward) = ws;
+             qmoe_gated_ffn_backward_error_at(
+                 dout.data_ptr(), dtype_code(f.type), ldd, x.data_ptr(), ldx,
+                 static_cast<uint8_t*>(data(xs)), w13.data_ptr(), w2.data_ptr(), kept.data_ptr(),
+                 static_cast<uint8_t*>(data(ks)), small(integer(a[7])), (float)real(a[8]), small(M),
+                 small(f.H), small(f.I), data(dx), data(dw13), data(dw2), ws.data_ptr(),
+                 (size_t)ws.numel(), static_cast<uint32_t*>(error.data_ptr()), c.stream()));
+    if (!given(a[12]) && M > 0) c.kept(kFfnBackward) = error;
     return pack_some({dx, dw13, dw2});
   });
 }

@@ -73,7 +73,8 @@ def _on(stream):
 def qmoe_default_read_error(stream=None):
     """(return code, flags) of the last moe_sort_tokens, qmoe_lora_linear, qmoe_gated_ffn and
     qmoe_gated_ffn_backward calls on the current device that were given no workspace, together;
-    their workspaces are kept until the next such call.  Synchronises the stream (default: the current one), on which, or before
+    their workspaces are kept until the next such call (a gated block's of more than 1 MiB is not,
+    its error word alone).  Synchronises the stream (default: the current one), on which, or before
     which, those calls were made."""
     rc, flags = qmoe.QMOE_OK, 0
     for workspace in (_module or _native()).default_workspaces():

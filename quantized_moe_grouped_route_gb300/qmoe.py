@@ -113,9 +113,13 @@ def _bind(L):
         "qmoe_checkpoint8_restore": (i32, [P, P, i32, i32, i32, P, P]),
         "qmoe_gated_ffn_workspace_size": (sz, [i32, i32, i32]),
         "qmoe_gated_ffn": (i32, [P, i32, i64, P, P, i32, f32, i32, i32, i32, P, P, P, P, sz, P]),
+        "qmoe_gated_ffn_error_at": (i32, [P, i32, i64, P, P, i32, f32, i32, i32, i32, P, P, P, P, sz,
+                                          P, P]),
         "qmoe_gated_ffn_backward_workspace_size": (sz, [i32, i32, i32, i32]),
         "qmoe_gated_ffn_backward": (i32, [P, i32, i64, P, i64, P, P, P, P, P, i32, f32, i32, i32,
                                           i32, P, P, P, P, sz, P]),
+        "qmoe_gated_ffn_backward_error_at": (i32, [P, i32, i64, P, i64, P, P, P, P, P, i32, f32, i32,
+                                                   i32, i32, P, P, P, P, sz, P, P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(L, name)

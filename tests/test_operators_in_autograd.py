@@ -1,6 +1,8 @@
 """What autograd has to know of the operators' calls: tangents, gradients that a call has none for,
 outputs that are written into, and the memory that a call leaves held."""
 
+import gc
+
 import pytest
 import torch
 import torch.autograd.forward_ad as fw
@@ -135,3 +137,38 @@ def test_an_output_that_requires_a_gradient():
         with torch.no_grad():
             assert torch.equal(q.qmoe_block_norm(x, post_weight=w, out=out)[0],
                                q.qmoe_block_norm(x, post_weight=w)[0])
+
+
+def _held():
+    """Bytes that tensors have asked for.  (memory_allocated counts the allocator's blocks, which it
+    splits only where more than 1 MiB would remain.)"""
+    gc.collect()
+    torch.cuda.synchronize()
+    return torch.cuda.memory_stats()["requested_bytes.all.current"]
+
+
+@pytest.mark.parametrize("bits", [16, 8])
+def test_no_workspace_is_held_after_a_call(bits):
+    """A gated block's call that brings no workspace leaves its outputs and an error word behind, no
+    more (a few allocations of 512 bytes)."""
+    M, H, I = 2000, 1024, 512
+    x, w13, w2 = (torch.randn(s, **KW) for s in ((M, H), (2 * I, H), (H, I)))
+
+    def step():
+        out, saved = q.qmoe_gated_ffn_saved(x, w13, w2, checkpoint=bits)
+        q.qmoe_gated_ffn_backward(out, x, w13, w2, saved)
+        q.qmoe_gated_ffn(x[:3], w13, w2)
+        assert q.qmoe_default_read_error() == (qmoe.QMOE_OK, 0)
+
+    _ = q.qmoe_gated_ffn(x[:3], w13, w2)  # the least of workspaces
+    tiny = torch.ones(1, 64, **KW)
+    small = torch.ones(16, 64, **KW), torch.ones(64, 8, **KW)
+    q.qmoe_gated_ffn_backward(tiny, tiny, *small, q.qmoe_gated_ffn_saved(tiny, *small)[1])
+    before = _held()
+    step()
+    assert _held() - before <= 4096
+    out, saved = q.qmoe_gated_ffn_saved(x, w13, w2, checkpoint=bits)
+    before = _held()
+    grads = q.qmoe_gated_ffn_backward(out, x, w13, w2, saved)
+    held = _held() - before - sum(2 * g.numel() for g in grads)
+    assert held <= 4096
