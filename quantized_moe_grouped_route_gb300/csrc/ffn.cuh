@@ -51,4 +51,12 @@ __device__ __forceinline__ float gated_backward(bool gelu, float limit, float u,
   return a * u;
 }
 
+// Tensor map of an operand [rows][cols], rows ld elements apart, in boxes of 64 columns.
+inline bool map_of(CUtensorMap* map, int dtype, const void* base, long long rows, int cols,
+                   long long ld, int box_rows) {
+  const uint64_t dims[2] = {(uint64_t)cols, (uint64_t)rows}, strides[1] = {(uint64_t)ld * 2};
+  const uint32_t box[2] = {64, (uint32_t)box_rows};
+  return make_tmap16(map, dtype, base, 2, dims, strides, box) == QMOE_OK;
+}
+
 }  // namespace qmoe

@@ -1,12 +1,12 @@
-// The gated feed-forward block for a decode batch (some 9 to 256 tokens), forward: the weights are
-// the rows of the MMA and the tokens its columns, so a product is one pass over the weights.
+// The gated feed-forward block for a decode batch (9 to 256 tokens), forward: the weights are the
+// rows of the MMA and the tokens its columns, so a product is one pass over the weights.
 //
-// A unit is 128 rows of weights (64 of u and the same 64 of g in the first product) by all tokens of
-// a tile.  Units are fewer than SMs, so a cluster of S CTAs shares one: each takes a segment of K
+// A unit is 128 rows of weights (64 of u and the same 64 of g in the first product) by all tokens.
+// Units are fewer than SMs, so a cluster of S CTAs shares one: each takes a segment of K
 // through a ring of TMA-loaded stages into an accumulator in TMEM (tcgen05, M = 128, N = tokens),
 // puts its sums into shared memory, and the CTAs add up each other's by distributed shared memory,
 // every CTA the tokens seg, seg + S, ..; the order of the sums is fixed.  Bound by the stream of the
-// weights; two CTAs fit an SM, so that the second product's first weights are already on their way
+// weights; up to 128 tokens two CTAs fit an SM, so that the second product's first weights are already on their way
 // while the first product ends (its launch is programmatic, and only the tokens' copies wait).
 // 48 tokens, H = 7168, I = 2048: 21.9 us in a graph (the weights' stream 13.2); 4096 x 1536: 14.5 (5.7).
 #include "cluster.cuh"
@@ -44,9 +44,7 @@ __global__ void __launch_bounds__(kThreads) ffn_few_kernel(const __grid_constant
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int seg = S > 1 ? (int)cluster_rank() : 0;
-  const int unit = (int)blockIdx.x / S;
-  const int tile = unit / p.blocks, block = unit - tile * p.blocks;
-  const int row0 = block * (UP ? 64 : 128), m0 = tile * p.tile_n;
+  const int row0 = (int)blockIdx.x / S * (UP ? 64 : 128);
   const int k0 = (int)((long long)p.ksteps * seg / S), k1 = (int)((long long)p.ksteps * (seg + 1) / S);
   if (threadIdx.x == 0) {
     for (int s = 0; s < stages; ++s) {
@@ -87,7 +85,7 @@ __global__ void __launch_bounds__(kThreads) ffn_few_kernel(const __grid_constant
       if (UP) tma_load_2d_if(lead, at + kWeightBytes / 2, &maps.w2, k * 64, row0, bar, pol_w);
     };
     auto tokens = [&](int k, int s) {
-      tma_load_2d_if(lead, base + s * stage_bytes + kWeightBytes, &maps.x, k * 64, m0,
+      tma_load_2d_if(lead, base + s * stage_bytes + kWeightBytes, &maps.x, k * 64, 0,
                      smem_u32(&full[s]), pol_x);
     };
     const int first = min(stages, k1 - k0);
@@ -141,19 +139,18 @@ __global__ void __launch_bounds__(kThreads) ffn_few_kernel(const __grid_constant
   // every thread: the accumulator is complete, and with it the ring is idle
   bool ok = warp_wait(smem_u32(accf), 0, abort_flag, p.err);
   tc_fence_after();
-  const int cols = min(p.tile_n, p.M - m0);
   float* sums = reinterpret_cast<float*>(smem);  // [token][128]
   if (ok) {
     const int q = warp & 3, half = warp >> 2;  // two warps a lane quarter, columns in turn
     const uint32_t tbase = tmem + ((uint32_t)(q * 32) << 16);
-    for (int c = 16 * half; c < cols; c += 32) {
+    for (int c = 16 * half; c < p.M; c += 32) {
       uint32_t r[16];
       tmem_ld_x16(tbase + c, r);
       tmem_wait_ld();
       tmem_ld_ready(r);
 #pragma unroll
       for (int k = 0; k < 16; ++k)
-        if (c + k < cols) sums[(c + k) * 128 + q * 32 + lane] = __uint_as_float(r[k]);
+        if (c + k < p.M) sums[(c + k) * 128 + q * 32 + lane] = __uint_as_float(r[k]);
     }
   }
   if (!UP) {  // what follows writes memory that earlier kernels may still read
@@ -171,7 +168,7 @@ __global__ void __launch_bounds__(kThreads) ffn_few_kernel(const __grid_constant
   const uint32_t sums0 = smem_u32(sums) + 16 * lane;
   const int n = row0 + 4 * lane;
   const bool gelu = p.activation == QMOE_ACT_GELU;
-  for (int c = seg + S * warp; c < cols; c += S * (kThreads / 32)) {
+  for (int c = seg + S * warp; c < p.M; c += S * (kThreads / 32)) {
     float4 v[kMaxSplits];
 #pragma unroll
     for (int i = 0; i < kMaxSplits; ++i)
@@ -194,33 +191,25 @@ __global__ void __launch_bounds__(kThreads) ffn_few_kernel(const __grid_constant
 #pragma unroll
     for (int e = 0; e < 4; ++e) o.v[e] = from_f32<T>(f[e]);
     if (n < p.N && (!UP || lane < 16))
-      *reinterpret_cast<uint2*>(reinterpret_cast<T*>(p.out) + (size_t)(m0 + c) * p.N + n) = o.raw;
+      *reinterpret_cast<uint2*>(reinterpret_cast<T*>(p.out) + (size_t)c * p.N + n) = o.raw;
   }
   // No CTA leaves while its sums may still be read; every value fetched above has gone into a
   // store, so the barrier need not order memory.
   if (S > 1) cluster_sync_relaxed();
 }
 
-bool map_of(CUtensorMap* map, int dtype, const void* base, long long rows, int cols, long long ld,
-            int box_rows) {
-  const uint64_t dims[2] = {(uint64_t)cols, (uint64_t)rows}, strides[1] = {(uint64_t)ld * 2};
-  const uint32_t box[2] = {64, (uint32_t)box_rows};
-  return make_tmap16(map, dtype, base, 2, dims, strides, box) == QMOE_OK;
-}
-
 template <class T, bool UP>
 cudaError_t run(const FfnProduct& f, int num_sms, cudaStream_t stream) {
   FfnFew p = {};
   static_cast<FfnProduct&>(p) = f;
-  p.tiles = (f.M + 255) / 256;
-  p.tile_n = ((f.M + p.tiles - 1) / p.tiles + 15) / 16 * 16;
-  p.blocks = UP ? (f.N + 63) / 64 : (f.N + 127) / 128;
+  p.tile_n = (f.M + 15) / 16 * 16;
   p.ksteps = (f.K + 63) / 64;
   p.tmem_cols = p.tile_n <= 32 ? 32 : p.tile_n <= 64 ? 64 : p.tile_n <= 128 ? 128 : 256;
-  const int units = p.tiles * p.blocks, stage = kWeightBytes + p.tile_n * 128;
+  const int units = UP ? (f.N + 63) / 64 : (f.N + 127) / 128, stage = kWeightBytes + p.tile_n * 128;
   // Segments of two steps or more, four at most, as many as there are SMs for: more of them cost
-  // the adding up what they save (128 tokens, 4096 x 1536: 19.2 us a call, by up to eight segments and
-  // two CTAs an SM 22.0, by two segments 26.2).
+  // the adding up what they save.  us a call in a graph by at most 2, 3, 4, 6 and 8 segments:
+  //   48 tokens, 4096 x 1536: 18.0, 15.7, 14.8, 15.0, 15.0;  7168 x 2048: 26.5, 23.3, 22.5, 22.7, 23.0
+  //   128 tokens, 4096 x 1536: 26.4, 21.8, 19.3, 20.2, 20.3;  7168 x 2048: 37.6, 31.7, 28.4, 28.7, 29.4
   p.splits = 1;
   while (p.splits < kMaxSplits && units * (p.splits + 1) <= num_sms &&
          p.ksteps >= 2 * (p.splits + 1))

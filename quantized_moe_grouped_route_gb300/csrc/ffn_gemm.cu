@@ -596,18 +596,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// A matrix [rows][cols] whose rows lie ld elements apart, in boxes of 64 columns, or in the
-// epilogue's staging tiles.
+// An output [rows][cols], rows ld elements apart, in the epilogue's staging tiles.
 bool map_out(CUtensorMap* map, int dtype, const void* base, long long rows, int cols, long long ld) {
   const uint64_t dims[2] = {(uint64_t)cols, (uint64_t)rows}, strides[1] = {(uint64_t)ld * 2};
   const uint32_t box[2] = {32, 32};
   return make_tmap16(map, dtype, base, 2, dims, strides, box, 64) == QMOE_OK;
-}
-bool map_of(CUtensorMap* map, int dtype, const void* base, long long rows, int cols, long long ld,
-            int box_rows) {
-  const uint64_t dims[2] = {(uint64_t)cols, (uint64_t)rows}, strides[1] = {(uint64_t)ld * 2};
-  const uint32_t box[2] = {64, (uint32_t)box_rows};
-  return make_tmap16(map, dtype, base, 2, dims, strides, box) == QMOE_OK;
 }
 
 template <class T, Op OP, bool CODES, bool PART>

@@ -358,7 +358,7 @@ struct FfnProduct {
   float* part;    // ffn_part_bytes
 };
 struct FfnGemm : FfnProduct {
-  int tile_n, tiles_m, tiles_n, ksteps, stages;
+  int tile_n, tiles_m, tiles_n, ksteps;
   int splits;  // segments of K
   int first;   // of its launch's units
 };
@@ -374,14 +374,20 @@ cudaError_t launch_ffn_finish(const FfnGemm& p, cudaStream_t stream);
 cudaError_t launch_ffn_product(const FfnProduct& f, int num_sms, cudaStream_t stream);
 // ... and up to three plain ones of one type in one launch, the longest K first
 cudaError_t launch_ffn_products(const FfnProduct* f, int count, int num_sms, cudaStream_t stream);
-// ffn_stream.cu, ffn_few.cu: kUp (nothing kept) and kNT for few tokens, which are the rows of a
+// ffn_stream.cu, ffn_few.cu: kUp (nothing kept) and kNT for few tokens, which are the columns of an
+// MMA whose rows are the weights'
 constexpr int kFfnStreamTokens = 8;
 cudaError_t launch_ffn_stream(const FfnProduct& f, cudaStream_t stream);
 struct FfnFew : FfnProduct {
-  int tile_n, tiles, blocks;  // tokens of a tile, tiles, blocks of 128 rows of weights
+  int tile_n;  // tokens, in whole MMA columns
   int ksteps, splits, stages, ring_bytes, tmem_cols;
 };
-constexpr int kFfnFewTokens = 128;
+// As many as an MMA has columns: up to there one pass over the weights is not slower than tiles of
+// 256 tokens are.  us a call in a graph, ffn_few.cu and (behind it) ffn_gemm.cu, of 9, 128, 144, 192 and 256:
+//   4096 x 1536: 13.3 (23.0), 19.3 (25.4), 19.3 (25.4), 21.1 (25.6), 24.9 (25.9)
+//   7168 x 2048: 20.6 (30.6), 28.4 (37.5), 26.7 (37.6), 29.6 (38.3), 34.9 (39.6)
+//   2048 x 1024: 8.9 (16.5), 14.2 (19.7), 14.6 (19.7), 16.1 (19.8), 19.4 (19.5)
+constexpr int kFfnFewTokens = 256;
 cudaError_t launch_ffn_few(const FfnProduct& f, int num_sms, cudaStream_t stream);
 
 }  // namespace qmoe

@@ -145,3 +145,13 @@ def test_a_corner_tile_of_many_steps(M, H, I):
             assert torch.equal(a, b)
         assert torch.equal(out, q.qmoe_gated_ffn(x, w13, w2))
     assert q.qmoe_default_read_error() == (qmoe.QMOE_OK, 0)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("M,H,I", [(113, 520, 328), (129, 72, 2056), (160, 1032, 328), (200, 4096, 96),
+                                   (241, 264, 264), (256, 520, 1000), (256, 8, 8)])
+def test_gated_ffn_of_large_decode_batches(M, H, I, dtype):
+    """The last batches whose tokens are an MMA's columns."""
+    ops.test_gated_ffn(M, H, I, "gelu" if M % 2 else "silu", 1.0 if I == 328 else math.inf, dtype)
+    if (H, dtype) == (4096, torch.bfloat16):
+        ops.test_gated_ffn_odd_tokens_stay_alone(M)
