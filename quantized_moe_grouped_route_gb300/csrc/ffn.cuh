@@ -9,8 +9,11 @@
 namespace qmoe {
 
 // Both activations are g * sigmoid(k(g)): SiLU with k(g) = g, GELU in its tanh form with
-// k(g) = 2 sqrt(2 / pi) (g + 0.044715 g^3), since (1 + tanh z) / 2 = sigmoid(2 z).  expf's and the
-// division's approximations are off by a few 2^-22, far below the rounding of what they enter.
+// k(g) = 2 sqrt(2 / pi) (g + 0.044715 g^3), since (1 + tanh z) / 2 = sigmoid(2 z).  expf's
+// approximation is documented as off by 2 + 1.173 |k| units in the last place (2^-23) and k is
+// by a few of its own, so the sigmoid by some (8 + 4 |k|) 2^-23, relative: below the half step of bf16
+// (2^-8) or fp16 (2^-11) by which h is rounded anyway for every |k| up to 1000, far beyond those at
+// which the sigmoid is another number than 0 and 1.
 constexpr float kGeluA = 1.5957691216057308f;  // 2 sqrt(2 / pi)
 constexpr float kGeluB = 0.044715f;
 

@@ -112,6 +112,38 @@ def test_kept_values_past_fp16(M, H, kind):
     assert kept[0, 9] == math.inf and not torch.isfinite(out[0]).any()
 
 
+# ------------------------------------------------------------- gates that are nearly closed
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("kind", ["silu", "gelu"])
+def test_activations_of_closed_gates(kind, dtype):
+    """Both activations are g sigmoid(k(g)).  exp's approximation is off by 2 + 1.173 |k| units in the
+    last place (2^-23) and k by a few of its own, so the sigmoid is off by (8 + 4 |k|) 2^-23, below
+    the rounding of what it enters for every k at which the result is a number of the type.  Weights
+    and tokens are rows of the identity: out is h, and the gradient of w13 is [du | dg]."""
+    n = 64
+    eye = torch.eye(n, device="cuda", dtype=dtype)
+    least = {"silu": (-80.0, -15.0), "gelu": (-9.0, -3.5)}[kind][dtype == torch.float16]
+    gates = torch.linspace(least, 10.0, n * n, device="cuda").view(n, n).to(dtype)
+    w13 = torch.cat([torch.full((n, n), 0.75, device="cuda", dtype=dtype), gates.t()])
+    out, saved = q.qmoe_gated_ffn_saved(eye, w13, eye, activation=ACTS[kind])
+    g, u = gates.double(), 0.75
+    A, B = math.sqrt(2 / math.pi), 0.044715
+    k, dk = (g, 1.0) if kind == "silu" else (2 * A * (g + B * g ** 3), 2 * A * (1 + 3 * B * g * g))
+    p, left = torch.sigmoid(k), torch.sigmoid(-k)
+    rel = (8 + 4 * k.abs()) * 2.0 ** -23
+    r, tiny = ROUND[dtype], ops.TINY[dtype]
+    h = g * p * u
+    _near(out, h, rel * h.abs() + r * h.abs() * (1 + rel) + tiny, "h")
+    _near(q.qmoe_gated_ffn(eye, w13, eye, activation=ACTS[kind]), h,
+          rel * h.abs() + r * h.abs() * (1 + rel) + tiny, "h of a call that keeps nothing")
+    dout = torch.full((n, n), 2.0, device="cuda", dtype=dtype)
+    dug = q.qmoe_gated_ffn_backward(dout, eye, w13, eye, saved, activation=ACTS[kind])[1].t()
+    du, dg = 2 * g * p, 2 * u * (p + g * p * left * dk)
+    terms = 2 * u * (p + (g * p * left * dk).abs())
+    _near(dug[:, :n], du, rel * du.abs() + r * du.abs() * (1 + rel) + tiny, "du")
+    _near(dug[:, n:], dg, 2 * rel * terms + r * (dg.abs() + 2 * rel * terms) + tiny, "dg")
+
+
 # ------------------------------------------------------ plans that only large sizes take
 WIDE = (2310, 1032, 2056)  # every product in tiles of 256 columns, with odd ends of M, N and K
 
