@@ -187,3 +187,15 @@ def test_gated_ffn_of_large_decode_batches(M, H, I, dtype):
     ops.test_gated_ffn(M, H, I, "gelu" if M % 2 else "silu", 1.0 if I == 328 else math.inf, dtype)
     if (H, dtype) == (4096, torch.bfloat16):
         ops.test_gated_ffn_odd_tokens_stay_alone(M)
+
+
+@pytest.mark.parametrize("c", [
+    _case(12000, 1001), _case(12000, 1001, torch.float16, gate="full", pad=3),
+    _case(30000, 65, gate="channel"), _case(30000, 65, residual=False, post=False),
+    _case(30000, 512, torch.float16, residual=False, post=False), _case(3000, 7168),
+    _case(12000, 1024, torch.float16, post=False, gate="token"), _case(6000, 1026, torch.float16),
+    _case(4000, 2048, torch.float32, residual=False)], ids=lambda c: "-".join(str(v) for v in c.values()))
+def test_norms_of_many_rows_a_cta(c):
+    """So many rows that each place of a ring of rows is used several times: all rows and sums."""
+    ops.test_block_norm(c)
+    ops.test_block_norm_backward(c)
