@@ -440,7 +440,7 @@ int qmoe_lora_linear(const void* x_dev, int dtype, long long ldx, const void* w_
  *               wanted, as without residual, gate and post_weight, where it would be y
  *   normed_dev  [M][H], with pre_weight_dev and only then
  *   post_rstd_dev, pre_rstd_dev  fp32 [M] or NULL; what the backward pass needs of the norms
- * Sums are fp32; fp32 rows whose squares' sum passes the range of fp32 give rstd 0.
+ * Sums are fp32; rows (of fp32 or bf16) whose squares' sum passes the range of fp32 give rstd 0.
  */
 int qmoe_block_norm(const void* y_dev, int dtype, long long ldy, const void* residual_dev,
                     long long ldr, float residual_scale, const void* gate_dev, int gate_dtype,

@@ -2,8 +2,8 @@
 its gate and residual, the gated feed-forward block (a shared expert next to the layer's, or a
 dense layer's), and activation checkpoints in 8 bits.
 
-Tensors, streams, workspaces and errors as in operators.py.  A matrix's rows may lie apart; the
-gated feed-forward block wants them 16-byte aligned.
+Tensors, streams, workspaces and errors as in operators.py.  Activations' rows may lie apart (the
+gated feed-forward block wants each 16-byte aligned and its own); weights are contiguous.
 
 Autograd: qmoe_block_norm and qmoe_gated_ffn on tensors that require a gradient are nodes of its
 graph, whose backward is the *_backward call of the same name (those calls and the checkpoints have

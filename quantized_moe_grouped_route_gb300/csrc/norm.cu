@@ -6,8 +6,12 @@
 // sums wait for never leaves them.  out is rounded once, when it is written; normed is made from
 // the sums before that rounding.  Bound by memory: four rows a token where all parts are there.
 // Of many rows each CTA takes one after the other, and copies the next ones to shared memory while
-// a row waits for its sums (norm.cuh), two CTAs an SM; few rows have a CTA each.  8192 rows of 7168
-// bf16: 88.8 us, 5.3 TB/s (straight loads of a row a CTA, 137); 16 rows: 3.0 us in a graph.
+// a row waits for its sums (norm.cuh), as many CTAs an SM as 1024 threads are: where two rows and the
+// vectors fit a CTA's share, in 16 bits with both norms and a residual at 7168 columns, with less
+// beside them at more widths.  Elsewhere, and of few rows, a row has a CTA and comes straight
+// from memory.  8192 rows of 7168 bf16: 81.6 us in a graph, 5.8 TB/s, with a token's gate 87.5 (straight 137);
+// 58.7 million elements straight at 1024 to 5120 and 8192 columns: 81 to 94 us, with a channel's or full gate 95
+// to 120 (full: five matrices), in fp32 half as many 73 to 78 (gated 77 to 124); 16 rows: 3.0 us.
 #include "norm.cuh"
 
 namespace qmoe {
