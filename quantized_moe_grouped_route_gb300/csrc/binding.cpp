@@ -18,7 +18,6 @@
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
-#include <torch/csrc/autograd/forward_grad.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <array>
@@ -224,13 +223,18 @@ PyObject* pack(std::initializer_list<at::Tensor> ts) {
   return r;
 }
 
-// No call has a derivative in forward mode: a tangent is refused, not dropped.
+// No call has a derivative in forward mode: a tangent is refused, not dropped.  (Tensors that autograd
+// has had nothing to do with are passed over by a look at a pointer.)
 bool carries_tangent(PyObject* const* a, Py_ssize_t n) {
-  if (!c10::AutogradState::get_tls_state().get_fw_grad_mode() ||
-      !torch::autograd::ForwardADLevel::try_get_by_idx(0))
-    return false;
-  for (Py_ssize_t i = 0; i < n; ++i)
-    if (THPVariable_Check(a[i]) && THPVariable_Unpack(a[i])._fw_grad(0).defined()) return true;
+  for (Py_ssize_t i = 0; i < n; ++i) {
+    PyObject* const o = a[i];
+    if (o == Py_None || PyBool_Check(o) || PyLong_CheckExact(o) || PyFloat_CheckExact(o) ||
+        !THPVariable_Check(o))
+      continue;
+    const at::Tensor& t = THPVariable_Unpack(o);
+    if (t.unsafeGetTensorImpl()->autograd_meta() && t._fw_grad(0).defined())
+      return c10::AutogradState::get_tls_state().get_fw_grad_mode();
+  }
   return false;
 }
 
