@@ -45,6 +45,30 @@ int check_norm(int dtype, int M, int H, const Gate& g, const void* post, const v
   return QMOE_OK;
 }
 
+// What the forward and backward kernels are both given.
+NormArgs norm_args(int M, int H, const void* y, long long ldy, float residual_scale, const Gate& g,
+                   const void* post, const void* pre, int weight_dtype, float weight_offset,
+                   float* post_rstd, float* pre_rstd) {
+  NormArgs a = {};
+  a.M = M;
+  a.H = H;
+  a.y = y;
+  a.ldy = ldy;
+  a.residual_scale = residual_scale;
+  a.gate = g.p;
+  a.gate_form = g.form;
+  a.gating = g.gating;
+  a.gate_fp32 = g.dtype == QMOE_DTYPE_FP32;
+  a.ldgate = g.ld;
+  a.post_weight = post;
+  a.pre_weight = pre;
+  a.weight_fp32 = weight_dtype == QMOE_DTYPE_FP32;
+  a.weight_offset = weight_offset;
+  a.post_rstd = post_rstd;
+  a.pre_rstd = pre_rstd;
+  return a;
+}
+
 // The widest chunk of elements in which a norm's rows and vectors move.
 int norm_chunk(int dtype, int H, const Gate& g, const void* post, const void* pre, int weight_dtype,
                Chunk chunk) {
@@ -89,26 +113,11 @@ int qmoe_block_norm(const void* y_dev, int dtype, long long ldy, const void* res
   int sms = 0;
   rc = device_info(&sms);
   if (rc != QMOE_OK) return rc;
-  NormArgs a = {};
-  a.M = M;
-  a.H = H;
-  a.y = y_dev;
-  a.ldy = ldy;
+  NormArgs a = norm_args(M, H, y_dev, ldy, residual_scale, g, post_weight_dev, pre_weight_dev,
+                         weight_dtype, weight_offset, post_rstd_dev, pre_rstd_dev);
   a.residual = residual_dev;
   a.ldr = ldr;
-  a.residual_scale = residual_scale;
-  a.gate = gate_dev;
-  a.gate_form = gate_form;
-  a.gating = gating;
-  a.gate_fp32 = gate_dtype == QMOE_DTYPE_FP32;
-  a.ldgate = ldgate;
-  a.post_weight = post_weight_dev;
-  a.pre_weight = pre_weight_dev;
-  a.weight_fp32 = weight_dtype == QMOE_DTYPE_FP32;
-  a.weight_offset = weight_offset;
   a.eps = eps;
-  a.post_rstd = post_rstd_dev;
-  a.pre_rstd = pre_rstd_dev;
   a.out = out_dev;
   a.normed = normed_dev;
   Chunk chunk;
@@ -183,24 +192,10 @@ int qmoe_block_norm_backward(const void* dout_dev, long long lddout, const void*
   int sms = 0;
   rc = device_info(&sms);
   if (rc != QMOE_OK) return rc;
-  NormArgs a = {};
-  a.M = M;
-  a.H = H;
+  NormArgs a = norm_args(M, H, y_dev, ldy, residual_scale, g, post_weight_dev, pre_weight_dev,
+                         weight_dtype, weight_offset, const_cast<float*>(post_rstd_dev),
+                         const_cast<float*>(pre_rstd_dev));
   a.units = norm_units(M, H);
-  a.y = y_dev;
-  a.ldy = ldy;
-  a.residual_scale = residual_scale;
-  a.gate = gate_dev;
-  a.gate_form = gate_form;
-  a.gating = gating;
-  a.gate_fp32 = gate_dtype == QMOE_DTYPE_FP32;
-  a.ldgate = ldgate;
-  a.post_weight = post_weight_dev;
-  a.pre_weight = pre_weight_dev;
-  a.weight_fp32 = weight_dtype == QMOE_DTYPE_FP32;
-  a.weight_offset = weight_offset;
-  a.post_rstd = const_cast<float*>(post_rstd_dev);
-  a.pre_rstd = const_cast<float*>(pre_rstd_dev);
   a.dout = dout_dev;
   a.lddout = lddout;
   a.dnormed = dnormed_dev;
