@@ -199,3 +199,37 @@ def test_norms_of_many_rows_a_cta(c):
     """So many rows that each place of a ring of rows is used several times: all rows and sums."""
     ops.test_block_norm(c)
     ops.test_block_norm_backward(c)
+
+
+@pytest.mark.parametrize("M", [3, 40, 300])
+def test_gated_ffn_of_the_largest_weights(M):
+    """Weights of more than 2^32 elements.  Of w2 only the last 64 columns are other than 0, so that all
+    results but h's product are those of these 64 of I, in the last rows of w13's halves."""
+    H, I, dt, few = 65536, 32776, torch.bfloat16, 64
+    g = _gen(1)
+    x, dout = _rows(g, M, H, dt), _rows(g, M, H, dt)
+    w13 = torch.empty(2 * I, H, dtype=dt, device="cuda").normal_(0.0, 1.5 * H ** -0.5, generator=g)
+    w2 = torch.zeros(H, I, dtype=dt, device="cuda")
+    w2[:, -few:].normal_(0.0, few ** -0.5, generator=g)
+    s13 = torch.cat([w13[I - few:I], w13[-few:]])
+    s2 = w2[:, -few:].contiguous()
+    r, u = ROUND[dt], ops.U
+    _, _, h, eh = ops._up("silu", math.inf, x, s13)
+    eh = eh + r * (h.abs() + eh)
+    w = s2.double()
+    ref = h @ w.t()
+    bound = eh @ w.abs().t() + (few + 4) * 2 * u * ((h.abs() + eh) @ w.abs().t())
+    _near(q.qmoe_gated_ffn(x, w13, w2), ref, bound + r * (ref.abs() + bound), "out")
+    out, (kept,) = q.qmoe_gated_ffn_saved(x, w13, w2)
+    _near(out, ref, bound + r * (ref.abs() + bound), "out beside what is kept")
+    dx, dw13, dw2 = q.qmoe_gated_ffn_backward(dout, x, w13, w2, (kept,))
+    kept = kept.double()
+    for at, where in ((slice(I - few, I), "the last"), (slice(0, few), "the first")):
+        half = slice(at.start + I, at.stop + I)
+        want = _ffn_grads("silu", math.inf, dout, x, torch.cat([w13[at], w13[half]]), w2[:, at],
+                          kept[:, at], kept[:, half], dt)
+        if where == "the last":
+            _near(dx, *want["dx"], "dx")
+        _near(torch.cat([dw13[at], dw13[half]]), *want["dw13"], "dw13, " + where)
+        _near(dw2[:, at], *want["dw2"], "dw2, " + where)
+    assert q.qmoe_default_read_error() == (qmoe.QMOE_OK, 0)
