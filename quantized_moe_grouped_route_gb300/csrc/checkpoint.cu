@@ -139,13 +139,12 @@ template <class T, int VEC>
 cudaError_t run(const CheckpointArgs& a, bool restore, int sms, cudaStream_t stream) {
   if (restore) {
     const long long units = (long long)a.M * (a.C / VEC);
-    restore_kernel<T, VEC><<<grid_of(units, kThreads * kAtOnce, sms), kThreads, 0, stream>>>(a);
-  } else {
-    const long long units = (long long)a.M * a.blocks;
-    pack_kernel<T, VEC><<<grid_of(units, kThreads / (kCkBlock / VEC) * kAtOnce, sms), kThreads, 0,
-                          stream>>>(a);
+    return launch_plain(restore_kernel<T, VEC>, grid_of(units, kThreads * kAtOnce, sms), kThreads,
+                        stream, a);
   }
-  return cudaGetLastError();
+  const long long units = (long long)a.M * a.blocks;
+  return launch_plain(pack_kernel<T, VEC>, grid_of(units, kThreads / (kCkBlock / VEC) * kAtOnce, sms),
+                      kThreads, stream, a);
 }
 
 template <class T>

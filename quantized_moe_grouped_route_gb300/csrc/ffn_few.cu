@@ -8,7 +8,7 @@
 // every CTA the tokens seg, seg + S, ..; the order of the sums is fixed.  Bound by the stream of the
 // weights; up to 128 tokens two CTAs fit an SM, so that the second product's first weights are already on their way
 // while the first product ends (its launch is programmatic, and only the tokens' copies wait).
-// 48 tokens, H = 7168, I = 2048: 21.9 us in a graph (the weights' stream 13.2); 4096 x 1536: 14.5 (5.7).
+// 48 tokens, H = 7168, I = 2048: 22.5 us in a graph (the weights' stream 13.2); 4096 x 1536: 14.8 (5.7).
 #include "cluster.cuh"
 #include "ffn.cuh"
 #include "mma.cuh"

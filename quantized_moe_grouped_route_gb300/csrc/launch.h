@@ -140,6 +140,18 @@ int resident_clusters(K* kernel, int size, int threads, size_t smem, int num_sms
   return cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess ? n : 0;
 }
 
+// A launch without attributes, whose own error is its answer: cudaGetLastError would hand over what an
+// earlier call has left.
+template <class... Params, class... Args>
+cudaError_t launch_plain(void (*kernel)(Params...), int grid, int threads, cudaStream_t stream,
+                         Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.stream = stream;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // Launch attribute that lets a kernel start while the previous kernel on the stream
 // finishes (it must then call grid_dep_wait before reading that kernel's outputs).
 // The forward uses it on every schedule but the wide prefill one, where kernels that

@@ -220,13 +220,12 @@ cudaError_t launch_repack(const uint8_t* w, const uint8_t* s, int E, int N, int 
                           cudaStream_t stream) {
   const long long words = (long long)E * N * (K / 8);
   const long long rows = (long long)E * N * (K / 128);
-  repack_codes_kernel<<<grid_for(words, 256, 1184), 256, 0, stream>>>(
-      w, E, N, K, w13 ? 1 : 0, reinterpret_cast<uint32_t*>(out_codes));
-  cudaError_t rc = cudaGetLastError();
+  const cudaError_t rc =
+      launch_plain(repack_codes_kernel, grid_for(words, 256, 1184), 256, stream, w, E, N, K,
+                   w13 ? 1 : 0, reinterpret_cast<uint32_t*>(out_codes));
   if (rc != cudaSuccess) return rc;
-  repack_scales_kernel<<<grid_for(rows, 256, 1184), 256, 0, stream>>>(
-      s, E, N, K, w13 ? 1 : 0, scale_layout, reinterpret_cast<uint2*>(out_scales));
-  return cudaGetLastError();
+  return launch_plain(repack_scales_kernel, grid_for(rows, 256, 1184), 256, stream, s, E, N, K,
+                      w13 ? 1 : 0, scale_layout, reinterpret_cast<uint2*>(out_scales));
 }
 
 cudaError_t launch_gather(const void* x, const int32_t* pair_pos, int M, int top_k, int H,
@@ -259,13 +258,11 @@ cudaError_t launch_combine(const float* ypart, const int32_t* ids, int M, int to
 }
 
 cudaError_t launch_selftest_dequant(uint16_t* out, cudaStream_t stream) {
-  selftest_dequant_kernel<<<256, 32, 0, stream>>>(out, dequant_mul());
-  return cudaGetLastError();
+  return launch_plain(selftest_dequant_kernel, 256, 32, stream, out, dequant_mul());
 }
 
 cudaError_t launch_selftest_timeout(unsigned int* err, long long limit_ns, cudaStream_t stream) {
-  selftest_timeout_kernel<<<1, 32, 0, stream>>>(err, limit_ns);
-  return cudaGetLastError();
+  return launch_plain(selftest_timeout_kernel, 1, 32, stream, err, limit_ns);
 }
 
 }  // namespace qmoe
