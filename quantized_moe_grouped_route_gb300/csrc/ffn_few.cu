@@ -2,12 +2,13 @@
 // rows of the MMA and the tokens its columns, so a product is one pass over the weights.
 //
 // A unit is 128 rows of weights (64 of u and the same 64 of g in the first product) by all tokens.
-// Units are fewer than SMs, so a cluster of S CTAs shares one: each takes a segment of K
-// through a ring of TMA-loaded stages into an accumulator in TMEM (tcgen05, M = 128, N = tokens),
-// puts its sums into shared memory, and the CTAs add up each other's by distributed shared memory,
-// every CTA the tokens seg, seg + S, ..; the order of the sums is fixed.  Bound by the stream of the
-// weights; up to 128 tokens two CTAs fit an SM, so that the second product's first weights are already on their way
-// while the first product ends (its launch is programmatic, and only the tokens' copies wait).
+// Units are fewer than SMs, so a cluster of S CTAs shares one: each takes a segment of K through a
+// ring of TMA-loaded stages into an accumulator in TMEM (tcgen05, M = 128, N = tokens), puts its
+// sums into shared memory, and the CTAs add up each other's by distributed shared memory, every CTA
+// the tokens seg, seg + S, ..; the order of the sums is fixed.  Bound by the stream of the weights;
+// up to 128 tokens two CTAs fit an SM, so that the second product's first weights are already on
+// their way while the first product ends (its launch is programmatic, and only the tokens' copies
+// wait).
 // 48 tokens, H = 7168, I = 2048: 22.5 us in a graph (the weights' stream 13.2); 4096 x 1536: 14.8 (5.7).
 #include "cluster.cuh"
 #include "ffn.cuh"

@@ -395,7 +395,8 @@ struct FfnFew : FfnProduct {
   int ksteps, splits, stages, ring_bytes, tmem_cols;
 };
 // As many as an MMA has columns: up to there one pass over the weights is not slower than tiles of
-// 256 tokens are.  us a call in a graph, ffn_few.cu and (behind it) ffn_gemm.cu, of 9, 128, 144, 192 and 256:
+// 256 tokens are.  us a call in a graph of 9, 128, 144, 192 and 256 tokens by ffn_few.cu, and
+// (behind it) by ffn_gemm.cu:
 //   4096 x 1536: 13.3 (23.0), 19.3 (25.4), 19.3 (25.4), 21.1 (25.6), 24.9 (25.9)
 //   7168 x 2048: 20.6 (30.6), 28.4 (37.5), 26.7 (37.6), 29.6 (38.3), 34.9 (39.6)
 //   2048 x 1024: 8.9 (16.5), 14.2 (19.7), 14.6 (19.7), 16.1 (19.8), 19.4 (19.5)

@@ -4,14 +4,15 @@
 //   normed = out * pre_rstd * (offset + pre_weight)    pre_rstd likewise from out
 // in one pass: a row of y and of the residual is read once into registers, and what the row's two
 // sums wait for never leaves them.  out is rounded once, when it is written; normed is made from
-// the sums before that rounding.  Bound by memory: four rows a token where all parts are there.
-// Of many rows each CTA takes one after the other, and copies the next ones to shared memory while
-// a row waits for its sums (norm.cuh), as many CTAs an SM as 1024 threads are: where two rows and the
+// the sums before that rounding.  Bound by memory: four rows a token where all parts are there. Of
+// many rows each CTA takes one after the other, and copies the next ones to shared memory while a
+// row waits for its sums (norm.cuh), as many CTAs an SM as 1024 threads are: where two rows and the
 // vectors fit a CTA's share, in 16 bits with both norms and a residual at 7168 columns, with less
-// beside them at more widths.  Elsewhere, and of few rows, a row has a CTA and comes straight
-// from memory.  8192 rows of 7168 bf16: 81.6 us in a graph, 5.8 TB/s, with a token's gate 87.5 (straight 137);
-// 58.7 million elements straight at 1024 to 5120 and 8192 columns: 81 to 94 us, with a channel's or full gate 95
-// to 120 (full: five matrices), in fp32 half as many 73 to 78 (gated 77 to 124); 16 rows: 3.0 us.
+// beside them at more widths.  Elsewhere, and of few rows, a row has a CTA and comes straight from
+// memory.  8192 rows of 7168 bf16: 81.6 us in a graph, 5.8 TB/s, with a token's gate 87.5 (straight
+// 137); 58.7 million elements straight at 1024 to 5120 and 8192 columns: 81 to 94 us, with a
+// channel's or full gate 95 to 120 (full: five matrices), in fp32 half as many 73 to 78 (gated 77
+// to 124); 16 rows: 3.0 us.
 #include "norm.cuh"
 
 namespace qmoe {

@@ -1,19 +1,19 @@
 // Gradients of the norms after and before a block (norm.cu).  With x^ = out * pre_rstd and
 // y^ = y * post_rstd, w the weights with their offset, <a, b> the mean over a row's elements:
 //   g = dout + pre_rstd * (dnormed w_pre - x^ <dnormed w_pre, x^>)       dpre = sum_m dnormed x^
-//   dresidual = residual_scale * g,   dgate = slope g v (g v summed over what shares a gate),  v = y^ w_post
+//   dresidual = residual_scale * g,   dgate = slope * sum of g v over what shares a gate,  v = y^ w_post
 //   d = gate * g,   dy = post_rstd * (d w_post - y^ <d w_post, y^>)       dpost = sum_m d y^
 // One pass over the rows: four are read and two written a token.  The sums over the tokens stay in
-// the registers of the threads that own the columns; each CTA (or warp) goes through many rows
-// and leaves one row of sums, and a second kernel adds those up in a fixed order.  A CTA that has
-// an SM to itself waits for its own sums, so the next rows are copied meanwhile (norm.cuh).  8192
-// rows of 7168 bf16: 139 us, 5.1 TB/s, and 4 for the second kernel (straight loads 452; with the
-// weights read from memory for each row, which the copies leave no L1 for, 244; rows held in
-// registers beside the sums, 211).  Other widths, 58.7 million elements each (bytes: 105): 4096
-// columns 171 us, 2048 158, 1024 162, where a CTA's up to four rows of shared memory leave no room for
-// all the CTAs that the grid has an SM; gated 170 to 310.  Rows that come straight (past 8192 columns, 660 us and
-// more; half as many elements of fp32 past 5632 columns with both norms and a residual, 650 to 670) spill
-// the registers of 1024 threads.
+// the registers of the threads that own the columns; each CTA (or warp) goes through many rows and
+// leaves one row of sums, and a second kernel adds those up in a fixed order.  A CTA that has an SM
+// to itself waits for its own sums, so the next rows are copied meanwhile (norm.cuh).  8192 rows of
+// 7168 bf16: 139 us, 5.1 TB/s, and 4 for the second kernel (straight loads 452; with the weights
+// read from memory for each row, which the copies leave no L1 for, 244; rows held in registers
+// beside the sums, 211).  Other widths, 58.7 million elements each (bytes: 105): 4096 columns 171
+// us, 2048 158, 1024 162, where a CTA's up to four rows of shared memory leave no room for all the
+// CTAs that the grid has an SM; gated 170 to 310.  Rows that come straight (past 8192 columns, 660
+// us and more; half as many elements of fp32 past 5632 columns with both norms and a residual, 650
+// to 670) spill the registers of 1024 threads.
 #include "norm.cuh"
 
 namespace qmoe {
